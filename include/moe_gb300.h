@@ -164,6 +164,111 @@ int moe_route_presplit(const uint16_t* x, const uint16_t* w_split, const float* 
                        int64_t E, int64_t k, int32_t* ids, float* w, float* logits, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------------- expert choice */
+
+/* Routing from logits that are there already (moe_route's, or a router of the
+ * caller's own), for the choices that moe_route does not make: sigmoid
+ * scores, a balance bias that only chooses, groups of experts, weights that
+ * are not renormalised, a scale.
+ *   s_e = 1 / (1 + exp(-z_e)) (MOE_SCORE_SIGMOID), or softmax(z)_e
+ *   a_e = s_e + bias_e, the value that chooses; without a bias, and with one
+ *         group or MOE_GROUP_MAX, a_e = z_e (s is increasing in z)
+ *   A_g = the largest a_e of the E / n_groups consecutive experts of group g
+ *         (MOE_GROUP_MAX), or the sum of its two largest (MOE_GROUP_TOP2)
+ *   ids = the k largest a_e in the top_groups groups of the largest A_g, the
+ *         largest first; equal values (groups and experts) go to the lower
+ *         index; +0 equals -0, a NaN is above +infinity
+ *   w_j = scale * s_j / (sum of the chosen s) with renorm, else scale * s_j
+ * An expert with z_e = -infinity is masked: it is chosen only where the
+ * chosen groups hold fewer than k others (lowest index first, weight 0), and
+ * adds nothing to its group's A_g.  A row with every expert masked gets
+ * weights 0.  The scores, sums and weights are fp32.
+ *   logits  [T, E] fp32, or bf16 (logits_bf16 != 0)
+ *   bias    [E] fp32 or NULL
+ *   ids     [T, k] int32 (out);  w [T, k] fp32 (out)
+ * Limits: k <= top_groups * E / n_groups, n_groups divides E; k <= 32,
+ * n_groups <= 32, E <= 1024.  A scale that is not finite is refused. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+int moe_route_select(const void* logits, int logits_bf16, const float* bias, int64_t T, int64_t E, int64_t k,
+                     int score, int64_t n_groups, int64_t top_groups, int group_score, int renorm, float scale,
+                     int32_t* ids, float* w, void* stream);
+
+/* The gradient of moe_route_select's weights with respect to the logits, the
+ * choice held fixed (the bias gets none):
+ *   dw[t,j] = sum_n dw_part[row_map[t*k+j], n]     (fixed order; row_map NULL:
+ *                                                   row t*k+j, so that with
+ *                                                   nparts 1 dw_part is dw)
+ *   sigmoid, renorm:  q_j = s_j / sum s, d_j = scale q_j (dw_j - sum_i q_i dw_i) (1 - s_j)
+ *   sigmoid:          d_j = scale s_j (1 - s_j) dw_j
+ *   softmax, renorm:  d_j = scale q_j (dw_j - sum_i q_i dw_i)
+ *   softmax:          d_e = scale s_e ([e chosen] dw_e - sum_i s_i dw_i) for EVERY expert e
+ * d_logits[t, ids[t,j]] = d_j and 0 at the other experts, but for the dense
+ * last form.  Masked experts (logit -infinity) get 0.
+ *   dw_part  [T*k, nparts] fp32; row_map [T*k] int32 or NULL
+ *   logits, ids  as in the forward;  d_logits [T, E] (out) of the logits' type
+ *   dw       [T, k] fp32 (out, nullable)
+ * Slots of one token name distinct experts.  An id outside [0, E) or a
+ * row_map entry outside [0, T*k) sets MOE_ERR_DEVICE (the slot is left out,
+ * row 0 is read). */
+int moe_route_select_bwd(const float* dw_part, int64_t nparts, const int32_t* row_map, const void* logits,
+                         int logits_bf16, const int32_t* ids, int64_t T, int64_t E, int64_t k, int score, int renorm,
+                         float scale, void* d_logits, float* dw, void* stream);
+
+/* The balance bias after a step: out_e = bias_e + rate * sign(mean load -
+ * load_e), load_e = counts[e] (moe_permute's counts, >= 0), compared in integers; an
+ * expert at the mean keeps its bias.  out may be bias.  E <= 1024. */
+int moe_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, float rate, float* out,
+                           void* stream);
+
+/* -------------------------------------------------------- 4-bit experts */
+
+/* The experts of a decode batch from 4-bit weights with group scales: for few
+ * tokens the bytes of the experts' weights are the cost.  Per expert, over
+ * the fused layouts of the bf16 GEMMs (K rows, N columns: gate_up K = H,
+ * N = 2I; down K = I, N = H):
+ *   W[r, n] = scale[r / group, n] * (q[r, n] - zero[r / group, n])
+ *   qweight  [E*K/8, N] 32-bit words: word [r/8, n] holds the 4-bit codes q of
+ *            rows r .. r+7 (r % 8 == 0) of column n, lowest nibble first
+ *   scales   [E*K/group, N] bf16
+ *   zeros    [E*K/group, N] bytes 0..15, or NULL for 8 everywhere
+ * group is 32, 64 or 128 and divides K; K and I are multiples of 64.
+ *
+ * Slots: ids [T, k] int32 names the expert of slot (t, j); the rows of h are
+ * in slot order (no permutation).  An id of -1 is an empty slot (a padded
+ * token): its h row is zero and it adds nothing to y, whatever h and w hold
+ * there.  Another id outside [0, E) sets MOE_ERR_DEVICE and is taken as
+ * empty.  ids NULL (E and k must be 1): one dense expert for every token.
+ * Codes minus zeros are exact integers, their products with the bf16 rows
+ * are summed in fp32 over each group and scaled in fp32. */
+
+/* h[t,j] = silu(x_t . Wg) * (x_t . Wu), e = ids[t,j], gate columns 0..I-1 of
+ * the expert's block and up columns I..2I-1.  x [T, H] bf16; h [T, k, I] bf16
+ * (out, one rounding). */
+int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t* qweight, const uint16_t* scales,
+                          const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t group,
+                          uint16_t* h, void* stream);
+
+/* y[t] = sum_j w[t,j] (h[t,j] . Wd) (+ y_shared[t]), summed in fp32 in
+ * increasing j.  h [T, k, I] bf16; w [T, k] fp32 (NULL: weight 1); y_shared
+ * [T, H] bf16 or NULL; y [T, H] bf16 (out). */
+int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
+                        const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
+                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* stream);
+
+/* bf16 weights [rows, N] to the layout above (rows = E*K), nearest codes, and
+ * back.  zeros NULL: scale = bf16(max|W| / 7) of each group, codes
+ * clamp(rint(W / scale) + 8, 0, 15).  With zeros: scale = bf16((max(W, 0) -
+ * min(W, 0)) / 15), zero = min(rint(-min(W, 0) / scale), 15), codes
+ * clamp(rint(W / scale) + zero, 0, 15).  A group of zeros has scale 0.  The weights
+ * must be finite.  Dequantised: scale * (q - zero) rounded to bf16. */
+int moe_w4_quantize(const uint16_t* weight, int64_t rows, int64_t N, int64_t group, uint32_t* qweight,
+                    uint16_t* scales, uint8_t* zeros, void* stream);
+int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t N,
+                      int64_t group, uint16_t* weight, void* stream);
+
 /* ---------------------------------------------------------------- permute */
 
 /* Bytes of workspace moe_permute needs: per-block expert histograms, the

@@ -15,6 +15,7 @@ P = ctypes.c_void_p
 I64 = ctypes.c_int64
 SZ = ctypes.c_size_t
 INT = ctypes.c_int
+F32 = ctypes.c_float
 
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
@@ -34,6 +35,13 @@ SIGNATURES = {
     "moe_route_split_weight": [P, I64, I64, P, P],
     "moe_route_presplit_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
     "moe_route_presplit": [P, P, P, I64, I64, I64, I64, P, P, P, P, SZ, P],
+    "moe_route_select": [P, INT, P, I64, I64, I64, INT, I64, I64, INT, INT, F32, P, P, P],
+    "moe_route_select_bwd": [P, I64, P, P, INT, P, I64, I64, I64, INT, INT, F32, P, P, P],
+    "moe_route_balance_bias": [P, P, I64, F32, P, P],
+    "moe_w4_gate_up_swiglu": [P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P],
+    "moe_w4_down_combine": [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P],
+    "moe_w4_quantize": [P, I64, I64, I64, P, P, P, P],
+    "moe_w4_dequantize": [P, P, P, I64, I64, I64, P, P],
     "moe_permute_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
     "moe_permute": [P, P, I64, I64, I64, P, P, P, P, P, P, SZ, P],
     "moe_permute_noalloc": [P, P, I64, I64, I64, P, P, P, P, P, P],

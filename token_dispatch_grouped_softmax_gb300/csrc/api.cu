@@ -198,6 +198,125 @@ int moe_route_presplit(const uint16_t* x, const uint16_t* w_split, const float* 
                                                 static_cast<cudaStream_t>(stream)));
 }
 
+/* ------------------------------------------------------- expert choice */
+
+int moe_route_select(const void* logits, int logits_bf16, const float* bias, int64_t T, int64_t E, int64_t k,
+                     int score, int64_t n_groups, int64_t top_groups, int group_score, int renorm, float scale,
+                     int32_t* ids, float* w, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || T > kMaxI32 || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
+  if (n_groups < 1 || top_groups < 1 || top_groups > n_groups || E % n_groups != 0 || k > top_groups * (E / n_groups))
+    return MOE_ERR_INVALID_ARG;
+  if (score < 0 || score > 1 || group_score < 0 || group_score > 1) return MOE_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;   // NaN or infinite
+  if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
+  if (E > moe::kMaxExperts || k > 32 || n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && !aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const moe::RouteChoice c{score == MOE_SCORE_SIGMOID, group_score == MOE_GROUP_TOP2, renorm != 0, (int)n_groups,
+                           (int)top_groups, scale};
+  return cuda_status(moe::launch_route_select(logits, logits_bf16 != 0, bias, T, E, k, c, ids, w,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_select_bwd(const float* dw_part, int64_t nparts, const int32_t* row_map, const void* logits,
+                         int logits_bf16, const int32_t* ids, int64_t T, int64_t E, int64_t k, int score, int renorm,
+                         float scale, void* d_logits, float* dw, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || k > E || nparts < 1 || nparts > kMaxI32 || T > kMaxI32 || T * k > kMaxI32)
+    return MOE_ERR_INVALID_ARG;
+  if (score < 0 || score > 1) return MOE_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dw_part || !logits || !ids || !d_logits)) return MOE_ERR_INVALID_ARG;
+  if (E > moe::kMaxExperts || k > 32) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!aligned16(logits) || !aligned16(d_logits))) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  moe::DeviceInfo dev;
+  const int rc = moe::current_device(&dev);
+  if (rc != MOE_OK) return rc;
+  const moe::RouteChoice c{score == MOE_SCORE_SIGMOID, 0, renorm != 0, 1, 1, scale};
+  return cuda_status(moe::launch_route_select_bwd(dw_part, (int)nparts, row_map, logits, logits_bf16 != 0, ids, T, E,
+                                                  k, c, d_logits, dw, dev.status,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, float rate, float* out,
+                           void* stream) {
+  if (E < 1 || !bias || !counts || !out || !(rate - rate == 0.f)) return MOE_ERR_INVALID_ARG;
+  if (E > moe::kMaxExperts) return MOE_ERR_UNSUPPORTED;
+  return cuda_status(moe::launch_route_balance_bias(bias, counts, E, rate, out, static_cast<cudaStream_t>(stream)));
+}
+
+/* -------------------------------------------------------- 4-bit experts */
+
+namespace {
+
+// What every call on 4-bit weights checks: sizes, K a multiple of the group
+// and N of 64, pointers.
+int w4_check(const uint32_t* qweight, const uint16_t* scales, int64_t E, int64_t K, int64_t N, int64_t group) {
+  if (E < 1 || K < 1 || N < 1 || !qweight || !scales) return MOE_ERR_INVALID_ARG;
+  if (E > moe::kMaxExperts || K > kMaxI32 || N > kMaxI32) return MOE_ERR_UNSUPPORTED;
+  if ((group != 32 && group != 64 && group != 128) || K % 64 != 0 || K % group != 0 || N % 64 != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(qweight) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t* qweight, const uint16_t* scales,
+                          const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t group,
+                          uint16_t* h, void* stream) {
+  if (T < 0 || k < 1 || k > E || I < 1 || T > kMaxI32 || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
+  if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
+  const int rc0 = w4_check(qweight, scales, E, H, 2 * I, group);
+  if (rc0 != MOE_OK) return rc0;
+  if (k > 32 || I % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!x || !h || !aligned16(x) || !aligned16(h) || !aligned16(zeros))) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  moe::DeviceInfo dev;
+  const int rc = moe::current_device(&dev);
+  if (rc != MOE_OK) return rc;
+  return cuda_status(moe::launch_w4_gate_up(x, ids, qweight, scales, zeros, T, H, E, k, I, group, h, dev,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
+                        const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
+                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* stream) {
+  if (T < 0 || k < 1 || k > E || I < 1 || T > kMaxI32 || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
+  if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
+  const int rc0 = w4_check(qweight, scales, E, I, H, group);
+  if (rc0 != MOE_OK) return rc0;
+  if (k > 32) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!h || !y || !aligned16(h) || !aligned16(y) || !aligned16(zeros) || !aligned16(y_shared)))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  moe::DeviceInfo dev;
+  const int rc = moe::current_device(&dev);
+  if (rc != MOE_OK) return rc;
+  return cuda_status(moe::launch_w4_down(h, ids, w, qweight, scales, zeros, y_shared, T, H, E, k, I, group, y, dev,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4_quantize(const uint16_t* weight, int64_t rows, int64_t N, int64_t group, uint32_t* qweight,
+                    uint16_t* scales, uint8_t* zeros, void* stream) {
+  if (!weight) return MOE_ERR_INVALID_ARG;
+  const int rc = w4_check(qweight, scales, 1, rows, N, group);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16(weight) || !aligned16(zeros)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_w4_quantize(weight, rows, N, group, qweight, scales, zeros,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t N,
+                      int64_t group, uint16_t* weight, void* stream) {
+  if (!weight) return MOE_ERR_INVALID_ARG;
+  const int rc = w4_check(qweight, scales, 1, rows, N, group);
+  if (rc != MOE_OK) return rc;
+  if (!aligned16(weight) || !aligned16(zeros)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_w4_dequantize(qweight, scales, zeros, rows, N, group, weight,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
 /* ---------------------------------------------------------------- permute */
 
 int moe_permute_workspace_size(int64_t T, int64_t k, int64_t E, size_t* bytes) {

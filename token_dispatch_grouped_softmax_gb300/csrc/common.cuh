@@ -22,6 +22,8 @@ enum : uint32_t {
   kKernPermute = 2,
   kKernGemm = 3,
   kKernCombine = 4,
+  kKernRouteSelect = 5,
+  kKernW4 = 6,
 };
 
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t code, uint32_t kernel,

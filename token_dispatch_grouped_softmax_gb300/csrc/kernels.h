@@ -106,6 +106,34 @@ cudaError_t launch_gather_dx(const uint16_t* dx_perm, const int32_t* row_map, co
 cudaError_t launch_route_bwd_weight(const uint16_t* x, const float* d_logits, int64_t T, int64_t H,
                                     int64_t E, float* d_w_router, cudaStream_t stream);
 
+// How moe_route_select chooses (route_select.cu).
+struct RouteChoice {
+  int sigmoid, top2, renorm;
+  int groups, top_groups;
+  float scale;
+};
+cudaError_t launch_route_select(const void* logits, bool bf16, const float* bias, int64_t T, int64_t E, int64_t k,
+                                const RouteChoice& c, int32_t* ids, float* w, cudaStream_t stream);
+cudaError_t launch_route_select_bwd(const float* dw_part, int nparts, const int32_t* row_map, const void* logits,
+                                    bool bf16, const int32_t* ids, int64_t T, int64_t E, int64_t k,
+                                    const RouteChoice& c, void* d_logits, float* dw, uint32_t* status,
+                                    cudaStream_t stream);
+cudaError_t launch_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, float rate, float* out,
+                                      cudaStream_t stream);
+
+// 4-bit experts of a decode batch (w4.cu).
+cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint32_t* q, const uint16_t* scales,
+                              const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I,
+                              int64_t group, uint16_t* h, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* wt, const uint32_t* q,
+                           const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T,
+                           int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y,
+                           const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64_t group, uint32_t* q,
+                               uint16_t* scales, uint8_t* zeros, cudaStream_t stream);
+cudaError_t launch_w4_dequantize(const uint32_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t rows,
+                                 int64_t N, int64_t group, uint16_t* w, cudaStream_t stream);
+
 // Expert-parallel dispatch pieces (ep.cu).
 size_t sort_chunks_workspace_bytes(int64_t A, int64_t B);
 cudaError_t launch_sort_chunks(const int32_t* counts, int64_t A, int64_t B, int64_t N, int32_t* src_of,

@@ -140,6 +140,202 @@ def route_split_weight(w_router, out=None):
     return w_split
 
 
+# ----------------------------------------------------------- expert choice
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError("%s must be one of %s" % (name, ", ".join(sorted(table))))
+    return table[value]
+
+
+def _need_logits(t, name="logits"):
+    if isinstance(t, torch.Tensor) and t.dtype == _BF16:
+        return _need(t, name, _BF16, 2)
+    return _need(t, name, torch.float32, 2)
+
+
+def route_select(logits, k, bias=None, score="softmax", n_groups=1, top_groups=1, group_score="top2", renorm=True,
+                 scale=1.0):
+    """ids [T, k] int32 and w [T, k] fp32 chosen from logits [T, E] (fp32 or bf16).
+
+    score "softmax" or "sigmoid"; bias [E] fp32 is added to the scores for the
+    choice alone; the top_groups best of n_groups groups of E / n_groups
+    consecutive experts take part, a group's value being its best expert's
+    ("max") or the sum of its two best ("top2"); renorm divides the chosen
+    scores by their sum; scale multiplies them.  A logit of -inf masks its
+    expert.  Equal values go to the lower index (moe_route_select)."""
+    _need_logits(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, 1)
+        if bias.shape[0] != E:
+            raise ValueError("bias must be [E]")
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    call("moe_route_select", _p(logits), logits.dtype == _BF16, _p(bias), T, E, k, _choice(_SCORES, score, "score"),
+         n_groups, top_groups, _choice(_GROUP_SCORES, group_score, "group_score"), bool(renorm), scale, _p(ids), _p(w),
+         _stream())
+    return ids, w
+
+
+def route_select_bwd(dw, logits, ids, score="softmax", renorm=True, scale=1.0, row_map=None):
+    """d_logits [T, E] of logits' type: the gradient of route_select's w for
+    upstream dw [T, k] fp32, the choice held fixed.
+
+    With row_map [T*k], dw is dw_part [T*k, nparts] from
+    grouped_gemm_down_bwd (permuted rows, summed here), and (d_logits, dw
+    [T, k]) is returned.  Softmax without renorm has a dense gradient."""
+    _need(dw, "dw", torch.float32, 2)
+    _need_logits(logits)
+    _need(ids, "ids", torch.int32, 2)
+    T, E = logits.shape
+    k = ids.shape[1]
+    if ids.shape[0] != T:
+        raise ValueError("ids must be [T, k]")
+    d_logits = torch.empty_like(logits)
+    dw_sum = None
+    nparts = 1
+    if row_map is not None:
+        _need(row_map, "row_map", torch.int32, 1)
+        if row_map.shape[0] != T * k or dw.shape[0] != T * k:
+            raise ValueError("row_map must hold T*k entries and dw must be [T*k, nparts]")
+        nparts = dw.shape[1]
+        dw_sum = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    elif dw.shape != ids.shape:
+        raise ValueError("dw must be [T, k]")
+    call("moe_route_select_bwd", _p(dw), nparts, _p(row_map), _p(logits), logits.dtype == _BF16, _p(ids), T, E, k,
+         _choice(_SCORES, score, "score"), bool(renorm), scale, _p(d_logits), _p(dw_sum), _stream())
+    return d_logits if row_map is None else (d_logits, dw_sum)
+
+
+def route_balance_bias(bias, counts, rate, out=None):
+    """bias + rate * sign(mean load - load) [E] fp32, the loads being permute's
+    counts [E] int32; out: an existing [E] fp32 tensor (bias itself to update in place)."""
+    _need(bias, "bias", torch.float32, 1)
+    _need(counts, "counts", torch.int32, 1)
+    E = bias.shape[0]
+    if counts.shape[0] != E:
+        raise ValueError("counts must be [E]")
+    if out is None:
+        out = torch.empty_like(bias)
+    else:
+        _need(out, "out", torch.float32, 1)
+        if out.shape[0] != E:
+            raise ValueError("out must be [E]")
+    call("moe_route_balance_bias", _p(bias), _p(counts), E, rate, _p(out), _stream())
+    return out
+
+
+# ----------------------------------------------------------- 4-bit experts
+
+def _w4(qweight, scales, zeros, K, N=None):
+    """(E, N, group) of 4-bit weights with K rows per expert."""
+    _need(qweight, "qweight", torch.int32, 2)
+    _need(scales, "scales", _BF16, 2)
+    words, n = qweight.shape
+    if K < 8 or K % 8 or words % (K // 8) or (N is not None and n != N):
+        raise ValueError("qweight must be [E*K/8, N] with K = %d%s" % (K, "" if N is None else ", N = %d" % N))
+    E = words // (K // 8)
+    if scales.shape[1] != n or E == 0 or scales.shape[0] % E or scales.shape[0] == 0 or K % (scales.shape[0] // E):
+        raise ValueError("scales must be [E*K/group, N]")
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, 2)
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must be [E*K/group, N]")
+    return E, n, K * E // scales.shape[0]
+
+
+def _w4_ids(ids, T, E):
+    """k of the slots' experts ids [T, k] (None: one dense expert)."""
+    if ids is None:
+        if E != 1:
+            raise ValueError("ids are needed with more than one expert")
+        return 1
+    _need(ids, "ids", torch.int32, 2)
+    if ids.shape[0] != T:
+        raise ValueError("ids must be [T, k]")
+    return ids.shape[1]
+
+
+def w4_gate_up_swiglu(x, ids, qweight, scales, zeros=None):
+    """h [T, k, I] bf16 with h[t, j] = silu(x_t . Wg) * (x_t . Wu) of the 4-bit
+    expert ids[t, j] (an id of -1: an empty slot, h = 0); rows in slot order.
+
+    qweight [E*H/8, 2I] int32 (eight 4-bit codes of consecutive rows per
+    word, lowest nibble first), scales [E*H/group, 2I] bf16, zeros of the same
+    shape uint8 or None for 8 (w4_quantize makes them).  ids None: one dense
+    expert."""
+    _need(x, "x", _BF16, 2)
+    T, H = x.shape
+    E, N, group = _w4(qweight, scales, zeros, H)
+    if N % 2:
+        raise ValueError("qweight must be [E*H/8, 2I]")
+    k = _w4_ids(ids, T, E)
+    h = torch.empty((T, k, N // 2), dtype=_BF16, device=x.device)
+    call("moe_w4_gate_up_swiglu", _p(x), _p(ids), _p(qweight), _p(scales), _p(zeros), T, H, E, k, N // 2, group,
+         _p(h), _stream())
+    return h
+
+
+def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=None):
+    """y [T, H] bf16 with y_t = sum_j w[t, j] (h[t, j] . Wd) (+ y_shared_t), e =
+    ids[t, j] (-1 adds nothing); h [T, k, I] bf16 in slot order, w [T, k] fp32
+    (None: 1), qweight [E*I/8, H] and scales [E*I/group, H] as in
+    w4_gate_up_swiglu.  ids None: one dense expert."""
+    _need(h, "h", _BF16, 3)
+    T, k, I = h.shape
+    E, H, group = _w4(qweight, scales, zeros, I)
+    if _w4_ids(ids, T, E) != k:
+        raise ValueError("h must be [T, k, I] and ids [T, k]")
+    if w is not None:
+        _need(w, "w", torch.float32, 2)
+        if tuple(w.shape) != (T, k):
+            raise ValueError("w must be [T, k]")
+    if y_shared is not None:
+        _need(y_shared, "y_shared", _BF16, 2)
+        if tuple(y_shared.shape) != (T, H):
+            raise ValueError("y_shared must be [T, H]")
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=h.device)
+    else:
+        _need(out, "out", _BF16, 2)
+        if tuple(out.shape) != (T, H):
+            raise ValueError("out must be [T, H]")
+    call("moe_w4_down_combine", _p(h), _p(ids), _p(w), _p(qweight), _p(scales), _p(zeros), _p(y_shared), T, H, E, k,
+         I, group, _p(out), _stream())
+    return out
+
+
+def w4_quantize(weight, group=128, zeros=False):
+    """(qweight [rows/8, N] int32, scales [rows/group, N] bf16, zeros uint8 or
+    None) of bf16 weights [rows, N] (gate_up [E*H, 2I] or down [E*I, H]),
+    group rows of a column sharing a scale (and a zero point with zeros=True)."""
+    _need(weight, "weight", _BF16, 2)
+    rows, N = weight.shape
+    if group not in (32, 64, 128) or rows % group:
+        raise ValueError("group must be 32, 64 or 128 and divide the rows")
+    dev = weight.device
+    q = torch.empty((rows // 8, N), dtype=torch.int32, device=dev)
+    scales = torch.empty((rows // group, N), dtype=_BF16, device=dev)
+    z = torch.empty((rows // group, N), dtype=torch.uint8, device=dev) if zeros else None
+    call("moe_w4_quantize", _p(weight), rows, N, group, _p(q), _p(scales), _p(z), _stream())
+    return q, scales, z
+
+
+def w4_dequantize(qweight, scales, zeros=None):
+    """bf16 weights [rows, N] of w4_quantize's layout: scale * (code - zero), one rounding."""
+    _need(qweight, "qweight", torch.int32, 2)
+    rows = qweight.shape[0] * 8
+    _, N, group = _w4(qweight, scales, zeros, rows)
+    w = torch.empty((rows, N), dtype=_BF16, device=qweight.device)
+    call("moe_w4_dequantize", _p(qweight), _p(scales), _p(zeros), rows, N, group, _p(w), _stream())
+    return w
+
+
 def permute(ids, E, w=None):
     """counts [E], offsets [E+1], row_map [R], src_row [R] (int32), and with w
     [T,k] fp32 also w_perm [R] fp32 (the gate weight of each permuted row)."""
