@@ -253,10 +253,13 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
 
 /* y[t] = sum_j w[t,j] (h[t,j] . Wd) (+ y_shared[t]), summed in fp32 in
  * increasing j.  h [T, k, I] bf16; w [T, k] fp32 (NULL: weight 1); y_shared
- * [T, H] bf16 or NULL; y [T, H] bf16 (out). */
+ * [T, H] bf16 or NULL; y [T, H] bf16 (out).  The workspace holds the slots'
+ * fp32 products. */
+int moe_w4_down_workspace_size(int64_t T, int64_t H, int64_t k, size_t* bytes);
 int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
                         const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
-                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* stream);
+                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* bf16 weights [rows, N] to the layout above (rows = E*K), nearest codes, and
  * back.  zeros NULL: scale = bf16(max|W| / 7) of each group, codes

@@ -39,7 +39,8 @@ SIGNATURES = {
     "moe_route_select_bwd": [P, I64, P, P, INT, P, I64, I64, I64, INT, INT, F32, P, P, P],
     "moe_route_balance_bias": [P, P, I64, F32, P, P],
     "moe_w4_gate_up_swiglu": [P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P],
-    "moe_w4_down_combine": [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P],
+    "moe_w4_down_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+    "moe_w4_down_combine": [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P, SZ, P],
     "moe_w4_quantize": [P, I64, I64, I64, P, P, P, P],
     "moe_w4_dequantize": [P, P, P, I64, I64, I64, P, P],
     "moe_permute_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],

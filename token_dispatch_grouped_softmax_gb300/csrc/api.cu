@@ -253,7 +253,7 @@ namespace {
 // and N of 64, pointers.
 int w4_check(const uint32_t* qweight, const uint16_t* scales, int64_t E, int64_t K, int64_t N, int64_t group) {
   if (E < 1 || K < 1 || N < 1 || !qweight || !scales) return MOE_ERR_INVALID_ARG;
-  if (E > moe::kMaxExperts || K > kMaxI32 || N > kMaxI32) return MOE_ERR_UNSUPPORTED;
+  if (N > (int64_t)1 << 20) return MOE_ERR_UNSUPPORTED;
   if ((group != 32 && group != 64 && group != 128) || K % 64 != 0 || K % group != 0 || N % 64 != 0)
     return MOE_ERR_UNSUPPORTED;
   if (!aligned16(qweight) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
@@ -269,7 +269,7 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
   if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
   const int rc0 = w4_check(qweight, scales, E, H, 2 * I, group);
   if (rc0 != MOE_OK) return rc0;
-  if (k > 32 || I % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  if (E > moe::kMaxExperts || H > (int64_t)1 << 20 || k > 32 || I % 64 != 0) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!x || !h || !aligned16(x) || !aligned16(h) || !aligned16(zeros))) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   moe::DeviceInfo dev;
@@ -279,22 +279,31 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
                                             static_cast<cudaStream_t>(stream)));
 }
 
+int moe_w4_down_workspace_size(int64_t T, int64_t H, int64_t k, size_t* bytes) {
+  if (!bytes || T < 0 || H < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  *bytes = moe::w4_down_workspace_bytes(T, k, H);
+  return MOE_OK;
+}
+
 int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
                         const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
-                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* stream) {
+                        int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   if (T < 0 || k < 1 || k > E || I < 1 || T > kMaxI32 || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
   if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
   const int rc0 = w4_check(qweight, scales, E, I, H, group);
   if (rc0 != MOE_OK) return rc0;
-  if (k > 32) return MOE_ERR_UNSUPPORTED;
+  if (E > moe::kMaxExperts || I > (int64_t)1 << 20 || k > 32) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!h || !y || !aligned16(h) || !aligned16(y) || !aligned16(zeros) || !aligned16(y_shared)))
     return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < moe::w4_down_workspace_bytes(T, k, H)))
+    return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;
   moe::DeviceInfo dev;
   const int rc = moe::current_device(&dev);
   if (rc != MOE_OK) return rc;
-  return cuda_status(moe::launch_w4_down(h, ids, w, qweight, scales, zeros, y_shared, T, H, E, k, I, group, y, dev,
-                                         static_cast<cudaStream_t>(stream)));
+  return cuda_status(moe::launch_w4_down(h, ids, w, qweight, scales, zeros, y_shared, T, H, E, k, I, group, y,
+                                         workspace, dev, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_w4_quantize(const uint16_t* weight, int64_t rows, int64_t N, int64_t group, uint32_t* qweight,

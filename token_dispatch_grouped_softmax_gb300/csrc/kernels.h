@@ -127,8 +127,9 @@ cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint3
                               int64_t group, uint16_t* h, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* wt, const uint32_t* q,
                            const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T,
-                           int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y,
+                           int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* ws,
                            const DeviceInfo& dev, cudaStream_t stream);
+size_t w4_down_workspace_bytes(int64_t T, int64_t k, int64_t H);
 cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64_t group, uint32_t* q,
                                uint16_t* scales, uint8_t* zeros, cudaStream_t stream);
 cudaError_t launch_w4_dequantize(const uint32_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t rows,

@@ -14,91 +14,430 @@ namespace moe {
 
 namespace {
 
-constexpr int kW4Cols = 128;   // columns (threads) per block
+constexpr int kW4Warps = 8;
+constexpr int kW4Threads = 32 * kW4Warps;
+constexpr int kW4MaxSlots = 2048;   // slots of one launch row (shared-memory lists)
 
-struct W4View {
+struct W4Params {
+  const uint16_t* rows;    // gate_up: x [T, K]; down: h [slots, K]
+  const int32_t* ids;      // [slots], NULL: one dense expert
   const uint32_t* q;
   const uint16_t* scales;
   const uint8_t* zeros;
-  int K, N, group;
+  uint16_t* h;             // gate_up's output [slots, N / 2]
+  float* part;             // down's products [slots, N]
+  uint32_t* status;
+  int K, N, E, k;
+  int slots, slots_per_row;
+  int group_units;         // units of 32 k in a group
+  int blocks;              // column blocks: 32 gate and 32 up columns, or 64 columns
 };
 
-// sum_k row[k] * W[k, n] of one column of expert e: the codes' integer
-// products are summed per group in fp32 and scaled once per group.
-__device__ __forceinline__ float w4_dot(const W4View& w, int e, int n, const float* row) {
-  float acc = 0.f;
-  const int words = w.group / 8;
-  const uint32_t* q = w.q + (int64_t)e * (w.K / 8) * w.N + n;
-  const int64_t g0 = (int64_t)e * (w.K / w.group);
-  for (int g = 0; g < w.K / w.group; ++g) {
-    const float zero = w.zeros ? (float)w.zeros[(g0 + g) * w.N + n] : 8.f;
-    float part = 0.f;
-    for (int r = 0; r < words; ++r) {
-      const uint32_t word = q[(int64_t)(g * words + r) * w.N];
-      const float* x = row + (g * words + r) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) part = fmaf((float)((word >> (4 * i)) & 15u) - zero, x[i], part);
-    }
-    acc = fmaf(__uint_as_float((uint32_t)w.scales[(g0 + g) * w.N + n] << 16), part, acc);
-  }
-  return acc;
+// A stage of a warp's ring: 32 k of 2 x 32 columns, of 8 NT rows, and the
+// columns' scales and zeros.
+template <int NT>
+struct W4Ring {
+  static constexpr int kQ = 0, kX = 1024, kScale = kX + 512 * NT, kZero = kScale + 128, kStage = kZero + 64;
+  static constexpr int kDepth = NT == 1 ? 6 : 4;
+  static constexpr int kRed = 16 * NT * 33;   // floats of one warp's partial sums
+};
+
+static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<2>::kDepth * W4Ring<2>::kStage, "the sort's counts fit the rings");
+
+// An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
+// of 8 NT rows numbered from chunk0.
+struct W4Active {
+  int expert, row0, rows, chunk0;
+};
+
+template <int NT>
+__host__ __device__ constexpr int w4_smem(int E, int slots) {
+  return kW4Warps * (W4Ring<NT>::kDepth * W4Ring<NT>::kStage + W4Ring<NT>::kRed * 4) + E * (int)sizeof(W4Active) +
+         (slots * 2 + 15) / 16 * 16 + 64;
 }
 
-// The expert of a slot: -1 when it is empty; ids NULL is one dense expert.
-__device__ __forceinline__ int slot_expert(const int32_t* ids, int64_t slot, int E, uint32_t* status) {
-  if (!ids) return 0;
-  const int e = ids[slot];
-  if (e < -1 || e >= E) {
-    report_status(status, kStatusDevice, kKernW4, 1);
-    return -1;
-  }
-  return e;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or 16 zero bytes without reading src.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__global__ void __launch_bounds__(kW4Cols) w4_gate_up_kernel(const uint16_t* __restrict__ x,
-                                                             const int32_t* __restrict__ ids, const W4View w, int E,
-                                                             int k, int I, uint16_t* __restrict__ h,
-                                                             uint32_t* status) {
-  extern __shared__ float row[];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t slot = blockIdx.x;
-  const int n = blockIdx.y * kW4Cols + threadIdx.x;
-  const int e = slot_expert(ids, slot, E, status);
-  for (int c = threadIdx.x; c < w.K; c += kW4Cols) row[c] = __uint_as_float((uint32_t)x[slot / k * w.K + c] << 16);
+// D += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Codes i and i + 4 of a word less the zero, as two bf16: 128 + code is the
+// bf16 0x4300 | code, and the difference of two such integers is exact.
+// zero2: 128 + zero in both halves.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t zero2) {
+  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&zero2));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// The experts of the slots of this launch row, and each expert's slots in
+// increasing order: a stable counting sort in shared memory (every block
+// sorts for itself and must find the same chunks).  Warp w counts and places
+// its eighth of the slots; cnt is [8][E] scratch.  Returns the number of
+// chunks.
+template <int NT>
+__device__ __forceinline__ int w4_lists(const W4Params& p, int slot0, int slots, int* cnt, W4Active* act,
+                                        uint16_t* list, uint64_t* warp_sum64) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kW4Warps * p.E; i += kW4Threads) cnt[i] = 0;
   __syncthreads();
-  if (n >= I) return;
-  float v = 0.f;
-  if (e >= 0) {
-    const float g = w4_dot(w, e, n, row), u = w4_dot(w, e, I + n, row);
-    v = g / (1.f + expf(-g)) * u;
+  const int s_begin = slots * warp / kW4Warps, s_end = slots * (warp + 1) / kW4Warps;
+  int* mine = cnt + warp * p.E;
+  auto expert_of = [&](int i) {   // -1: an empty slot, or none
+    if (i >= s_end) return -1;
+    const int e = p.ids ? p.ids[slot0 + i] : 0;
+    if (e >= 0 && e < p.E) return e;
+    if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+    return -1;
+  };
+  for (int i0 = s_begin; i0 < s_end; i0 += 32) {
+    const int e = expert_of(i0 + lane);
+    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
   }
-  h[slot * I + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  __syncthreads();
+  // thread i: experts [i * per, (i + 1) * per); prefix of (rows, experts, chunks)
+  const int per = (p.E + kW4Threads - 1) / kW4Threads;
+  auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + 8 * NT - 1) / (8 * NT)) << 40; };
+  uint64_t sum = 0;
+  for (int q = 0; q < per; ++q) {
+    const int e = tid * per + q;
+    if (e >= p.E) break;
+    int n = 0;
+    for (int w = 0; w < kW4Warps; ++w) n += cnt[w * p.E + e];
+    if (n) sum += packed(n);
+  }
+  uint64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) warp_sum64[warp] = incl;
+  __syncthreads();
+  uint64_t before = incl - sum, total = 0;
+  for (int w = 0; w < kW4Warps; ++w) {
+    const uint64_t s = warp_sum64[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  for (int q = 0; q < per; ++q) {
+    const int e = tid * per + q;
+    if (e >= p.E) break;
+    const int row0 = (int)(before & 0xFFFFF);
+    int n = 0;
+    for (int w = 0; w < kW4Warps; ++w) {   // counts to first places
+      const int c = cnt[w * p.E + e];
+      cnt[w * p.E + e] = row0 + n;
+      n += c;
+    }
+    if (n) {
+      act[(int)(before >> 20 & 0xFFFFF)] = W4Active{e, row0, n, (int)(before >> 40)};
+      before += packed(n);
+    }
+  }
+  __syncthreads();
+  for (int i0 = s_begin; i0 < s_end; i0 += 32) {
+    const int e = expert_of(i0 + lane);
+    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    int place = 0;
+    if (e >= 0) {
+      place = mine[e] + __popc(peers & ((1u << lane) - 1u));
+      list[place] = (uint16_t)(i0 + lane);
+    }
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] = place + __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  return (int)(total >> 40);
 }
 
-__global__ void __launch_bounds__(kW4Cols) w4_down_kernel(const uint16_t* __restrict__ h,
-                                                          const int32_t* __restrict__ ids,
-                                                          const float* __restrict__ wt, const W4View w, int E, int k,
-                                                          const uint16_t* __restrict__ y_shared,
-                                                          uint16_t* __restrict__ y, uint32_t* status) {
-  extern __shared__ float row[];
+// Persistent: a block takes consecutive items (chunk of an expert's rows,
+// column block); its 8 warps split K, each streaming its own 32-k units
+// through a ring of lane-private copies, and add their sums in warp order.
+//
+// Per unit a lane holds one 16-byte vector of codes per column set: columns
+// 4g .. 4g+3 (g = lane / 4), k = 8t .. 8t+7 (t = lane % 4).  The k order
+// inside an mma is free as long as A and B agree: step s of the unit takes
+// codes (2s, 2s+4) and (2s+1, 2s+5) of the word, and the same of x.  A rows
+// are weight columns (two tiles a set), B columns the expert's rows.
+template <int NT, bool GATE_UP>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
+  using Ring = W4Ring<NT>;
+  extern __shared__ __align__(128) uint8_t w4_smem_raw[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = w4_smem_raw + warp * (Ring::kDepth * Ring::kStage);
+  float* red = reinterpret_cast<float*>(w4_smem_raw + kW4Warps * Ring::kDepth * Ring::kStage);
+  W4Active* act = reinterpret_cast<W4Active*>(red + kW4Warps * Ring::kRed);
+  uint64_t* sums = reinterpret_cast<uint64_t*>(act + p.E);
+  uint16_t* list = reinterpret_cast<uint16_t*>(sums + kW4Warps);
+  int* cnt = reinterpret_cast<int*>(w4_smem_raw);   // [8][E] over the rings, before they are used
   pdl_wait();
   pdl_trigger();
-  const int64_t t = blockIdx.x;
-  const int n = blockIdx.y * kW4Cols + threadIdx.x;
-  float acc = 0.f;
+  const int slot0 = blockIdx.y * p.slots_per_row;
+  const int slots = min(p.slots_per_row, p.slots - slot0);
+  const int chunks = w4_lists<NT>(p, slot0, slots, cnt, act, list, sums);
+  const int half = GATE_UP ? p.N / 2 : 32;   // columns from the first set to the second
+  if (GATE_UP && p.ids) {                    // empty slots: zero rows
+    for (int i = blockIdx.x; i < slots; i += gridDim.x) {
+      const int e = p.ids[slot0 + i];
+      if (e < 0 || e >= p.E)
+        for (int c = tid; c < half / 8; c += kW4Threads)
+          reinterpret_cast<uint4*>(p.h + (int64_t)(slot0 + i) * half)[c] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  const int64_t items = (int64_t)chunks * p.blocks;
+  const int begin = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  if (begin >= end) return;
+  const int units = p.K / 32;
+  const int u0 = units * warp / kW4Warps, u1 = units * (warp + 1) / kW4Warps;
+
+  // the loader: item li, unit lu, and where its next copies come from
+  int li = begin, lu = u0, la = 0;
+  while (li / p.blocks >= act[la].chunk0 + (act[la].rows + 8 * NT - 1) / (8 * NT)) ++la;
+  const uint32_t* lq = nullptr;
+  const uint16_t* lx[NT];
+  int64_t lsg = 0;   // first scale of the expert's column block
+  auto load_item = [&]() {
+    const int chunk = li / p.blocks, cb = li - chunk * p.blocks;
+    while (chunk >= act[la].chunk0 + (act[la].rows + 8 * NT - 1) / (8 * NT)) ++la;
+    const W4Active a = act[la];
+    const int col = cb * (GATE_UP ? 32 : 64);
+    lq = p.q + ((int64_t)a.expert * (p.K / 8) + u0 * 4 + t) * p.N + col + 4 * g;
+    lsg = (int64_t)a.expert * (units / p.group_units) * p.N + col;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (chunk - a.chunk0) * 8 * NT + n * 8 + g;
+      lx[n] = nullptr;
+      if (r < a.rows) {
+        const int slot = slot0 + list[a.row0 + r];
+        lx[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 32 + 8 * t;
+      }
+    }
+  };
+  int lstage = 0;
+  auto issue = [&]() {
+    if (li < end && u0 < u1) {
+      if (lu == u0) load_item();
+      const uint32_t s = smem_u32(ring + lstage * Ring::kStage);
+      cp_async16(s + Ring::kQ + lane * 16, lq);
+      cp_async16(s + Ring::kQ + 512 + lane * 16, lq + half);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        cp_async16_or_zero(s + Ring::kX + n * 512 + lane * 16, lx[n] ? lx[n] : p.rows, lx[n] != nullptr);
+      if (lu == u0 || lu % p.group_units == 0) {
+        const int set = (lane >> 3) & 1, c = 4 * (lane & 7);
+        const int64_t at = lsg + (int64_t)(lu / p.group_units) * p.N + set * half + c;
+        if (lane < 16) cp_async8(s + Ring::kScale + lane * 8, p.scales + at);
+        else if (p.zeros) cp_async4(s + Ring::kZero + (lane - 16) * 4, p.zeros + at);
+      }
+      lq += 4 * (int64_t)p.N;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (lx[n]) lx[n] += 32;
+      if (++lu == u1) {
+        lu = u0;
+        ++li;
+      }
+    }
+    if (++lstage == Ring::kDepth) lstage = 0;
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int d = 0; d < Ring::kDepth - 1; ++d) issue();
+
+  int stage = 0, ca = 0;
+#pragma unroll 1
+  for (int item = begin; item < end; ++item) {
+    float tot[2][2][NT][4], acc[2][2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 16 * NT; ++i) {
+      (&tot[0][0][0][0])[i] = 0.f;
+      (&acc[0][0][0][0])[i] = 0.f;
+    }
+    float scale[2][4];
+    uint32_t zero2[2][4];
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+      issue();
+      cp_async_wait_group<Ring::kDepth - 1>();
+      __syncwarp();   // every lane's copies of this stage are visible (scales are shared by the warp)
+      const uint8_t* s = ring + stage * Ring::kStage;
+      if (u == u0 || u % p.group_units == 0) {
+#pragma unroll
+        for (int set = 0; set < 2; ++set) {
+          const uint2 v = *reinterpret_cast<const uint2*>(s + Ring::kScale + (set * 8 + g) * 8);
+          scale[set][0] = bf16_lo(v.x);
+          scale[set][1] = bf16_hi(v.x);
+          scale[set][2] = bf16_lo(v.y);
+          scale[set][3] = bf16_hi(v.y);
+          const uint32_t z = p.zeros ? *reinterpret_cast<const uint32_t*>(s + Ring::kZero + (set * 8 + g) * 4)
+                                     : 0x08080808u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) zero2[set][c] = 0x43004300u + ((z >> (8 * c)) & 15u) * 0x00010001u;
+        }
+      }
+      uint32_t b[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kX + n * 512 + lane * 16);
+        b[n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+        b[n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+        b[n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+        b[n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+      }
+#pragma unroll
+      for (int set = 0; set < 2; ++set) {
+        const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kQ + set * 512 + lane * 16);
+        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const uint32_t a[4] = {
+                w4_pair(word[2 * hf], 2 * st, zero2[set][2 * hf]), w4_pair(word[2 * hf + 1], 2 * st, zero2[set][2 * hf + 1]),
+                w4_pair(word[2 * hf], 2 * st + 1, zero2[set][2 * hf]),
+                w4_pair(word[2 * hf + 1], 2 * st + 1, zero2[set][2 * hf + 1])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(acc[set][hf][n], a, b[n][2 * st], b[n][2 * st + 1]);
+          }
+      }
+      if (u + 1 == u1 || (u + 1) % p.group_units == 0) {
+#pragma unroll
+        for (int set = 0; set < 2; ++set)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                tot[set][hf][n][r] = fmaf(scale[set][2 * hf + (r >> 1)], acc[set][hf][n][r], tot[set][hf][n][r]);
+                acc[set][hf][n][r] = 0.f;
+              }
+      }
+      __syncwarp();   // the stage is read before a later issue() overwrites it
+      if (++stage == Ring::kDepth) stage = 0;
+    }
+    // join the warps' sums: value (set, column, row) of lane (column / 4, row / 2)
+    float* mine = red + warp * Ring::kRed;
+#pragma unroll
+    for (int set = 0; set < 2; ++set)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            mine[((set * NT + n) * 8 + (r & 1) * 4 + 2 * hf + (r >> 1)) * 33 + lane] = tot[set][hf][n][r];
+    __syncthreads();
+    const int chunk = item / p.blocks, cb = item - chunk * p.blocks;
+    while (chunk >= act[ca].chunk0 + (act[ca].rows + 8 * NT - 1) / (8 * NT)) ++ca;
+    const W4Active a = act[ca];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = (chunk - a.chunk0) * 8 * NT + n * 8 + warp;   // this warp's row, lane's column
+      if (r < a.rows) {
+        float v[2] = {0.f, 0.f};
+        const int at = ((warp & 1) * 4 + (lane & 3)) * 33 + (lane >> 2) * 4 + (warp >> 1);
+#pragma unroll
+        for (int set = 0; set < 2; ++set)
+#pragma unroll
+          for (int w = 0; w < kW4Warps; ++w) v[set] += red[w * Ring::kRed + (set * NT + n) * 8 * 33 + at];
+        const int64_t slot = slot0 + list[a.row0 + r];
+        if (GATE_UP) {
+          const float y = v[0] / (1.f + expf(-v[0])) * v[1];
+          p.h[slot * half + cb * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        } else {
+          p.part[slot * p.N + cb * 64 + lane] = v[0];
+          p.part[slot * p.N + cb * 64 + 32 + lane] = v[1];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  cp_async_wait_group<0>();
+}
+
+// y[t] = sum_j w[t, j] part[t, j] (+ y_shared[t]) over the slots in use, 8
+// columns per thread.
+__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ part,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ wt,
+                                                         const uint16_t* __restrict__ y_shared, int64_t T, int E, int k,
+                                                         int H, uint16_t* __restrict__ y) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int nch = H / 8;
+  const int64_t t = i / nch;
+  const int c = (int)(i - t * nch) * 8;
+  if (t >= T) return;
+  float acc[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+#pragma unroll 4
   for (int j = 0; j < k; ++j) {
     const int64_t slot = t * k + j;
-    const int e = slot_expert(ids, slot, E, status);
-    if (e < 0) continue;
-    __syncthreads();
-    for (int c = threadIdx.x; c < w.K; c += kW4Cols) row[c] = __uint_as_float((uint32_t)h[slot * w.K + c] << 16);
-    __syncthreads();
-    if (n < w.N) acc = fmaf(wt ? wt[slot] : 1.f, w4_dot(w, e, n, row), acc);
+    const int e = ids ? ids[slot] : 0;
+    if (e < 0 || e >= E) continue;
+    const float w = wt ? wt[slot] : 1.f;
+    const float4 a = *reinterpret_cast<const float4*>(part + slot * H + c);
+    const float4 b = *reinterpret_cast<const float4*>(part + slot * H + c + 4);
+    acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
+    acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
   }
-  if (n >= w.N) return;
-  if (y_shared) acc += __uint_as_float((uint32_t)y_shared[t * w.N + n] << 16);
-  y[t * w.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
+  if (y_shared) {
+    float f[8];
+    unpack8(*reinterpret_cast<const uint4*>(y_shared + t * H + c), f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] += f[q];
+  }
+  *reinterpret_cast<uint4*>(y + t * H + c) = pack8(acc);
+}
+
+template <int NT, bool GATE_UP>
+cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
+  if (!configured[dev.ordinal].load()) {
+    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 w4_smem<NT>(kMaxExperts, kW4MaxSlots));
+    if (err != cudaSuccess) return err;
+    configured[dev.ordinal].store(1);
+  }
+  const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
+  const int64_t most = (int64_t)std::min(p.slots_per_row, p.slots) * p.blocks;   // every slot its own chunk
+  return launch_pdl(w4_kernel<NT, GATE_UP>, dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows),
+                    dim3(kW4Threads), w4_smem<NT>(p.E, std::min(p.slots_per_row, p.slots)), stream, 1, p);
+}
+
+template <bool GATE_UP>
+cudaError_t launch_w4_rows(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
+  // 8 rows a chunk while the experts in use hold few rows each, else 16
+  return (int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k ? launch_w4<1, GATE_UP>(p, dev, stream)
+                                                                   : launch_w4<2, GATE_UP>(p, dev, stream);
 }
 
 // One thread per (group, column) of [rows, N] bf16 weights.
@@ -164,18 +503,51 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
 cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint32_t* q, const uint16_t* scales,
                               const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I,
                               int64_t group, uint16_t* h, const DeviceInfo& dev, cudaStream_t stream) {
-  const W4View w{q, scales, zeros, (int)H, (int)(2 * I), (int)group};
-  return launch_pdl(w4_gate_up_kernel, dim3((unsigned)(T * k), (unsigned)((I + kW4Cols - 1) / kW4Cols)),
-                    dim3(kW4Cols), (size_t)H * 4, stream, 1, x, ids, w, (int)E, (int)k, (int)I, h, dev.status);
+  W4Params p{};
+  p.rows = x;
+  p.ids = ids;
+  p.q = q;
+  p.scales = scales;
+  p.zeros = zeros;
+  p.h = h;
+  p.status = dev.status;
+  p.K = (int)H;
+  p.N = (int)(2 * I);
+  p.E = (int)E;
+  p.k = (int)k;
+  p.slots = (int)(T * k);
+  p.slots_per_row = (int)(kW4MaxSlots / k * k);
+  p.group_units = (int)(group / 32);
+  p.blocks = (int)(I / 32);
+  return launch_w4_rows<true>(p, dev, stream);
 }
+
+size_t w4_down_workspace_bytes(int64_t T, int64_t k, int64_t H) { return (size_t)(T * k * H * 4); }
 
 cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* wt, const uint32_t* q,
                            const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T,
-                           int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y,
+                           int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* ws,
                            const DeviceInfo& dev, cudaStream_t stream) {
-  const W4View w{q, scales, zeros, (int)I, (int)H, (int)group};
-  return launch_pdl(w4_down_kernel, dim3((unsigned)T, (unsigned)((H + kW4Cols - 1) / kW4Cols)), dim3(kW4Cols),
-                    (size_t)I * 4, stream, 1, h, ids, wt, w, (int)E, (int)k, y_shared, y, dev.status);
+  W4Params p{};
+  p.rows = h;
+  p.ids = ids;
+  p.q = q;
+  p.scales = scales;
+  p.zeros = zeros;
+  p.part = static_cast<float*>(ws);
+  p.status = dev.status;
+  p.K = (int)I;
+  p.N = (int)H;
+  p.E = (int)E;
+  p.k = (int)k;
+  p.slots = (int)(T * k);
+  p.slots_per_row = (int)(kW4MaxSlots / k * k);
+  p.group_units = (int)(group / 32);
+  p.blocks = (int)(H / 64);
+  const cudaError_t err = launch_w4_rows<false>(p, dev, stream);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(w4_combine_kernel, dim3((unsigned)((T * (H / 8) + 255) / 256)), dim3(256), 0, stream, 1,
+                    static_cast<const float*>(ws), ids, wt, y_shared, T, (int)E, (int)k, (int)H, y);
 }
 
 cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64_t group, uint32_t* q,

@@ -305,8 +305,11 @@ def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=N
         _need(out, "out", _BF16, 2)
         if tuple(out.shape) != (T, H):
             raise ValueError("out must be [T, H]")
+    nbytes = ctypes.c_size_t(0)
+    call("moe_w4_down_workspace_size", T, H, k, ctypes.byref(nbytes))
+    ws = _ws(nbytes.value, h.device)
     call("moe_w4_down_combine", _p(h), _p(ids), _p(w), _p(qweight), _p(scales), _p(zeros), _p(y_shared), T, H, E, k,
-         I, group, _p(out), _stream())
+         I, group, _p(out), _p(ws), ws.numel(), _stream())
     return out
 
 
