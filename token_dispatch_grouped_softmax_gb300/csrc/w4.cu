@@ -29,19 +29,19 @@ struct W4Params {
   uint32_t* status;
   int K, N, E, k;
   int slots, slots_per_row;
-  int group_units;         // units of 32 k in a group
+  int split_log2;          // 2^split_log2 warps share a column block's K
   int blocks;              // column blocks: 32 gate and 32 up columns, or 64 columns
+  int block_items;         // items of one chunk: blocks / (8 >> split_log2), rounded up
 };
 
-// A stage of a warp's ring: 32 k of 2 x 32 columns, of 8 NT rows, and the
-// columns' scales and zeros.
+// A stage of a warp's ring: a unit of 64 k of 2 x 32 columns, of 8 NT rows,
+// and the scales and zeros of the columns (two groups where a group is 32).
 template <int NT>
 struct W4Ring {
-  static constexpr int kQ = 0, kX = 1024, kScale = kX + 512 * NT, kZero = kScale + 128, kStage = kZero + 64;
-  static constexpr int kDepth = NT == 1 ? 6 : 4;
+  static constexpr int kX = 2048, kScale = kX + 1024 * NT, kZero = kScale + 256, kStage = kZero + 128;
+  static constexpr int kDepth = NT == 1 ? 3 : 2;
   static constexpr int kRed = 16 * NT * 33;   // floats of one warp's partial sums
 };
-
 static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<2>::kDepth * W4Ring<2>::kStage, "the sort's counts fit the rings");
 
 // An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
@@ -78,14 +78,9 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word less the zero, as two bf16: 128 + code is the
-// bf16 0x4300 | code, and the difference of two such integers is exact.
-// zero2: 128 + zero in both halves.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t zero2) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&zero2));
-  return *reinterpret_cast<const uint32_t*>(&d);
+// Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 | code.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
+  return ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
 
 // The experts of the slots of this launch row, and each expert's slots in
@@ -172,16 +167,58 @@ __device__ __forceinline__ int w4_lists(const W4Params& p, int slot0, int slots,
   return (int)(total >> 40);
 }
 
+// The same for at most 32 slots, by one warp: experts in the order of their
+// first slot.
+template <int NT>
+__device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Active* act, uint16_t* list, int* chunks) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int e = -1;
+    if (lane < slots) {
+      e = p.ids ? p.ids[lane] : 0;
+      if (e < 0 || e >= p.E) {
+        if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+        e = -1;
+      }
+    }
+    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    const int n = __popc(peers), first = __ffs(peers) - 1;
+    const bool leads = e >= 0 && lane == first;
+    const int mine = leads ? n | (n + 8 * NT - 1) / (8 * NT) << 16 : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int before = incl - mine;
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    if (leads) act[__popc(leaders & ((1u << lane) - 1u))] = W4Active{e, before & 0xFFFF, n, before >> 16};
+    const int row0 = __shfl_sync(0xffffffffu, before & 0xFFFF, first);
+    if (e >= 0) list[row0 + __popc(peers & ((1u << lane) - 1u))] = (uint16_t)lane;
+    if (lane == 31) *chunks = incl >> 16;
+  }
+  __syncthreads();
+  return *chunks;
+}
+
 // Persistent: a block takes consecutive items (chunk of an expert's rows,
-// column block); its 8 warps split K, each streaming its own 32-k units
-// through a ring of lane-private copies, and add their sums in warp order.
+// column blocks).  2^split_log2 of its 8 warps share a column block, each
+// with its part of K, and their sums are added in that order; a warp streams
+// 64-k units through a ring of its own.
 //
-// Per unit a lane holds one 16-byte vector of codes per column set: columns
+// Per 32 k a lane holds one 16-byte vector of codes per column set: columns
 // 4g .. 4g+3 (g = lane / 4), k = 8t .. 8t+7 (t = lane % 4).  The k order
-// inside an mma is free as long as A and B agree: step s of the unit takes
-// codes (2s, 2s+4) and (2s+1, 2s+5) of the word, and the same of x.  A rows
-// are weight columns (two tiles a set), B columns the expert's rows.
-template <int NT, bool GATE_UP>
+// inside an mma is free as long as A and B agree: step s takes codes (2s,
+// 2s+4) and (2s+1, 2s+5) of the word, and the same of x.  A rows are weight
+// columns (two tiles a set), B columns the expert's rows.
+//
+// The codes go into the mma as 128 + q, an or with no subtraction; the sum
+// over the group of (128 + zero) x, from one more mma with a tile of ones, is
+// taken off before the scale: sum (q - zero) x = sum (128 + q) x - (128 +
+// zero) sum x.  Every product is exact; the fp32 sums round at 128 + q
+// instead of q - zero, some 2^-19 of the terms, 2^10 below the bf16 result.
+template <int NT, bool GATE_UP, int GROUP>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
   using Ring = W4Ring<NT>;
   extern __shared__ __align__(128) uint8_t w4_smem_raw[];
@@ -197,7 +234,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
-  const int chunks = w4_lists<NT>(p, slot0, slots, cnt, act, list, sums);
+  const int chunks = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, reinterpret_cast<int*>(sums))
+                                   : w4_lists<NT>(p, slot0, slots, cnt, act, list, sums);
   const int half = GATE_UP ? p.N / 2 : 32;   // columns from the first set to the second
   if (GATE_UP && p.ids) {                    // empty slots: zero rows
     for (int i = blockIdx.x; i < slots; i += gridDim.x) {
@@ -207,58 +245,85 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
           reinterpret_cast<uint4*>(p.h + (int64_t)(slot0 + i) * half)[c] = make_uint4(0, 0, 0, 0);
     }
   }
-  const int64_t items = (int64_t)chunks * p.blocks;
+  const int64_t items = (int64_t)chunks * p.block_items;
   const int begin = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
   if (begin >= end) return;
-  const int units = p.K / 32;
-  const int u0 = units * warp / kW4Warps, u1 = units * (warp + 1) / kW4Warps;
+  const int split = 1 << p.split_log2, wide = kW4Warps >> p.split_log2;   // warps of a block, blocks of an item
+  const int part = warp & (split - 1), sub = warp >> p.split_log2;
+  const int units = p.K / 64;
+  const int u0 = units * part / split, u1 = units * (part + 1) / split;
+  const int groups = p.K / GROUP;
+  auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
-  // the loader: item li, unit lu, and where its next copies come from
-  int li = begin, lu = u0, la = 0;
-  while (li / p.blocks >= act[la].chunk0 + (act[la].rows + 8 * NT - 1) / (8 * NT)) ++la;
+  // the loader: item (lchunk, lblock), unit lu, and where its next copies come from
+  int litem = begin, lchunk = begin / p.block_items, lblock = begin - lchunk * p.block_items;
+  int la = 0, lu = u0, lstage = 0;
+  while (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
+  int ca = la, cchunk = lchunk, cblock = lblock;   // the same of the item being computed
   const uint32_t* lq = nullptr;
   const uint16_t* lx[NT];
-  int64_t lsg = 0;   // first scale of the expert's column block
+  const uint16_t* ls = nullptr;
+  const uint8_t* lz = nullptr;
+  bool lon = false;   // the item has a column block for this warp
+  const int64_t n4 = 4 * (int64_t)p.N;
+  const int scol = ((lane >> 3) & 1) * half + 4 * (lane & 7);   // lanes 0..15 copy scales, 16..31 zeros
   auto load_item = [&]() {
-    const int chunk = li / p.blocks, cb = li - chunk * p.blocks;
-    while (chunk >= act[la].chunk0 + (act[la].rows + 8 * NT - 1) / (8 * NT)) ++la;
+    if (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;   // chunks come one after another
     const W4Active a = act[la];
-    const int col = cb * (GATE_UP ? 32 : 64);
-    lq = p.q + ((int64_t)a.expert * (p.K / 8) + u0 * 4 + t) * p.N + col + 4 * g;
-    lsg = (int64_t)a.expert * (units / p.group_units) * p.N + col;
+    const int block = lblock * wide + sub;
+    lon = block < p.blocks;
+    const int col = block * (GATE_UP ? 32 : 64);
+    lq = p.q + ((int64_t)a.expert * (p.K / 8) + u0 * 8 + t) * p.N + col + 4 * g;
+    const int64_t sg = ((int64_t)a.expert * groups + (GROUP <= 64 ? u0 * (64 / GROUP) : u0 / (GROUP / 64))) * p.N + col + scol;
+    ls = p.scales + sg;
+    lz = p.zeros + sg;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = (chunk - a.chunk0) * 8 * NT + n * 8 + g;
+      const int r = (lchunk - a.chunk0) * 8 * NT + n * 8 + g;
       lx[n] = nullptr;
       if (r < a.rows) {
         const int slot = slot0 + list[a.row0 + r];
-        lx[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 32 + 8 * t;
+        lx[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 64 + 8 * t;
       }
     }
   };
-  int lstage = 0;
   auto issue = [&]() {
-    if (li < end && u0 < u1) {
+    if (litem < end) {
       if (lu == u0) load_item();
-      const uint32_t s = smem_u32(ring + lstage * Ring::kStage);
-      cp_async16(s + Ring::kQ + lane * 16, lq);
-      cp_async16(s + Ring::kQ + 512 + lane * 16, lq + half);
+      if (lon) {
+        const uint32_t s = smem_u32(ring + lstage * Ring::kStage) + lane * 16;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        cp_async16_or_zero(s + Ring::kX + n * 512 + lane * 16, lx[n] ? lx[n] : p.rows, lx[n] != nullptr);
-      if (lu == u0 || lu % p.group_units == 0) {
-        const int set = (lane >> 3) & 1, c = 4 * (lane & 7);
-        const int64_t at = lsg + (int64_t)(lu / p.group_units) * p.N + set * half + c;
-        if (lane < 16) cp_async8(s + Ring::kScale + lane * 8, p.scales + at);
-        else if (p.zeros) cp_async4(s + Ring::kZero + (lane - 16) * 4, p.zeros + at);
+        for (int i = 0; i < 2; ++i) {
+          cp_async16(s + i * 1024, lq);
+          cp_async16(s + i * 1024 + 512, lq + half);
+          lq += n4;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const bool on = lx[n] != nullptr;
+          const uint16_t* src = on ? lx[n] : p.rows;
+          cp_async16_or_zero(s + Ring::kX + n * 1024, src, on);
+          cp_async16_or_zero(s + Ring::kX + n * 1024 + 512, src + 32, on);
+          if (on) lx[n] += 64;
+        }
+        if (GROUP <= 64 || lu == u0 || (lu & 1) == 0) {
+          const uint32_t d = smem_u32(ring + lstage * Ring::kStage);
+#pragma unroll
+          for (int i = 0; i < (GROUP == 32 ? 2 : 1); ++i) {
+            if (lane < 16) cp_async8(d + Ring::kScale + i * 128 + lane * 8, ls);
+            else if (p.zeros) cp_async4(d + Ring::kZero + i * 64 + (lane - 16) * 4, lz);
+            ls += p.N;
+            lz += p.N;
+          }
+        }
       }
-      lq += 4 * (int64_t)p.N;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (lx[n]) lx[n] += 32;
       if (++lu == u1) {
         lu = u0;
-        ++li;
+        ++litem;
+        if (++lblock == p.block_items) {
+          lblock = 0;
+          ++lchunk;
+        }
       }
     }
     if (++lstage == Ring::kDepth) lstage = 0;
@@ -267,74 +332,87 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
 #pragma unroll 1
   for (int d = 0; d < Ring::kDepth - 1; ++d) issue();
 
-  int stage = 0, ca = 0;
+  int stage = 0;
 #pragma unroll 1
   for (int item = begin; item < end; ++item) {
-    float tot[2][2][NT][4], acc[2][2][NT][4];
+    float tot[2][2][NT][4], acc[2][2][NT][4], sum[NT][4];
 #pragma unroll
     for (int i = 0; i < 16 * NT; ++i) {
       (&tot[0][0][0][0])[i] = 0.f;
       (&acc[0][0][0][0])[i] = 0.f;
     }
-    float scale[2][4];
-    uint32_t zero2[2][4];
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) (&sum[0][0])[i] = 0.f;
+    float scale[2][4], zero[2][4];
+    const bool on = cblock * wide + sub < p.blocks;
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
       issue();
       cp_async_wait_group<Ring::kDepth - 1>();
       __syncwarp();   // every lane's copies of this stage are visible (scales are shared by the warp)
       const uint8_t* s = ring + stage * Ring::kStage;
-      if (u == u0 || u % p.group_units == 0) {
+      if (on) {
 #pragma unroll
-        for (int set = 0; set < 2; ++set) {
-          const uint2 v = *reinterpret_cast<const uint2*>(s + Ring::kScale + (set * 8 + g) * 8);
-          scale[set][0] = bf16_lo(v.x);
-          scale[set][1] = bf16_hi(v.x);
-          scale[set][2] = bf16_lo(v.y);
-          scale[set][3] = bf16_hi(v.y);
-          const uint32_t z = p.zeros ? *reinterpret_cast<const uint32_t*>(s + Ring::kZero + (set * 8 + g) * 4)
-                                     : 0x08080808u;
+        for (int i = 0; i < 2; ++i) {   // 32 k each
+          if (GROUP == 32 || (i == 0 && (GROUP == 64 || u == u0 || (u & 1) == 0))) {
+            const int gi = GROUP == 32 ? i : 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) zero2[set][c] = 0x43004300u + ((z >> (8 * c)) & 15u) * 0x00010001u;
-        }
-      }
-      uint32_t b[NT][4];
+            for (int set = 0; set < 2; ++set) {
+              const uint2 v = *reinterpret_cast<const uint2*>(s + Ring::kScale + gi * 128 + (set * 8 + g) * 8);
+              scale[set][0] = bf16_lo(v.x);
+              scale[set][1] = bf16_hi(v.x);
+              scale[set][2] = bf16_lo(v.y);
+              scale[set][3] = bf16_hi(v.y);
+              const uint32_t z = p.zeros ? *reinterpret_cast<const uint32_t*>(s + Ring::kZero + gi * 64 + (set * 8 + g) * 4)
+                                         : 0x08080808u;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kX + n * 512 + lane * 16);
-        b[n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
-        b[n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
-        b[n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
-        b[n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
-      }
-#pragma unroll
-      for (int set = 0; set < 2; ++set) {
-        const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kQ + set * 512 + lane * 16);
-        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint32_t a[4] = {
-                w4_pair(word[2 * hf], 2 * st, zero2[set][2 * hf]), w4_pair(word[2 * hf + 1], 2 * st, zero2[set][2 * hf + 1]),
-                w4_pair(word[2 * hf], 2 * st + 1, zero2[set][2 * hf]),
-                w4_pair(word[2 * hf + 1], 2 * st + 1, zero2[set][2 * hf + 1])};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(acc[set][hf][n], a, b[n][2 * st], b[n][2 * st + 1]);
+              for (int c = 0; c < 4; ++c) zero[set][c] = -(128.f + (float)((z >> (8 * c)) & 15u));
+            }
           }
-      }
-      if (u + 1 == u1 || (u + 1) % p.group_units == 0) {
+          uint32_t b[NT][4];
 #pragma unroll
-        for (int set = 0; set < 2; ++set)
+          for (int n = 0; n < NT; ++n) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kX + n * 1024 + i * 512 + lane * 16);
+            b[n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+            b[n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+            b[n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+            b[n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            mma_16816(sum[n], ones, b[n][0], b[n][1]);
+            mma_16816(sum[n], ones, b[n][2], b[n][3]);
+          }
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+          for (int set = 0; set < 2; ++set) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s + i * 1024 + set * 512 + lane * 16);
+            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                tot[set][hf][n][r] = fmaf(scale[set][2 * hf + (r >> 1)], acc[set][hf][n][r], tot[set][hf][n][r]);
-                acc[set][hf][n][r] = 0.f;
+              for (int st = 0; st < 2; ++st) {
+                const uint32_t a[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
+                                       w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(acc[set][hf][n], a, b[n][2 * st], b[n][2 * st + 1]);
               }
+          }
+          if (GROUP == 32 || (i == 1 && (GROUP == 64 || u + 1 == u1 || (u & 1) != 0))) {
+#pragma unroll
+            for (int set = 0; set < 2; ++set)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    const int c = 2 * hf + (r >> 1);
+                    const float d = fmaf(zero[set][c], sum[n][r & 1], acc[set][hf][n][r]);
+                    tot[set][hf][n][r] = fmaf(scale[set][c], d, tot[set][hf][n][r]);
+                    acc[set][hf][n][r] = 0.f;
+                  }
+#pragma unroll
+            for (int i2 = 0; i2 < 4 * NT; ++i2) (&sum[0][0])[i2] = 0.f;
+          }
+        }
       }
       __syncwarp();   // the stage is read before a later issue() overwrites it
       if (++stage == Ring::kDepth) stage = 0;
@@ -351,44 +429,52 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
           for (int r = 0; r < 4; ++r)
             mine[((set * NT + n) * 8 + (r & 1) * 4 + 2 * hf + (r >> 1)) * 33 + lane] = tot[set][hf][n][r];
     __syncthreads();
-    const int chunk = item / p.blocks, cb = item - chunk * p.blocks;
-    while (chunk >= act[ca].chunk0 + (act[ca].rows + 8 * NT - 1) / (8 * NT)) ++ca;
+    if (cchunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
     const W4Active a = act[ca];
+    const int at = ((warp & 1) * 4 + (lane & 3)) * 33 + (lane >> 2) * 4 + (warp >> 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = (chunk - a.chunk0) * 8 * NT + n * 8 + warp;   // this warp's row, lane's column
-      if (r < a.rows) {
+      const int r = (cchunk - a.chunk0) * 8 * NT + n * 8 + warp;   // this warp's row, lane's column
+      if (r >= a.rows) continue;
+      const int64_t slot = slot0 + list[a.row0 + r];
+      for (int b = 0; b < wide; ++b) {
+        const int block = cblock * wide + b;
+        if (block >= p.blocks) break;
+        const float* from = red + b * split * Ring::kRed + n * 8 * 33 + at;
         float v[2] = {0.f, 0.f};
-        const int at = ((warp & 1) * 4 + (lane & 3)) * 33 + (lane >> 2) * 4 + (warp >> 1);
+        for (int w = 0; w < split; ++w)
 #pragma unroll
-        for (int set = 0; set < 2; ++set)
-#pragma unroll
-          for (int w = 0; w < kW4Warps; ++w) v[set] += red[w * Ring::kRed + (set * NT + n) * 8 * 33 + at];
-        const int64_t slot = slot0 + list[a.row0 + r];
+          for (int set = 0; set < 2; ++set) v[set] += from[w * Ring::kRed + set * NT * 8 * 33];
         if (GATE_UP) {
           const float y = v[0] / (1.f + expf(-v[0])) * v[1];
-          p.h[slot * half + cb * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+          p.h[slot * half + block * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
         } else {
-          p.part[slot * p.N + cb * 64 + lane] = v[0];
-          p.part[slot * p.N + cb * 64 + 32 + lane] = v[1];
+          p.part[slot * p.N + block * 64 + lane] = v[0];
+          p.part[slot * p.N + block * 64 + 32 + lane] = v[1];
         }
       }
     }
     __syncthreads();
+    if (++cblock == p.block_items) {
+      cblock = 0;
+      ++cchunk;
+    }
   }
   cp_async_wait_group<0>();
 }
 
+constexpr int kW4CombineThreads = 64;   // small blocks: one token's columns spread over several SMs
+
 // y[t] = sum_j w[t, j] part[t, j] (+ y_shared[t]) over the slots in use, 8
 // columns per thread.
-__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(kW4CombineThreads) w4_combine_kernel(const float* __restrict__ part,
                                                          const int32_t* __restrict__ ids,
                                                          const float* __restrict__ wt,
                                                          const uint16_t* __restrict__ y_shared, int64_t T, int E, int k,
                                                          int H, uint16_t* __restrict__ y) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * kW4CombineThreads + threadIdx.x;
   const int nch = H / 8;
   const int64_t t = i / nch;
   const int c = (int)(i - t * nch) * 8;
@@ -396,18 +482,31 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict
   float acc[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) acc[q] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int64_t slot = t * k + j;
-    const int e = ids ? ids[slot] : 0;
-    if (e < 0 || e >= E) continue;
-    const float w = wt ? wt[slot] : 1.f;
-    const float4 a = *reinterpret_cast<const float4*>(part + slot * H + c);
-    const float4 b = *reinterpret_cast<const float4*>(part + slot * H + c + 4);
-    acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
-    acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
-    acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
-    acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+  for (int j0 = 0; j0 < k; j0 += 8) {   // eight slots' loads in flight
+    float w[8];
+    bool on[8];
+    float4 v[8][2];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int64_t slot = t * k + j0 + q;
+      on[q] = j0 + q < k;
+      if (on[q]) {
+        const int e = ids ? ids[slot] : 0;
+        w[q] = wt ? wt[slot] : 1.f;
+        const float4* src = reinterpret_cast<const float4*>(part + slot * H + c);
+        v[q][0] = src[0];   // of an empty slot: whatever the workspace holds, not used
+        v[q][1] = src[1];
+        on[q] = e >= 0 && e < E;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (on[q]) {
+        acc[0] = fmaf(w[q], v[q][0].x, acc[0]); acc[1] = fmaf(w[q], v[q][0].y, acc[1]);
+        acc[2] = fmaf(w[q], v[q][0].z, acc[2]); acc[3] = fmaf(w[q], v[q][0].w, acc[3]);
+        acc[4] = fmaf(w[q], v[q][1].x, acc[4]); acc[5] = fmaf(w[q], v[q][1].y, acc[5]);
+        acc[6] = fmaf(w[q], v[q][1].z, acc[6]); acc[7] = fmaf(w[q], v[q][1].w, acc[7]);
+      }
   }
   if (y_shared) {
     float f[8];
@@ -418,26 +517,42 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict
   *reinterpret_cast<uint4*>(y + t * H + c) = pack8(acc);
 }
 
-template <int NT, bool GATE_UP>
+template <int NT, bool GATE_UP, int GROUP>
 cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
   if (!configured[dev.ordinal].load()) {
-    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  w4_smem<NT>(kMaxExperts, kW4MaxSlots));
     if (err != cudaSuccess) return err;
     configured[dev.ordinal].store(1);
   }
   const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
-  const int64_t most = (int64_t)std::min(p.slots_per_row, p.slots) * p.blocks;   // every slot its own chunk
-  return launch_pdl(w4_kernel<NT, GATE_UP>, dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows),
+  const int64_t most = (int64_t)std::min(p.slots_per_row, p.slots) * p.block_items;   // every slot its own chunk
+  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP>, dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows),
                     dim3(kW4Threads), w4_smem<NT>(p.E, std::min(p.slots_per_row, p.slots)), stream, 1, p);
 }
 
-template <bool GATE_UP>
+template <bool GATE_UP, int GROUP>
 cudaError_t launch_w4_rows(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
   // 8 rows a chunk while the experts in use hold few rows each, else 16
-  return (int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k ? launch_w4<1, GATE_UP>(p, dev, stream)
-                                                                   : launch_w4<2, GATE_UP>(p, dev, stream);
+  return (int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k ? launch_w4<1, GATE_UP, GROUP>(p, dev, stream)
+                                                                   : launch_w4<2, GATE_UP, GROUP>(p, dev, stream);
+}
+
+// K's split over warps and the launch of the group's kernel.  The split is
+// a rule on K alone, so that a row's sums do not depend on the batch: the
+// most warps (8 at most) whose shares of K's 64-k units are equal, or nearly
+// (at least 16 units a warp).
+template <bool GATE_UP>
+cudaError_t launch_w4_group(W4Params& p, int64_t group, const DeviceInfo& dev, cudaStream_t stream) {
+  const int units = p.K / 64;
+  p.split_log2 = 3;
+  while (p.split_log2 > 0 && units % (1 << p.split_log2) != 0 && units < (16 << p.split_log2)) --p.split_log2;
+  const int wide = kW4Warps >> p.split_log2;
+  p.block_items = (p.blocks + wide - 1) / wide;
+  if (group == 32) return launch_w4_rows<GATE_UP, 32>(p, dev, stream);
+  if (group == 64) return launch_w4_rows<GATE_UP, 64>(p, dev, stream);
+  return launch_w4_rows<GATE_UP, 128>(p, dev, stream);
 }
 
 // One thread per (group, column) of [rows, N] bf16 weights.
@@ -517,9 +632,8 @@ cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint3
   p.k = (int)k;
   p.slots = (int)(T * k);
   p.slots_per_row = (int)(kW4MaxSlots / k * k);
-  p.group_units = (int)(group / 32);
   p.blocks = (int)(I / 32);
-  return launch_w4_rows<true>(p, dev, stream);
+  return launch_w4_group<true>(p, group, dev, stream);
 }
 
 size_t w4_down_workspace_bytes(int64_t T, int64_t k, int64_t H) { return (size_t)(T * k * H * 4); }
@@ -542,12 +656,11 @@ cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* w
   p.k = (int)k;
   p.slots = (int)(T * k);
   p.slots_per_row = (int)(kW4MaxSlots / k * k);
-  p.group_units = (int)(group / 32);
   p.blocks = (int)(H / 64);
-  const cudaError_t err = launch_w4_rows<false>(p, dev, stream);
+  const cudaError_t err = launch_w4_group<false>(p, group, dev, stream);
   if (err != cudaSuccess) return err;
-  return launch_pdl(w4_combine_kernel, dim3((unsigned)((T * (H / 8) + 255) / 256)), dim3(256), 0, stream, 1,
-                    static_cast<const float*>(ws), ids, wt, y_shared, T, (int)E, (int)k, (int)H, y);
+  return launch_pdl(w4_combine_kernel, dim3((unsigned)((T * (H / 8) + kW4CombineThreads - 1) / kW4CombineThreads)),
+                    dim3(kW4CombineThreads), 0, stream, 1, static_cast<const float*>(ws), ids, wt, y_shared, T, (int)E, (int)k, (int)H, y);
 }
 
 cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64_t group, uint32_t* q,
