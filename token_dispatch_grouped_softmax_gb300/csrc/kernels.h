@@ -69,6 +69,10 @@ bool encode_tensor_map_2d_bf16(CUtensorMap* map, const void* base, const cuuint6
                                const cuuint64_t* strides, const cuuint32_t* box,
                                const cuuint32_t* estr);
 
+// A 3-D tensor map without interleave, out-of-range elements read as zero.
+bool encode_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
+
 size_t route_workspace_bytes(int64_t T, int64_t H, int64_t E);
 bool route_on_tensor_cores(int64_t H, int64_t E);
 size_t route_presplit_workspace_bytes(int64_t T, int64_t H, int64_t E);

@@ -19,30 +19,36 @@ constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4MaxSlots = 2048;   // slots of one launch row (shared-memory lists)
 
 struct W4Params {
+  CUtensorMap tm_q;        // codes as [E*K/8 rows][2 halves of the columns][N/2], boxes of 8 x 2 x 32 words
+  CUtensorMap tm_scale;    // scales the same way, boxes of (64 / group, or 1) x 2 x 32
+  CUtensorMap tm_zero;
   const uint16_t* rows;    // gate_up: x [T, K]; down: h [slots, K]
   const int32_t* ids;      // [slots], NULL: one dense expert
-  const uint32_t* q;
-  const uint16_t* scales;
-  const uint8_t* zeros;
   uint16_t* h;             // gate_up's output [slots, N / 2]
   float* part;             // down's products [slots, N]
   uint32_t* status;
+  uint64_t wait_limit_ns;
   int K, N, E, k;
   int slots, slots_per_row;
+  int has_zeros;
   int split_log2;          // 2^split_log2 warps share a column block's K
-  int blocks;              // column blocks: 32 gate and 32 up columns, or 64 columns
+  int blocks;              // column blocks: columns 32 b .. 32 b + 31 of both halves
   int block_items;         // items of one chunk: blocks / (8 >> split_log2), rounded up
 };
 
-// A stage of a warp's ring: a unit of 64 k of 2 x 32 columns, of 8 NT rows,
-// and the scales and zeros of the columns (two groups where a group is 32).
-template <int NT>
+// A stage of a warp's ring: a unit of 64 k of 2 x 32 columns (two swizzled
+// 8 x 128-byte atoms), and the columns' scales and zeros (two groups where a
+// group is 32).
+template <int NT, int GROUP>
 struct W4Ring {
-  static constexpr int kX = 2048, kScale = kX + 1024 * NT, kZero = kScale + 256, kStage = kZero + 128;
-  static constexpr int kDepth = NT == 1 ? 3 : 2;
+  static constexpr int kRows = GROUP == 32 ? 2 : 1;   // group rows of a unit
+  static constexpr int kQ = 2048, kScale = 128 * kRows, kZero = 128;   // TMA destinations are 128-byte aligned
+  static constexpr int kDepth = NT == 1 ? 3 : 4;
   static constexpr int kRed = 16 * NT * 33;   // floats of one warp's partial sums
+  static constexpr int kBlocksPerSm = NT == 1 ? 3 : 2;
 };
-static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<2>::kDepth * W4Ring<2>::kStage, "the sort's counts fit the rings");
+static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<1, 128>::kDepth * W4Ring<1, 128>::kQ,
+              "the sort's counts fit the rings");
 
 // An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
 // of 8 NT rows numbered from chunk0.
@@ -50,24 +56,20 @@ struct W4Active {
   int expert, row0, rows, chunk0;
 };
 
-template <int NT>
-__host__ __device__ constexpr int w4_smem(int E, int slots) {
-  return kW4Warps * (W4Ring<NT>::kDepth * W4Ring<NT>::kStage + W4Ring<NT>::kRed * 4) + E * (int)sizeof(W4Active) +
-         (slots * 2 + 15) / 16 * 16 + 64;
+template <int NT, int GROUP>
+__host__ __device__ constexpr int w4_smem(int E, int slots, bool zeros) {
+  using R = W4Ring<NT, GROUP>;
+  return 1024 + kW4Warps * (R::kDepth * (R::kQ + R::kScale + (zeros ? R::kZero : 0) + 8) + R::kRed * 4) +
+         (E < slots ? E : slots) * (int)sizeof(W4Active) + (slots * 2 + 15) / 16 * 16 + 128;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes, or 16 zero bytes without reading src.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
 }
 
 // D += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators.
@@ -76,6 +78,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D = A B.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 | code.
@@ -205,13 +215,15 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
 // Persistent: a block takes consecutive items (chunk of an expert's rows,
 // column blocks).  2^split_log2 of its 8 warps share a column block, each
 // with its part of K, and their sums are added in that order; a warp streams
-// 64-k units through a ring of its own.
+// 64-k units through a ring of its own, filled by TMA.
 //
-// Per 32 k a lane holds one 16-byte vector of codes per column set: columns
-// 4g .. 4g+3 (g = lane / 4), k = 8t .. 8t+7 (t = lane % 4).  The k order
-// inside an mma is free as long as A and B agree: step s takes codes (2s,
-// 2s+4) and (2s+1, 2s+5) of the word, and the same of x.  A rows are weight
-// columns (two tiles a set), B columns the expert's rows.
+// Per 32 k a lane holds one 16-byte vector of codes per half: columns 4g ..
+// 4g+3, k = 8t .. 8t+7 (g = lane / 4, t = lane % 4).  In the ring these are
+// 128-byte lines (row, half) in the 128-byte swizzle, read without bank
+// conflicts.  The k order inside an mma is free as long as A and B agree:
+// step s takes codes (2s, 2s+4) and (2s+1, 2s+5) of the word, and the same of
+// x.  A rows are weight columns (two tiles a half), B columns the expert's
+// rows.
 //
 // The codes go into the mma as 128 + q, an or with no subtraction; the sum
 // over the group of (128 + zero) x, from one more mma with a tile of ones, is
@@ -219,24 +231,42 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
 // zero) sum x.  Every product is exact; the fp32 sums round at 128 + q
 // instead of q - zero, some 2^-19 of the terms, 2^10 below the bf16 result.
 template <int NT, bool GATE_UP, int GROUP>
-__global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
-  using Ring = W4Ring<NT>;
-  extern __shared__ __align__(128) uint8_t w4_smem_raw[];
+__global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
+    w4_kernel(const __grid_constant__ W4Params p) {
+  using Ring = W4Ring<NT, GROUP>;
+  extern __shared__ uint8_t w4_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = w4_smem_raw + warp * (Ring::kDepth * Ring::kStage);
-  float* red = reinterpret_cast<float*>(w4_smem_raw + kW4Warps * Ring::kDepth * Ring::kStage);
+  const int n_act = min(p.E, min(p.slots_per_row, p.slots));
+  // rings | scale rings | zero rings | sums of the warps | experts in use | slot lists
+  uint8_t* ring = smem + warp * (Ring::kDepth * Ring::kQ);
+  uint8_t* scales = smem + kW4Warps * Ring::kDepth * Ring::kQ;
+  uint8_t* zeros = scales + kW4Warps * Ring::kDepth * Ring::kScale;
+  float* red = reinterpret_cast<float*>(zeros + (p.has_zeros ? kW4Warps * Ring::kDepth * Ring::kZero : 0));
   W4Active* act = reinterpret_cast<W4Active*>(red + kW4Warps * Ring::kRed);
-  uint64_t* sums = reinterpret_cast<uint64_t*>(act + p.E);
-  uint16_t* list = reinterpret_cast<uint16_t*>(sums + kW4Warps);
-  int* cnt = reinterpret_cast<int*>(w4_smem_raw);   // [8][E] over the rings, before they are used
+  uint64_t* sums = reinterpret_cast<uint64_t*>(act + n_act);
+  uint64_t* bars = sums + kW4Warps;
+  int* abort_flag = reinterpret_cast<int*>(bars + kW4Warps * Ring::kDepth);
+  uint16_t* list = reinterpret_cast<uint16_t*>(abort_flag + 2);
+  int* cnt = reinterpret_cast<int*>(smem);   // [8][E] over the rings, before they are used
+  scales += warp * (Ring::kDepth * Ring::kScale);
+  zeros += warp * (Ring::kDepth * Ring::kZero);
+  const uint32_t bar0 = smem_u32(bars + warp * Ring::kDepth);
+  if (lane == 0) {
+    for (int d = 0; d < Ring::kDepth; ++d) mbar_init(bar0 + 8 * d, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_scale);
+  }
   pdl_wait();
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
   const int chunks = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, reinterpret_cast<int*>(sums))
                                    : w4_lists<NT>(p, slot0, slots, cnt, act, list, sums);
-  const int half = GATE_UP ? p.N / 2 : 32;   // columns from the first set to the second
+  const int half = p.N / 2;
   if (GATE_UP && p.ids) {                    // empty slots: zero rows
     for (int i = blockIdx.x; i < slots; i += gridDim.x) {
       const int e = p.ids[slot0 + i];
@@ -248,174 +278,179 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
   const int64_t items = (int64_t)chunks * p.block_items;
   const int begin = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
   if (begin >= end) return;
+  fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
+  __syncthreads();
   const int split = 1 << p.split_log2, wide = kW4Warps >> p.split_log2;   // warps of a block, blocks of an item
   const int part = warp & (split - 1), sub = warp >> p.split_log2;
   const int units = p.K / 64;
   const int u0 = units * part / split, u1 = units * (part + 1) / split;
-  const int groups = p.K / GROUP;
   auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
-  // the loader: item (lchunk, lblock), unit lu, and where its next copies come from
+  // the loader: item (lchunk, lblock) and unit lu of the next copies
   int litem = begin, lchunk = begin / p.block_items, lblock = begin - lchunk * p.block_items;
   int la = 0, lu = u0, lstage = 0;
   while (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
   int ca = la, cchunk = lchunk, cblock = lblock;   // the same of the item being computed
-  const uint32_t* lq = nullptr;
-  const uint16_t* lx[NT];
-  const uint16_t* ls = nullptr;
-  const uint8_t* lz = nullptr;
-  bool lon = false;   // the item has a column block for this warp
-  const int64_t n4 = 4 * (int64_t)p.N;
-  const int scol = ((lane >> 3) & 1) * half + 4 * (lane & 7);   // lanes 0..15 copy scales, 16..31 zeros
-  auto load_item = [&]() {
-    if (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;   // chunks come one after another
-    const W4Active a = act[la];
-    const int block = lblock * wide + sub;
-    lon = block < p.blocks;
-    const int col = block * (GATE_UP ? 32 : 64);
-    lq = p.q + ((int64_t)a.expert * (p.K / 8) + u0 * 8 + t) * p.N + col + 4 * g;
-    const int64_t sg = ((int64_t)a.expert * groups + (GROUP <= 64 ? u0 * (64 / GROUP) : u0 / (GROUP / 64))) * p.N + col + scol;
-    ls = p.scales + sg;
-    lz = p.zeros + sg;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = (lchunk - a.chunk0) * 8 * NT + n * 8 + g;
-      lx[n] = nullptr;
-      if (r < a.rows) {
-        const int slot = slot0 + list[a.row0 + r];
-        lx[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 64 + 8 * t;
+  auto issue = [&]() {   // only items with a column block for this warp take a stage
+    while (litem < end && lblock * wide + sub >= p.blocks) {   // only an item's last blocks may be missing
+      ++litem;
+      if (++lblock == p.block_items) {
+        lblock = 0;
+        ++lchunk;
       }
     }
-  };
-  auto issue = [&]() {
-    if (litem < end) {
-      if (lu == u0) load_item();
-      if (lon) {
-        const uint32_t s = smem_u32(ring + lstage * Ring::kStage) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          cp_async16(s + i * 1024, lq);
-          cp_async16(s + i * 1024 + 512, lq + half);
-          lq += n4;
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const bool on = lx[n] != nullptr;
-          const uint16_t* src = on ? lx[n] : p.rows;
-          cp_async16_or_zero(s + Ring::kX + n * 1024, src, on);
-          cp_async16_or_zero(s + Ring::kX + n * 1024 + 512, src + 32, on);
-          if (on) lx[n] += 64;
-        }
-        if (GROUP <= 64 || lu == u0 || (lu & 1) == 0) {
-          const uint32_t d = smem_u32(ring + lstage * Ring::kStage);
-#pragma unroll
-          for (int i = 0; i < (GROUP == 32 ? 2 : 1); ++i) {
-            if (lane < 16) cp_async8(d + Ring::kScale + i * 128 + lane * 8, ls);
-            else if (p.zeros) cp_async4(d + Ring::kZero + i * 64 + (lane - 16) * 4, lz);
-            ls += p.N;
-            lz += p.N;
-          }
-        }
-      }
-      if (++lu == u1) {
-        lu = u0;
-        ++litem;
-        if (++lblock == p.block_items) {
-          lblock = 0;
-          ++lchunk;
-        }
+    if (litem >= end) return;
+    if (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;   // chunks come one after another
+    const int expert = act[la].expert;
+    if (lane == 0) {
+      const uint32_t bar = bar0 + 8 * lstage;
+      const int col = (lblock * wide + sub) * 32;
+      const bool sc = GROUP <= 64 || lu == u0 || (lu & 1) == 0;
+      const uint32_t bytes = Ring::kQ + (sc ? Ring::kRows * (p.has_zeros ? 192 : 128) : 0);
+      mbar_arrive_expect_tx(bar, bytes);
+      tma_load_3d(smem_u32(ring + lstage * Ring::kQ), &p.tm_q, col, 0, expert * (p.K / 8) + lu * 8, bar);
+      if (sc) {
+        const int row = expert * (p.K / GROUP) + (GROUP <= 64 ? lu * Ring::kRows : lu >> 1);
+        tma_load_3d(smem_u32(scales + lstage * Ring::kScale), &p.tm_scale, col, 0, row, bar);
+        if (p.has_zeros) tma_load_3d(smem_u32(zeros + lstage * Ring::kZero), &p.tm_zero, col, 0, row, bar);
       }
     }
     if (++lstage == Ring::kDepth) lstage = 0;
-    cp_async_commit();
+    if (++lu == u1) {
+      lu = u0;
+      ++litem;
+      if (++lblock == p.block_items) {
+        lblock = 0;
+        ++lchunk;
+      }
+    }
   };
+  if (u0 < u1) {
 #pragma unroll 1
-  for (int d = 0; d < Ring::kDepth - 1; ++d) issue();
+    for (int d = 0; d < Ring::kDepth; ++d) issue();
+  }
+  const uint32_t q_at = t * 256 + ((g ^ 2 * t) << 4);   // line 2t; the second half's line is the next, its chunk ^ 1
 
   int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
 #pragma unroll 1
   for (int item = begin; item < end; ++item) {
-    float tot[2][2][NT][4], acc[2][2][NT][4], sum[NT][4];
+    if (cchunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
+    const W4Active a = act[ca];
+    const int row_first = (cchunk - a.chunk0) * 8 * NT;
+    float tot[2][2][NT][4];
 #pragma unroll
-    for (int i = 0; i < 16 * NT; ++i) {
-      (&tot[0][0][0][0])[i] = 0.f;
-      (&acc[0][0][0][0])[i] = 0.f;
-    }
+    for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
+    if (cblock * wide + sub < p.blocks && u0 < u1 && ok) {
+      const uint16_t* x[NT];
+      uint4 xn[NT];
 #pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) (&sum[0][0])[i] = 0.f;
-    float scale[2][4], zero[2][4];
-    const bool on = cblock * wide + sub < p.blocks;
+      for (int n = 0; n < NT; ++n) {
+        const int r = row_first + n * 8 + g;
+        x[n] = nullptr;
+        xn[n] = make_uint4(0, 0, 0, 0);
+        if (r < a.rows) {
+          const int slot = slot0 + list[a.row0 + r];
+          x[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 64 + 8 * t;
+          xn[n] = __ldg(reinterpret_cast<const uint4*>(x[n]));
+        }
+      }
+      float acc[2][2][NT][4], sum[NT][4];
+      if (GROUP == 128) {
+#pragma unroll
+        for (int i = 0; i < 16 * NT; ++i) (&acc[0][0][0][0])[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) (&sum[0][0])[i] = 0.f;
+      }
+      uint2 sraw[2];
+      uint32_t zraw[2] = {0x08080808u, 0x08080808u};
 #pragma unroll 1
-    for (int u = u0; u < u1; ++u) {
-      issue();
-      cp_async_wait_group<Ring::kDepth - 1>();
-      __syncwarp();   // every lane's copies of this stage are visible (scales are shared by the warp)
-      const uint8_t* s = ring + stage * Ring::kStage;
-      if (on) {
+      for (int u = u0; u < u1; ++u) {
+        if (!mbar_wait_warp(bar0 + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 2, kKernW4)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* s = ring + stage * Ring::kQ;
+        auto read_scales = [&](int row) {
+#pragma unroll
+          for (int set = 0; set < 2; ++set) {
+            sraw[set] = *reinterpret_cast<const uint2*>(scales + stage * Ring::kScale + (row * 2 + set) * 64 + g * 8);
+            if (p.has_zeros)
+              zraw[set] = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + (row * 2 + set) * 32 + g * 4);
+          }
+        };
+        if (GROUP == 128 && (u == u0 || (u & 1) == 0)) read_scales(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {   // 32 k each
-          if (GROUP == 32 || (i == 0 && (GROUP == 64 || u == u0 || (u & 1) == 0))) {
-            const int gi = GROUP == 32 ? i : 0;
-#pragma unroll
-            for (int set = 0; set < 2; ++set) {
-              const uint2 v = *reinterpret_cast<const uint2*>(s + Ring::kScale + gi * 128 + (set * 8 + g) * 8);
-              scale[set][0] = bf16_lo(v.x);
-              scale[set][1] = bf16_hi(v.x);
-              scale[set][2] = bf16_lo(v.y);
-              scale[set][3] = bf16_hi(v.y);
-              const uint32_t z = p.zeros ? *reinterpret_cast<const uint32_t*>(s + Ring::kZero + gi * 64 + (set * 8 + g) * 4)
-                                         : 0x08080808u;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) zero[set][c] = -(128.f + (float)((z >> (8 * c)) & 15u));
-            }
-          }
           uint32_t b[NT][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s + Ring::kX + n * 1024 + i * 512 + lane * 16);
+            const uint4 v = xn[n];
+            if (x[n] && (i == 0 || u + 1 < u1)) {
+              x[n] += 32;
+              xn[n] = __ldg(reinterpret_cast<const uint4*>(x[n]));
+            }
             b[n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
             b[n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
             b[n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
             b[n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
             const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-            mma_16816(sum[n], ones, b[n][0], b[n][1]);
+            if (GROUP == 32 || (GROUP == 64 && i == 0)) mma_16816_first(sum[n], ones, b[n][0], b[n][1]);
+            else mma_16816(sum[n], ones, b[n][0], b[n][1]);
             mma_16816(sum[n], ones, b[n][2], b[n][3]);
           }
 #pragma unroll
           for (int set = 0; set < 2; ++set) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s + i * 1024 + set * 512 + lane * 16);
+            const uint4 v = *reinterpret_cast<const uint4*>(s + i * 1024 + (set ? (q_at ^ 16) + 128 : q_at));
             const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int st = 0; st < 2; ++st) {
-                const uint32_t a[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
+                const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
                                        w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_16816(acc[set][hf][n], a, b[n][2 * st], b[n][2 * st + 1]);
+                for (int n = 0; n < NT; ++n) {
+                  if (st == 0 && (GROUP == 32 || (GROUP == 64 && i == 0)))
+                    mma_16816_first(acc[set][hf][n], w, b[n][0], b[n][1]);
+                  else
+                    mma_16816(acc[set][hf][n], w, b[n][2 * st], b[n][2 * st + 1]);
+                }
               }
           }
           if (GROUP == 32 || (i == 1 && (GROUP == 64 || u + 1 == u1 || (u & 1) != 0))) {
+            if (GROUP <= 64) read_scales(GROUP == 32 ? i : 0);
 #pragma unroll
             for (int set = 0; set < 2; ++set)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
+              for (int c = 0; c < 4; ++c) {   // the lane's four columns
+                const uint32_t sp = c < 2 ? sraw[set].x : sraw[set].y;
+                const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
+                const float zero = __uint_as_float(0x43000000u | ((zraw[set] >> (8 * c)) & 15u) << 16);   // 128 + zero
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    const int c = 2 * hf + (r >> 1);
-                    const float d = fmaf(zero[set][c], sum[n][r & 1], acc[set][hf][n][r]);
-                    tot[set][hf][n][r] = fmaf(scale[set][c], d, tot[set][hf][n][r]);
-                    acc[set][hf][n][r] = 0.f;
+                  for (int r = 0; r < 2; ++r) {
+                    float& v = acc[set][c >> 1][n][(c & 1) * 2 + r];
+                    float& o = tot[set][c >> 1][n][(c & 1) * 2 + r];
+                    o = fmaf(scale, fmaf(-zero, sum[n][r], v), o);
+                    if (GROUP == 128) v = 0.f;
                   }
+              }
+            if (GROUP == 128) {
 #pragma unroll
-            for (int i2 = 0; i2 < 4 * NT; ++i2) (&sum[0][0])[i2] = 0.f;
+              for (int i2 = 0; i2 < 4 * NT; ++i2) (&sum[0][0])[i2] = 0.f;
+            }
           }
         }
+        __syncwarp();   // every lane has read the stage
+        issue();        // into the same stage
+        if (++stage == Ring::kDepth) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      __syncwarp();   // the stage is read before a later issue() overwrites it
-      if (++stage == Ring::kDepth) stage = 0;
     }
     // join the warps' sums: value (set, column, row) of lane (column / 4, row / 2)
     float* mine = red + warp * Ring::kRed;
@@ -429,12 +464,10 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
           for (int r = 0; r < 4; ++r)
             mine[((set * NT + n) * 8 + (r & 1) * 4 + 2 * hf + (r >> 1)) * 33 + lane] = tot[set][hf][n][r];
     __syncthreads();
-    if (cchunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
-    const W4Active a = act[ca];
     const int at = ((warp & 1) * 4 + (lane & 3)) * 33 + (lane >> 2) * 4 + (warp >> 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = (cchunk - a.chunk0) * 8 * NT + n * 8 + warp;   // this warp's row, lane's column
+      const int r = row_first + n * 8 + warp;   // this warp's row
       if (r >= a.rows) continue;
       const int64_t slot = slot0 + list[a.row0 + r];
       for (int b = 0; b < wide; ++b) {
@@ -442,6 +475,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
         if (block >= p.blocks) break;
         const float* from = red + b * split * Ring::kRed + n * 8 * 33 + at;
         float v[2] = {0.f, 0.f};
+#pragma unroll 4
         for (int w = 0; w < split; ++w)
 #pragma unroll
           for (int set = 0; set < 2; ++set) v[set] += from[w * Ring::kRed + set * NT * 8 * 33];
@@ -449,8 +483,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
           const float y = v[0] / (1.f + expf(-v[0])) * v[1];
           p.h[slot * half + block * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
         } else {
-          p.part[slot * p.N + block * 64 + lane] = v[0];
-          p.part[slot * p.N + block * 64 + 32 + lane] = v[1];
+          p.part[slot * p.N + block * 32 + lane] = v[0];
+          p.part[slot * p.N + half + block * 32 + lane] = v[1];
         }
       }
     }
@@ -460,7 +494,14 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const W4Params p) {
       ++cchunk;
     }
   }
-  cp_async_wait_group<0>();
+  if (!ok && lane == 0) {   // stopped early: the copies in flight land (bounded) before the block's memory goes
+    for (int d = 0; d < Ring::kDepth; ++d) {
+      const uint64_t t0 = globaltimer_ns();
+      const uint32_t par = d < stage ? phase ^ 1u : phase;
+      while (!mbar_try_wait(bar0 + 8 * d, par) && globaltimer_ns() - t0 < p.wait_limit_ns) {
+      }
+    }
+  }
 }
 
 constexpr int kW4CombineThreads = 64;   // small blocks: one token's columns spread over several SMs
@@ -519,17 +560,20 @@ __global__ void __launch_bounds__(kW4CombineThreads) w4_combine_kernel(const flo
 
 template <int NT, bool GATE_UP, int GROUP>
 cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
+  using Ring = W4Ring<NT, GROUP>;
   static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
   if (!configured[dev.ordinal].load()) {
     const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 w4_smem<NT>(kMaxExperts, kW4MaxSlots));
+                                                 w4_smem<NT, GROUP>(kMaxExperts, kW4MaxSlots, true));
     if (err != cudaSuccess) return err;
     configured[dev.ordinal].store(1);
   }
+  const int row_slots = std::min(p.slots_per_row, p.slots);
   const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
-  const int64_t most = (int64_t)std::min(p.slots_per_row, p.slots) * p.block_items;   // every slot its own chunk
-  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP>, dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows),
-                    dim3(kW4Threads), w4_smem<NT>(p.E, std::min(p.slots_per_row, p.slots)), stream, 1, p);
+  const int64_t most = (int64_t)row_slots * p.block_items;   // every slot its own chunk
+  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP>,
+                    dim3((unsigned)std::min<int64_t>(most, Ring::kBlocksPerSm * dev.num_sms), (unsigned)rows),
+                    dim3(kW4Threads), w4_smem<NT, GROUP>(p.E, row_slots, p.has_zeros), stream, 1, p);
 }
 
 template <bool GATE_UP, int GROUP>
@@ -544,7 +588,26 @@ cudaError_t launch_w4_rows(const W4Params& p, const DeviceInfo& dev, cudaStream_
 // most warps (8 at most) whose shares of K's 64-k units are equal, or nearly
 // (at least 16 units a warp).
 template <bool GATE_UP>
-cudaError_t launch_w4_group(W4Params& p, int64_t group, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scales, const uint8_t* zeros,
+                            int64_t group, const DeviceInfo& dev, cudaStream_t stream) {
+  const cuuint64_t half = p.N / 2, rows = (cuuint64_t)p.E * p.K;
+  auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, cuuint64_t bytes, const void* base, cuuint64_t n,
+                    cuuint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[3] = {half, 2, n}, strides[2] = {half * bytes, (cuuint64_t)p.N * bytes};
+    const cuuint32_t box[3] = {32, 2, box_rows};
+    return encode_tensor_map_3d(map, type, base, dims, strides, box, swizzle);
+  };
+  const cuuint32_t box_rows = group == 32 ? 2 : 1;
+  if (!encode(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, q, rows / 8, 8, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&p.tm_scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, rows / group, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  p.has_zeros = zeros != nullptr;
+  if (zeros && !encode(&p.tm_zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, rows / group, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  p.status = dev.status;
+  p.wait_limit_ns = dev.wait_limit_ns;
+  p.slots_per_row = kW4MaxSlots / p.k * p.k;
+  p.blocks = (int)(half / 32);
   const int units = p.K / 64;
   p.split_log2 = 3;
   while (p.split_log2 > 0 && units % (1 << p.split_log2) != 0 && units < (16 << p.split_log2)) --p.split_log2;
@@ -621,19 +684,13 @@ cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint3
   W4Params p{};
   p.rows = x;
   p.ids = ids;
-  p.q = q;
-  p.scales = scales;
-  p.zeros = zeros;
   p.h = h;
-  p.status = dev.status;
   p.K = (int)H;
   p.N = (int)(2 * I);
   p.E = (int)E;
   p.k = (int)k;
   p.slots = (int)(T * k);
-  p.slots_per_row = (int)(kW4MaxSlots / k * k);
-  p.blocks = (int)(I / 32);
-  return launch_w4_group<true>(p, group, dev, stream);
+  return launch_w4_group<true>(p, q, scales, zeros, group, dev, stream);
 }
 
 size_t w4_down_workspace_bytes(int64_t T, int64_t k, int64_t H) { return (size_t)(T * k * H * 4); }
@@ -645,19 +702,13 @@ cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* w
   W4Params p{};
   p.rows = h;
   p.ids = ids;
-  p.q = q;
-  p.scales = scales;
-  p.zeros = zeros;
   p.part = static_cast<float*>(ws);
-  p.status = dev.status;
   p.K = (int)I;
   p.N = (int)H;
   p.E = (int)E;
   p.k = (int)k;
   p.slots = (int)(T * k);
-  p.slots_per_row = (int)(kW4MaxSlots / k * k);
-  p.blocks = (int)(H / 64);
-  const cudaError_t err = launch_w4_group<false>(p, group, dev, stream);
+  const cudaError_t err = launch_w4_group<false>(p, q, scales, zeros, group, dev, stream);
   if (err != cudaSuccess) return err;
   return launch_pdl(w4_combine_kernel, dim3((unsigned)((T * (H / 8) + kW4CombineThreads - 1) / kW4CombineThreads)),
                     dim3(kW4CombineThreads), 0, stream, 1, static_cast<const float*>(ws), ids, wt, y_shared, T, (int)E, (int)k, (int)H, y);
