@@ -88,9 +88,12 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 | code.
+// Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 |
+// code.  One lop3 with the shift before it: (a & b) | c is table 0xEA.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
-  return ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+  return v;
 }
 
 // The experts of the slots of this launch row, and each expert's slots in
@@ -286,51 +289,59 @@ __global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
   const int u0 = units * part / split, u1 = units * (part + 1) / split;
   auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
-  // the loader: item (lchunk, lblock) and unit lu of the next copies
+  // the loader: item (lchunk, lblock), unit lu of the next copies, and their
+  // coordinates; only items with a column block for this warp take stages
   int litem = begin, lchunk = begin / p.block_items, lblock = begin - lchunk * p.block_items;
   int la = 0, lu = u0, lstage = 0;
   while (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
   int ca = la, cchunk = lchunk, cblock = lblock;   // the same of the item being computed
-  auto issue = [&]() {   // only items with a column block for this warp take a stage
-    while (litem < end && lblock * wide + sub >= p.blocks) {   // only an item's last blocks may be missing
-      ++litem;
-      if (++lblock == p.block_items) {
+  int lcol = 0, lqrow = 0, lsrow = 0;
+  auto next_item = [&]() {   // litem, or the next one with a column block for this warp
+    for (; litem < end; ++litem, ++lblock) {
+      if (lblock == p.block_items) {
         lblock = 0;
         ++lchunk;
       }
+      if (lblock * wide + sub < p.blocks) break;
     }
     if (litem >= end) return;
     if (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;   // chunks come one after another
     const int expert = act[la].expert;
+    lcol = (lblock * wide + sub) * 32;
+    lqrow = expert * (p.K / 8);
+    lsrow = expert * (p.K / GROUP);
+  };
+  next_item();
+  auto issue = [&]() {
+    if (litem >= end) return;
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * lstage;
-      const int col = (lblock * wide + sub) * 32;
       const bool sc = GROUP <= 64 || lu == u0 || (lu & 1) == 0;
       const uint32_t bytes = Ring::kQ + (sc ? Ring::kRows * (p.has_zeros ? 192 : 128) : 0);
       mbar_arrive_expect_tx(bar, bytes);
-      tma_load_3d(smem_u32(ring + lstage * Ring::kQ), &p.tm_q, col, 0, expert * (p.K / 8) + lu * 8, bar);
+      tma_load_3d(smem_u32(ring + lstage * Ring::kQ), &p.tm_q, lcol, 0, lqrow + lu * 8, bar);
       if (sc) {
-        const int row = expert * (p.K / GROUP) + (GROUP <= 64 ? lu * Ring::kRows : lu >> 1);
-        tma_load_3d(smem_u32(scales + lstage * Ring::kScale), &p.tm_scale, col, 0, row, bar);
-        if (p.has_zeros) tma_load_3d(smem_u32(zeros + lstage * Ring::kZero), &p.tm_zero, col, 0, row, bar);
+        const int row = lsrow + (GROUP <= 64 ? lu * Ring::kRows : lu >> 1);
+        tma_load_3d(smem_u32(scales + lstage * Ring::kScale), &p.tm_scale, lcol, 0, row, bar);
+        if (p.has_zeros) tma_load_3d(smem_u32(zeros + lstage * Ring::kZero), &p.tm_zero, lcol, 0, row, bar);
       }
     }
     if (++lstage == Ring::kDepth) lstage = 0;
     if (++lu == u1) {
       lu = u0;
       ++litem;
-      if (++lblock == p.block_items) {
-        lblock = 0;
-        ++lchunk;
-      }
+      ++lblock;
+      next_item();
     }
   };
-  if (u0 < u1) {
 #pragma unroll 1
-    for (int d = 0; d < Ring::kDepth; ++d) issue();
-  }
+  for (int d = 0; d < Ring::kDepth; ++d) issue();
   const uint32_t q_at = t * 256 + ((g ^ 2 * t) << 4);   // line 2t; the second half's line is the next, its chunk ^ 1
 
+  // this lane's rows of the chunk, and their vectors of the next unit: loaded a
+  // unit ahead (the first unit's again at an item's end, for the next block)
+  const uint16_t* x[NT];
+  uint4 xn[NT][2];
   int stage = 0;
   uint32_t phase = 0;
   bool ok = true;
@@ -339,23 +350,24 @@ __global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
     if (cchunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
     const W4Active a = act[ca];
     const int row_first = (cchunk - a.chunk0) * 8 * NT;
-    float tot[2][2][NT][4];
-#pragma unroll
-    for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
-    if (cblock * wide + sub < p.blocks && u0 < u1 && ok) {
-      const uint16_t* x[NT];
-      uint4 xn[NT];
+    if (cblock == 0 || item == begin) {   // another chunk: its rows
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = row_first + n * 8 + g;
         x[n] = nullptr;
-        xn[n] = make_uint4(0, 0, 0, 0);
+        xn[n][0] = xn[n][1] = make_uint4(0, 0, 0, 0);
         if (r < a.rows) {
           const int slot = slot0 + list[a.row0 + r];
           x[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 64 + 8 * t;
-          xn[n] = __ldg(reinterpret_cast<const uint4*>(x[n]));
+          xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n]));
+          xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + 32));
         }
       }
+    }
+    float tot[2][2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
+    if (cblock * wide + sub < p.blocks && ok) {
       float acc[2][2][NT][4], sum[NT][4];
       if (GROUP == 128) {
 #pragma unroll
@@ -381,24 +393,31 @@ __global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
           }
         };
         if (GROUP == 128 && (u == u0 || (u & 1) == 0)) read_scales(0);
+        uint32_t b[2][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = xn[n][i];
+            b[i][n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+            b[i][n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+            b[i][n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+            b[i][n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+          }
+          if (x[n]) {
+            const uint16_t* next = x[n] + (u + 1 < u1 ? (u + 1 - u0) * 64 : 0);
+            xn[n][0] = __ldg(reinterpret_cast<const uint4*>(next));
+            xn[n][1] = __ldg(reinterpret_cast<const uint4*>(next + 32));
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {   // 32 k each
-          uint32_t b[NT][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint4 v = xn[n];
-            if (x[n] && (i == 0 || u + 1 < u1)) {
-              x[n] += 32;
-              xn[n] = __ldg(reinterpret_cast<const uint4*>(x[n]));
-            }
-            b[n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
-            b[n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
-            b[n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
-            b[n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
             const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-            if (GROUP == 32 || (GROUP == 64 && i == 0)) mma_16816_first(sum[n], ones, b[n][0], b[n][1]);
-            else mma_16816(sum[n], ones, b[n][0], b[n][1]);
-            mma_16816(sum[n], ones, b[n][2], b[n][3]);
+            if (GROUP == 32 || (GROUP == 64 && i == 0)) mma_16816_first(sum[n], ones, b[i][n][0], b[i][n][1]);
+            else mma_16816(sum[n], ones, b[i][n][0], b[i][n][1]);
+            mma_16816(sum[n], ones, b[i][n][2], b[i][n][3]);
           }
 #pragma unroll
           for (int set = 0; set < 2; ++set) {
@@ -413,9 +432,9 @@ __global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                   if (st == 0 && (GROUP == 32 || (GROUP == 64 && i == 0)))
-                    mma_16816_first(acc[set][hf][n], w, b[n][0], b[n][1]);
+                    mma_16816_first(acc[set][hf][n], w, b[i][n][0], b[i][n][1]);
                   else
-                    mma_16816(acc[set][hf][n], w, b[n][2 * st], b[n][2 * st + 1]);
+                    mma_16816(acc[set][hf][n], w, b[i][n][2 * st], b[i][n][2 * st + 1]);
                 }
               }
           }
