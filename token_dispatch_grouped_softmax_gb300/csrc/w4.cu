@@ -19,8 +19,8 @@ constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4MaxSlots = 2048;   // slots of one launch row (shared-memory lists)
 
 struct W4Params {
-  CUtensorMap tm_q;        // codes as [E*K/8 rows][2 halves of the columns][N/2], boxes of 8 x 2 x 32 words
-  CUtensorMap tm_scale;    // scales the same way, boxes of (64 / group, or 1) x 2 x 32
+  CUtensorMap tm_q;        // codes as [E*K/8 rows][2 halves of the columns][N/2], boxes of 16 x 2 x 32 words
+  CUtensorMap tm_scale;    // scales the same way, boxes of (128 / group) x 2 x 32
   CUtensorMap tm_zero;
   const uint16_t* rows;    // gate_up: x [T, K]; down: h [slots, K]
   const int32_t* ids;      // [slots], NULL: one dense expert
@@ -30,38 +30,15 @@ struct W4Params {
   uint64_t wait_limit_ns;
   int K, N, E, k;
   int slots, slots_per_row;
-  int has_zeros;
-  int split_log2;          // 2^split_log2 warps share a column block's K
+  int parts_log2;          // a sum over K is 2^parts_log2 partial sums
   int blocks;              // column blocks: columns 32 b .. 32 b + 31 of both halves
-  int block_items;         // items of one chunk: blocks / (8 >> split_log2), rounded up
 };
-
-// A stage of a warp's ring: a unit of 64 k of 2 x 32 columns (two swizzled
-// 8 x 128-byte atoms), and the columns' scales and zeros (two groups where a
-// group is 32).
-template <int NT, int GROUP>
-struct W4Ring {
-  static constexpr int kRows = GROUP == 32 ? 2 : 1;   // group rows of a unit
-  static constexpr int kQ = 2048, kScale = 128 * kRows, kZero = 128;   // TMA destinations are 128-byte aligned
-  static constexpr int kDepth = NT == 1 ? 3 : 4;
-  static constexpr int kRed = 16 * NT * 33;   // floats of one warp's partial sums
-  static constexpr int kBlocksPerSm = NT == 1 ? 3 : 2;
-};
-static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<1, 128>::kDepth * W4Ring<1, 128>::kQ,
-              "the sort's counts fit the rings");
 
 // An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
 // of 8 NT rows numbered from chunk0.
 struct W4Active {
   int expert, row0, rows, chunk0;
 };
-
-template <int NT, int GROUP>
-__host__ __device__ constexpr int w4_smem(int E, int slots, bool zeros) {
-  using R = W4Ring<NT, GROUP>;
-  return 1024 + kW4Warps * (R::kDepth * (R::kQ + R::kScale + (zeros ? R::kZero : 0) + 8) + R::kRed * 4) +
-         (E < slots ? E : slots) * (int)sizeof(W4Active) + (slots * 2 + 15) / 16 * 16 + 128;
-}
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
                                             uint32_t bar) {
@@ -215,10 +192,30 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
   return *chunks;
 }
 
-// Persistent: a block takes consecutive items (chunk of an expert's rows,
-// column blocks).  2^split_log2 of its 8 warps share a column block, each
-// with its part of K, and their sums are added in that order; a warp streams
-// 64-k units through a ring of its own, filled by TMA.
+// Zero rows of h for the empty slots, shared out over the blocks.
+__device__ __forceinline__ void w4_zero_rows(const W4Params& p, int slot0, int slots) {
+  const int I = p.N / 2;
+  for (int i = blockIdx.x; i < slots; i += gridDim.x) {
+    const int e = p.ids[slot0 + i];
+    if (e >= 0 && e < p.E) continue;
+    for (int c = threadIdx.x; c < I / 8; c += kW4Threads)
+      reinterpret_cast<uint4*>(p.h + (int64_t)(slot0 + i) * I)[c] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ float w4_swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Persistent: a block takes consecutive items (a chunk of an expert's rows, a
+// column block of 32 columns in each half), and every sum over K is a sum of
+// 2^parts_log2 partial sums added in order, whoever computes them, so that a
+// row's result does not depend on the batch.  While a block has eight items
+// or more, each warp takes a whole item (its partial sums pass through shared
+// memory of its own, no barrier) and the warps' neighbouring column blocks
+// read whole DRAM pages of a row together.  The items left over (all of them
+// in a small batch) are shared: a warp to each part of an item's K, joined in
+// shared memory.  A unit of the stream is 128 k, filled by TMA into a ring of
+// the warp's own, two units deep; every group ends at a place known at
+// compile time.
 //
 // Per 32 k a lane holds one 16-byte vector of codes per half: columns 4g ..
 // 4g+3, k = 8t .. 8t+7 (g = lane / 4, t = lane % 4).  In the ring these are
@@ -233,28 +230,42 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
 // taken off before the scale: sum (q - zero) x = sum (128 + q) x - (128 +
 // zero) sum x.  Every product is exact; the fp32 sums round at 128 + q
 // instead of q - zero, some 2^-19 of the terms, 2^10 below the bf16 result.
-template <int NT, bool GATE_UP, int GROUP>
-__global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
-    w4_kernel(const __grid_constant__ W4Params p) {
-  using Ring = W4Ring<NT, GROUP>;
+template <int NT, int GROUP, bool ZEROS>
+struct W4Ring {
+  static constexpr int kRows = 128 / GROUP;   // group rows of a unit
+  static constexpr int kQ = 4096, kScale = 128 * kRows, kZero = ZEROS ? (64 * kRows + 127) / 128 * 128 : 0;
+  static constexpr int kDepth = 2;
+  static constexpr int kBytes = kW4Warps * kDepth * (kQ + kScale + kZero);
+  static constexpr int kPart = 16 * NT * 32;   // floats of a warp's partial sums
+};
+static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<1, 128, false>::kDepth * W4Ring<1, 128, false>::kQ,
+              "the sort's counts fit the rings");
+
+template <int NT, int GROUP, bool ZEROS>
+__host__ __device__ constexpr int w4_smem(int E, int slots) {
+  using Ring = W4Ring<NT, GROUP, ZEROS>;
+  return 1024 + Ring::kBytes + kW4Warps * (Ring::kPart * 4 + Ring::kDepth * 8) +
+         (E < slots ? E : slots) * (int)sizeof(W4Active) + (slots * 2 + 15) / 16 * 16 + 128;
+}
+
+template <int NT, bool GATE_UP, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant__ W4Params p) {
+  using Ring = W4Ring<NT, GROUP, ZEROS>;
   extern __shared__ uint8_t w4_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int n_act = min(p.E, min(p.slots_per_row, p.slots));
-  // rings | scale rings | zero rings | sums of the warps | experts in use | slot lists
   uint8_t* ring = smem + warp * (Ring::kDepth * Ring::kQ);
-  uint8_t* scales = smem + kW4Warps * Ring::kDepth * Ring::kQ;
-  uint8_t* zeros = scales + kW4Warps * Ring::kDepth * Ring::kScale;
-  float* red = reinterpret_cast<float*>(zeros + (p.has_zeros ? kW4Warps * Ring::kDepth * Ring::kZero : 0));
-  W4Active* act = reinterpret_cast<W4Active*>(red + kW4Warps * Ring::kRed);
-  uint64_t* sums = reinterpret_cast<uint64_t*>(act + n_act);
-  uint64_t* bars = sums + kW4Warps;
+  uint8_t* scales = smem + kW4Warps * Ring::kDepth * Ring::kQ + warp * (Ring::kDepth * Ring::kScale);
+  uint8_t* zeros = smem + kW4Warps * Ring::kDepth * (Ring::kQ + Ring::kScale) + warp * (Ring::kDepth * Ring::kZero);
+  float* sums_of_parts = reinterpret_cast<float*>(smem + Ring::kBytes);   // [8 warps][16 NT values][32 lanes]
+  W4Active* act = reinterpret_cast<W4Active*>(sums_of_parts + kW4Warps * Ring::kPart);
+  uint64_t* scratch = reinterpret_cast<uint64_t*>(act + n_act);
+  uint64_t* bars = scratch + kW4Warps;
   int* abort_flag = reinterpret_cast<int*>(bars + kW4Warps * Ring::kDepth);
   uint16_t* list = reinterpret_cast<uint16_t*>(abort_flag + 2);
   int* cnt = reinterpret_cast<int*>(smem);   // [8][E] over the rings, before they are used
-  scales += warp * (Ring::kDepth * Ring::kScale);
-  zeros += warp * (Ring::kDepth * Ring::kZero);
   const uint32_t bar0 = smem_u32(bars + warp * Ring::kDepth);
   if (lane == 0) {
     for (int d = 0; d < Ring::kDepth; ++d) mbar_init(bar0 + 8 * d, 1);
@@ -267,251 +278,267 @@ __global__ void __launch_bounds__(kW4Threads, W4Ring<NT, GROUP>::kBlocksPerSm)
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
-  const int chunks = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, reinterpret_cast<int*>(sums))
-                                   : w4_lists<NT>(p, slot0, slots, cnt, act, list, sums);
+  const int chunks = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, reinterpret_cast<int*>(scratch))
+                                   : w4_lists<NT>(p, slot0, slots, cnt, act, list, scratch);
   const int half = p.N / 2;
-  if (GATE_UP && p.ids) {                    // empty slots: zero rows
-    for (int i = blockIdx.x; i < slots; i += gridDim.x) {
-      const int e = p.ids[slot0 + i];
-      if (e < 0 || e >= p.E)
-        for (int c = tid; c < half / 8; c += kW4Threads)
-          reinterpret_cast<uint4*>(p.h + (int64_t)(slot0 + i) * half)[c] = make_uint4(0, 0, 0, 0);
-    }
-  }
-  const int64_t items = (int64_t)chunks * p.block_items;
+  if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
+  const int64_t items = (int64_t)chunks * p.blocks;
   const int begin = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
-  if (begin >= end) return;
   fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
   __syncthreads();
-  const int split = 1 << p.split_log2, wide = kW4Warps >> p.split_log2;   // warps of a block, blocks of an item
-  const int part = warp & (split - 1), sub = warp >> p.split_log2;
-  const int units = p.K / 64;
-  const int u0 = units * part / split, u1 = units * (part + 1) / split;
+  if (begin >= end) return;
+  const int units = (p.K + 127) / 128;
   auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
-  // the loader: item (lchunk, lblock), unit lu of the next copies, and their
-  // coordinates; only items with a column block for this warp take stages
-  int litem = begin, lchunk = begin / p.block_items, lblock = begin - lchunk * p.block_items;
-  int la = 0, lu = u0, lstage = 0;
-  while (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
-  int ca = la, cchunk = lchunk, cblock = lblock;   // the same of the item being computed
-  int lcol = 0, lqrow = 0, lsrow = 0;
-  auto next_item = [&]() {   // litem, or the next one with a column block for this warp
-    for (; litem < end; ++litem, ++lblock) {
-      if (lblock == p.block_items) {
-        lblock = 0;
-        ++lchunk;
-      }
-      if (lblock * wide + sub < p.blocks) break;
-    }
-    if (litem >= end) return;
-    if (lchunk >= act[la].chunk0 + chunks_of(act[la])) ++la;   // chunks come one after another
-    const int expert = act[la].expert;
-    lcol = (lblock * wide + sub) * 32;
-    lqrow = expert * (p.K / 8);
-    lsrow = expert * (p.K / GROUP);
+  // The warp's segments: segment s < whole is part s % parts of the warp's
+  // whole item s / parts; then one part of a shared item in each pass.
+  const int parts = 1 << p.parts_log2, together = kW4Warps >> p.parts_log2;   // items shared at once
+  int left = (end - begin) & (kW4Warps - 1), passes = (left + together - 1) >> (3 - p.parts_log2);
+  if (passes >= parts) left = passes = 0;   // sharing would take as long: one more round of whole items
+  const int whole = (end - left - begin + kW4Warps - 1) / kW4Warps << p.parts_log2;
+  const int segments = whole + passes;
+  auto item_of = [&](int s) {   // end or more: none
+    if (s >= whole) return end - left + (s - whole) * together + (warp >> p.parts_log2);
+    const int item = begin + warp + (s >> p.parts_log2) * kW4Warps;
+    return item < end - left ? item : end;
   };
-  next_item();
+  auto part_of = [&](int s) { return (s >= whole ? warp : s) & (parts - 1); };
+
+  // the loader: segment, the next unit's coordinates, and the stage
+  int lseg = -1, lu = 0, lu_end = 0, lstage = 0, la = 0;
+  int lcol = 0, lqrow = 0, lsrow = 0;
+  auto next_segment = [&]() {   // the next segment with units
+    while (++lseg < segments) {
+      const int item = item_of(lseg), part = part_of(lseg);
+      if (item >= end) continue;
+      lu = units * part >> p.parts_log2;
+      lu_end = units * (part + 1) >> p.parts_log2;
+      if (lu == lu_end) continue;
+      const int chunk = item / p.blocks;
+      while (chunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
+      const int expert = act[la].expert;
+      lcol = (item - chunk * p.blocks) * 32;
+      lqrow = expert * (p.K / 8) + lu * 16;
+      lsrow = expert * (p.K / GROUP) + lu * Ring::kRows;
+      return;
+    }
+  };
   auto issue = [&]() {
-    if (litem >= end) return;
+    if (lu == lu_end) {
+      if (lseg >= segments) return;
+      next_segment();
+      if (lseg >= segments) return;
+    }
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * lstage;
-      const bool sc = GROUP <= 64 || lu == u0 || (lu & 1) == 0;
-      const uint32_t bytes = Ring::kQ + (sc ? Ring::kRows * (p.has_zeros ? 192 : 128) : 0);
-      mbar_arrive_expect_tx(bar, bytes);
-      tma_load_3d(smem_u32(ring + lstage * Ring::kQ), &p.tm_q, lcol, 0, lqrow + lu * 8, bar);
-      if (sc) {
-        const int row = lsrow + (GROUP <= 64 ? lu * Ring::kRows : lu >> 1);
-        tma_load_3d(smem_u32(scales + lstage * Ring::kScale), &p.tm_scale, lcol, 0, row, bar);
-        if (p.has_zeros) tma_load_3d(smem_u32(zeros + lstage * Ring::kZero), &p.tm_zero, lcol, 0, row, bar);
-      }
+      mbar_arrive_expect_tx(bar, Ring::kQ + Ring::kRows * (ZEROS ? 192 : 128));
+      tma_load_3d(smem_u32(ring) + lstage * Ring::kQ, &p.tm_q, lcol, 0, lqrow, bar);
+      tma_load_3d(smem_u32(scales) + lstage * Ring::kScale, &p.tm_scale, lcol, 0, lsrow, bar);
+      if (ZEROS) tma_load_3d(smem_u32(zeros) + lstage * Ring::kZero, &p.tm_zero, lcol, 0, lsrow, bar);
     }
-    if (++lstage == Ring::kDepth) lstage = 0;
-    if (++lu == u1) {
-      lu = u0;
-      ++litem;
-      ++lblock;
-      next_item();
-    }
+    lqrow += 16;
+    lsrow += Ring::kRows;
+    lstage ^= 1;
+    ++lu;
   };
-#pragma unroll 1
-  for (int d = 0; d < Ring::kDepth; ++d) issue();
-  const uint32_t q_at = t * 256 + ((g ^ 2 * t) << 4);   // line 2t; the second half's line is the next, its chunk ^ 1
+  issue();
+  issue();
+  const uint32_t q_at = smem_u32(ring) + t * 256 + ((g ^ 2 * t) << 4);   // line 2t; the second half's line is the next, its chunk ^ 1
 
-  // this lane's rows of the chunk, and their vectors of the next unit: loaded a
-  // unit ahead (the first unit's again at an item's end, for the next block)
   const uint16_t* x[NT];
-  uint4 xn[NT][2];
-  int stage = 0;
+  uint4 xn[NT][2];   // this lane's vectors of the next 64 k
+  int x_chunk = -1;  // the chunk that x is of
+  int ca = 0, stage = 0;
   uint32_t phase = 0;
   bool ok = true;
+  W4Active a = act[0];
+  float* mine = sums_of_parts + warp * Ring::kPart + lane;
 #pragma unroll 1
-  for (int item = begin; item < end; ++item) {
-    if (cchunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
-    const W4Active a = act[ca];
-    const int row_first = (cchunk - a.chunk0) * 8 * NT;
-    if (cblock == 0 || item == begin) {   // another chunk: its rows
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int r = row_first + n * 8 + g;
-        x[n] = nullptr;
-        xn[n][0] = xn[n][1] = make_uint4(0, 0, 0, 0);
-        if (r < a.rows) {
-          const int slot = slot0 + list[a.row0 + r];
-          x[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + u0 * 64 + 8 * t;
-          xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n]));
-          xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + 32));
-        }
-      }
-    }
+  for (int seg = 0; seg < segments; ++seg) {
+    const int item = item_of(seg), part = part_of(seg);
+    const int u0 = units * part >> p.parts_log2, u1 = units * (part + 1) >> p.parts_log2;
+    int chunk = 0, block = 0, row_first = 0;
     float tot[2][2][NT][4];
 #pragma unroll
     for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
-    if (cblock * wide + sub < p.blocks && ok) {
-      float acc[2][2][NT][4], sum[NT][4];
-      if (GROUP == 128) {
+    if (item < end) {
+      chunk = item / p.blocks;
+      block = item - chunk * p.blocks;
+      while (chunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
+      a = act[ca];
+      row_first = (chunk - a.chunk0) * 8 * NT;
+    }
+    if (item < end && u0 < u1 && ok) {
+      if (chunk != x_chunk || seg >= whole || part == 0) {
+        x_chunk = chunk;
 #pragma unroll
-        for (int i = 0; i < 16 * NT; ++i) (&acc[0][0][0][0])[i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) (&sum[0][0])[i] = 0.f;
+        for (int n = 0; n < NT; ++n) {
+          const int r = row_first + n * 8 + g;
+          x[n] = nullptr;
+          xn[n][0] = xn[n][1] = make_uint4(0, 0, 0, 0);
+          if (r < a.rows) {
+            const int slot = slot0 + list[a.row0 + r];
+            x[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + 8 * t;
+            xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n] + u0 * 128));
+            xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + u0 * 128 + 32));
+          }
+        }
       }
-      uint2 sraw[2];
-      uint32_t zraw[2] = {0x08080808u, 0x08080808u};
+      int next_k = u0 * 128 + 64;   // the 64 k to load ahead
 #pragma unroll 1
       for (int u = u0; u < u1; ++u) {
         if (!mbar_wait_warp(bar0 + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 2, kKernW4)) {
           ok = false;
           break;
         }
-        const uint8_t* s = ring + stage * Ring::kQ;
-        auto read_scales = [&](int row) {
+        float acc[2][2][NT][4], sum[NT][4];
 #pragma unroll
-          for (int set = 0; set < 2; ++set) {
-            sraw[set] = *reinterpret_cast<const uint2*>(scales + stage * Ring::kScale + (row * 2 + set) * 64 + g * 8);
-            if (p.has_zeros)
-              zraw[set] = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + (row * 2 + set) * 32 + g * 4);
-          }
-        };
-        if (GROUP == 128 && (u == u0 || (u & 1) == 0)) read_scales(0);
-        uint32_t b[2][NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 v = xn[n][i];
-            b[i][n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
-            b[i][n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
-            b[i][n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
-            b[i][n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
-          }
-          if (x[n]) {
-            const uint16_t* next = x[n] + (u + 1 < u1 ? (u + 1 - u0) * 64 : 0);
-            xn[n][0] = __ldg(reinterpret_cast<const uint4*>(next));
-            xn[n][1] = __ldg(reinterpret_cast<const uint4*>(next + 32));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {   // 32 k each
+        for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
+          if (j == 1 && u * 128 + 64 >= p.K) break;
+          uint32_t b[2][NT][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-            if (GROUP == 32 || (GROUP == 64 && i == 0)) mma_16816_first(sum[n], ones, b[i][n][0], b[i][n][1]);
-            else mma_16816(sum[n], ones, b[i][n][0], b[i][n][1]);
-            mma_16816(sum[n], ones, b[i][n][2], b[i][n][3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 v = xn[n][i];
+              b[i][n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+              b[i][n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+              b[i][n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+              b[i][n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+            }
+            if (x[n] && next_k < p.K) {
+              xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k));
+              xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k + 32));
+            }
           }
+          next_k += 64;
 #pragma unroll
-          for (int set = 0; set < 2; ++set) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s + i * 1024 + (set ? (q_at ^ 16) + 128 : q_at));
-            const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < 2; ++i) {   // 32 k each
+            const bool first = GROUP == 32 || (GROUP == 64 && i == 0) || (GROUP == 128 && i == 0 && j == 0);
+            const bool last = GROUP == 32 || (GROUP == 64 && i == 1) || (GROUP == 128 && i == 1 && j == 1);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+              if (first) mma_16816_first(sum[n], ones, b[i][n][0], b[i][n][1]);
+              else mma_16816(sum[n], ones, b[i][n][0], b[i][n][1]);
+              mma_16816(sum[n], ones, b[i][n][2], b[i][n][3]);
+            }
 #pragma unroll
-              for (int st = 0; st < 2; ++st) {
-                const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
-                                       w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
+            for (int set = 0; set < 2; ++set) {
+              const uint32_t at = (set ? (q_at ^ 16) + 128 : q_at) + stage * Ring::kQ + (2 * j + i) * 1024;
+              uint32_t word[4];
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                           : "r"(at));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  if (st == 0 && (GROUP == 32 || (GROUP == 64 && i == 0)))
-                    mma_16816_first(acc[set][hf][n], w, b[i][n][0], b[i][n][1]);
-                  else
-                    mma_16816(acc[set][hf][n], w, b[i][n][2 * st], b[i][n][2 * st + 1]);
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                  const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
+                                         w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    if (st == 0 && first) mma_16816_first(acc[set][hf][n], w, b[i][n][0], b[i][n][1]);
+                    else mma_16816(acc[set][hf][n], w, b[i][n][2 * st], b[i][n][2 * st + 1]);
+                  }
+                }
+            }
+            if (last) {
+              const int row = GROUP == 32 ? 2 * j + i : GROUP == 64 ? j : 0;
+#pragma unroll
+              for (int set = 0; set < 2; ++set) {
+                const uint2 sr = *reinterpret_cast<const uint2*>(scales + stage * Ring::kScale + (row * 2 + set) * 64 + g * 8);
+                uint32_t zr = 0;
+                if (ZEROS) zr = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + (row * 2 + set) * 32 + g * 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {   // the lane's four columns
+                  const uint32_t sp = c < 2 ? sr.x : sr.y;
+                  const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
+                  const float zero = ZEROS ? __uint_as_float(0x43000000u | ((zr >> (8 * c)) & 15u) << 16) : 136.f;   // 128 + zero
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                      float& o = tot[set][c >> 1][n][(c & 1) * 2 + r];
+                      o = fmaf(scale, fmaf(-zero, sum[n][r], acc[set][c >> 1][n][(c & 1) * 2 + r]), o);
+                    }
                 }
               }
-          }
-          if (GROUP == 32 || (i == 1 && (GROUP == 64 || u + 1 == u1 || (u & 1) != 0))) {
-            if (GROUP <= 64) read_scales(GROUP == 32 ? i : 0);
-#pragma unroll
-            for (int set = 0; set < 2; ++set)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {   // the lane's four columns
-                const uint32_t sp = c < 2 ? sraw[set].x : sraw[set].y;
-                const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
-                const float zero = __uint_as_float(0x43000000u | ((zraw[set] >> (8 * c)) & 15u) << 16);   // 128 + zero
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int r = 0; r < 2; ++r) {
-                    float& v = acc[set][c >> 1][n][(c & 1) * 2 + r];
-                    float& o = tot[set][c >> 1][n][(c & 1) * 2 + r];
-                    o = fmaf(scale, fmaf(-zero, sum[n][r], v), o);
-                    if (GROUP == 128) v = 0.f;
-                  }
-              }
-            if (GROUP == 128) {
-#pragma unroll
-              for (int i2 = 0; i2 < 4 * NT; ++i2) (&sum[0][0])[i2] = 0.f;
             }
           }
         }
         __syncwarp();   // every lane has read the stage
         issue();        // into the same stage
-        if (++stage == Ring::kDepth) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        stage ^= 1;
+        phase ^= stage == 0;
       }
     }
-    // join the warps' sums: value (set, column, row) of lane (column / 4, row / 2)
-    float* mine = red + warp * Ring::kRed;
+    if (seg < whole) {
+      if (item >= end) continue;
+      // the parts' sums in order, through this lane's shared memory
+      if (part > 0) {
 #pragma unroll
-    for (int set = 0; set < 2; ++set)
+        for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] += mine[i * 32];
+      }
+      if (part + 1 < parts) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+        for (int i = 0; i < 16 * NT; ++i) mine[i * 32] = (&tot[0][0][0][0])[i];
+        continue;
+      }
+      // columns 4g .. 4g+3 of rows 2t, 2t+1 are this lane's
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            mine[((set * NT + n) * 8 + (r & 1) * 4 + 2 * hf + (r >> 1)) * 33 + lane] = tot[set][hf][n][r];
+        for (int r = 0; r < 2; ++r) {
+          const int row = row_first + n * 8 + 2 * t + r;
+          if (row >= a.rows) continue;
+          const int64_t slot = slot0 + list[a.row0 + row];
+          float v[2][4];
+#pragma unroll
+          for (int set = 0; set < 2; ++set)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[set][c] = tot[set][c >> 1][n][(c & 1) * 2 + r];
+          if (GATE_UP) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[0][c] = w4_swiglu(v[0][c], v[1][c]);
+            *reinterpret_cast<uint2*>(p.h + slot * half + block * 32 + 4 * g) =
+                make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
+          } else {
+#pragma unroll
+            for (int set = 0; set < 2; ++set)
+              *reinterpret_cast<float4*>(p.part + slot * p.N + set * half + block * 32 + 4 * g) =
+                  make_float4(v[set][0], v[set][1], v[set][2], v[set][3]);
+          }
+        }
+      continue;
+    }
+    // a shared item: its parts' sums meet in shared memory, and its warps
+    // share the values out: value i of the first half and of the second
+#pragma unroll
+    for (int i = 0; i < 16 * NT; ++i) mine[i * 32] = (&tot[0][0][0][0])[i];
     __syncthreads();
-    const int at = ((warp & 1) * 4 + (lane & 3)) * 33 + (lane >> 2) * 4 + (warp >> 1);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = row_first + n * 8 + warp;   // this warp's row
-      if (r >= a.rows) continue;
-      const int64_t slot = slot0 + list[a.row0 + r];
-      for (int b = 0; b < wide; ++b) {
-        const int block = cblock * wide + b;
-        if (block >= p.blocks) break;
-        const float* from = red + b * split * Ring::kRed + n * 8 * 33 + at;
-        float v[2] = {0.f, 0.f};
-#pragma unroll 4
-        for (int w = 0; w < split; ++w)
-#pragma unroll
-          for (int set = 0; set < 2; ++set) v[set] += from[w * Ring::kRed + set * NT * 8 * 33];
+    if (item < end) {
+      const float* from = sums_of_parts + (warp - part) * Ring::kPart + lane;
+      for (int i = part; i < 8 * NT; i += parts) {   // i = (hf * NT + n) * 4 + r
+        const int r = i & 3, n = (i >> 2) % NT, hf = (i >> 2) / NT;
+        const int row = row_first + n * 8 + 2 * t + (r & 1);
+        if (row >= a.rows) continue;
+        float v0 = from[i * 32], v1 = from[(8 * NT + i) * 32];
+        for (int w = 1; w < parts; ++w) {
+          v0 += from[w * Ring::kPart + i * 32];
+          v1 += from[w * Ring::kPart + (8 * NT + i) * 32];
+        }
+        const int64_t slot = slot0 + list[a.row0 + row];
+        const int col = block * 32 + 4 * g + 2 * hf + (r >> 1);
         if (GATE_UP) {
-          const float y = v[0] / (1.f + expf(-v[0])) * v[1];
-          p.h[slot * half + block * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+          p.h[slot * half + col] = __bfloat16_as_ushort(__float2bfloat16_rn(w4_swiglu(v0, v1)));
         } else {
-          p.part[slot * p.N + block * 32 + lane] = v[0];
-          p.part[slot * p.N + half + block * 32 + lane] = v[1];
+          p.part[slot * p.N + col] = v0;
+          p.part[slot * p.N + half + col] = v1;
         }
       }
     }
     __syncthreads();
-    if (++cblock == p.block_items) {
-      cblock = 0;
-      ++cchunk;
-    }
   }
   if (!ok && lane == 0) {   // stopped early: the copies in flight land (bounded) before the block's memory goes
     for (int d = 0; d < Ring::kDepth; ++d) {
@@ -577,64 +604,57 @@ __global__ void __launch_bounds__(kW4CombineThreads) w4_combine_kernel(const flo
   *reinterpret_cast<uint4*>(y + t * H + c) = pack8(acc);
 }
 
-template <int NT, bool GATE_UP, int GROUP>
+template <int NT, bool GATE_UP, int GROUP, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
-  using Ring = W4Ring<NT, GROUP>;
   static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
   if (!configured[dev.ordinal].load()) {
-    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 w4_smem<NT, GROUP>(kMaxExperts, kW4MaxSlots, true));
+    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP, GROUP, ZEROS>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 w4_smem<NT, GROUP, ZEROS>(kMaxExperts, kW4MaxSlots));
     if (err != cudaSuccess) return err;
     configured[dev.ordinal].store(1);
   }
   const int row_slots = std::min(p.slots_per_row, p.slots);
   const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
-  const int64_t most = (int64_t)row_slots * p.block_items;   // every slot its own chunk
-  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP>,
-                    dim3((unsigned)std::min<int64_t>(most, Ring::kBlocksPerSm * dev.num_sms), (unsigned)rows),
-                    dim3(kW4Threads), w4_smem<NT, GROUP>(p.E, row_slots, p.has_zeros), stream, 1, p);
+  const int64_t most = (int64_t)row_slots * p.blocks;   // every slot its own chunk
+  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP, ZEROS>,
+                    dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows), dim3(kW4Threads),
+                    w4_smem<NT, GROUP, ZEROS>(p.E, row_slots), stream, 1, p);
 }
 
 template <bool GATE_UP, int GROUP>
-cudaError_t launch_w4_rows(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_w4_rows(const W4Params& p, bool zeros, const DeviceInfo& dev, cudaStream_t stream) {
   // 8 rows a chunk while the experts in use hold few rows each, else 16
-  return (int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k ? launch_w4<1, GATE_UP, GROUP>(p, dev, stream)
-                                                                   : launch_w4<2, GATE_UP, GROUP>(p, dev, stream);
+  if ((int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k)
+    return zeros ? launch_w4<1, GATE_UP, GROUP, true>(p, dev, stream) : launch_w4<1, GATE_UP, GROUP, false>(p, dev, stream);
+  return zeros ? launch_w4<2, GATE_UP, GROUP, true>(p, dev, stream) : launch_w4<2, GATE_UP, GROUP, false>(p, dev, stream);
 }
 
-// K's split over warps and the launch of the group's kernel.  The split is
-// a rule on K alone, so that a row's sums do not depend on the batch: the
-// most warps (8 at most) whose shares of K's 64-k units are equal, or nearly
-// (at least 16 units a warp).
+// The tensor maps, K's parts, and the launch of the group's kernel.
 template <bool GATE_UP>
 cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scales, const uint8_t* zeros,
                             int64_t group, const DeviceInfo& dev, cudaStream_t stream) {
   const cuuint64_t half = p.N / 2, rows = (cuuint64_t)p.E * p.K;
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, cuuint64_t bytes, const void* base, cuuint64_t n,
-                    cuuint32_t box_rows, CUtensorMapSwizzle swizzle) {
+                    int box_rows, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[3] = {half, 2, n}, strides[2] = {half * bytes, (cuuint64_t)p.N * bytes};
-    const cuuint32_t box[3] = {32, 2, box_rows};
+    const cuuint32_t box[3] = {32, 2, (cuuint32_t)box_rows};
     return encode_tensor_map_3d(map, type, base, dims, strides, box, swizzle);
   };
-  const cuuint32_t box_rows = group == 32 ? 2 : 1;
-  if (!encode(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, q, rows / 8, 8, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode(&p.tm_scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, rows / group, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
-    return cudaErrorInvalidValue;
-  p.has_zeros = zeros != nullptr;
-  if (zeros && !encode(&p.tm_zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, rows / group, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+  const int group_rows = (int)(128 / group);
+  if (!encode(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, q, rows / 8, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&p.tm_scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, rows / group, group_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      (zeros && !encode(&p.tm_zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, rows / group, group_rows, CU_TENSOR_MAP_SWIZZLE_NONE)))
     return cudaErrorInvalidValue;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
   p.slots_per_row = kW4MaxSlots / p.k * p.k;
   p.blocks = (int)(half / 32);
-  const int units = p.K / 64;
-  p.split_log2 = 3;
-  while (p.split_log2 > 0 && units % (1 << p.split_log2) != 0 && units < (16 << p.split_log2)) --p.split_log2;
-  const int wide = kW4Warps >> p.split_log2;
-  p.block_items = (p.blocks + wide - 1) / wide;
-  if (group == 32) return launch_w4_rows<GATE_UP, 32>(p, dev, stream);
-  if (group == 64) return launch_w4_rows<GATE_UP, 64>(p, dev, stream);
-  return launch_w4_rows<GATE_UP, 128>(p, dev, stream);
+  const int units = (p.K + 127) / 128;
+  p.parts_log2 = units >= 16 ? 3 : units >= 4 ? 2 : units >= 2 ? 1 : 0;
+  if (group == 32) return launch_w4_rows<GATE_UP, 32>(p, zeros != nullptr, dev, stream);
+  if (group == 64) return launch_w4_rows<GATE_UP, 64>(p, zeros != nullptr, dev, stream);
+  return launch_w4_rows<GATE_UP, 128>(p, zeros != nullptr, dev, stream);
 }
 
 // One thread per (group, column) of [rows, N] bf16 weights.
