@@ -290,30 +290,30 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   const int units = (p.K + 127) / 128;
   auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
-  // The warp's segments: segment s < whole is part s % parts of the warp's
-  // whole item s / parts; then one part of a shared item in each pass.
+  // The warp's runs: run s < whole is an item of its own over the whole of K,
+  // then one part of a shared item in each pass.
   const int parts = 1 << p.parts_log2, together = kW4Warps >> p.parts_log2;   // items shared at once
   int left = (end - begin) & (kW4Warps - 1), passes = (left + together - 1) >> (3 - p.parts_log2);
   if (passes >= parts) left = passes = 0;   // sharing would take as long: one more round of whole items
-  const int whole = (end - left - begin + kW4Warps - 1) / kW4Warps << p.parts_log2;
-  const int segments = whole + passes;
+  const int whole = (end - left - begin + kW4Warps - 1) / kW4Warps;
+  const int runs = whole + passes;
+  const int part = warp & (parts - 1);                                        // of the shared items
+  const int part_u0 = units * part >> p.parts_log2, part_u1 = units * (part + 1) >> p.parts_log2;
   auto item_of = [&](int s) {   // end or more: none
     if (s >= whole) return end - left + (s - whole) * together + (warp >> p.parts_log2);
-    const int item = begin + warp + (s >> p.parts_log2) * kW4Warps;
+    const int item = begin + warp + s * kW4Warps;
     return item < end - left ? item : end;
   };
-  auto part_of = [&](int s) { return (s >= whole ? warp : s) & (parts - 1); };
 
-  // the loader: segment, the next unit's coordinates, and the stage
-  int lseg = -1, lu = 0, lu_end = 0, lstage = 0, la = 0;
+  // the loader: run, the next unit's coordinates, and the stage
+  int lrun = -1, lu = 0, lu_end = 0, lstage = 0, la = 0;
   int lcol = 0, lqrow = 0, lsrow = 0;
-  auto next_segment = [&]() {   // the next segment with units
-    while (++lseg < segments) {
-      const int item = item_of(lseg), part = part_of(lseg);
+  auto next_run = [&]() {   // the next run that has an item
+    while (++lrun < runs) {
+      const int item = item_of(lrun);
       if (item >= end) continue;
-      lu = units * part >> p.parts_log2;
-      lu_end = units * (part + 1) >> p.parts_log2;
-      if (lu == lu_end) continue;
+      lu = lrun < whole ? 0 : part_u0;
+      lu_end = lrun < whole ? units : part_u1;
       const int chunk = item / p.blocks;
       while (chunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
       const int expert = act[la].expert;
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   };
   auto issue = [&]() {
     if (lu == lu_end) {
-      if (lseg >= segments) return;
-      next_segment();
-      if (lseg >= segments) return;
+      if (lrun >= runs) return;
+      next_run();
+      if (lrun >= runs) return;
     }
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * lstage;
@@ -354,22 +354,21 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   W4Active a = act[0];
   float* mine = sums_of_parts + warp * Ring::kPart + lane;
 #pragma unroll 1
-  for (int seg = 0; seg < segments; ++seg) {
-    const int item = item_of(seg), part = part_of(seg);
-    const int u0 = units * part >> p.parts_log2, u1 = units * (part + 1) >> p.parts_log2;
-    int chunk = 0, block = 0, row_first = 0;
+  for (int run = 0; run < runs; ++run) {
+    const int item = item_of(run);
+    const bool shared = run >= whole;
+    const int u0 = shared ? part_u0 : 0, u1 = shared ? part_u1 : units;
+    int block = 0, row_first = 0;
     float tot[2][2][NT][4];
 #pragma unroll
     for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
     if (item < end) {
-      chunk = item / p.blocks;
+      const int chunk = item / p.blocks;
       block = item - chunk * p.blocks;
       while (chunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
       a = act[ca];
       row_first = (chunk - a.chunk0) * 8 * NT;
-    }
-    if (item < end && u0 < u1 && ok) {
-      if (chunk != x_chunk || seg >= whole || part == 0) {
+      if (chunk != x_chunk || shared) {
         x_chunk = chunk;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -384,9 +383,25 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
           }
         }
       }
-      int next_k = u0 * 128 + 64;   // the 64 k to load ahead
+    }
+    if (item < end && ok) {
+      int next_k = u0 * 128 + 64;   // the 64 k to load ahead; past the end the first, for the next item
+      int part_end = shared ? u1 : units >> p.parts_log2, parts_done = 0;
 #pragma unroll 1
       for (int u = u0; u < u1; ++u) {
+        if (u == part_end) {   // the parts' sums in order, through this lane's shared memory
+          if (parts_done > 0) {
+#pragma unroll
+            for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] += mine[i * 32];
+          }
+#pragma unroll
+          for (int i = 0; i < 16 * NT; ++i) {
+            mine[i * 32] = (&tot[0][0][0][0])[i];
+            (&tot[0][0][0][0])[i] = 0.f;
+          }
+          ++parts_done;
+          part_end = units * (parts_done + 1) >> p.parts_log2;
+        }
         if (!mbar_wait_warp(bar0 + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 2, kKernW4)) {
           ok = false;
           break;
@@ -396,6 +411,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
         for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
           if (j == 1 && u * 128 + 64 >= p.K) break;
           uint32_t b[2][NT][4];
+          if (next_k >= p.K) next_k = 0;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -406,7 +422,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
               b[i][n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
               b[i][n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
             }
-            if (x[n] && next_k < p.K) {
+            if (x[n]) {
               xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k));
               xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k + 32));
             }
@@ -473,17 +489,11 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
         phase ^= stage == 0;
       }
     }
-    if (seg < whole) {
+    if (!shared) {
       if (item >= end) continue;
-      // the parts' sums in order, through this lane's shared memory
-      if (part > 0) {
+      if (parts > 1) {
 #pragma unroll
         for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] += mine[i * 32];
-      }
-      if (part + 1 < parts) {
-#pragma unroll
-        for (int i = 0; i < 16 * NT; ++i) mine[i * 32] = (&tot[0][0][0][0])[i];
-        continue;
       }
       // columns 4g .. 4g+3 of rows 2t, 2t+1 are this lane's
 #pragma unroll
@@ -651,7 +661,7 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
   p.slots_per_row = kW4MaxSlots / p.k * p.k;
   p.blocks = (int)(half / 32);
   const int units = (p.K + 127) / 128;
-  p.parts_log2 = units >= 16 ? 3 : units >= 4 ? 2 : units >= 2 ? 1 : 0;
+  p.parts_log2 = units >= 32 ? 3 : units >= 8 ? 2 : units >= 2 ? 1 : 0;   // about four units a part
   if (group == 32) return launch_w4_rows<GATE_UP, 32>(p, zeros != nullptr, dev, stream);
   if (group == 64) return launch_w4_rows<GATE_UP, 64>(p, zeros != nullptr, dev, stream);
   return launch_w4_rows<GATE_UP, 128>(p, zeros != nullptr, dev, stream);
