@@ -110,4 +110,5 @@ def check(name, rc):
 
 
 def call(name, *args):
-    return check(name, getattr(load(), name)(*args))
+    rc = getattr(_lib or load(), name)(*args)
+    return rc if rc == MOE_OK else check(name, rc)

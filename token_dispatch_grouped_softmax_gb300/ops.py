@@ -8,6 +8,7 @@ library's CUDA kernels; there is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -16,12 +17,20 @@ from ._lib import call
 _BF16 = torch.bfloat16
 
 
+# The current device and its current stream's handle without torch's wrapper
+# objects (3 us a call on GB300's host) where this torch has the raw accessors.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype, ndim=None):
@@ -29,10 +38,9 @@ def _need(t, name, dtype, ndim=None):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor (the path runs only on the GPU)" % name)
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         # the kernels run on the current device and would be handed another GPU's memory
-        raise ValueError("%s is on %s but the current device is cuda:%d" % (name, t.device,
-                                                                           torch.cuda.current_device()))
+        raise ValueError("%s is on %s but the current device is cuda:%d" % (name, t.device, _current_device()))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
@@ -281,6 +289,13 @@ def w4_gate_up_swiglu(x, ids, qweight, scales, zeros=None):
     return h
 
 
+@functools.lru_cache(maxsize=256)
+def _w4_down_workspace(T, H, k):
+    nbytes = ctypes.c_size_t(0)
+    call("moe_w4_down_workspace_size", T, H, k, ctypes.byref(nbytes))
+    return nbytes.value
+
+
 def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=None):
     """y [T, H] bf16 with y_t = sum_j w[t, j] (h[t, j] . Wd) (+ y_shared_t), e =
     ids[t, j] (-1 adds nothing); h [T, k, I] bf16 in slot order, w [T, k] fp32
@@ -305,9 +320,7 @@ def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=N
         _need(out, "out", _BF16, 2)
         if tuple(out.shape) != (T, H):
             raise ValueError("out must be [T, H]")
-    nbytes = ctypes.c_size_t(0)
-    call("moe_w4_down_workspace_size", T, H, k, ctypes.byref(nbytes))
-    ws = _ws(nbytes.value, h.device)
+    ws = _ws(_w4_down_workspace(T, H, k), h.device)
     call("moe_w4_down_combine", _p(h), _p(ids), _p(w), _p(qweight), _p(scales), _p(zeros), _p(y_shared), T, H, E, k,
          I, group, _p(out), _p(ws), ws.numel(), _stream())
     return out
