@@ -228,7 +228,7 @@ int moe_route_select(const void* logits, int logits_bf16, const float* bias, int
   if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;   // NaN or infinite
   if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
   if (E > moe::kMaxExperts || k > 32 || n_groups > 32) return MOE_ERR_UNSUPPORTED;
-  if (T > 0 && !aligned16(logits)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!aligned16(logits) || !aligned16(bias))) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   const moe::RouteChoice c{score == MOE_SCORE_SIGMOID, group_score == MOE_GROUP_TOP2, renorm != 0, (int)n_groups,
                            (int)top_groups, scale};

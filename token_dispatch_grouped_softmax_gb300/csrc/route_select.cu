@@ -23,12 +23,12 @@ namespace {
 
 constexpr int kSelWarps = 8;   // tokens per block
 
-// Order-preserving key of a value: larger value, larger key; +0 and -0 are
-// one key; every NaN is above +inf.  0 is below every value's key.
+// Order-preserving key of the result of an fp32 addition: larger value,
+// larger key; NaN (an addition's NaN is positive) above +inf.  0 is below
+// every value's key.
 __device__ __forceinline__ uint32_t value_key(float v) {
-  if (v != v) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(v + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
@@ -42,64 +42,6 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_a
 __device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// The experts of the k largest keys of the warp, equal keys to the lowest
-// expert: slot j's in lane j.  A lane holds the keys of experts e0 + i * step.
-// Each round takes the warp's largest leading key.  Up to 8 keys a lane sorts
-// them once (stable adjacent exchanges: 28 of them at 8) and its leading key
-// is key[0]; above that it scans its keys in each round (a sort grows with NV^2).
-template <int NV>
-__device__ __forceinline__ int choose(uint32_t (&key)[NV], int e0, int step, int k, int lane) {
-  int chosen = 0;
-  if constexpr (NV <= 8) {
-    int at[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) at[i] = e0 + i * step;
-#pragma unroll
-    for (int a = 0; a < NV - 1; ++a)
-#pragma unroll
-      for (int b = NV - 1; b > a; --b) {
-        const bool up = key[b] > key[b - 1];
-        const uint32_t hi = max(key[b], key[b - 1]), lo = min(key[b], key[b - 1]);
-        const int ahi = up ? at[b] : at[b - 1], alo = up ? at[b - 1] : at[b];
-        key[b - 1] = hi;
-        key[b] = lo;
-        at[b - 1] = ahi;
-        at[b] = alo;
-      }
-    for (int j = 0; j < k; ++j) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
-      const uint32_t low = __reduce_min_sync(0xffffffffu, key[0] == top ? (uint32_t)at[0] : 0xFFFFFFFFu);
-      if ((uint32_t)at[0] == low) {   // this lane held it (experts are distinct)
-#pragma unroll
-        for (int i = 0; i < NV - 1; ++i) {
-          key[i] = key[i + 1];
-          at[i] = at[i + 1];
-        }
-        key[NV - 1] = 0;
-        at[NV - 1] = -1;
-      }
-      if (lane == j) chosen = (int)low;
-    }
-  } else {
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) best = max(best, key[i]);
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      uint32_t mine = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (key[i] == top) mine = (uint32_t)(e0 + i * step);
-      const uint32_t low = __reduce_min_sync(0xffffffffu, mine);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if ((uint32_t)(e0 + i * step) == low) key[i] = 0;
-      if (lane == j) chosen = (int)low;
-    }
-  }
-  return chosen;
-}
-
 struct SelectParams {
   const void* logits;
   const float* bias;
@@ -112,9 +54,31 @@ struct SelectParams {
   float scale;
 };
 
-// NV: values per lane (per_group <= NV << lanes_log2).
-template <int NV, typename Z>
+// Four consecutive logits (16 or 8 bytes).
+__device__ __forceinline__ void load_logits4(const float* p, float* v) {
+  const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+__device__ __forceinline__ void load_logits4(const uint16_t* p, float* v) {
+  const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+}
+
+// NV values per lane, of the lane's group; value i is member l + i L of the
+// group (l the lane's place among the group's L lanes), or with QUADS member
+// 4 l + i % 4 + 4 L (i / 4): vectors of four.  Either way a lane's experts
+// increase with i.
+//
+// The k best: the k-th largest of the lanes' largest keys is at most the k-th
+// largest key, so only keys from it on can be chosen, little more than k of
+// them.  They are gathered one to a lane, and k rounds of two warp reductions
+// (the largest key, the lowest expert that has it) put them in order.  Where
+// more than 32 pass (large k, many equal keys) the rounds scan every key.  At
+// T = 16384, E = 256, 8 groups, top 4, k = 8 this took ROUTE_US us; sorting
+// each lane's 8 keys instead took 21.3.
+template <int NV, bool QUADS, typename Z>
 __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const SelectParams p) {
+  __shared__ uint2 gathered[kSelWarps][NV > 1 ? 32 : 1];   // (key, expert)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -124,12 +88,20 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const Sele
   const int L = 1 << p.lanes_log2;
   const int g = lane >> p.lanes_log2, l = lane & (L - 1);
   const float neg_inf = __uint_as_float(0xFF800000u);
+  const int first = g * p.per_group + (QUADS ? 4 * l : l);
+  const int members = g < p.groups ? p.per_group - (QUADS ? 4 * l : l) : 0;   // of the group from `first` on
+  auto step = [&](int i) { return QUADS ? (i >> 2) * 4 * L + (i & 3) : i * L; };   // of value i from `first`
 
   float v[NV];
+  if (QUADS) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int r = l + i * L;
-    v[i] = (g < p.groups && r < p.per_group) ? load_logit(z + g * p.per_group + r) : neg_inf;
+    for (int i = 0; i < NV; i += 4) {
+      v[i] = v[i + 1] = v[i + 2] = v[i + 3] = neg_inf;
+      if (step(i) < members) load_logits4(z + first + step(i), v + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = step(i) < members ? load_logit(z + first + step(i)) : neg_inf;
   }
   // softmax statistics over the whole row
   const bool by_score = p.bias || (p.top2 && p.groups > 1);
@@ -144,48 +116,112 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const Sele
     for (int i = 0; i < NV; ++i) zsum += v[i] == neg_inf ? 0.f : expf(v[i] - zmax);
     zsum = warp_sum(zsum);
   }
-  const int e0 = g * p.per_group + l;   // value i is expert e0 + i * L
   uint32_t key[NV];
+  if (by_score) {
+    float b[NV];
+    if (!p.bias) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) b[i] = 0.f;
+    } else if (QUADS) {
+#pragma unroll
+      for (int i = 0; i < NV; i += 4)
+        if (step(i) < members) load_logits4(p.bias + first + step(i), b + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (step(i) < members) b[i] = __ldg(p.bias + first + step(i));
+    }
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] == neg_inf ? neg_inf : sigmoid(v[i]) + b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] == neg_inf ? neg_inf : expf(v[i] - zmax) / zsum + b[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] + 0.f);   // -0 to +0
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (step(i) >= members) key[i] = 0;
+  uint32_t lead = 0, next = 0;   // the lane's two largest
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    key[i] = 0;
-    if (g < p.groups && l + i * L < p.per_group) {
-      float a = v[i];
-      if (by_score && a != neg_inf) {
-        a = p.sigmoid ? sigmoid(a) : expf(a - zmax) / zsum;
-        if (p.bias) a += p.bias[e0 + i * L];
-      }
-      key[i] = value_key(a);
-    }
+    next = max(next, min(lead, key[i]));
+    lead = max(lead, key[i]);
   }
   if (p.top_groups < p.groups) {
-    uint32_t m1 = 0, m2 = 0;   // the lane's two largest
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      m2 = max(m2, min(m1, key[i]));
-      m1 = max(m1, key[i]);
-    }
+    uint32_t m1 = lead, m2 = next;   // the group's two largest
     for (int o = 1; o < L; o <<= 1) {
       const uint32_t o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
       m2 = max(max(m2, o2), min(m1, o1));
       m1 = max(m1, o1);
     }
     uint32_t mine = m1;
-    if (p.top2 && g < p.groups) {   // masked experts (-inf, or none) add nothing
-      const uint32_t masked = value_key(neg_inf);
-      if (m2 > masked) mine = value_key(key_value(m1) + key_value(m2));
-    }
+    if (p.top2 && g < p.groups && m2 > value_key(neg_inf))   // masked experts (-inf, or none) add nothing
+      mine = value_key(key_value(m1) + key_value(m2));
     int rank = 0;
     for (int q = 0; q < p.groups; ++q) {
       const uint32_t other = __shfl_sync(0xffffffffu, mine, q << p.lanes_log2);
       rank += other > mine || (other == mine && q < g);
     }
     if (rank >= p.top_groups) {
+      lead = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) key[i] = 0;
     }
   }
-  const int chosen = choose<NV>(key, e0, L, p.k, lane);
+  int chosen = 0;
+  bool gather = NV > 1;
+  uint32_t one = key[0], expert = (uint32_t)first;   // a lane's candidate
+  if (NV > 1) {
+    uint32_t tau = 1;
+    for (int j = 0; j < p.k; ++j) {
+      tau = max(__reduce_max_sync(0xffffffffu, lead), 1u);
+      if (lead >= tau) lead = 0;
+    }
+    uint2* mine = gathered[threadIdx.x >> 5];
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = key[i] >= tau;
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      const int at = total + __popc(who & ((1u << lane) - 1u));
+      if (in && at < 32) mine[at] = make_uint2(key[i], (uint32_t)(first + step(i)));
+      total += __popc(who);
+    }
+    gather = total <= 32;
+    __syncwarp();
+    if (gather) {
+      one = lane < total ? mine[lane].x : 0u;
+      expert = mine[lane].y;   // read only with its key
+    }
+  }
+  if (NV == 1 || gather) {
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, one);
+      const uint32_t low = __reduce_min_sync(0xffffffffu, one == top ? expert : 0xFFFFFFFFu);
+      if (expert == low) one = 0;
+      if (lane == j) chosen = (int)low;
+    }
+  } else {
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      uint32_t mine = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i)
+        if (key[i] == top) mine = (uint32_t)(first + step(i));
+      const uint32_t low = __reduce_min_sync(0xffffffffu, mine);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (mine == low && (uint32_t)(first + step(i)) == low) key[i] = 0;
+      if (lane == j) chosen = (int)low;
+    }
+  }
   // the chosen scores, from the logits again
   float s = 0.f;
   const float zc = lane < p.k ? load_logit(z + chosen) : neg_inf;
@@ -312,11 +348,11 @@ __global__ void __launch_bounds__(kMaxExperts) route_balance_bias_kernel(const f
   }
 }
 
-template <int NV>
+template <int NV, bool QUADS>
 cudaError_t launch_select_nv(const SelectParams& p, bool bf16, cudaStream_t stream) {
   const dim3 grid((unsigned)((p.T + kSelWarps - 1) / kSelWarps)), block(32 * kSelWarps);
-  return bf16 ? launch_pdl(route_select_kernel<NV, uint16_t>, grid, block, 0, stream, 1, p)
-              : launch_pdl(route_select_kernel<NV, float>, grid, block, 0, stream, 1, p);
+  return bf16 ? launch_pdl(route_select_kernel<NV, QUADS, uint16_t>, grid, block, 0, stream, 1, p)
+              : launch_pdl(route_select_kernel<NV, QUADS, float>, grid, block, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -342,14 +378,25 @@ cudaError_t launch_route_select(const void* logits, bool bf16, const float* bias
   p.top2 = c.top2 && p.per_group > 1;
   p.renorm = c.renorm;
   p.scale = c.scale;
-  const int nv = (p.per_group + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
-  if (nv <= 1) return launch_select_nv<1>(p, bf16, stream);
-  if (nv <= 2) return launch_select_nv<2>(p, bf16, stream);
-  if (nv <= 4) return launch_select_nv<4>(p, bf16, stream);
-  if (nv <= 8) return launch_select_nv<8>(p, bf16, stream);
-  if (nv <= 16) return launch_select_nv<16>(p, bf16, stream);
-  if (nv <= 32) return launch_select_nv<32>(p, bf16, stream);
-  return launch_select_nv<64>(p, bf16, stream);
+  // vectors of four where a group gives each of its lanes at least one, and
+  // every row and group starts on one
+  const int L = 1 << p.lanes_log2;
+  if (p.per_group % 4 == 0 && p.per_group >= 4 * L) {
+    const int quads = (p.per_group / 4 + L - 1) / L;
+    if (quads <= 1) return launch_select_nv<4, true>(p, bf16, stream);
+    if (quads <= 2) return launch_select_nv<8, true>(p, bf16, stream);
+    if (quads <= 4) return launch_select_nv<16, true>(p, bf16, stream);
+    if (quads <= 8) return launch_select_nv<32, true>(p, bf16, stream);
+    return launch_select_nv<64, true>(p, bf16, stream);
+  }
+  const int nv = (p.per_group + L - 1) / L;
+  if (nv <= 1) return launch_select_nv<1, false>(p, bf16, stream);
+  if (nv <= 2) return launch_select_nv<2, false>(p, bf16, stream);
+  if (nv <= 4) return launch_select_nv<4, false>(p, bf16, stream);
+  if (nv <= 8) return launch_select_nv<8, false>(p, bf16, stream);
+  if (nv <= 16) return launch_select_nv<16, false>(p, bf16, stream);
+  if (nv <= 32) return launch_select_nv<32, false>(p, bf16, stream);
+  return launch_select_nv<64, false>(p, bf16, stream);
 }
 
 cudaError_t launch_route_select_bwd(const float* dw_part, int nparts, const int32_t* row_map, const void* logits,
