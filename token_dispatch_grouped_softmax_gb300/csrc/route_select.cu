@@ -64,6 +64,61 @@ __device__ __forceinline__ void load_logits4(const uint16_t* p, float* v) {
   v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
 }
 
+// Drops the keys of the groups that are out, finds the candidates and gathers
+// up to 32 of them, (key, expert) in `out`; returns their number.
+template <int NV, typename ExpertOf>
+__device__ __forceinline__ int find_candidates(const SelectParams& p, uint32_t (&key)[NV], int g, int l, int lane,
+                                               ExpertOf expert_of, uint2* out) {
+  const int L = 1 << p.lanes_log2;
+  const uint32_t masked = value_key(__uint_as_float(0xFF800000u));
+  uint32_t lead = 0, next = 0;   // the lane's two largest
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    next = max(next, min(lead, key[i]));
+    lead = max(lead, key[i]);
+  }
+  if (p.top_groups < p.groups) {
+    uint32_t m1 = lead, m2 = next;   // the group's two largest
+    for (int o = 1; o < L; o <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      m2 = max(max(m2, o2), min(m1, o1));
+      m1 = max(m1, o1);
+    }
+    uint32_t mine = m1;
+    if (p.top2 && g < p.groups && m2 > masked)   // masked experts (-inf, or none) add nothing
+      mine = value_key(key_value(m1) + key_value(m2));
+    int rank = 0;   // groups before this one: the group's lanes share the comparisons out
+    for (int q0 = 0; q0 < p.groups; q0 += L) {
+      const int q = min(q0 + l, p.groups - 1);
+      const uint32_t other = __shfl_sync(0xffffffffu, mine, q << p.lanes_log2);
+      rank += q == q0 + l && (other > mine || (other == mine && q < g));
+    }
+    for (int o = 1; o < L; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (rank >= p.top_groups) {
+      lead = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = 0;
+    }
+  }
+  if (NV == 1) return 0;   // one candidate a lane as it is
+  uint32_t tau = 1;
+  for (int j = 0; j < p.k; ++j) {
+    tau = max(__reduce_max_sync(0xffffffffu, lead), 1u);
+    if (lead >= tau) lead = 0;
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool in = key[i] >= tau;
+    const uint32_t who = __ballot_sync(0xffffffffu, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) out[at] = make_uint2(key[i], expert_of(i));
+    n += __popc(who);
+  }
+  __syncwarp();
+  return n;
+}
+
 // NV values per lane, of the lane's group; value i is member l + i L of the
 // group (l the lane's place among the group's L lanes), or with QUADS member
 // 4 l + i % 4 + 4 L (i / 4): vectors of four.  Either way a lane's experts
@@ -73,10 +128,14 @@ __device__ __forceinline__ void load_logits4(const uint16_t* p, float* v) {
 // largest key, so only keys from it on can be chosen, little more than k of
 // them.  They are gathered one to a lane, and k rounds of two warp reductions
 // (the largest key, the lowest expert that has it) put them in order.  Where
-// more than 32 pass (large k, many equal keys) the rounds scan every key.  At
-// T = 16384, E = 256, 8 groups, top 4, k = 8 this took ROUTE_US us; sorting
-// each lane's 8 keys instead took 21.3.
-template <int NV, bool QUADS, typename Z>
+// more than 32 pass (large k, many equal keys) the rounds scan every key.
+// The instructions of a token bound it (845 at E = 256 with 8 groups, a third
+// of them the exact sigmoids): 15.7 us for 16384 tokens, where sorting each
+// lane's 8 keys took 21.3, and 3.6 us for 4096 tokens of E = 128 by softmax.
+// Finding the candidates by approximate sigmoids took 23.1 us.
+enum { kByLogit, kBySigmoid, kBySoftmax };   // what chooses
+
+template <int NV, bool QUADS, int MODE, typename Z>
 __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const SelectParams p) {
   __shared__ uint2 gathered[kSelWarps][NV > 1 ? 32 : 1];   // (key, expert)
   pdl_wait();
@@ -104,9 +163,8 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const Sele
     for (int i = 0; i < NV; ++i) v[i] = step(i) < members ? load_logit(z + first + step(i)) : neg_inf;
   }
   // softmax statistics over the whole row
-  const bool by_score = p.bias || (p.top2 && p.groups > 1);
   float zmax = 0.f, zsum = 1.f;
-  if (!p.sigmoid && (by_score || !p.renorm)) {
+  if (MODE == kBySoftmax || (!p.sigmoid && !p.renorm)) {
     zmax = neg_inf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) zmax = fmaxf(zmax, v[i]);
@@ -116,89 +174,40 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const Sele
     for (int i = 0; i < NV; ++i) zsum += v[i] == neg_inf ? 0.f : expf(v[i] - zmax);
     zsum = warp_sum(zsum);
   }
+  float b[NV];   // what is added to the score
+#pragma unroll
+  for (int i = 0; i < NV; ++i) b[i] = 0.f;
+  if (MODE != kByLogit && p.bias) {
+#pragma unroll
+    for (int i = 0; i < NV; i += QUADS ? 4 : 1)
+      if (step(i) < members) {
+        if (QUADS) load_logits4(p.bias + first + step(i), b + i);
+        else b[i] = __ldg(p.bias + first + step(i));
+      }
+  }
+  // the key of the value that chooses
+  auto choice_key = [&](float zi, float bi) {
+    if (MODE == kByLogit) return value_key(zi + 0.f);   // -0 to +0
+    const float s = MODE == kBySigmoid ? sigmoid(zi) : expf(zi - zmax) / zsum;
+    return zi == neg_inf ? value_key(neg_inf) : value_key(s + bi);
+  };
   uint32_t key[NV];
-  if (by_score) {
-    float b[NV];
-    if (!p.bias) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) b[i] = 0.f;
-    } else if (QUADS) {
-#pragma unroll
-      for (int i = 0; i < NV; i += 4)
-        if (step(i) < members) load_logits4(p.bias + first + step(i), b + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (step(i) < members) b[i] = __ldg(p.bias + first + step(i));
-    }
-    if (p.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] == neg_inf ? neg_inf : sigmoid(v[i]) + b[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] == neg_inf ? neg_inf : expf(v[i] - zmax) / zsum + b[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = value_key(v[i] + 0.f);   // -0 to +0
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (step(i) >= members) key[i] = 0;
-  uint32_t lead = 0, next = 0;   // the lane's two largest
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    next = max(next, min(lead, key[i]));
-    lead = max(lead, key[i]);
-  }
-  if (p.top_groups < p.groups) {
-    uint32_t m1 = lead, m2 = next;   // the group's two largest
-    for (int o = 1; o < L; o <<= 1) {
-      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
-      m2 = max(max(m2, o2), min(m1, o1));
-      m1 = max(m1, o1);
-    }
-    uint32_t mine = m1;
-    if (p.top2 && g < p.groups && m2 > value_key(neg_inf))   // masked experts (-inf, or none) add nothing
-      mine = value_key(key_value(m1) + key_value(m2));
-    int rank = 0;
-    for (int q = 0; q < p.groups; ++q) {
-      const uint32_t other = __shfl_sync(0xffffffffu, mine, q << p.lanes_log2);
-      rank += other > mine || (other == mine && q < g);
-    }
-    if (rank >= p.top_groups) {
-      lead = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = 0;
-    }
-  }
-  int chosen = 0;
-  bool gather = NV > 1;
+  for (int i = 0; i < NV; ++i) key[i] = step(i) < members ? choice_key(v[i], b[i]) : 0u;
+  uint2* mine = gathered[threadIdx.x >> 5];
+  const int total = find_candidates<NV>(p, key, g, l, lane, [&](int i) { return (uint32_t)(first + step(i)); }, mine);
+  const bool gather = NV > 1 && total <= 32;
   uint32_t one = key[0], expert = (uint32_t)first;   // a lane's candidate
-  if (NV > 1) {
-    uint32_t tau = 1;
-    for (int j = 0; j < p.k; ++j) {
-      tau = max(__reduce_max_sync(0xffffffffu, lead), 1u);
-      if (lead >= tau) lead = 0;
-    }
-    uint2* mine = gathered[threadIdx.x >> 5];
-    int total = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = key[i] >= tau;
-      const uint32_t who = __ballot_sync(0xffffffffu, in);
-      const int at = total + __popc(who & ((1u << lane) - 1u));
-      if (in && at < 32) mine[at] = make_uint2(key[i], (uint32_t)(first + step(i)));
-      total += __popc(who);
-    }
-    gather = total <= 32;
-    __syncwarp();
-    if (gather) {
-      one = lane < total ? mine[lane].x : 0u;
-      expert = mine[lane].y;   // read only with its key
+  if (gather) {
+    one = 0;
+    if (lane < total) {
+      one = mine[lane].x;
+      expert = mine[lane].y;
     }
   }
-  if (NV == 1 || gather) {
+  // k rounds: the warp's largest key, equal keys to the lowest expert
+  int chosen = 0;
+  if (gather || NV == 1) {
     for (int j = 0; j < p.k; ++j) {
       const uint32_t top = __reduce_max_sync(0xffffffffu, one);
       const uint32_t low = __reduce_min_sync(0xffffffffu, one == top ? expert : 0xFFFFFFFFu);
@@ -254,10 +263,40 @@ struct SelectBwdParams {
   float scale;
 };
 
+// A lane's NV consecutive-by-vector elements of a row: element i of lane l is
+// V (l + 32 (i / V)) + i % V, in vectors of V elements of 16 bytes; or, with
+// V 1, l + 32 i.
+template <int V>
+__device__ __forceinline__ int row_element(int lane, int i) {
+  return V * (lane + 32 * (i / V)) + i % V;
+}
+template <int V>
+__device__ __forceinline__ void load_vec(const float* p, float* v) {
+  if (V == 4) load_logits4(p, v);
+  else v[0] = *p;
+}
+template <int V>
+__device__ __forceinline__ void load_vec(const uint16_t* p, float* v) {
+  if (V == 8) unpack8(__ldg(reinterpret_cast<const uint4*>(p)), v);
+  else v[0] = load_logit(p);
+}
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+  if (V == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else *p = v[0];
+}
+template <int V>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float* v) {
+  if (V == 8) *reinterpret_cast<uint4*>(p) = pack8(v);
+  else store_grad(p, v[0]);
+}
+
 // One warp per token: lane j < k holds slot j.  The row is filled (zeros, or
-// the dense part of the softmax without renormalisation), then the chosen
-// elements are written over it.
-template <typename Z>
+// the dense part of the softmax without renormalisation, whose row stays in
+// registers between its maximum, its sum and its gradient), then the chosen
+// elements are written over it: bound by the write of d_logits.
+// NV >= E / 32 elements a lane for the dense form; NV 0: the other forms.
+template <int NV, int V, typename Z>
 __global__ void __launch_bounds__(32 * kSelWarps) route_select_bwd_kernel(const SelectBwdParams p) {
   pdl_wait();
   pdl_trigger();
@@ -267,6 +306,21 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_bwd_kernel(const 
   const Z* z = static_cast<const Z*>(p.logits) + (int64_t)t * p.E;
   Z* dz = static_cast<Z*>(p.d_logits) + (int64_t)t * p.E;
   const float neg_inf = __uint_as_float(0xFF800000u);
+  constexpr int N = NV > 0 ? NV : 1;
+  float v[N];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[i + c] = neg_inf;
+      if (row_element<V>(lane, i) < p.E) load_vec<V>(z + row_element<V>(lane, i), v + i);
+    }
+  } else {
+    float zero[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) zero[c] = 0.f;
+    for (int c = V * lane; c < p.E; c += 32 * V) store_vec<V>(dz + c, zero);
+  }
   float dwj = 0.f, zc = neg_inf;
   int e = -1;
   if (lane < p.k) {
@@ -288,10 +342,9 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_bwd_kernel(const 
     if (p.dw) p.dw[i] = dwj;
     if (e >= 0) zc = load_logit(z + e);
   }
-  float d = 0.f;        // the chosen element's gradient
-  if (p.renorm || p.sigmoid) {
-    for (int c = lane; c < p.E; c += 32) store_grad(dz + c, 0.f);
-    float u;            // the slot's score, renormalised when asked
+  float d;        // the chosen element's gradient
+  if constexpr (NV == 0) {
+    float u;      // the slot's score, renormalised when asked
     if (p.sigmoid) {
       u = lane < p.k ? sigmoid(zc) : 0.f;
     } else {
@@ -308,19 +361,24 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_bwd_kernel(const 
     if (p.sigmoid) d *= sigmoid(-zc);   // 1 - s without cancellation
   } else {
     float zmax = neg_inf;
-    for (int c = lane; c < p.E; c += 32) zmax = fmaxf(zmax, load_logit(z + c));
+#pragma unroll
+    for (int i = 0; i < N; ++i) zmax = fmaxf(zmax, v[i]);
     zmax = warp_max(zmax);
     float zsum = 0.f;
-    for (int c = lane; c < p.E; c += 32) {
-      const float v = load_logit(z + c);
-      zsum += v == neg_inf ? 0.f : expf(v - zmax);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = v[i] == neg_inf ? 0.f : expf(v[i] - zmax);
+      zsum += v[i];
     }
     zsum = warp_sum(zsum);
     const float pj = zc == neg_inf ? 0.f : expf(zc - zmax) / zsum;
     const float mean = warp_sum(pj * dwj);
-    for (int c = lane; c < p.E; c += 32) {
-      const float v = load_logit(z + c);
-      store_grad(dz + c, v == neg_inf ? 0.f : p.scale * (expf(v - zmax) / zsum) * -mean);
+    const float f = zsum == 0.f ? 0.f : p.scale * -mean / zsum;   // a row of masked experts: 0
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[i + c] *= f;
+      if (row_element<V>(lane, i) < p.E) store_vec<V>(dz + row_element<V>(lane, i), v + i);
     }
     d = p.scale * pj * (dwj - mean);
   }
@@ -335,24 +393,50 @@ __global__ void __launch_bounds__(kMaxExperts) route_balance_bias_kernel(const f
                                                                          float rate, float* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ unsigned long long total;
+  __shared__ long long part[32];
   const int e = threadIdx.x;
-  if (e == 0) total = 0;
-  __syncthreads();
   const long long n = e < E ? counts[e] : 0;
-  if (e < E) atomicAdd(&total, (unsigned long long)n);   // integers: the order does not matter
+  long long sum = n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((e & 31) == 0) part[e >> 5] = sum;
   __syncthreads();
   if (e < E) {
-    const long long d = (long long)total - (long long)E * n;
+    long long total = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) total += part[w];
+    const long long d = total - (long long)E * n;
     out[e] = bias[e] + (d > 0 ? rate : d < 0 ? -rate : 0.f);
   }
 }
 
+template <int NV, bool QUADS, int MODE>
+cudaError_t launch_select_mode(const SelectParams& p, bool bf16, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.T + kSelWarps - 1) / kSelWarps)), block(32 * kSelWarps);
+  return bf16 ? launch_pdl(route_select_kernel<NV, QUADS, MODE, uint16_t>, grid, block, 0, stream, 1, p)
+              : launch_pdl(route_select_kernel<NV, QUADS, MODE, float>, grid, block, 0, stream, 1, p);
+}
+
 template <int NV, bool QUADS>
 cudaError_t launch_select_nv(const SelectParams& p, bool bf16, cudaStream_t stream) {
+  if (!p.bias && !(p.top2 && p.groups > 1)) return launch_select_mode<NV, QUADS, kByLogit>(p, bf16, stream);
+  return p.sigmoid ? launch_select_mode<NV, QUADS, kBySigmoid>(p, bf16, stream)
+                   : launch_select_mode<NV, QUADS, kBySoftmax>(p, bf16, stream);
+}
+
+template <int V, typename Z>
+cudaError_t launch_bwd_v(const SelectBwdParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)((p.T + kSelWarps - 1) / kSelWarps)), block(32 * kSelWarps);
-  return bf16 ? launch_pdl(route_select_kernel<NV, QUADS, uint16_t>, grid, block, 0, stream, 1, p)
-              : launch_pdl(route_select_kernel<NV, QUADS, float>, grid, block, 0, stream, 1, p);
+  if (p.renorm || p.sigmoid) return launch_pdl(route_select_bwd_kernel<0, V, Z>, grid, block, 0, stream, 1, p);
+  const int nv = (p.E + 32 * V - 1) / (32 * V) * V;
+  if constexpr (V == 1) {
+    if (nv <= 1) return launch_pdl(route_select_bwd_kernel<1, V, Z>, grid, block, 0, stream, 1, p);
+    if (nv <= 2) return launch_pdl(route_select_bwd_kernel<2, V, Z>, grid, block, 0, stream, 1, p);
+  }
+  if constexpr (V <= 4)
+    if (nv <= 4) return launch_pdl(route_select_bwd_kernel<4, V, Z>, grid, block, 0, stream, 1, p);
+  if (nv <= 8) return launch_pdl(route_select_bwd_kernel<8, V, Z>, grid, block, 0, stream, 1, p);
+  if (nv <= 16) return launch_pdl(route_select_bwd_kernel<16, V, Z>, grid, block, 0, stream, 1, p);
+  return launch_pdl(route_select_bwd_kernel<32, V, Z>, grid, block, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -405,9 +489,9 @@ cudaError_t launch_route_select_bwd(const float* dw_part, int nparts, const int3
                                     cudaStream_t stream) {
   const SelectBwdParams p{dw_part, row_map, logits, ids, d_logits, dw, status, (int)T, (int)E, (int)k, nparts,
                           c.sigmoid, c.renorm, c.scale};
-  const dim3 grid((unsigned)((T + kSelWarps - 1) / kSelWarps)), block(32 * kSelWarps);
-  return bf16 ? launch_pdl(route_select_bwd_kernel<uint16_t>, grid, block, 0, stream, 1, p)
-              : launch_pdl(route_select_bwd_kernel<float>, grid, block, 0, stream, 1, p);
+  // rows in 16-byte vectors where every row starts on one
+  if (bf16) return E % 8 == 0 ? launch_bwd_v<8, uint16_t>(p, stream) : launch_bwd_v<1, uint16_t>(p, stream);
+  return E % 4 == 0 ? launch_bwd_v<4, float>(p, stream) : launch_bwd_v<1, float>(p, stream);
 }
 
 cudaError_t launch_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, float rate, float* out,
