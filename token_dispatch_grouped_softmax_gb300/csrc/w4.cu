@@ -74,42 +74,52 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
 }
 
 // The experts of the slots of this launch row, and each expert's slots in
-// increasing order: a stable counting sort in shared memory (every block
-// sorts for itself and must find the same chunks).  Warp w counts and places
-// its eighth of the slots; cnt is [8][E] scratch.  Returns the number of
-// chunks.
+// increasing order (every block sorts for itself and must find the same
+// chunks).  bits is [E] rows of w4_bit_row(slots) words of scratch: bit i of
+// row e says that slot i is expert e's, so a slot's place is a count of the
+// bits before it, whatever order they were set in; the row's last word is the
+// expert's first place.  Returns the numbers of chunks (low 32 bits) and of
+// experts in use.  For 360 slots of 128 experts it takes LIST_CYCLES cycles;
+// counting with __match_any_sync took 6900.
+__host__ __device__ constexpr int w4_bit_row(int slots) { return ((slots + 31) / 32 + 1) | 1; }   // odd: no bank conflicts
+
 template <int NT>
-__device__ __forceinline__ int w4_lists(const W4Params& p, int slot0, int slots, int* cnt, W4Active* act,
-                                        uint16_t* list, uint64_t* warp_sum64) {
+__device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int slots, uint32_t* bits, W4Active* act,
+                                             uint16_t* list, uint64_t* warp_sum64) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kW4Warps * p.E; i += kW4Threads) cnt[i] = 0;
-  __syncthreads();
-  const int s_begin = slots * warp / kW4Warps, s_end = slots * (warp + 1) / kW4Warps;
-  int* mine = cnt + warp * p.E;
-  auto expert_of = [&](int i) {   // -1: an empty slot, or none
-    if (i >= s_end) return -1;
-    const int e = p.ids ? p.ids[slot0 + i] : 0;
-    if (e >= 0 && e < p.E) return e;
-    if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
-    return -1;
-  };
-  for (int i0 = s_begin; i0 < s_end; i0 += 32) {
-    const int e = expert_of(i0 + lane);
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-    __syncwarp();
+  const int words = (slots + 31) / 32, stride = w4_bit_row(slots);
+  int e_of[kW4MaxSlots / kW4Threads];
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j) {
+    const int i = j * kW4Threads + tid;
+    e_of[j] = -1;
+    if (i < slots) {
+      const int e = p.ids ? p.ids[slot0 + i] : 0;
+      if (e >= 0 && e < p.E) e_of[j] = e;
+      else if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+    }
   }
+  for (int i = tid; i < p.E * stride; i += kW4Threads) bits[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
+    if (e_of[j] >= 0) atomicOr(&bits[e_of[j] * stride + j * (kW4Threads / 32) + warp], 1u << lane);
   __syncthreads();
   // thread i: experts [i * per, (i + 1) * per); prefix of (rows, experts, chunks)
   const int per = (p.E + kW4Threads - 1) / kW4Threads;
   auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + 8 * NT - 1) / (8 * NT)) << 40; };
-  uint64_t sum = 0;
-  for (int q = 0; q < per; ++q) {
-    const int e = tid * per + q;
-    if (e >= p.E) break;
+  auto rows_of = [&](int e) {
     int n = 0;
-    for (int w = 0; w < kW4Warps; ++w) n += cnt[w * p.E + e];
-    if (n) sum += packed(n);
+    for (int w = 0; w < words; ++w) n += __popc(bits[e * stride + w]);
+    return n;
+  };
+  int n_of[kMaxExperts / kW4Threads];
+  uint64_t sum = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kW4Threads; ++q) {
+    const int e = tid * per + q;
+    n_of[q] = q < per && e < p.E ? rows_of(e) : 0;
+    if (n_of[q]) sum += packed(n_of[q]);
   }
   uint64_t incl = sum;
 #pragma unroll
@@ -120,47 +130,39 @@ __device__ __forceinline__ int w4_lists(const W4Params& p, int slot0, int slots,
   if (lane == 31) warp_sum64[warp] = incl;
   __syncthreads();
   uint64_t before = incl - sum, total = 0;
+#pragma unroll
   for (int w = 0; w < kW4Warps; ++w) {
     const uint64_t s = warp_sum64[w];
     if (w < warp) before += s;
     total += s;
   }
-  for (int q = 0; q < per; ++q) {
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kW4Threads; ++q) {
     const int e = tid * per + q;
-    if (e >= p.E) break;
-    const int row0 = (int)(before & 0xFFFFF);
-    int n = 0;
-    for (int w = 0; w < kW4Warps; ++w) {   // counts to first places
-      const int c = cnt[w * p.E + e];
-      cnt[w * p.E + e] = row0 + n;
-      n += c;
-    }
-    if (n) {
-      act[(int)(before >> 20 & 0xFFFFF)] = W4Active{e, row0, n, (int)(before >> 40)};
-      before += packed(n);
+    if (n_of[q]) {
+      act[(int)(before >> 20 & 0xFFFFF)] = W4Active{e, (int)(before & 0xFFFFF), n_of[q], (int)(before >> 40)};
+      bits[e * stride + stride - 1] = (uint32_t)(before & 0xFFFFF);
+      before += packed(n_of[q]);
     }
   }
   __syncthreads();
-  for (int i0 = s_begin; i0 < s_end; i0 += 32) {
-    const int e = expert_of(i0 + lane);
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    int place = 0;
-    if (e >= 0) {
-      place = mine[e] + __popc(peers & ((1u << lane) - 1u));
-      list[place] = (uint16_t)(i0 + lane);
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
+    if (e_of[j] >= 0) {
+      const uint32_t* row = bits + e_of[j] * stride;
+      const int at = j * (kW4Threads / 32) + warp;   // the word of slot j * kW4Threads + tid
+      int place = (int)row[stride - 1] + __popc(row[at] & ((1u << lane) - 1u));
+      for (int w = 0; w < at; ++w) place += __popc(row[w]);
+      list[place] = (uint16_t)(j * kW4Threads + tid);
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] = place + __popc(peers);
-    __syncwarp();
-  }
-  __syncthreads();
-  return (int)(total >> 40);
+  return (total >> 40) | (total >> 20 & 0xFFFFF) << 32;
 }
 
 // The same for at most 32 slots, by one warp: experts in the order of their
 // first slot.
 template <int NT>
-__device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Active* act, uint16_t* list, int* chunks) {
+__device__ __forceinline__ uint64_t w4_lists_small(const W4Params& p, int slots, W4Active* act, uint16_t* list,
+                                                   uint64_t* result) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int e = -1;
@@ -171,7 +173,9 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
         e = -1;
       }
     }
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    uint32_t peers = 0;
+#pragma unroll 8
+    for (int j = 0; j < slots; ++j) peers |= (uint32_t)(__shfl_sync(0xffffffffu, e, j) == e) << j;
     const int n = __popc(peers), first = __ffs(peers) - 1;
     const bool leads = e >= 0 && lane == first;
     const int mine = leads ? n | (n + 8 * NT - 1) / (8 * NT) << 16 : 0;
@@ -184,13 +188,14 @@ __device__ __forceinline__ int w4_lists_small(const W4Params& p, int slots, W4Ac
     const int before = incl - mine;
     const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
     if (leads) act[__popc(leaders & ((1u << lane) - 1u))] = W4Active{e, before & 0xFFFF, n, before >> 16};
-    const int row0 = __shfl_sync(0xffffffffu, before & 0xFFFF, first);
+    const int row0 = __shfl_sync(0xffffffffu, before & 0xFFFF, first & 31);
     if (e >= 0) list[row0 + __popc(peers & ((1u << lane) - 1u))] = (uint16_t)lane;
-    if (lane == 31) *chunks = incl >> 16;
+    if (lane == 31) *result = (uint64_t)(incl >> 16) | (uint64_t)__popc(leaders) << 32;
   }
   __syncthreads();
-  return *chunks;
+  return *result;
 }
+
 
 // Zero rows of h for the empty slots, shared out over the blocks.
 __device__ __forceinline__ void w4_zero_rows(const W4Params& p, int slot0, int slots) {
@@ -238,8 +243,14 @@ struct W4Ring {
   static constexpr int kBytes = kW4Warps * kDepth * (kQ + kScale + kZero);
   static constexpr int kPart = 16 * NT * 32;   // floats of a warp's partial sums
 };
-static_assert(kW4Warps * kMaxExperts * 4 <= kW4Warps * W4Ring<1, 128, false>::kDepth * W4Ring<1, 128, false>::kQ,
-              "the sort's counts fit the rings");
+// Slots of one launch row: what the lists hold, and what the sort's bits may
+// take of the rings.
+__host__ __device__ constexpr int w4_row_slots(int E, int k) {
+  int slots = kW4MaxSlots;
+  while (E * w4_bit_row(slots) * 4 > W4Ring<1, 128, false>::kBytes) slots -= 32;
+  return slots / k * k;
+}
+static_assert(w4_row_slots(kMaxExperts, 32) >= 32, "a token's slots fit one launch row");
 
 template <int NT, int GROUP, bool ZEROS>
 __host__ __device__ constexpr int w4_smem(int E, int slots) {
@@ -264,8 +275,9 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   uint64_t* scratch = reinterpret_cast<uint64_t*>(act + n_act);
   uint64_t* bars = scratch + kW4Warps;
   int* abort_flag = reinterpret_cast<int*>(bars + kW4Warps * Ring::kDepth);
+  int* first_act = abort_flag + 1;
   uint16_t* list = reinterpret_cast<uint16_t*>(abort_flag + 2);
-  int* cnt = reinterpret_cast<int*>(smem);   // [8][E] over the rings, before they are used
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem);   // over the rings, before they are used
   const uint32_t bar0 = smem_u32(bars + warp * Ring::kDepth);
   if (lane == 0) {
     for (int d = 0; d < Ring::kDepth; ++d) mbar_init(bar0 + 8 * d, 1);
@@ -278,15 +290,22 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
-  const int chunks = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, reinterpret_cast<int*>(scratch))
-                                   : w4_lists<NT>(p, slot0, slots, cnt, act, list, scratch);
+  const uint64_t found = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, scratch)
+                                       : w4_lists<NT>(p, slot0, slots, bits, act, list, scratch);
+  const uint32_t chunks = (uint32_t)found;
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
-  const int64_t items = (int64_t)chunks * p.blocks;
-  const int begin = (int)(items * blockIdx.x / gridDim.x), end = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  // this block's items: an even share, the first blocks one more
+  const uint32_t items = chunks * (uint32_t)p.blocks, share = items / gridDim.x, more = items - share * gridDim.x;
+  const int begin = (int)(blockIdx.x * share + min(blockIdx.x, more));
+  const int end = begin + (int)share + (blockIdx.x < more ? 1 : 0);
+  if (begin >= end) return;
+  // the expert of its first chunk
+  const int first_chunk = begin / p.blocks;
+  for (int i = tid; i < (int)(found >> 32); i += kW4Threads)
+    if (first_chunk >= act[i].chunk0 && first_chunk < act[i].chunk0 + (act[i].rows + 8 * NT - 1) / (8 * NT)) *first_act = i;
   fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
   __syncthreads();
-  if (begin >= end) return;
   const int units = (p.K + 127) / 128;
   auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
 
@@ -306,7 +325,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   };
 
   // the loader: run, the next unit's coordinates, and the stage
-  int lrun = -1, lu = 0, lu_end = 0, lstage = 0, la = 0;
+  int lrun = -1, lu = 0, lu_end = 0, lstage = 0, la = *first_act;
   int lcol = 0, lqrow = 0, lsrow = 0;
   auto next_run = [&]() {   // the next run that has an item
     while (++lrun < runs) {
@@ -348,7 +367,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   const uint16_t* x[NT];
   uint4 xn[NT][2];   // this lane's vectors of the next 64 k
   int x_chunk = -1;  // the chunk that x is of
-  int ca = 0, stage = 0;
+  int ca = *first_act, stage = 0;
   uint32_t phase = 0;
   bool ok = true;
   W4Active a = act[0];
@@ -658,7 +677,7 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
     return cudaErrorInvalidValue;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
-  p.slots_per_row = kW4MaxSlots / p.k * p.k;
+  p.slots_per_row = w4_row_slots(p.E, p.k);
   p.blocks = (int)(half / 32);
   const int units = (p.K + 127) / 128;
   p.parts_log2 = units >= 32 ? 3 : units >= 8 ? 2 : units >= 2 ? 1 : 0;   // about four units a part
