@@ -88,7 +88,11 @@ SHAPES = [  # T, H, E, k, I, group, zeros, empty
     (3, 2048, 16, 4, 768, 128, False, 0.0), (5, 320, 3, 3, 192, 64, False, 0.3), (8, 128, 4, 1, 64, 32, False, 0.0),
     (9, 512, 4, 4, 128, 128, True, 0.2), (17, 384, 60, 6, 256, 64, True, 0.1), (33, 128, 2, 2, 448, 64, False, 0.0),
     (64, 256, 32, 8, 128, 128, False, 0.05), (70, 640, 8, 5, 64, 64, True, 0.0), (130, 64, 3, 2, 128, 32, False, 0.5),
-    (300, 128, 128, 8, 64, 64, False, 0.0)]
+    (300, 128, 128, 8, 64, 64, False, 0.0),
+    # more than eight items for each of the GPU's blocks: whole items a warp, then shared ones; K of an odd number of
+    # 64 rows, of parts of unequal length, of one part
+    (64, 192, 60, 6, 1408, 64, True, 0.1), (64, 640, 60, 6, 1408, 32, False, 0.0), (40, 1152, 64, 8, 1024, 128, True, 0.0),
+    (64, 2816, 60, 6, 192, 64, True, 0.1), (64, 2880, 60, 6, 640, 32, True, 0.0), (48, 4096, 64, 8, 128, 128, False, 0.0)]
 
 
 @pytest.mark.parametrize("T,H,E,k,I,group,zeros,empty", SHAPES)
@@ -178,10 +182,11 @@ def test_dense_expert():
     assert torch.equal(y, check_down(moe, h.cpu(), zero, np.ones((T, 1), np.float32), *qd, group))
 
 
-def test_a_token_does_not_depend_on_the_batch():
-    """Each token alone gives the bits it has in the batch."""
+@pytest.mark.parametrize("T,H,E,k,I,group", [(40, 512, 6, 3, 256, 128), (64, 2048, 64, 6, 1472, 64)])
+def test_a_token_does_not_depend_on_the_batch(T, H, E, k, I, group):
+    """Each token alone gives the bits it has in the batch: from items shared
+    by a block's warps (a small batch) and from whole items of a warp."""
     moe = lib()
-    T, H, E, k, I, group = 40, 512, 6, 3, 256, 128
     ids = i32(ids_of(3, T, E, k))
     qg, qd = dev_of(*weights(1, E, H, 2 * I, group, False)), dev_of(*weights(2, E, I, H, group, False))
     x = rows_of(1, T, H).to(dev())

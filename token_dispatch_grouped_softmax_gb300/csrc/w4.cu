@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
+constexpr int kW4Rows = 8;          // rows of a chunk: the columns of an mma
 constexpr int kW4MaxSlots = 2048;   // slots of one launch row (shared-memory lists)
 
 struct W4Params {
@@ -35,7 +36,7 @@ struct W4Params {
 };
 
 // An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
-// of 8 NT rows numbered from chunk0.
+// of kW4Rows numbered from chunk0.
 struct W4Active {
   int expert, row0, rows, chunk0;
 };
@@ -83,7 +84,6 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
 // counting with __match_any_sync took 6900.
 __host__ __device__ constexpr int w4_bit_row(int slots) { return ((slots + 31) / 32 + 1) | 1; }   // odd: no bank conflicts
 
-template <int NT>
 __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int slots, uint32_t* bits, W4Active* act,
                                              uint16_t* list, uint64_t* warp_sum64) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -107,7 +107,7 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
   __syncthreads();
   // thread i: experts [i * per, (i + 1) * per); prefix of (rows, experts, chunks)
   const int per = (p.E + kW4Threads - 1) / kW4Threads;
-  auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + 8 * NT - 1) / (8 * NT)) << 40; };
+  auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + kW4Rows - 1) / kW4Rows) << 40; };
   auto rows_of = [&](int e) {
     int n = 0;
     for (int w = 0; w < words; ++w) n += __popc(bits[e * stride + w]);
@@ -160,7 +160,6 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
 
 // The same for at most 32 slots, by one warp: experts in the order of their
 // first slot.
-template <int NT>
 __device__ __forceinline__ uint64_t w4_lists_small(const W4Params& p, int slots, W4Active* act, uint16_t* list,
                                                    uint64_t* result) {
   if (threadIdx.x < 32) {
@@ -178,7 +177,7 @@ __device__ __forceinline__ uint64_t w4_lists_small(const W4Params& p, int slots,
     for (int j = 0; j < slots; ++j) peers |= (uint32_t)(__shfl_sync(0xffffffffu, e, j) == e) << j;
     const int n = __popc(peers), first = __ffs(peers) - 1;
     const bool leads = e >= 0 && lane == first;
-    const int mine = leads ? n | (n + 8 * NT - 1) / (8 * NT) << 16 : 0;
+    const int mine = leads ? n | (n + kW4Rows - 1) / kW4Rows << 16 : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,33 +234,33 @@ __device__ __forceinline__ float w4_swiglu(float g, float u) { return g / (1.f +
 // taken off before the scale: sum (q - zero) x = sum (128 + q) x - (128 +
 // zero) sum x.  Every product is exact; the fp32 sums round at 128 + q
 // instead of q - zero, some 2^-19 of the terms, 2^10 below the bf16 result.
-template <int NT, int GROUP, bool ZEROS>
+template <int GROUP, bool ZEROS>
 struct W4Ring {
   static constexpr int kRows = 128 / GROUP;   // group rows of a unit
   static constexpr int kQ = 4096, kScale = 128 * kRows, kZero = ZEROS ? (64 * kRows + 127) / 128 * 128 : 0;
   static constexpr int kDepth = 2;
   static constexpr int kBytes = kW4Warps * kDepth * (kQ + kScale + kZero);
-  static constexpr int kPart = 16 * NT * 32;   // floats of a warp's partial sums
+  static constexpr int kPart = 16 * 32;   // floats of a warp's partial sums
 };
 // Slots of one launch row: what the lists hold, and what the sort's bits may
 // take of the rings.
 __host__ __device__ constexpr int w4_row_slots(int E, int k) {
   int slots = kW4MaxSlots;
-  while (E * w4_bit_row(slots) * 4 > W4Ring<1, 128, false>::kBytes) slots -= 32;
+  while (E * w4_bit_row(slots) * 4 > W4Ring<128, false>::kBytes) slots -= 32;
   return slots / k * k;
 }
 static_assert(w4_row_slots(kMaxExperts, 32) >= 32, "a token's slots fit one launch row");
 
-template <int NT, int GROUP, bool ZEROS>
+template <int GROUP, bool ZEROS>
 __host__ __device__ constexpr int w4_smem(int E, int slots) {
-  using Ring = W4Ring<NT, GROUP, ZEROS>;
+  using Ring = W4Ring<GROUP, ZEROS>;
   return 1024 + Ring::kBytes + kW4Warps * (Ring::kPart * 4 + Ring::kDepth * 8) +
          (E < slots ? E : slots) * (int)sizeof(W4Active) + (slots * 2 + 15) / 16 * 16 + 128;
 }
 
-template <int NT, bool GATE_UP, int GROUP, bool ZEROS>
+template <bool GATE_UP, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant__ W4Params p) {
-  using Ring = W4Ring<NT, GROUP, ZEROS>;
+  using Ring = W4Ring<GROUP, ZEROS>;
   extern __shared__ uint8_t w4_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   uint8_t* ring = smem + warp * (Ring::kDepth * Ring::kQ);
   uint8_t* scales = smem + kW4Warps * Ring::kDepth * Ring::kQ + warp * (Ring::kDepth * Ring::kScale);
   uint8_t* zeros = smem + kW4Warps * Ring::kDepth * (Ring::kQ + Ring::kScale) + warp * (Ring::kDepth * Ring::kZero);
-  float* sums_of_parts = reinterpret_cast<float*>(smem + Ring::kBytes);   // [8 warps][16 NT values][32 lanes]
+  float* sums_of_parts = reinterpret_cast<float*>(smem + Ring::kBytes);   // [8 warps][16 values][32 lanes]
   W4Active* act = reinterpret_cast<W4Active*>(sums_of_parts + kW4Warps * Ring::kPart);
   uint64_t* scratch = reinterpret_cast<uint64_t*>(act + n_act);
   uint64_t* bars = scratch + kW4Warps;
@@ -290,8 +289,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
-  const uint64_t found = p.slots <= 32 ? w4_lists_small<NT>(p, slots, act, list, scratch)
-                                       : w4_lists<NT>(p, slot0, slots, bits, act, list, scratch);
+  const uint64_t found = p.slots <= 32 ? w4_lists_small(p, slots, act, list, scratch)
+                                       : w4_lists(p, slot0, slots, bits, act, list, scratch);
   const uint32_t chunks = (uint32_t)found;
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
@@ -303,11 +302,11 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   // the expert of its first chunk
   const int first_chunk = begin / p.blocks;
   for (int i = tid; i < (int)(found >> 32); i += kW4Threads)
-    if (first_chunk >= act[i].chunk0 && first_chunk < act[i].chunk0 + (act[i].rows + 8 * NT - 1) / (8 * NT)) *first_act = i;
+    if (first_chunk >= act[i].chunk0 && first_chunk < act[i].chunk0 + (act[i].rows + kW4Rows - 1) / kW4Rows) *first_act = i;
   fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
   __syncthreads();
   const int units = (p.K + 127) / 128;
-  auto chunks_of = [](const W4Active& a) { return (a.rows + 8 * NT - 1) / (8 * NT); };
+  auto chunks_of = [](const W4Active& a) { return (a.rows + kW4Rows - 1) / kW4Rows; };
 
   // The warp's runs: run s < whole is an item of its own over the whole of K,
   // then one part of a shared item in each pass.
@@ -364,8 +363,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   issue();
   const uint32_t q_at = smem_u32(ring) + t * 256 + ((g ^ 2 * t) << 4);   // line 2t; the second half's line is the next, its chunk ^ 1
 
-  const uint16_t* x[NT];
-  uint4 xn[NT][2];   // this lane's vectors of the next 64 k
+  const uint16_t* x;  // this lane's row of the chunk, if it has one
+  uint4 xn[2];       // its vectors of the next 64 k
   int x_chunk = -1;  // the chunk that x is of
   int ca = *first_act, stage = 0;
   uint32_t phase = 0;
@@ -378,28 +377,24 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
     const bool shared = run >= whole;
     const int u0 = shared ? part_u0 : 0, u1 = shared ? part_u1 : units;
     int block = 0, row_first = 0;
-    float tot[2][2][NT][4];
+    float tot[2][2][4];
 #pragma unroll
-    for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] = 0.f;
+    for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] = 0.f;
     if (item < end) {
       const int chunk = item / p.blocks;
       block = item - chunk * p.blocks;
       while (chunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
       a = act[ca];
-      row_first = (chunk - a.chunk0) * 8 * NT;
+      row_first = (chunk - a.chunk0) * kW4Rows;
       if (chunk != x_chunk || shared) {
         x_chunk = chunk;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int r = row_first + n * 8 + g;
-          x[n] = nullptr;
-          xn[n][0] = xn[n][1] = make_uint4(0, 0, 0, 0);
-          if (r < a.rows) {
-            const int slot = slot0 + list[a.row0 + r];
-            x[n] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + 8 * t;
-            xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n] + u0 * 128));
-            xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + u0 * 128 + 32));
-          }
+        x = nullptr;
+        xn[0] = xn[1] = make_uint4(0, 0, 0, 0);
+        if (row_first + g < a.rows) {
+          const int slot = slot0 + list[a.row0 + row_first + g];
+          x = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + 8 * t;
+          xn[0] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128));
+          xn[1] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128 + 32));
         }
       }
     }
@@ -411,12 +406,12 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
         if (u == part_end) {   // the parts' sums in order, through this lane's shared memory
           if (parts_done > 0) {
 #pragma unroll
-            for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] += mine[i * 32];
+            for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] += mine[i * 32];
           }
 #pragma unroll
-          for (int i = 0; i < 16 * NT; ++i) {
-            mine[i * 32] = (&tot[0][0][0][0])[i];
-            (&tot[0][0][0][0])[i] = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            mine[i * 32] = (&tot[0][0][0])[i];
+            (&tot[0][0][0])[i] = 0.f;
           }
           ++parts_done;
           part_end = units * (parts_done + 1) >> p.parts_log2;
@@ -425,39 +420,33 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
           ok = false;
           break;
         }
-        float acc[2][2][NT][4], sum[NT][4];
+        float acc[2][2][4], sum[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
           if (j == 1 && u * 128 + 64 >= p.K) break;
-          uint32_t b[2][NT][4];
+          uint32_t b[2][4];
           if (next_k >= p.K) next_k = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 v = xn[n][i];
-              b[i][n][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
-              b[i][n][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
-              b[i][n][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
-              b[i][n][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
-            }
-            if (x[n]) {
-              xn[n][0] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k));
-              xn[n][1] = __ldg(reinterpret_cast<const uint4*>(x[n] + next_k + 32));
-            }
+          for (int i = 0; i < 2; ++i) {
+            const uint4 v = xn[i];
+            b[i][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+            b[i][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+            b[i][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+            b[i][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+          }
+          if (x) {
+            xn[0] = __ldg(reinterpret_cast<const uint4*>(x + next_k));
+            xn[1] = __ldg(reinterpret_cast<const uint4*>(x + next_k + 32));
           }
           next_k += 64;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {   // 32 k each
             const bool first = GROUP == 32 || (GROUP == 64 && i == 0) || (GROUP == 128 && i == 0 && j == 0);
             const bool last = GROUP == 32 || (GROUP == 64 && i == 1) || (GROUP == 128 && i == 1 && j == 1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-              if (first) mma_16816_first(sum[n], ones, b[i][n][0], b[i][n][1]);
-              else mma_16816(sum[n], ones, b[i][n][0], b[i][n][1]);
-              mma_16816(sum[n], ones, b[i][n][2], b[i][n][3]);
-            }
+            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+            if (first) mma_16816_first(sum, ones, b[i][0], b[i][1]);
+            else mma_16816(sum, ones, b[i][0], b[i][1]);
+            mma_16816(sum, ones, b[i][2], b[i][3]);
 #pragma unroll
             for (int set = 0; set < 2; ++set) {
               const uint32_t at = (set ? (q_at ^ 16) + 128 : q_at) + stage * Ring::kQ + (2 * j + i) * 1024;
@@ -471,11 +460,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
                 for (int st = 0; st < 2; ++st) {
                   const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
                                          w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
-#pragma unroll
-                  for (int n = 0; n < NT; ++n) {
-                    if (st == 0 && first) mma_16816_first(acc[set][hf][n], w, b[i][n][0], b[i][n][1]);
-                    else mma_16816(acc[set][hf][n], w, b[i][n][2 * st], b[i][n][2 * st + 1]);
-                  }
+                  if (st == 0 && first) mma_16816_first(acc[set][hf], w, b[i][0], b[i][1]);
+                  else mma_16816(acc[set][hf], w, b[i][2 * st], b[i][2 * st + 1]);
                 }
             }
             if (last) {
@@ -489,14 +475,12 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
                 for (int c = 0; c < 4; ++c) {   // the lane's four columns
                   const uint32_t sp = c < 2 ? sr.x : sr.y;
                   const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
-                  const float zero = ZEROS ? __uint_as_float(0x43000000u | ((zr >> (8 * c)) & 15u) << 16) : 136.f;   // 128 + zero
+                  const float zero = ZEROS ? __uint_as_float(__byte_perm(zr, 0x43000000u, 0x7044 | c << 8)) : 136.f;   // 128 + zero: 0x43zz0000
 #pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                      float& o = tot[set][c >> 1][n][(c & 1) * 2 + r];
-                      o = fmaf(scale, fmaf(-zero, sum[n][r], acc[set][c >> 1][n][(c & 1) * 2 + r]), o);
-                    }
+                  for (int r = 0; r < 2; ++r) {
+                    float& o = tot[set][c >> 1][(c & 1) * 2 + r];
+                    o = fmaf(scale, fmaf(-zero, sum[r], acc[set][c >> 1][(c & 1) * 2 + r]), o);
+                  }
                 }
               }
             }
@@ -512,50 +496,48 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
       if (item >= end) continue;
       if (parts > 1) {
 #pragma unroll
-        for (int i = 0; i < 16 * NT; ++i) (&tot[0][0][0][0])[i] += mine[i * 32];
+        for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] += mine[i * 32];
       }
       // columns 4g .. 4g+3 of rows 2t, 2t+1 are this lane's
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int r = 0; r < 2; ++r) {
+        const int row = row_first + 2 * t + r;
+        if (row >= a.rows) continue;
+        const int64_t slot = slot0 + list[a.row0 + row];
+        float v[2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = row_first + n * 8 + 2 * t + r;
-          if (row >= a.rows) continue;
-          const int64_t slot = slot0 + list[a.row0 + row];
-          float v[2][4];
+        for (int set = 0; set < 2; ++set)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[set][c] = tot[set][c >> 1][(c & 1) * 2 + r];
+        if (GATE_UP) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[0][c] = w4_swiglu(v[0][c], v[1][c]);
+          *reinterpret_cast<uint2*>(p.h + slot * half + block * 32 + 4 * g) =
+              make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
+        } else {
 #pragma unroll
           for (int set = 0; set < 2; ++set)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[set][c] = tot[set][c >> 1][n][(c & 1) * 2 + r];
-          if (GATE_UP) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[0][c] = w4_swiglu(v[0][c], v[1][c]);
-            *reinterpret_cast<uint2*>(p.h + slot * half + block * 32 + 4 * g) =
-                make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
-          } else {
-#pragma unroll
-            for (int set = 0; set < 2; ++set)
-              *reinterpret_cast<float4*>(p.part + slot * p.N + set * half + block * 32 + 4 * g) =
-                  make_float4(v[set][0], v[set][1], v[set][2], v[set][3]);
-          }
+            *reinterpret_cast<float4*>(p.part + slot * p.N + set * half + block * 32 + 4 * g) =
+                make_float4(v[set][0], v[set][1], v[set][2], v[set][3]);
         }
+      }
       continue;
     }
     // a shared item: its parts' sums meet in shared memory, and its warps
     // share the values out: value i of the first half and of the second
 #pragma unroll
-    for (int i = 0; i < 16 * NT; ++i) mine[i * 32] = (&tot[0][0][0][0])[i];
+    for (int i = 0; i < 16; ++i) mine[i * 32] = (&tot[0][0][0])[i];
     __syncthreads();
     if (item < end) {
       const float* from = sums_of_parts + (warp - part) * Ring::kPart + lane;
-      for (int i = part; i < 8 * NT; i += parts) {   // i = (hf * NT + n) * 4 + r
-        const int r = i & 3, n = (i >> 2) % NT, hf = (i >> 2) / NT;
-        const int row = row_first + n * 8 + 2 * t + (r & 1);
+      for (int i = part; i < 8; i += parts) {   // i = hf * 4 + r
+        const int r = i & 3, hf = i >> 2;
+        const int row = row_first + 2 * t + (r & 1);
         if (row >= a.rows) continue;
-        float v0 = from[i * 32], v1 = from[(8 * NT + i) * 32];
+        float v0 = from[i * 32], v1 = from[(8 + i) * 32];
         for (int w = 1; w < parts; ++w) {
           v0 += from[w * Ring::kPart + i * 32];
-          v1 += from[w * Ring::kPart + (8 * NT + i) * 32];
+          v1 += from[w * Ring::kPart + (8 + i) * 32];
         }
         const int64_t slot = slot0 + list[a.row0 + row];
         const int col = block * 32 + 4 * g + 2 * hf + (r >> 1);
@@ -633,30 +615,22 @@ __global__ void __launch_bounds__(kW4CombineThreads) w4_combine_kernel(const flo
   *reinterpret_cast<uint4*>(y + t * H + c) = pack8(acc);
 }
 
-template <int NT, bool GATE_UP, int GROUP, bool ZEROS>
+template <bool GATE_UP, int GROUP, bool ZEROS>
 cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
   if (!configured[dev.ordinal].load()) {
-    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<NT, GATE_UP, GROUP, ZEROS>,
+    const cudaError_t err = cudaFuncSetAttribute(w4_kernel<GATE_UP, GROUP, ZEROS>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 w4_smem<NT, GROUP, ZEROS>(kMaxExperts, kW4MaxSlots));
+                                                 w4_smem<GROUP, ZEROS>(kMaxExperts, kW4MaxSlots));
     if (err != cudaSuccess) return err;
     configured[dev.ordinal].store(1);
   }
   const int row_slots = std::min(p.slots_per_row, p.slots);
   const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
   const int64_t most = (int64_t)row_slots * p.blocks;   // every slot its own chunk
-  return launch_pdl(w4_kernel<NT, GATE_UP, GROUP, ZEROS>,
+  return launch_pdl(w4_kernel<GATE_UP, GROUP, ZEROS>,
                     dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows), dim3(kW4Threads),
-                    w4_smem<NT, GROUP, ZEROS>(p.E, row_slots), stream, 1, p);
-}
-
-template <bool GATE_UP, int GROUP>
-cudaError_t launch_w4_rows(const W4Params& p, bool zeros, const DeviceInfo& dev, cudaStream_t stream) {
-  // 8 rows a chunk while the experts in use hold few rows each, else 16
-  if ((int64_t)p.slots <= (int64_t)4 * p.E || p.slots <= 8 * p.k)
-    return zeros ? launch_w4<1, GATE_UP, GROUP, true>(p, dev, stream) : launch_w4<1, GATE_UP, GROUP, false>(p, dev, stream);
-  return zeros ? launch_w4<2, GATE_UP, GROUP, true>(p, dev, stream) : launch_w4<2, GATE_UP, GROUP, false>(p, dev, stream);
+                    w4_smem<GROUP, ZEROS>(p.E, row_slots), stream, 1, p);
 }
 
 // The tensor maps, K's parts, and the launch of the group's kernel.
@@ -680,10 +654,12 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
   p.slots_per_row = w4_row_slots(p.E, p.k);
   p.blocks = (int)(half / 32);
   const int units = (p.K + 127) / 128;
-  p.parts_log2 = units >= 32 ? 3 : units >= 8 ? 2 : units >= 2 ? 1 : 0;   // about four units a part
-  if (group == 32) return launch_w4_rows<GATE_UP, 32>(p, zeros != nullptr, dev, stream);
-  if (group == 64) return launch_w4_rows<GATE_UP, 64>(p, zeros != nullptr, dev, stream);
-  return launch_w4_rows<GATE_UP, 128>(p, zeros != nullptr, dev, stream);
+  p.parts_log2 = units >= 32 ? 3 : units >= 4 ? 2 : units >= 2 ? 1 : 0;
+  if (group == 32)
+    return zeros ? launch_w4<GATE_UP, 32, true>(p, dev, stream) : launch_w4<GATE_UP, 32, false>(p, dev, stream);
+  if (group == 64)
+    return zeros ? launch_w4<GATE_UP, 64, true>(p, dev, stream) : launch_w4<GATE_UP, 64, false>(p, dev, stream);
+  return zeros ? launch_w4<GATE_UP, 128, true>(p, dev, stream) : launch_w4<GATE_UP, 128, false>(p, dev, stream);
 }
 
 // One thread per (group, column) of [rows, N] bf16 weights.
