@@ -30,6 +30,41 @@ def _range(name):
     return nvtx.range(name) if nvtx is not None else contextlib.nullcontext()
 
 
+@dataclass(frozen=True)
+class Routing:
+    """How experts are chosen from the router's logits (ops.route_select):
+    softmax or sigmoid scores, the best top_groups of n_groups groups of
+    experts, weights renormalised over the chosen experts or not, and scaled.
+    Without one (routing=None) the layer routes by ops.route."""
+    score: str = "softmax"
+    n_groups: int = 1
+    top_groups: int = 1
+    group_score: str = "top2"
+    renorm: bool = True
+    scale: float = 1.0
+
+    @property
+    def dense_gradient(self):
+        """Whether the logits of experts that were not chosen have a gradient too."""
+        return self.score == "softmax" and not self.renorm
+
+    def select(self, logits, k, balance_bias=None):
+        return ops.route_select(logits, k, balance_bias, self.score, self.n_groups, self.top_groups, self.group_score,
+                                self.renorm, self.scale)
+
+
+def _route(x, w_router, k, bias, w_split, routing, balance_bias):
+    """ids, w and, with a Routing, the logits that they were chosen from."""
+    if routing is None:
+        if balance_bias is not None:
+            raise ValueError("balance_bias needs a Routing")
+        ids, w = ops.route(x, w_router, k, bias, w_split=w_split)
+        return ids, w, None
+    logits = ops.route_logits(x, w_router, bias, w_split)
+    ids, w = routing.select(logits, k, balance_bias)
+    return ids, w, logits
+
+
 @dataclass
 class ForwardState:
     """What the forward keeps for the backward."""
@@ -47,10 +82,12 @@ class ForwardState:
     h_w: torch.Tensor | None = None        # bf16 w * h [R, I]
     x_perm: torch.Tensor | None = None     # bf16 [R, H] when the rows were materialised
     y_shared: torch.Tensor | None = None
+    logits: torch.Tensor | None = None     # fp32 [T, E], with a Routing
+    routing: Routing | None = None
 
 
 def moe_forward(x, w_router, gate_up, down, k, bias=None, sh_gate_up=None, sh_down=None,
-                save_for_backward=False, fused_gather=False, w_split=None):
+                save_for_backward=False, fused_gather=False, w_split=None, routing=None, balance_bias=None):
     """y [T, H] bf16 and the ForwardState.
 
     fused_gather: the grouped gate_up GEMM gathers the token rows itself (the
@@ -59,12 +96,17 @@ def moe_forward(x, w_router, gate_up, down, k, bias=None, sh_gate_up=None, sh_do
     streams them with 128-row TMA tiles, which measures ~2.5x faster for the
     GEMM on GB300.
     w_split: W_r's bf16 split (ops.route_split_weight), prepared once while
-    W_r does not change; the same results as without it."""
+    W_r does not change; the same results as without it.
+    routing, balance_bias: a Routing, and the [E] fp32 bias that it adds to the
+    scores for the choice alone (bias is added to the logits)."""
     T, H = x.shape
     E = w_router.shape[1]
     I = down.shape[0] // E
+    if save_for_backward and routing is not None and routing.dense_gradient:
+        raise ValueError("softmax without renorm has a gradient at every expert's logit, which the layer's backward "
+                         "does not carry into dX (ops.route_select_bwd gives it)")
     with _range("moe.route"):
-        ids, w = ops.route(x, w_router, k, bias, w_split=w_split)
+        ids, w, logits = _route(x, w_router, k, bias, w_split, routing, balance_bias)
     w_perm = None
     with _range("moe.permute"):
         if save_for_backward:
@@ -93,7 +135,7 @@ def moe_forward(x, w_router, gate_up, down, k, bias=None, sh_gate_up=None, sh_do
     with _range("moe.combine"):
         y = ops.unpermute_combine(y_perm, row_map, w, y_shared)
     st = ForwardState(x, ids, w, counts, offsets, row_map, src_row, h, y_perm, w_perm, gu_pre, h_w, x_perm,
-                      y_shared)
+                      y_shared, logits, routing)
     return y, st
 
 
@@ -111,7 +153,11 @@ def moe_backward(dy, st: ForwardState, w_router, gate_up, down, want_dw_router=F
     with _range("moe.down_bwd"):
         dgu, d_down, dw_part = ops.grouped_gemm_down_bwd(dy_perm, st.h_w, st.gu_pre, st.w_perm, st.offsets, down)
     with _range("moe.route_bwd"):
-        d_logits, dw = ops.route_bwd(dw_part, st.row_map, st.w, st.ids, E)
+        if st.routing is None:
+            d_logits, dw = ops.route_bwd(dw_part, st.row_map, st.w, st.ids, E)
+        else:
+            r = st.routing
+            d_logits, dw = ops.route_select_bwd(dw_part, st.logits, st.ids, r.score, r.renorm, r.scale, st.row_map)
     with _range("moe.gate_up_bwd"):
         if st.x_perm is not None:
             dx_perm, d_gate_up = ops.grouped_gemm_gate_up_bwd(dgu, st.x_perm, None, st.offsets, gate_up)
@@ -145,12 +191,39 @@ class MoELayerFunction(torch.autograd.Function):
         return (g["dx"], g.get("d_w_router"), g["d_gate_up"], g["d_down"], None, None)
 
 
-class MoELayer(torch.nn.Module):
-    """Routed SwiGLU experts over the fused layout gate_up [E*H, 2I], down [E*I, H]."""
+class RoutedMoELayerFunction(torch.autograd.Function):
+    """MoELayerFunction with a Routing: y and the experts' loads (permute's
+    counts, for ops.route_balance_bias).  The balance bias chooses only and has no gradient."""
 
-    def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, device="cuda"):
+    @staticmethod
+    def forward(ctx, x, w_router, gate_up, down, k, bias, routing, balance_bias):
+        y, st = moe_forward(x.contiguous(), w_router.contiguous(), gate_up.contiguous(), down.contiguous(), k, bias,
+                            save_for_backward=True, routing=routing, balance_bias=balance_bias)
+        ctx.st = st
+        ctx.save_for_backward(w_router, gate_up, down)
+        ctx.mark_non_differentiable(st.counts)
+        return y, st.counts
+
+    @staticmethod
+    def backward(ctx, dy, _):
+        w_router, gate_up, down = ctx.saved_tensors
+        g = moe_backward(dy.contiguous(), ctx.st, w_router, gate_up, down, want_dw_router=ctx.needs_input_grad[1])
+        return (g["dx"], g.get("d_w_router"), g["d_gate_up"], g["d_down"], None, None, None, None)
+
+
+class MoELayer(torch.nn.Module):
+    """Routed SwiGLU experts over the fused layout gate_up [E*H, 2I], down [E*I, H].
+
+    routing: a Routing; the layer then holds a balance bias (a buffer, zeros at
+    first) that update_balance_bias moves by the loads of the last forward."""
+
+    def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, device="cuda", routing=None):
         super().__init__()
         self.k = top_k
+        self.routing = routing
+        if routing is not None:
+            self.register_buffer("balance_bias", torch.zeros(n_experts, dtype=torch.float32, device=device))
+            self.last_counts = None
         self.w_router = torch.nn.Parameter(torch.empty(hidden, n_experts, dtype=torch.float32, device=device))
         self.gate_up = torch.nn.Parameter(torch.empty(n_experts * hidden, 2 * inter, dtype=torch.bfloat16,
                                                       device=device))
@@ -158,7 +231,119 @@ class MoELayer(torch.nn.Module):
                                                    device=device))
 
     def forward(self, x, bias=None):
+        if self.routing is not None:
+            y, self.last_counts = RoutedMoELayerFunction.apply(x, self.w_router, self.gate_up, self.down, self.k, bias,
+                                                               self.routing, self.balance_bias)
+            return y
         return MoELayerFunction.apply(x, self.w_router, self.gate_up, self.down, self.k, bias)
+
+    def update_balance_bias(self, rate):
+        """balance_bias += rate * sign(mean load - load) by the last forward's loads."""
+        if self.routing is None or self.last_counts is None:
+            raise ValueError("update_balance_bias needs a layer with a Routing after a forward")
+        ops.route_balance_bias(self.balance_bias, self.last_counts, rate, out=self.balance_bias)
+
+
+@dataclass
+class W4Experts:
+    """The experts' weights in 4 bits: gate_up and down as (qweight, scales,
+    zeros or None) of ops.w4_quantize, with the number of experts."""
+    gate_up: tuple
+    down: tuple
+    n_experts: int
+
+    @classmethod
+    def quantize(cls, gate_up, down, n_experts, group=128, zeros=False):
+        """From gate_up [E*H, 2I] and down [E*I, H] in bf16."""
+        return cls(ops.w4_quantize(gate_up, group, zeros), ops.w4_quantize(down, group, zeros), n_experts)
+
+    def dequantize(self):
+        """gate_up and down in bf16."""
+        return ops.w4_dequantize(*self.gate_up), ops.w4_dequantize(*self.down)
+
+
+# From this many rows an expert on, the 4-bit kernels' chunks of 8 rows (each
+# of which decodes the weights again) cost more than one decoding to bf16 and
+# the bf16 grouped GEMMs.
+W4_MAX_ROWS_PER_EXPERT = 48
+
+
+def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None, routing=None, balance_bias=None):
+    """y [T, H] bf16 of a decode batch through 4-bit experts (W4Experts), and the slots' ids and w.
+
+    route -> gate_up + SwiGLU -> down + combine, rows in slot order with no
+    permutation.  shared: a W4Experts of one expert, always active.  A batch
+    of more than W4_MAX_ROWS_PER_EXPERT rows per expert decodes the weights to
+    bf16 for this call and runs moe_forward's grouped GEMMs on them."""
+    T, H = x.shape
+    E = experts.n_experts
+    if w_router.shape[1] != E:
+        raise ValueError("w_router must be [H, E] for the experts' E")
+    with _range("moe.route"):
+        ids, w, _ = _route(x, w_router, k, bias, w_split, routing, balance_bias)
+    y_shared = None
+    if shared is not None:
+        with _range("moe.shared_expert"):
+            y_shared = ops.w4_down_combine(ops.w4_gate_up_swiglu(x, None, *shared.gate_up), None, None, *shared.down)
+    if T * k > W4_MAX_ROWS_PER_EXPERT * E:
+        gate_up, down = experts.dequantize()
+        with _range("moe.permute"):
+            _, offsets, row_map, _ = ops.permute(ids, E)
+        with _range("moe.permute_rows"):
+            x_perm = ops.permute_rows_scatter(x, row_map, k)
+        with _range("moe.gate_up"):
+            h, _, _ = ops.grouped_gemm_gate_up_swiglu(x_perm, None, offsets, gate_up, down.shape[0] // E)
+        with _range("moe.down"):
+            y_perm = ops.grouped_gemm_down(h, offsets, down, H)
+        with _range("moe.combine"):
+            return ops.unpermute_combine(y_perm, row_map, w, y_shared), ids, w
+    with _range("moe.gate_up"):
+        h = ops.w4_gate_up_swiglu(x, ids, *experts.gate_up)
+    with _range("moe.down"):
+        return ops.w4_down_combine(h, ids, w, *experts.down, y_shared=y_shared), ids, w
+
+
+class DecodeGraph:
+    """moe_forward_w4 captured once as a CUDA graph for a fixed token count:
+    write a step's tokens into ``x`` (or pass them to ``__call__``); a replay
+    is one launch and writes ``y``, ``ids`` and ``w``, which the next replay
+    overwrites.  Routing stays on the device, so one capture serves any
+    routing.  As ForwardGraph, it makes W_r's bf16 split once
+    (``refresh_router_split()`` after changing W_r)."""
+
+    def __init__(self, T, w_router, experts, k, bias=None, shared=None, routing=None, balance_bias=None):
+        H, E = w_router.shape
+        self.args = (w_router, experts, k, bias, shared)
+        self.routing, self.balance_bias = routing, balance_bias
+        self.w_split = ops.route_split_weight(w_router) if ops.route_supports_split(H, E) else None
+        self.x = torch.zeros((T, H), dtype=torch.bfloat16, device=w_router.device)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):          # one-time library set-up happens outside the capture
+            for _ in range(2):
+                self._forward()
+        torch.cuda.current_stream().wait_stream(side)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.y, self.ids, self.w = self._forward()
+
+    def _forward(self):
+        return moe_forward_w4(self.x, *self.args, w_split=self.w_split, routing=self.routing,
+                              balance_bias=self.balance_bias)
+
+    def refresh_router_split(self):
+        """Re-derives W_r's split (in place, where the graph reads it) after W_r changed."""
+        if self.w_split is not None:
+            ops.route_split_weight(self.args[0], out=self.w_split)
+
+    def replay(self):
+        """Runs the layer on the current contents of ``x``; returns ``y``."""
+        self.graph.replay()
+        return self.y
+
+    def __call__(self, x):
+        self.x.copy_(x)
+        return self.replay()
 
 
 class ForwardGraph:

@@ -166,6 +166,11 @@ def _need_logits(t, name="logits"):
     return _need(t, name, torch.float32, 2)
 
 
+def route_logits(x, w_router, bias=None, w_split=None):
+    """The router's logits [T, E] fp32 alone (moe_route), for route_select."""
+    return route(x, w_router, 1, bias, return_logits=True, w_split=w_split)[2]
+
+
 def route_select(logits, k, bias=None, score="softmax", n_groups=1, top_groups=1, group_score="top2", renorm=True,
                  scale=1.0):
     """ids [T, k] int32 and w [T, k] fp32 chosen from logits [T, E] (fp32 or bf16).
