@@ -662,9 +662,9 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
   return zeros ? launch_w4<GATE_UP, 128, true>(p, dev, stream) : launch_w4<GATE_UP, 128, false>(p, dev, stream);
 }
 
-// One thread per (group, column) of [rows, N] bf16 weights.
+// One thread per group and 2 columns of [rows, N] bf16 weights.
 //   symmetric: scale = bf16(max|w| / 7), q = clamp(rint(w / scale) + 8, 0, 15)
-//   zeros:     scale = bf16((max(w, 0) - min(w, 0)) / 15), zero = clamp(rint(-min(w, 0) / scale), 0, 15),
+//   zeros:     scale = bf16((max(w, 0) - min(w, 0)) / 15), zero = min(rint(-min(w, 0) / scale), 15),
 //              q = clamp(rint(w / scale) + zero, 0, 15)
 // A group of zeros has scale 0 and q = zero.
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const uint16_t* __restrict__ w, int64_t groups, int N,
@@ -673,34 +673,49 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const uint16_t* __rest
   pdl_wait();
   pdl_trigger();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= groups * N) return;
-  const int64_t g = i / N;
-  const int n = (int)(i - g * N);
+  const int nv = N / 2;
+  if (i >= groups * nv) return;
+  const int64_t g = i / nv;
+  const int n = (int)(i - g * nv) * 2;
   const uint16_t* src = w + g * group * N + n;
-  float lo = 0.f, hi = 0.f;
+  float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f}, s[2], zero[2];
+#pragma unroll 16
   for (int r = 0; r < group; ++r) {
-    const float v = __uint_as_float((uint32_t)src[(int64_t)r * N] << 16);
-    lo = fminf(lo, v);
-    hi = fmaxf(hi, v);
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(src + (int64_t)r * N);
+    lo[0] = fminf(lo[0], bf16_lo(v));
+    hi[0] = fmaxf(hi[0], bf16_lo(v));
+    lo[1] = fminf(lo[1], bf16_hi(v));
+    hi[1] = fmaxf(hi[1], bf16_hi(v));
   }
-  const float want = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
-  const __nv_bfloat16 sb = __float2bfloat16_rn(want);
-  const float s = __bfloat162float(sb);
-  const float zero = zeros ? (s > 0.f ? fminf(rintf(-lo / s), 15.f) : 0.f) : 8.f;
-  scales[i] = __bfloat16_as_ushort(sb);
-  if (zeros) zeros[i] = (uint8_t)zero;
+  uint32_t sbits = 0, zbits = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float want = zeros ? (hi[c] - lo[c]) / 15.f : fmaxf(hi[c], -lo[c]) / 7.f;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(want);
+    s[c] = __bfloat162float(sb);
+    zero[c] = zeros ? (s[c] > 0.f ? fminf(rintf(-lo[c] / s[c]), 15.f) : 0.f) : 8.f;
+    sbits |= (uint32_t)__bfloat16_as_ushort(sb) << (16 * c);
+    zbits |= (uint32_t)zero[c] << (8 * c);
+  }
+  *reinterpret_cast<uint32_t*>(scales + g * N + n) = sbits;
+  if (zeros) *reinterpret_cast<uint16_t*>(zeros + g * N + n) = (uint16_t)zbits;
   for (int r = 0; r < group; r += 8) {
-    uint32_t word = 0;
+    uint32_t word[2] = {0, 0};
+#pragma unroll
     for (int b = 0; b < 8; ++b) {
-      const float v = __uint_as_float((uint32_t)src[(int64_t)(r + b) * N] << 16);
-      const float c = s > 0.f ? fminf(fmaxf(rintf(v / s) + zero, 0.f), 15.f) : zero;
-      word |= (uint32_t)c << (4 * b);
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(src + (int64_t)(r + b) * N);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float code = s[c] > 0.f ? fminf(fmaxf(rintf((c ? bf16_hi(v) : bf16_lo(v)) / s[c]) + zero[c], 0.f), 15.f) : zero[c];
+        word[c] |= (uint32_t)code << (4 * b);
+      }
     }
-    q[(g * group + r) / 8 * N + n] = word;
+    *reinterpret_cast<uint2*>(q + (g * group + r) / 8 * N + n) = make_uint2(word[0], word[1]);
   }
 }
 
-// One thread per word: scale * (q - zero) in fp32, rounded to bf16.
+// One thread per word row and 8 columns: scale * (q - zero) in fp32, rounded
+// to bf16, written as 8 vectors of 16 bytes.
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __restrict__ q,
                                                             const uint16_t* __restrict__ scales,
                                                             const uint8_t* __restrict__ zeros, int64_t words, int N,
@@ -708,16 +723,26 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
   pdl_wait();
   pdl_trigger();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= words * N) return;
-  const int64_t r = i / N;
-  const int n = (int)(i - r * N);
+  const int nv = N / 8;
+  if (i >= words * nv) return;
+  const int64_t r = i / nv;
+  const int n = (int)(i - r * nv) * 8;
   const int64_t sg = r * 8 / group * N + n;
-  const float s = __uint_as_float((uint32_t)scales[sg] << 16);
-  const float zero = zeros ? (float)zeros[sg] : 8.f;
-  const uint32_t word = q[i];
+  const uint4* src = reinterpret_cast<const uint4*>(q + r * N + n);
+  const uint4 a = src[0], b = src[1];
+  const uint32_t word[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float s[8], zero[8];
+  unpack8(*reinterpret_cast<const uint4*>(scales + sg), s);
+  const uint2 z = zeros ? *reinterpret_cast<const uint2*>(zeros + sg) : make_uint2(0x08080808u, 0x08080808u);
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    w[(r * 8 + b) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s * ((float)((word >> (4 * b)) & 15u) - zero)));
+  for (int c = 0; c < 8; ++c) zero[c] = (float)(((c < 4 ? z.x : z.y) >> (8 * (c & 3))) & 255u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = s[c] * ((float)((word[c] >> (4 * k)) & 15u) - zero[c]);
+    *reinterpret_cast<uint4*>(w + (r * 8 + k) * N + n) = pack8(v);
+  }
 }
 
 }  // namespace
@@ -760,14 +785,14 @@ cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* w
 
 cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64_t group, uint32_t* q,
                                uint16_t* scales, uint8_t* zeros, cudaStream_t stream) {
-  const int64_t n = rows / group * N;
+  const int64_t n = rows / group * (N / 2);
   return launch_pdl(w4_quantize_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, 1, w, rows / group,
                     (int)N, (int)group, q, scales, zeros);
 }
 
 cudaError_t launch_w4_dequantize(const uint32_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t rows,
                                  int64_t N, int64_t group, uint16_t* w, cudaStream_t stream) {
-  const int64_t n = rows / 8 * N;
+  const int64_t n = rows / 8 * (N / 8);
   return launch_pdl(w4_dequantize_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, 1, q, scales,
                     zeros, rows / 8, (int)N, (int)group, w);
 }
