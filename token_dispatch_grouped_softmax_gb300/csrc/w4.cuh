@@ -68,8 +68,9 @@ __host__ __device__ constexpr int w4_row_slots(int E, int k, int most, int bytes
   return slots / k * k;
 }
 
-// ROWS: rows of a chunk.  SLOTS: the most slots of a launch row.  By a block
-// of THREADS; warp_sums holds one word a warp.
+// ROWS: rows of a chunk.  SLOTS: the most slots of a launch row.  By the
+// first THREADS threads of the block, which takes part in the barriers;
+// warp_sums holds one word a warp of them.
 template <int ROWS, int THREADS, int SLOTS>
 __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int slots, uint32_t* bits, W4Active* act,
                                              uint16_t* list, uint64_t* warp_sums) {
@@ -81,13 +82,13 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
   for (int j = 0; j < SLOTS / THREADS; ++j) {
     const int i = j * THREADS + tid;
     e_of[j] = -1;
-    if (i < slots) {
+    if (tid < THREADS && i < slots) {
       const int e = p.ids ? p.ids[slot0 + i] : 0;
       if (e >= 0 && e < p.E) e_of[j] = e;
       else if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
     }
   }
-  for (int i = tid; i < p.E * stride; i += THREADS) bits[i] = 0;
+  for (int i = tid; i < p.E * stride; i += blockDim.x) bits[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < SLOTS / THREADS; ++j)
@@ -118,7 +119,7 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
     const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
   }
-  if (lane == 31) warp_sums[warp] = incl;
+  if (lane == 31 && tid < THREADS) warp_sums[warp] = incl;
   __syncthreads();
   uint64_t before = incl - sum, total = 0;
 #pragma unroll

@@ -16,11 +16,30 @@ namespace moe {
 namespace {
 
 constexpr int kWideRows = 64;
-constexpr int kWideThreads = 512;     // warp 0 TMA, 1 MMA, 4..7 totals, 8..15 decoding
+constexpr int kWideThreads = 896;     // warp 0 TMA, 1 MMA, 4..11 totals, 12..27 decoders
+constexpr int kListThreads = 512;     // of them in the sort of the slots
+constexpr int kTotalWarps = 8;        // four of the tile's 128 columns, for each half of the rows
 constexpr int kWideMaxSlots = 4096;   // slots of one launch row
-constexpr int kWideDecoders = 8;
-constexpr int kQStages = 4, kAbStages = 2, kDBuffers = 4;
+constexpr int kDecoders = 8;          // warps of a decoder group; two groups take the steps in turn
+constexpr int kQStages = 4, kAbStages = 3, kDBuffers = 4;
 constexpr int kABytes = 128 * 128 * 2, kBBytes = kWideRows * 128 * 2;   // a step: 128 k
+
+// The MMA and the commit by one elected lane of the converged warp.  (The
+// same lane issues both: a commit follows the MMAs of its own thread.)
+__device__ __forceinline__ void mma_elected(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
+}
 
 template <int GROUP, bool ZEROS>
 struct WideRing {
@@ -38,8 +57,10 @@ __host__ __device__ constexpr int wide_smem(int E, int slots) {
          (slots * 2 + 15) / 16 * 16 + 512;
 }
 
+// No memory clobber, so that a run of them and the loads around them overlap:
+// ordered by the proxy fence that follows (an asm with a memory clobber).
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
 // Codes i and i + 4 of a word less the zero, as two bf16 (exact: 128 + code
@@ -56,7 +77,9 @@ __device__ __forceinline__ uint32_t w4_less_zero(uint32_t word, int i, uint32_t 
 //   TMA      codes, scales and zeros of the step, four stages deep
 //   decoders codes -> A [128 columns][128 k] and x rows -> B [rows][128 k],
 //            both K-major in the 128-byte swizzle; within 8 k the order is
-//            k0 k4 k1 k5 k2 k6 k3 k7, as the codes come apart
+//            k0 k4 k1 k5 k2 k6 k3 k7, as the codes come apart.  A step is some
+//            1300 cycles of waits, loads and conversions one after another to
+//            its warps: two groups of them take the steps in turn
 //   MMA      a group's products into a fresh TMEM buffer (four of 64 columns)
 //   totals   buffer -> registers, a lane to a column: one scale for all rows
 // Every wait is bounded (MOE_ERR_TIMEOUT in the status word).
@@ -91,18 +114,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
   if (tid == 0) {
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(full_q(s), 1);
-      mbar_init(empty_q(s), kWideDecoders + 4);
+      mbar_init(empty_q(s), kDecoders + kTotalWarps);
     }
     for (int s = 0; s < kAbStages; ++s) {
-      mbar_init(full_ab(s), kWideDecoders);
+      mbar_init(full_ab(s), kDecoders);
       mbar_init(empty_ab(s), 1);
     }
     for (int s = 0; s < kDBuffers; ++s) {
       mbar_init(full_d(s), 1);
-      mbar_init(empty_d(s), 4);
+      mbar_init(empty_d(s), kTotalWarps);
     }
-    mbar_init(exch_full, 2);
-    mbar_init(exch_empty, 2);
+    mbar_init(exch_full, kTotalWarps / 2);
+    mbar_init(exch_empty, kTotalWarps / 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -118,7 +141,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem);   // over the rings, before they are used
-  const uint64_t found = w4_lists<kWideRows, kWideThreads, kWideMaxSlots>(p, slot0, slots, bits, act, list, scratch);
+  const uint64_t found = w4_lists<kWideRows, kListThreads, kWideMaxSlots>(p, slot0, slots, bits, act, list, scratch);
   const uint32_t chunks = (uint32_t)found;
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
@@ -199,9 +222,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
+    // The warp stays converged and an elected lane issues: the descriptors
+    // are then uniform registers.
     int stage = 0, buf = 0;
     uint32_t phase = 0, dphase = 0;
     bool ok = true, issued_any = false;
+    const uint64_t desc = umma_desc(0, 16, 1024);   // addresses are added in units of 16 bytes
     for (int item = begin; item < end && ok; ++item) {
       const Item it = item_at(item);
       const int cols = (it.rows + 15) & ~15;
@@ -210,21 +236,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
       for (int st = 0; st < steps && ok; ++st) {
         if (!(ok = wait(full_ab(stage), phase, 9))) break;
         tc_fence_after();
-        const uint32_t sA = ab + stage * (kABytes + kBBytes), sB = sA + kABytes;
+        const uint64_t da = desc + ((ab + stage * (kABytes + kBBytes)) >> 4), db = da + (kABytes >> 4);
         const int subs = subs_of(st);
-        for (int sub = 0; sub < subs; ++sub) {
+#pragma unroll
+        for (int sub = 0; sub < Ring::kSubs; ++sub) {
+          if (sub >= subs) break;
           if (!(ok = wait(empty_d(buf), dphase ^ 1u, 10))) break;
           tc_fence_after();
-          if (lane == 0) {
+          const uint32_t d = tmem_base + 64u * (uint32_t)buf;
 #pragma unroll
-            for (int i = 0; i < GROUP / 16; ++i) {
-              const int kk = sub * (GROUP / 16) + i;   // 16 k: panel kk / 4, 32 bytes kk % 4
-              tc_mma_bf16(tmem_base + 64u * buf, umma_desc(sA + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                          umma_desc(sB + (kk >> 2) * (kWideRows * 128) + (kk & 3) * 32, 16, 1024), idesc, i != 0 ? 1u : 0u);
-            }
-            tc_commit(full_d(buf));
+          for (int i = 0; i < GROUP / 16; ++i) {
+            const int kk = sub * (GROUP / 16) + i;   // 16 k: panel kk / 4, 32 bytes kk % 4
+            mma_elected(d, da + (kk >> 2) * 1024 + (kk & 3) * 2, db + (kk >> 2) * (kWideRows * 8) + (kk & 3) * 2, idesc,
+                        i != 0 ? 1u : 0u);
           }
-          __syncwarp();
+          commit_elected(full_d(buf));
           issued_any = true;
           if (++buf == kDBuffers) {
             buf = 0;
@@ -232,23 +258,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
           }
         }
         if (!ok) break;
-        if (lane == 0) tc_commit(empty_ab(stage));
-        __syncwarp();
+        commit_elected(empty_ab(stage));
         if (++stage == kAbStages) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    if (issued_any && lane == 0) {   // every MMA has finished before the tensor memory is freed
-      tc_commit(drain);
+    if (issued_any) {   // every MMA has finished before the tensor memory is freed
+      commit_elected(drain);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < p.wait_limit_ns) {
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------- totals: a lane to a column
+  } else if (warp >= 4 && warp < 4 + kTotalWarps) {
+    // --------------------- totals: a lane to a column, a half of the rows
+    constexpr int kRows = kWideRows / 2;
+    const int row0 = ((warp - 4) >> 2) * kRows;
     const int m = (warp & 3) * 32 + lane, set = m >> 6, c = m & 63;   // column c of half `set`
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int stage = 0, buf = 0;
@@ -256,9 +283,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
     bool ok = true;
     for (int item = begin; item < end && ok; ++item) {
       const Item it = item_at(item);
-      float tot[kWideRows];
+      const int rows = it.rows - row0;   // of this half, may be none
+      float tot[kRows];
 #pragma unroll
-      for (int n = 0; n < kWideRows; ++n) tot[n] = 0.f;
+      for (int n = 0; n < kRows; ++n) tot[n] = 0.f;
       for (int st = 0; st < steps && ok; ++st) {
         if (!(ok = wait(full_q(stage), phase, 11))) break;
         const int subs = subs_of(st);
@@ -268,10 +296,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
           if (!(ok = wait(full_d(buf), dphase, 12))) break;
           tc_fence_after();
 #pragma unroll
-          for (int n0 = 0; n0 < kWideRows; n0 += 16)
-            if (n0 < it.rows) {
+          for (int n0 = 0; n0 < kRows; n0 += 16)
+            if (n0 < rows) {
               float d[16];
-              tmem_ld16(tmem_base + lanes + 64u * buf + n0, d);
+              tmem_ld16(tmem_base + lanes + 64u * buf + row0 + n0, d);
 #pragma unroll
               for (int n = 0; n < 16; ++n) tot[n0 + n] = fmaf(scale, d[n], tot[n0 + n]);
             }
@@ -298,17 +326,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
         if (set == 1) {
           if (!(ok = wait(exch_empty, xphase ^ 1u, 13))) break;
 #pragma unroll
-          for (int n = 0; n < kWideRows; ++n)
-            if (n < it.rows) exchange[n * 64 + c] = tot[n];
+          for (int n = 0; n < kRows; ++n)
+            if (n < rows) exchange[(row0 + n) * 64 + c] = tot[n];
           __syncwarp();
           if (lane == 0) mbar_arrive(exch_full);
         } else {
           if (!(ok = wait(exch_full, xphase, 14))) break;
 #pragma unroll
-          for (int n = 0; n < kWideRows; ++n)
-            if (n < it.rows && col < half) {
-              const int64_t slot = slot0 + list[it.a.row0 + it.row_first + n];
-              p.h[slot * half + col] = __bfloat16_as_ushort(__float2bfloat16_rn(w4_swiglu(tot[n], exchange[n * 64 + c])));
+          for (int n = 0; n < kRows; ++n)
+            if (n < rows && col < half) {
+              const int64_t slot = slot0 + list[it.a.row0 + it.row_first + row0 + n];
+              p.h[slot * half + col] = __bfloat16_as_ushort(__float2bfloat16_rn(w4_swiglu(tot[n], exchange[(row0 + n) * 64 + c])));
             }
           __syncwarp();
           if (lane == 0) mbar_arrive(exch_empty);
@@ -316,22 +344,25 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
         xphase ^= 1u;
       } else {
 #pragma unroll
-        for (int n = 0; n < kWideRows; ++n)
-          if (n < it.rows && col < half) {
-            const int64_t slot = slot0 + list[it.a.row0 + it.row_first + n];
+        for (int n = 0; n < kRows; ++n)
+          if (n < rows && col < half) {
+            const int64_t slot = slot0 + list[it.a.row0 + it.row_first + row0 + n];
             p.part[slot * p.N + set * half + col] = tot[n];
           }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 4 + kTotalWarps) {
     // -------------------------------------------------------- decoders
-    const int dw = warp - 8, dtid = tid - 256;
+    const int dw = (warp - 4 - kTotalWarps) % kDecoders, group = (warp - 4 - kTotalWarps) / kDecoders;
+    const int dtid = dw * 32 + lane;
     const int g = lane >> 2, t = lane & 3;
     const int xrow = dtid >> 4, xchunk = dtid & 15;   // rows xrow + 16 j, 16-byte chunk of the step's 128 k
-    int stage = 0, astage = 0;
+    // step s of the block (over all its items) is group s % 2's, in code
+    // stage s % kQStages and A, B stage s % kAbStages
+    int stage = group, astage = group, turn = group;   // turn: this group's next step of the item
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
-    for (int item = begin; item < end && ok; ++item) {
+    for (int item = begin; item < end && ok; ++item, turn -= steps) {
       const Item it = item_at(item);
       const uint16_t* x[4];
       uint4 xn[4];
@@ -351,8 +382,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
           x[j] = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K;
         }
       }
-      load_x(0);
-      for (int st = 0; st < steps; ++st) {
+      load_x(turn);
+      for (; turn < steps; turn += 2) {
         if (!(ok = wait(empty_ab(astage), aphase ^ 1u, 15))) break;
         const uint32_t sA = ab + astage * (kABytes + kBBytes), sB = sA + kABytes;
 #pragma unroll
@@ -364,21 +395,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
                         __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                         __byte_perm(v.y, v.w, 0x7632));
           }
-        if (st + 1 < steps) load_x(st + 1);
+        load_x(turn + 2);   // past K: zeros
         if (!(ok = wait(full_q(stage), phase, 16))) break;
+        // two pieces of 32 columns of a half x 4 word rows
+        uint4 v[2];
+        uint32_t zr[2] = {0x08080808u, 0x08080808u};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {   // 32 columns of a half x 4 word rows each
+        for (int q = 0; q < 2; ++q) {
           const int sub = dw * 2 + q, b = sub >> 3, set = (sub >> 2) & 1, rq = sub & 3;
           const int line = (rq * 4 + t) * 2 + set;
-          const uint4 v = *reinterpret_cast<const uint4*>(codes + stage * Ring::kQ + b * 4096 + line * 128 + ((g ^ (line & 7)) << 4));
-          uint32_t zr = 0x08080808u;
+          v[q] = *reinterpret_cast<const uint4*>(codes + stage * Ring::kQ + b * 4096 + line * 128 + ((g ^ (line & 7)) << 4));
           if (ZEROS)
-            zr = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + b * Ring::kZeroBox + ((rq * 32 / GROUP) * 2 + set) * 32 + g * 4);
-          const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+            zr[q] = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + b * Ring::kZeroBox + ((rq * 32 / GROUP) * 2 + set) * 32 + g * 4);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int sub = dw * 2 + q, b = sub >> 3, set = (sub >> 2) & 1, rq = sub & 3;
+          const uint32_t word[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
           const int r = rq * 4 + t;   // word row: 16-byte chunk r of the column's 128 k
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t zero2 = 0x43004300u + ((zr >> (8 * j)) & 255u) * 0x00010001u;
+            const uint32_t zero2 = 0x43004300u + ((zr[q] >> (8 * j)) & 255u) * 0x00010001u;
             const int row = set * 64 + b * 32 + g * 4 + j;
             st_shared16(sA + (r >> 3) * 16384 + row * 128 + (((r & 7) ^ (row & 7)) << 4), w4_less_zero(word[j], 0, zero2),
                         w4_less_zero(word[j], 1, zero2), w4_less_zero(word[j], 2, zero2), w4_less_zero(word[j], 3, zero2));
@@ -390,12 +427,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
           mbar_arrive(full_ab(astage));
           mbar_arrive(empty_q(stage));
         }
-        if (++stage == kQStages) {
-          stage = 0;
+        if ((stage += 2) >= kQStages) {
+          stage -= kQStages;
           phase ^= 1u;
         }
-        if (++astage == kAbStages) {
-          astage = 0;
+        if ((astage += 2) >= kAbStages) {
+          astage -= kAbStages;
           aphase ^= 1u;
         }
       }
