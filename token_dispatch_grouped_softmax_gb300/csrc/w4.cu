@@ -8,7 +8,7 @@
 // of one column, lowest nibble first.  A slot whose id is -1 is empty.
 #include <algorithm>
 
-#include "w4.cuh"
+#include "kernels.h"
 
 namespace moe {
 
@@ -18,7 +18,191 @@ constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Rows = 8;          // rows of a chunk: the columns of an mma
 constexpr int kW4MaxSlots = 2048;   // slots of one launch row (shared-memory lists)
-constexpr int kW4WideRows = 10;     // rows an expert from which the tcgen05 kernel is taken
+
+struct W4Params {
+  CUtensorMap tm_q;        // codes as [E*K/8 rows][2 halves of the columns][N/2], boxes of 16 x 2 x 32 words
+  CUtensorMap tm_scale;    // scales the same way, boxes of (128 / group) x 2 x 32
+  CUtensorMap tm_zero;
+  const uint16_t* rows;    // gate_up: x [T, K]; down: h [slots, K]
+  const int32_t* ids;      // [slots], NULL: one dense expert
+  uint16_t* h;             // gate_up's output [slots, N / 2]
+  float* part;             // down's products [slots, N]
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int K, N, E, k;
+  int slots, slots_per_row;
+  int parts_log2;          // a sum over K is 2^parts_log2 partial sums
+  int blocks;              // column blocks: columns 32 b .. 32 b + 31 of both halves
+};
+
+// An expert in use: its rows are list[row0 .. row0 + rows), cut into chunks
+// of kW4Rows numbered from chunk0.
+struct W4Active {
+  int expert, row0, rows, chunk0;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 |
+// code.  One lop3 with the shift before it: (a & b) | c is table 0xEA.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+  return v;
+}
+
+// The experts of the slots of this launch row, and each expert's slots in
+// increasing order (every block sorts for itself and must find the same
+// chunks).  bits is scratch, [E] rows of w4_bit_row(slots) words: bit i of row
+// e says that slot i is expert e's, so a slot's place is a count of the bits
+// before it, whatever order they were set in; the row's last word is the
+// expert's first place.  Behind them, 16 bits for each word: the bits set in
+// the row's words before it.  Returns the numbers of chunks (low 32 bits) and
+// of experts in use.  (Counting with __match_any_sync took 6900 cycles for
+// 360 slots of 128 experts, most of it in that instruction.)
+__host__ __device__ constexpr int w4_bit_row(int slots) { return ((slots + 31) / 32 + 1) | 1; }   // odd: no bank conflicts
+
+// Slots that a launch row can take: at most `most`, whole tokens, and the
+// sort's scratch in `bytes`.
+__host__ __device__ constexpr int w4_row_slots(int E, int k, int most, int bytes) {
+  int slots = most;
+  while (E * w4_bit_row(slots) * 6 > bytes) slots -= 32;
+  return slots / k * k;
+}
+
+__device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int slots, uint32_t* bits, W4Active* act,
+                                             uint16_t* list, uint64_t* warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int words = (slots + 31) / 32, stride = w4_bit_row(slots);
+  uint16_t* before_word = reinterpret_cast<uint16_t*>(bits + p.E * stride);
+  int e_of[kW4MaxSlots / kW4Threads];
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j) {
+    const int i = j * kW4Threads + tid;
+    e_of[j] = -1;
+    if (i < slots) {
+      const int e = p.ids ? p.ids[slot0 + i] : 0;
+      if (e >= 0 && e < p.E) e_of[j] = e;
+      else if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+    }
+  }
+  for (int i = tid; i < p.E * stride; i += kW4Threads) bits[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
+    if (e_of[j] >= 0) atomicOr(&bits[e_of[j] * stride + j * (kW4Warps) + warp], 1u << lane);
+  __syncthreads();
+  // thread i: experts [i * per, (i + 1) * per); prefix of (rows, experts, chunks)
+  const int per = (p.E + kW4Threads - 1) / kW4Threads;
+  auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + kW4Rows - 1) / kW4Rows) << 40; };
+  auto rows_of = [&](int e) {
+    int n = 0;
+    for (int w = 0; w < words; ++w) {
+      before_word[e * stride + w] = (uint16_t)n;
+      n += __popc(bits[e * stride + w]);
+    }
+    return n;
+  };
+  int n_of[kMaxExperts / kW4Threads];
+  uint64_t sum = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kW4Threads; ++q) {
+    const int e = tid * per + q;
+    n_of[q] = q < per && e < p.E ? rows_of(e) : 0;
+    if (n_of[q]) sum += packed(n_of[q]);
+  }
+  uint64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  uint64_t before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kW4Warps; ++w) {
+    const uint64_t s = warp_sums[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+#pragma unroll
+  for (int q = 0; q < kMaxExperts / kW4Threads; ++q) {
+    const int e = tid * per + q;
+    if (n_of[q]) {
+      act[(int)(before >> 20 & 0xFFFFF)] = W4Active{e, (int)(before & 0xFFFFF), n_of[q], (int)(before >> 40)};
+      bits[e * stride + stride - 1] = (uint32_t)(before & 0xFFFFF);
+      before += packed(n_of[q]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
+    if (e_of[j] >= 0) {
+      const uint32_t* row = bits + e_of[j] * stride;
+      const int at = j * (kW4Warps) + warp;   // the word of slot j * kW4Threads + tid
+      const int place = (int)row[stride - 1] + before_word[e_of[j] * stride + at] + __popc(row[at] & ((1u << lane) - 1u));
+      list[place] = (uint16_t)(j * kW4Threads + tid);
+    }
+  return (total >> 40) | (total >> 20 & 0xFFFFF) << 32;
+}
+
+// The same for at most 32 slots, by one warp: experts in the order of their
+// first slot.
+__device__ __forceinline__ uint64_t w4_lists_small(const W4Params& p, int slots, W4Active* act, uint16_t* list,
+                                                   uint64_t* result) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int e = -1;
+    if (lane < slots) {
+      e = p.ids ? p.ids[lane] : 0;
+      if (e < 0 || e >= p.E) {
+        if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+        e = -1;
+      }
+    }
+    uint32_t peers = 0;
+#pragma unroll 8
+    for (int j = 0; j < slots; ++j) peers |= (uint32_t)(__shfl_sync(0xffffffffu, e, j) == e) << j;
+    const int n = __popc(peers), first = __ffs(peers) - 1;
+    const bool leads = e >= 0 && lane == first;
+    const int mine = leads ? n | (n + kW4Rows - 1) / kW4Rows << 16 : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int before = incl - mine;
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    if (leads) act[__popc(leaders & ((1u << lane) - 1u))] = W4Active{e, before & 0xFFFF, n, before >> 16};
+    const int row0 = __shfl_sync(0xffffffffu, before & 0xFFFF, first & 31);
+    if (e >= 0) list[row0 + __popc(peers & ((1u << lane) - 1u))] = (uint16_t)lane;
+    if (lane == 31) *result = (uint64_t)(incl >> 16) | (uint64_t)__popc(leaders) << 32;
+  }
+  __syncthreads();
+  return *result;
+}
+
+// Zero rows of h for the empty slots, shared out over the blocks.
+__device__ __forceinline__ void w4_zero_rows(const W4Params& p, int slot0, int slots) {
+  const int I = p.N / 2;
+  for (int i = blockIdx.x; i < slots; i += gridDim.x) {
+    const int e = p.ids[slot0 + i];
+    if (e >= 0 && e < p.E) continue;
+    for (int c = threadIdx.x; c < I / 8; c += kW4Threads)
+      reinterpret_cast<uint4*>(p.h + (int64_t)(slot0 + i) * I)[c] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ float w4_swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // D += A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulators.
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -109,8 +293,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
-  const uint64_t found = p.slots <= 32 ? w4_lists_small<kW4Rows>(p, slots, act, list, scratch)
-                                       : w4_lists<kW4Rows, kW4Threads, kW4MaxSlots>(p, slot0, slots, bits, act, list, scratch);
+  const uint64_t found = p.slots <= 32 ? w4_lists_small(p, slots, act, list, scratch)
+                                       : w4_lists(p, slot0, slots, bits, act, list, scratch);
   const uint32_t chunks = (uint32_t)found;
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
@@ -471,7 +655,6 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
     return cudaErrorInvalidValue;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
-  if ((int64_t)p.slots >= (int64_t)kW4WideRows * p.E) return launch_w4_wide(p, GATE_UP, group, zeros != nullptr, dev, stream);
   p.slots_per_row = w4_row_slots(p.E, p.k, kW4MaxSlots, W4Ring<128, false>::kBytes);
   p.blocks = (int)(half / 32);
   const int units = (p.K + 127) / 128;
