@@ -2,7 +2,9 @@
 
 Each .cu file is compiled in parallel into _build/, then linked into a shared
 library next to this file.  The CUDA runtime is linked as a shared library so
-the process shares one runtime (current device, streams) with PyTorch.
+the process shares one runtime (current device, streams) with PyTorch.  Beside
+it _binding.so is built from csrc/binding.cpp with the host compiler: the
+Python extension of the calls of a decode step.
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -40,14 +45,36 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    for out, deps in ((LIB, _deps()), (BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
+        if not os.path.exists(out):
+            return False
+        t = os.path.getmtime(out)
+        if not all(os.path.getmtime(d) <= t for d in deps):
+            return False
+    return True
+
+
+def _build_binding(verbose):
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = BINDING + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+           "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           "-I" + sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on %s:\n%s\n%s" % (cmd[0], BINDING_SRC, r.stdout, r.stderr))
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout, r.stderr)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libmoe_gb300.so when missing or older than its sources."""
+    """Compile and link libmoe_gb300.so and _binding.so when missing or older than their sources."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -64,8 +91,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + \
         ["-Xlinker", "-rpath=/usr/local/cuda/lib64"]

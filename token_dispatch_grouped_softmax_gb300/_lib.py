@@ -103,6 +103,22 @@ def load():
     return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The Python extension of the decode step's calls (csrc/binding.cpp), on the loaded library."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        from . import _binding as ext
+        ext.bind(check, *(ctypes.cast(getattr(lib, name), P).value for name in (
+            "moe_route_select", "moe_route_select_bwd", "moe_route_balance_bias", "moe_w4_gate_up_swiglu",
+            "moe_w4_down_workspace_size", "moe_w4_down_combine")))
+        _binding = ext
+    return _binding
+
+
 def check(name, rc):
     if rc != MOE_OK:
         raise MoEError(name, rc)

@@ -8,11 +8,10 @@ library's CUDA kernels; there is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
-from ._lib import call
+from ._lib import binding, call
 
 _BF16 = torch.bfloat16
 
@@ -160,11 +159,9 @@ def _choice(table, value, name):
     return table[value]
 
 
-def _need_logits(t, name="logits"):
-    if isinstance(t, torch.Tensor) and t.dtype == _BF16:
-        return _need(t, name, _BF16, 2)
-    return _need(t, name, torch.float32, 2)
-
+# The functions up to w4_down_combine check their tensors, allocate and call
+# in the extension _binding (csrc/binding.cpp): a decode step's kernels run for
+# a few microseconds, less than the same done in Python.
 
 def route_logits(x, w_router, bias=None, w_split=None):
     """The router's logits [T, E] fp32 alone (moe_route), for route_select."""
@@ -181,18 +178,8 @@ def route_select(logits, k, bias=None, score="softmax", n_groups=1, top_groups=1
     ("max") or the sum of its two best ("top2"); renorm divides the chosen
     scores by their sum; scale multiplies them.  A logit of -inf masks its
     expert.  Equal values go to the lower index (moe_route_select)."""
-    _need_logits(logits)
-    T, E = logits.shape
-    if bias is not None:
-        _need(bias, "bias", torch.float32, 1)
-        if bias.shape[0] != E:
-            raise ValueError("bias must be [E]")
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    call("moe_route_select", _p(logits), logits.dtype == _BF16, _p(bias), T, E, k, _choice(_SCORES, score, "score"),
-         n_groups, top_groups, _choice(_GROUP_SCORES, group_score, "group_score"), bool(renorm), scale, _p(ids), _p(w),
-         _stream())
-    return ids, w
+    return binding().route_select(logits, k, bias, _choice(_SCORES, score, "score"), n_groups, top_groups,
+                                  _choice(_GROUP_SCORES, group_score, "group_score"), bool(renorm), scale)
 
 
 def route_select_bwd(dw, logits, ids, score="softmax", renorm=True, scale=1.0, row_map=None):
@@ -202,77 +189,16 @@ def route_select_bwd(dw, logits, ids, score="softmax", renorm=True, scale=1.0, r
     With row_map [T*k], dw is dw_part [T*k, nparts] from
     grouped_gemm_down_bwd (permuted rows, summed here), and (d_logits, dw
     [T, k]) is returned.  Softmax without renorm has a dense gradient."""
-    _need(dw, "dw", torch.float32, 2)
-    _need_logits(logits)
-    _need(ids, "ids", torch.int32, 2)
-    T, E = logits.shape
-    k = ids.shape[1]
-    if ids.shape[0] != T:
-        raise ValueError("ids must be [T, k]")
-    d_logits = torch.empty_like(logits)
-    dw_sum = None
-    nparts = 1
-    if row_map is not None:
-        _need(row_map, "row_map", torch.int32, 1)
-        if row_map.shape[0] != T * k or dw.shape[0] != T * k:
-            raise ValueError("row_map must hold T*k entries and dw must be [T*k, nparts]")
-        nparts = dw.shape[1]
-        dw_sum = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    elif dw.shape != ids.shape:
-        raise ValueError("dw must be [T, k]")
-    call("moe_route_select_bwd", _p(dw), nparts, _p(row_map), _p(logits), logits.dtype == _BF16, _p(ids), T, E, k,
-         _choice(_SCORES, score, "score"), bool(renorm), scale, _p(d_logits), _p(dw_sum), _stream())
-    return d_logits if row_map is None else (d_logits, dw_sum)
+    return binding().route_select_bwd(dw, logits, ids, _choice(_SCORES, score, "score"), bool(renorm), scale, row_map)
 
 
 def route_balance_bias(bias, counts, rate, out=None):
     """bias + rate * sign(mean load - load) [E] fp32, the loads being permute's
     counts [E] int32; out: an existing [E] fp32 tensor (bias itself to update in place)."""
-    _need(bias, "bias", torch.float32, 1)
-    _need(counts, "counts", torch.int32, 1)
-    E = bias.shape[0]
-    if counts.shape[0] != E:
-        raise ValueError("counts must be [E]")
-    if out is None:
-        out = torch.empty_like(bias)
-    else:
-        _need(out, "out", torch.float32, 1)
-        if out.shape[0] != E:
-            raise ValueError("out must be [E]")
-    call("moe_route_balance_bias", _p(bias), _p(counts), E, rate, _p(out), _stream())
-    return out
+    return binding().route_balance_bias(bias, counts, rate, out)
 
 
 # ----------------------------------------------------------- 4-bit experts
-
-def _w4(qweight, scales, zeros, K, N=None):
-    """(E, N, group) of 4-bit weights with K rows per expert."""
-    _need(qweight, "qweight", torch.int32, 2)
-    _need(scales, "scales", _BF16, 2)
-    words, n = qweight.shape
-    if K < 8 or K % 8 or words % (K // 8) or (N is not None and n != N):
-        raise ValueError("qweight must be [E*K/8, N] with K = %d%s" % (K, "" if N is None else ", N = %d" % N))
-    E = words // (K // 8)
-    if scales.shape[1] != n or E == 0 or scales.shape[0] % E or scales.shape[0] == 0 or K % (scales.shape[0] // E):
-        raise ValueError("scales must be [E*K/group, N]")
-    if zeros is not None:
-        _need(zeros, "zeros", torch.uint8, 2)
-        if zeros.shape != scales.shape:
-            raise ValueError("zeros must be [E*K/group, N]")
-    return E, n, K * E // scales.shape[0]
-
-
-def _w4_ids(ids, T, E):
-    """k of the slots' experts ids [T, k] (None: one dense expert)."""
-    if ids is None:
-        if E != 1:
-            raise ValueError("ids are needed with more than one expert")
-        return 1
-    _need(ids, "ids", torch.int32, 2)
-    if ids.shape[0] != T:
-        raise ValueError("ids must be [T, k]")
-    return ids.shape[1]
-
 
 def w4_gate_up_swiglu(x, ids, qweight, scales, zeros=None):
     """h [T, k, I] bf16 with h[t, j] = silu(x_t . Wg) * (x_t . Wu) of the 4-bit
@@ -282,23 +208,7 @@ def w4_gate_up_swiglu(x, ids, qweight, scales, zeros=None):
     word, lowest nibble first), scales [E*H/group, 2I] bf16, zeros of the same
     shape uint8 or None for 8 (w4_quantize makes them).  ids None: one dense
     expert."""
-    _need(x, "x", _BF16, 2)
-    T, H = x.shape
-    E, N, group = _w4(qweight, scales, zeros, H)
-    if N % 2:
-        raise ValueError("qweight must be [E*H/8, 2I]")
-    k = _w4_ids(ids, T, E)
-    h = torch.empty((T, k, N // 2), dtype=_BF16, device=x.device)
-    call("moe_w4_gate_up_swiglu", _p(x), _p(ids), _p(qweight), _p(scales), _p(zeros), T, H, E, k, N // 2, group,
-         _p(h), _stream())
-    return h
-
-
-@functools.lru_cache(maxsize=256)
-def _w4_down_workspace(T, H, k):
-    nbytes = ctypes.c_size_t(0)
-    call("moe_w4_down_workspace_size", T, H, k, ctypes.byref(nbytes))
-    return nbytes.value
+    return binding().w4_gate_up_swiglu(x, ids, qweight, scales, zeros)
 
 
 def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=None):
@@ -306,29 +216,7 @@ def w4_down_combine(h, ids, w, qweight, scales, zeros=None, y_shared=None, out=N
     ids[t, j] (-1 adds nothing); h [T, k, I] bf16 in slot order, w [T, k] fp32
     (None: 1), qweight [E*I/8, H] and scales [E*I/group, H] as in
     w4_gate_up_swiglu.  ids None: one dense expert."""
-    _need(h, "h", _BF16, 3)
-    T, k, I = h.shape
-    E, H, group = _w4(qweight, scales, zeros, I)
-    if _w4_ids(ids, T, E) != k:
-        raise ValueError("h must be [T, k, I] and ids [T, k]")
-    if w is not None:
-        _need(w, "w", torch.float32, 2)
-        if tuple(w.shape) != (T, k):
-            raise ValueError("w must be [T, k]")
-    if y_shared is not None:
-        _need(y_shared, "y_shared", _BF16, 2)
-        if tuple(y_shared.shape) != (T, H):
-            raise ValueError("y_shared must be [T, H]")
-    if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=h.device)
-    else:
-        _need(out, "out", _BF16, 2)
-        if tuple(out.shape) != (T, H):
-            raise ValueError("out must be [T, H]")
-    ws = _ws(_w4_down_workspace(T, H, k), h.device)
-    call("moe_w4_down_combine", _p(h), _p(ids), _p(w), _p(qweight), _p(scales), _p(zeros), _p(y_shared), T, H, E, k,
-         I, group, _p(out), _p(ws), ws.numel(), _stream())
-    return out
+    return binding().w4_down_combine(h, ids, w, qweight, scales, zeros, y_shared, out)
 
 
 def w4_quantize(weight, group=128, zeros=False):
@@ -350,8 +238,15 @@ def w4_quantize(weight, group=128, zeros=False):
 def w4_dequantize(qweight, scales, zeros=None):
     """bf16 weights [rows, N] of w4_quantize's layout: scale * (code - zero), one rounding."""
     _need(qweight, "qweight", torch.int32, 2)
-    rows = qweight.shape[0] * 8
-    _, N, group = _w4(qweight, scales, zeros, rows)
+    _need(scales, "scales", _BF16, 2)
+    rows, N = qweight.shape[0] * 8, qweight.shape[1]
+    if scales.shape[1] != N or scales.shape[0] == 0 or rows % scales.shape[0]:
+        raise ValueError("scales must be [rows/group, N]")
+    group = rows // scales.shape[0]
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, 2)
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must be [rows/group, N]")
     w = torch.empty((rows, N), dtype=_BF16, device=qweight.device)
     call("moe_w4_dequantize", _p(qweight), _p(scales), _p(zeros), rows, N, group, _p(w), _stream())
     return w
