@@ -92,7 +92,9 @@ SHAPES = [  # T, H, E, k, I, group, zeros, empty
     # more than eight items for each of the GPU's blocks: whole items a warp, then shared ones; K of an odd number of
     # 64 rows, of parts of unequal length, of one part
     (64, 192, 60, 6, 1408, 64, True, 0.1), (64, 640, 60, 6, 1408, 32, False, 0.0), (40, 1152, 64, 8, 1024, 128, True, 0.0),
-    (64, 2816, 60, 6, 192, 64, True, 0.1), (64, 2880, 60, 6, 640, 32, True, 0.0), (48, 4096, 64, 8, 128, 128, False, 0.0)]
+    (64, 2816, 60, 6, 192, 64, True, 0.1), (64, 2880, 60, 6, 640, 32, True, 0.0), (48, 4096, 64, 8, 128, 128, False, 0.0),
+    # many experts: the slots of a launch row are few, so several rows
+    (50, 64, 1000, 8, 64, 64, False, 0.1)]
 
 
 @pytest.mark.parametrize("T,H,E,k,I,group,zeros,empty", SHAPES)
@@ -295,6 +297,33 @@ def test_bad_ids_are_reported():
         moe.w4_down_combine(h, wrong, None, *qd)
         with pytest.raises(moe.MoEError):
             moe.sync_status()
+    moe.sync_status()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """With no copies issued, the kernel's bounded waits give up, the status
+    says so, the context stays usable and the next call is right."""
+    moe = lib()
+    T, H, E, k, I, group = 9, 256, 4, 2, 128, 64
+    qg, qd = dev_of(*weights(1, E, H, 2 * I, group, False)), dev_of(*weights(2, E, I, H, group, True))
+    x = rows_of(1, T, H).to(dev())
+    ids = i32(ids_of(3, T, E, k))
+    h0 = moe.w4_gate_up_swiglu(x, ids, *qg)
+    y0 = moe.w4_down_combine(h0, ids, None, *qd)
+    moe.set_wait_limit_ns(20_000_000)
+    try:
+        for call in (lambda: moe.w4_gate_up_swiglu(x, ids, *qg), lambda: moe.w4_down_combine(h0, ids, None, *qd)):
+            moe._lib.call("moe_test_stall_gemm_producer", 1)
+            call()
+            moe._lib.call("moe_test_stall_gemm_producer", 0)
+            with pytest.raises(moe.MoEError) as err:
+                moe.sync_status()
+            assert err.value.status == 4
+    finally:
+        moe._lib.call("moe_test_stall_gemm_producer", 0)
+        moe.set_wait_limit_ns(0)
+    assert torch.equal(moe.w4_gate_up_swiglu(x, ids, *qg), h0)
+    assert torch.equal(moe.w4_down_combine(h0, ids, None, *qd), y0)
     moe.sync_status()
 
 

@@ -31,6 +31,7 @@ struct W4Params {
   uint64_t wait_limit_ns;
   int K, N, E, k;
   int slots, slots_per_row;
+  int stall;               // test hook: issue no copies
   int parts_log2;          // a sum over K is 2^parts_log2 partial sums
   int blocks;              // column blocks: columns 32 b .. 32 b + 31 of both halves
 };
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
       next_run();
       if (lrun >= runs) return;
     }
-    if (lane == 0) {
+    if (lane == 0 && !p.stall) {
       const uint32_t bar = bar0 + 8 * lstage;
       mbar_arrive_expect_tx(bar, Ring::kQ + Ring::kRows * (ZEROS ? 192 : 128));
       tma_load_3d(smem_u32(ring) + lstage * Ring::kQ, &p.tm_q, lcol, 0, lqrow, bar);
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
     }
     __syncthreads();
   }
-  if (!ok && lane == 0) {   // stopped early: the copies in flight land (bounded) before the block's memory goes
+  if (!ok && lane == 0 && !p.stall) {   // stopped early: the copies in flight land (bounded) before the block's memory goes
     for (int d = 0; d < Ring::kDepth; ++d) {
       const uint64_t t0 = globaltimer_ns();
       const uint32_t par = d < stage ? phase ^ 1u : phase;
@@ -655,6 +656,7 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
     return cudaErrorInvalidValue;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
+  p.stall = dev.test_stall_producer;
   p.slots_per_row = w4_row_slots(p.E, p.k, kW4MaxSlots, W4Ring<128, false>::kBytes);
   p.blocks = (int)(half / 32);
   const int units = (p.K + 127) / 128;
