@@ -33,6 +33,7 @@ struct W4Params {
   int slots, slots_per_row;
   int stall;               // test hook: issue no copies
   int parts_log2;          // a sum over K is 2^parts_log2 partial sums
+  uint32_t blocks_magic, grid_magic;   // 2^32 / blocks and / the grid's blocks
   int blocks;              // column blocks: columns 32 b .. 32 b + 31 of both halves
 };
 
@@ -59,9 +60,15 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
   return v;
 }
 
+// n / d with magic = floor((2^32 - 1) / d): at most one too small before the fix.
+__device__ __forceinline__ uint32_t w4_div(uint32_t n, uint32_t d, uint32_t magic) {
+  const uint32_t q = __umulhi(n, magic);
+  return q + (n - q * d >= d);
+}
+
 // The experts of the slots of this launch row, and each expert's slots in
 // increasing order (every block sorts for itself and must find the same
-// chunks).  bits is scratch, [E] rows of w4_bit_row(slots) words: bit i of row
+// chunks).  bits is scratch, zeroed, [E] rows of w4_bit_row(slots) words: bit i of row
 // e says that slot i is expert e's, so a slot's place is a count of the bits
 // before it, whatever order they were set in; the row's last word is the
 // expert's first place.  Behind them, 16 bits for each word: the bits set in
@@ -85,17 +92,17 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
   uint16_t* before_word = reinterpret_cast<uint16_t*>(bits + p.E * stride);
   int e_of[kW4MaxSlots / kW4Threads];
 #pragma unroll
-  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j) {
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j) {   // all the loads in flight
     const int i = j * kW4Threads + tid;
     e_of[j] = -1;
-    if (i < slots) {
-      const int e = p.ids ? p.ids[slot0 + i] : 0;
-      if (e >= 0 && e < p.E) e_of[j] = e;
-      else if (e != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
-    }
+    if (i < slots) e_of[j] = p.ids ? __ldg(p.ids + slot0 + i) : 0;
   }
-  for (int i = tid; i < p.E * stride; i += kW4Threads) bits[i] = 0;
-  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
+    if (e_of[j] < 0 || e_of[j] >= p.E) {
+      if (e_of[j] != -1 && blockIdx.x == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+      e_of[j] = -1;
+    }
 #pragma unroll
   for (int j = 0; j < kW4MaxSlots / kW4Threads; ++j)
     if (e_of[j] >= 0) atomicOr(&bits[e_of[j] * stride + j * (kW4Warps) + warp], 1u << lane);
@@ -290,22 +297,25 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_scale);
   }
-  pdl_wait();
-  pdl_trigger();
   const int slot0 = blockIdx.y * p.slots_per_row;
   const int slots = min(p.slots_per_row, p.slots - slot0);
+  if (p.slots > 32)   // the sort's bits
+    for (int i = tid; i < p.E * w4_bit_row(slots); i += kW4Threads) bits[i] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   const uint64_t found = p.slots <= 32 ? w4_lists_small(p, slots, act, list, scratch)
                                        : w4_lists(p, slot0, slots, bits, act, list, scratch);
   const uint32_t chunks = (uint32_t)found;
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
   // this block's items: an even share, the first blocks one more
-  const uint32_t items = chunks * (uint32_t)p.blocks, share = items / gridDim.x, more = items - share * gridDim.x;
+  const uint32_t items = chunks * (uint32_t)p.blocks, share = w4_div(items, gridDim.x, p.grid_magic), more = items - share * gridDim.x;
   const int begin = (int)(blockIdx.x * share + min(blockIdx.x, more));
   const int end = begin + (int)share + (blockIdx.x < more ? 1 : 0);
   if (begin >= end) return;
   // the expert of its first chunk
-  const int first_chunk = begin / p.blocks;
+  const int first_chunk = (int)w4_div(begin, p.blocks, p.blocks_magic);
   for (int i = tid; i < (int)(found >> 32); i += kW4Threads)
     if (first_chunk >= act[i].chunk0 && first_chunk < act[i].chunk0 + (act[i].rows + kW4Rows - 1) / kW4Rows) *first_act = i;
   fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
       if (item >= end) continue;
       lu = lrun < whole ? 0 : part_u0;
       lu_end = lrun < whole ? units : part_u1;
-      const int chunk = item / p.blocks;
+      const int chunk = (int)w4_div(item, p.blocks, p.blocks_magic);
       while (chunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
       const int expert = act[la].expert;
       lcol = (item - chunk * p.blocks) * 32;
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] = 0.f;
     if (item < end) {
-      const int chunk = item / p.blocks;
+      const int chunk = (int)w4_div(item, p.blocks, p.blocks_magic);
       block = item - chunk * p.blocks;
       while (chunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
       a = act[ca];
@@ -400,6 +410,9 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
           x = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + 8 * t;
           xn[0] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128));
           xn[1] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128 + 32));
+          // The rest of the run's row into L1, 128 bytes a lane: the loads 64 k ahead would each wait for L2.
+          for (int c = u0 * 128 + 64 * (t + 1); c < min(u1 * 128, p.K); c += 256)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(x - 8 * t + c));
         }
       }
     }
@@ -633,9 +646,12 @@ cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t str
   const int row_slots = std::min(p.slots_per_row, p.slots);
   const int rows = (p.slots + p.slots_per_row - 1) / p.slots_per_row;
   const int64_t most = (int64_t)row_slots * p.blocks;   // every slot its own chunk
-  return launch_pdl(w4_kernel<GATE_UP, GROUP, ZEROS>,
-                    dim3((unsigned)std::min<int64_t>(most, 2 * dev.num_sms), (unsigned)rows), dim3(kW4Threads),
-                    w4_smem<GROUP, ZEROS>(p.E, row_slots), stream, 1, p);
+  W4Params q = p;
+  const unsigned grid = (unsigned)std::min<int64_t>(most, 2 * dev.num_sms);
+  q.grid_magic = 0xFFFFFFFFu / grid;
+  q.blocks_magic = 0xFFFFFFFFu / (uint32_t)p.blocks;
+  return launch_pdl(w4_kernel<GATE_UP, GROUP, ZEROS>, dim3(grid, (unsigned)rows), dim3(kW4Threads),
+                    w4_smem<GROUP, ZEROS>(p.E, row_slots), stream, 1, q);
 }
 
 // The tensor maps, K's parts, and the launch of the group's kernel.
