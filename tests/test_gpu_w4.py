@@ -94,7 +94,11 @@ SHAPES = [  # T, H, E, k, I, group, zeros, empty
     (64, 192, 60, 6, 1408, 64, True, 0.1), (64, 640, 60, 6, 1408, 32, False, 0.0), (40, 1152, 64, 8, 1024, 128, True, 0.0),
     (64, 2816, 60, 6, 192, 64, True, 0.1), (64, 2880, 60, 6, 640, 32, True, 0.0), (48, 4096, 64, 8, 128, 128, False, 0.0),
     # many experts: the slots of a launch row are few, so several rows
-    (50, 64, 1000, 8, 64, 64, False, 0.1)]
+    (50, 64, 1000, 8, 64, 64, False, 0.1),
+    # few slots, a warp to each part of a sum: eight parts (blocks of a cluster, one and two sums a warp), parts of
+    # unequal length, the most slots a token, empty ones
+    (1, 4096, 6, 4, 4160, 64, True, 0.0), (2, 64, 40, 32, 192, 32, True, 0.3), (1, 4160, 4, 2, 128, 32, False, 0.0),
+    (4, 128, 9, 2, 704, 64, True, 0.4), (1, 2048, 3, 1, 2880, 64, False, 0.0), (3, 64, 33, 17, 1024, 64, False, 0.2)]
 
 
 @pytest.mark.parametrize("T,H,E,k,I,group,zeros,empty", SHAPES)
@@ -184,10 +188,11 @@ def test_dense_expert():
     assert torch.equal(y, check_down(moe, h.cpu(), zero, np.ones((T, 1), np.float32), *qd, group))
 
 
-@pytest.mark.parametrize("T,H,E,k,I,group", [(40, 512, 6, 3, 256, 128), (64, 2048, 64, 6, 1472, 64)])
+@pytest.mark.parametrize("T,H,E,k,I,group", [(40, 512, 6, 3, 256, 128), (64, 2048, 64, 6, 1472, 64), (40, 4096, 16, 4, 1408, 128)])
 def test_a_token_does_not_depend_on_the_batch(T, H, E, k, I, group):
-    """Each token alone gives the bits it has in the batch: from items shared
-    by a block's warps (a small batch) and from whole items of a warp."""
+    """Each token alone gives the bits it has in the batch: from the kernel of
+    few slots, from items shared by a block's warps and from whole items of a
+    warp."""
     moe = lib()
     ids = i32(ids_of(3, T, E, k))
     qg, qd = dev_of(*weights(1, E, H, 2 * I, group, False)), dev_of(*weights(2, E, I, H, group, False))
@@ -300,11 +305,13 @@ def test_bad_ids_are_reported():
     moe.sync_status()
 
 
-def test_a_wait_that_runs_out_is_reported():
-    """With no copies issued, the kernel's bounded waits give up, the status
-    says so, the context stays usable and the next call is right."""
+@pytest.mark.parametrize("T", [2, 200])
+def test_a_wait_that_runs_out_is_reported(T):
+    """With no copies issued, the bounded waits (of the kernel of few slots, and
+    of the other) give up, the status says so, the context stays usable and the
+    next call is right."""
     moe = lib()
-    T, H, E, k, I, group = 9, 256, 4, 2, 128, 64
+    H, E, k, I, group = 256, 4, 2, 128, 64
     qg, qd = dev_of(*weights(1, E, H, 2 * I, group, False)), dev_of(*weights(2, E, I, H, group, True))
     x = rows_of(1, T, H).to(dev())
     ids = i32(ids_of(3, T, E, k))

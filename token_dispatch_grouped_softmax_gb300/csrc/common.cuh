@@ -244,6 +244,12 @@ __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// Four floats to a shared::cluster address (16-byte aligned).
+__device__ __forceinline__ void st_shared_cluster_f32x4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 // Arrive (release at cluster scope) on an mbarrier given by its
 // shared::cluster address, which may be in the other CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

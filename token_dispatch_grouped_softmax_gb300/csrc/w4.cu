@@ -270,6 +270,92 @@ __host__ __device__ constexpr int w4_smem(int E, int slots) {
          (E < slots ? E : slots) * (int)sizeof(W4Active) + (slots * 2 + 15) / 16 * 16 + 128;
 }
 
+// One unit: tot += its 128 k's products.  xn holds the lane's vectors of x's
+// next 64 k and is loaded a step ahead, from next_k on; past the end the
+// first, for the next item.  q_at, scales, zeros: the lane's place in the
+// stage; of SETS halves of the columns (two: lines of both halves in turn).
+template <int GROUP, bool ZEROS, int SETS>
+__device__ __forceinline__ void w4_unit(float (&tot)[SETS][2][4], uint4 (&xn)[2], const uint16_t* x, int& next_k, int K, int k0,
+                                        uint32_t q_at, const uint8_t* scales, const uint8_t* zeros) {
+  float acc[SETS][2][4], sum[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
+    if (j == 1 && k0 + 64 >= K) break;
+    uint32_t b[2][4];
+    if (next_k >= K) next_k = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = xn[i];
+      b[i][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
+      b[i][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
+      b[i][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
+      b[i][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
+    }
+    if (x) {
+      xn[0] = __ldg(reinterpret_cast<const uint4*>(x + next_k));
+      xn[1] = __ldg(reinterpret_cast<const uint4*>(x + next_k + 32));
+    }
+    next_k += 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // 32 k each
+      const bool first = GROUP == 32 || (GROUP == 64 && i == 0) || (GROUP == 128 && i == 0 && j == 0);
+      const bool last = GROUP == 32 || (GROUP == 64 && i == 1) || (GROUP == 128 && i == 1 && j == 1);
+      const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+      if (first) mma_16816_first(sum, ones, b[i][0], b[i][1]);
+      else mma_16816(sum, ones, b[i][0], b[i][1]);
+      mma_16816(sum, ones, b[i][2], b[i][3]);
+#pragma unroll
+      for (int set = 0; set < SETS; ++set) {
+        const uint32_t at = SETS == 2 ? (set ? (q_at ^ 16) + 128 : q_at) + (2 * j + i) * 1024 : (q_at ^ i << 6) + (2 * j + i) * 512;
+        uint32_t word[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                     : "r"(at));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
+                                   w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
+            if (st == 0 && first) mma_16816_first(acc[set][hf], w, b[i][0], b[i][1]);
+            else mma_16816(acc[set][hf], w, b[i][2 * st], b[i][2 * st + 1]);
+          }
+      }
+      if (last) {
+        const int row = GROUP == 32 ? 2 * j + i : GROUP == 64 ? j : 0;
+#pragma unroll
+        for (int set = 0; set < SETS; ++set) {
+          const uint2 sr = *reinterpret_cast<const uint2*>(scales + (row * SETS + set) * 64);
+          uint32_t zr = 0;
+          if (ZEROS) zr = *reinterpret_cast<const uint32_t*>(zeros + (row * SETS + set) * 32);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {   // the lane's four columns
+            const uint32_t sp = c < 2 ? sr.x : sr.y;
+            const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
+            const float zero = ZEROS ? __uint_as_float(__byte_perm(zr, 0x43000000u, 0x7044 | c << 8)) : 136.f;   // 128 + zero: 0x43zz0000
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float& o = tot[set][c >> 1][(c & 1) * 2 + r];
+              o = fmaf(scale, fmaf(-zero, sum[r], acc[set][c >> 1][(c & 1) * 2 + r]), o);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// Stopped early: the copies in flight land (bounded) before the block's
+// memory goes.
+__device__ __forceinline__ void w4_land(uint32_t bar0, int depth, int stage, uint32_t phase, uint64_t limit_ns) {
+  for (int d = 0; d < depth; ++d) {
+    const uint64_t t0 = globaltimer_ns();
+    const uint32_t par = d < stage ? phase ^ 1u : phase;
+    while (!mbar_try_wait(bar0 + 8 * d, par) && globaltimer_ns() - t0 < limit_ns) {
+    }
+  }
+}
+
 template <bool GATE_UP, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant__ W4Params p) {
   using Ring = W4Ring<GROUP, ZEROS>;
@@ -438,72 +524,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
           ok = false;
           break;
         }
-        float acc[2][2][4], sum[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
-          if (j == 1 && u * 128 + 64 >= p.K) break;
-          uint32_t b[2][4];
-          if (next_k >= p.K) next_k = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 v = xn[i];
-            b[i][0] = __byte_perm(v.x, v.z, 0x5410);   // x0 x4
-            b[i][1] = __byte_perm(v.x, v.z, 0x7632);   // x1 x5
-            b[i][2] = __byte_perm(v.y, v.w, 0x5410);   // x2 x6
-            b[i][3] = __byte_perm(v.y, v.w, 0x7632);   // x3 x7
-          }
-          if (x) {
-            xn[0] = __ldg(reinterpret_cast<const uint4*>(x + next_k));
-            xn[1] = __ldg(reinterpret_cast<const uint4*>(x + next_k + 32));
-          }
-          next_k += 64;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {   // 32 k each
-            const bool first = GROUP == 32 || (GROUP == 64 && i == 0) || (GROUP == 128 && i == 0 && j == 0);
-            const bool last = GROUP == 32 || (GROUP == 64 && i == 1) || (GROUP == 128 && i == 1 && j == 1);
-            const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-            if (first) mma_16816_first(sum, ones, b[i][0], b[i][1]);
-            else mma_16816(sum, ones, b[i][0], b[i][1]);
-            mma_16816(sum, ones, b[i][2], b[i][3]);
-#pragma unroll
-            for (int set = 0; set < 2; ++set) {
-              const uint32_t at = (set ? (q_at ^ 16) + 128 : q_at) + stage * Ring::kQ + (2 * j + i) * 1024;
-              uint32_t word[4];
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
-                           : "r"(at));
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                  const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
-                                         w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
-                  if (st == 0 && first) mma_16816_first(acc[set][hf], w, b[i][0], b[i][1]);
-                  else mma_16816(acc[set][hf], w, b[i][2 * st], b[i][2 * st + 1]);
-                }
-            }
-            if (last) {
-              const int row = GROUP == 32 ? 2 * j + i : GROUP == 64 ? j : 0;
-#pragma unroll
-              for (int set = 0; set < 2; ++set) {
-                const uint2 sr = *reinterpret_cast<const uint2*>(scales + stage * Ring::kScale + (row * 2 + set) * 64 + g * 8);
-                uint32_t zr = 0;
-                if (ZEROS) zr = *reinterpret_cast<const uint32_t*>(zeros + stage * Ring::kZero + (row * 2 + set) * 32 + g * 4);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {   // the lane's four columns
-                  const uint32_t sp = c < 2 ? sr.x : sr.y;
-                  const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
-                  const float zero = ZEROS ? __uint_as_float(__byte_perm(zr, 0x43000000u, 0x7044 | c << 8)) : 136.f;   // 128 + zero: 0x43zz0000
-#pragma unroll
-                  for (int r = 0; r < 2; ++r) {
-                    float& o = tot[set][c >> 1][(c & 1) * 2 + r];
-                    o = fmaf(scale, fmaf(-zero, sum[r], acc[set][c >> 1][(c & 1) * 2 + r]), o);
-                  }
-                }
-              }
-            }
-          }
-        }
+        w4_unit<GROUP, ZEROS, 2>(tot, xn, x, next_k, p.K, u * 128, q_at + stage * Ring::kQ, scales + stage * Ring::kScale + g * 8,
+                                 zeros + stage * Ring::kZero + g * 4);
         __syncwarp();   // every lane has read the stage
         issue();        // into the same stage
         stage ^= 1;
@@ -569,14 +591,207 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
     }
     __syncthreads();
   }
-  if (!ok && lane == 0 && !p.stall) {   // stopped early: the copies in flight land (bounded) before the block's memory goes
-    for (int d = 0; d < Ring::kDepth; ++d) {
-      const uint64_t t0 = globaltimer_ns();
-      const uint32_t par = d < stage ? phase ^ 1u : phase;
-      while (!mbar_try_wait(bar0 + 8 * d, par) && globaltimer_ns() - t0 < p.wait_limit_ns) {
-      }
+  if (!ok && lane == 0 && !p.stall) w4_land(bar0, Ring::kDepth, stage, phase, p.wait_limit_ns);
+}
+
+// The products of a few slots, all blocks at once on the GPU: a cluster takes
+// a slot (gate_up) or a token's slots (down, with the combine) and a column
+// block, a warp one part of a slot's sum over K, of one half of the columns
+// (gate_up) or both (down).  The sums meet in the first block's shared memory
+// and its first warp adds them in the order of the other kernels: the same
+// bits.  No lists, and one launch for down: one token, top-8 of 128 experts,
+// H 2048, I 768, down takes 6.0 us instead of 7.4 (4 tokens 11.8 instead of
+// 13.9); one token, top-2 of 16, H 2048, I 1408, gate_up 5.1 instead of 6.2.
+// Halves of the columns for down too took 7.3: clusters of eight blocks.
+template <bool GATE_UP, int GROUP, bool ZEROS>
+struct W4SlotRing {
+  static constexpr int kSets = GATE_UP ? 1 : 2;   // halves of a warp's sum
+  static constexpr int kRows = 128 / GROUP;       // group rows of a unit
+  static constexpr int kQ = 2048 * kSets, kScale = (64 * kSets * kRows + 127) / 128 * 128;
+  static constexpr int kZero = ZEROS ? (32 * kSets * kRows + 127) / 128 * 128 : 0;
+  static constexpr int kDepth = 4 / kSets;
+  static constexpr int kBytes = kW4Warps * kDepth * (kQ + kScale + kZero);
+};
+
+template <bool GATE_UP, int GROUP, bool ZEROS>
+__host__ __device__ constexpr int w4_slots_smem(int sums) {
+  using Ring = W4SlotRing<GATE_UP, GROUP, ZEROS>;
+  return 1024 + Ring::kBytes + sums * Ring::kSets * 32 * 4 + kW4Warps * Ring::kDepth * 8 + 16;
+}
+
+struct W4SlotArgs {
+  int per;            // slots of a cluster: 1, or k and their combine
+  int cluster_log2;   // blocks of a cluster
+  const float* wt;
+  const uint16_t* y_shared;
+  uint16_t* y;
+};
+
+template <bool GATE_UP, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_slots_kernel(const __grid_constant__ W4Params p, const W4SlotArgs s) {
+  using Ring = W4SlotRing<GATE_UP, GROUP, ZEROS>;
+  constexpr int kSets = Ring::kSets, kSplit = 2 - kSets;   // kSplit: bits of a sum's number for its half
+  extern __shared__ uint8_t w4_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int parts = 1 << p.parts_log2, slot_shift = p.parts_log2 + kSplit;
+  const int sums = s.per << slot_shift;   // sum n: slot, part, half
+  uint8_t* ring = smem + warp * (Ring::kDepth * Ring::kQ);
+  uint8_t* scales = smem + kW4Warps * Ring::kDepth * Ring::kQ + warp * (Ring::kDepth * Ring::kScale);
+  uint8_t* zeros = smem + kW4Warps * Ring::kDepth * (Ring::kQ + Ring::kScale) + warp * (Ring::kDepth * Ring::kZero);
+  float* met = reinterpret_cast<float*>(smem + Ring::kBytes);   // [sums][kSets][32 columns], of the cluster's first block
+  uint64_t* bars = reinterpret_cast<uint64_t*>(met + sums * kSets * 32);
+  int* abort_flag = reinterpret_cast<int*>(bars + kW4Warps * Ring::kDepth);
+  const uint32_t bar0 = smem_u32(bars + warp * Ring::kDepth);
+  if (lane == 0) {
+    for (int d = 0; d < Ring::kDepth; ++d) mbar_init(bar0 + 8 * d, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_scale);
+  }
+  __syncthreads();
+  cluster_arrive_release();   // this block runs: its shared memory may be written
+  pdl_wait();
+  pdl_trigger();
+  const int rank = blockIdx.x & ((1 << s.cluster_log2) - 1), block = blockIdx.x >> s.cluster_log2;
+  const int slot0 = blockIdx.y * s.per, half = p.N / 2;
+  int expert = -1;   // of slot slot0 + lane
+  float weight = 1.f;
+  if (lane < s.per) {
+    expert = p.ids ? p.ids[slot0 + lane] : 0;
+    if (!GATE_UP && s.wt) weight = s.wt[slot0 + lane];
+    if (expert < 0 || expert >= p.E) {
+      if (expert != -1 && blockIdx.x == 0 && warp == 0) report_status(p.status, kStatusDevice, kKernW4, 1);
+      expert = -1;
     }
   }
+  const int units = (p.K + 127) / 128, stride = kW4Warps << s.cluster_log2;
+  auto next_sum = [&](int n) {   // from n on, the first of the warp's sums whose slot has an expert
+    while (n < sums && __shfl_sync(0xffffffffu, expert, n >> slot_shift) < 0) n += stride;
+    return n;
+  };
+  const int first = next_sum(rank * kW4Warps + warp);
+
+  // the loader: the sum, the next unit's coordinates, and the stage
+  int ln = first, lu = 0, lu_end = 0, lstage = 0, lqrow = 0, lsrow = 0;
+  auto open = [&]() {
+    if (ln >= sums) return;
+    const int part = ln >> kSplit & (parts - 1), e = __shfl_sync(0xffffffffu, expert, ln >> slot_shift);
+    lu = units * part >> p.parts_log2;
+    lu_end = units * (part + 1) >> p.parts_log2;
+    lqrow = e * (p.K / 8) + lu * 16;
+    lsrow = e * (p.K / GROUP) + lu * Ring::kRows;
+  };
+  auto issue = [&]() {
+    if (ln >= sums) return;
+    if (lane == 0 && !p.stall) {
+      const uint32_t bar = bar0 + 8 * lstage;
+      mbar_arrive_expect_tx(bar, Ring::kQ + Ring::kRows * kSets * (ZEROS ? 96 : 64));
+      tma_load_3d(smem_u32(ring) + lstage * Ring::kQ, &p.tm_q, block * 32, ln & kSplit, lqrow, bar);
+      tma_load_3d(smem_u32(scales) + lstage * Ring::kScale, &p.tm_scale, block * 32, ln & kSplit, lsrow, bar);
+      if (ZEROS) tma_load_3d(smem_u32(zeros) + lstage * Ring::kZero, &p.tm_zero, block * 32, ln & kSplit, lsrow, bar);
+    }
+    lqrow += 16;
+    lsrow += Ring::kRows;
+    lstage = (lstage + 1) & (Ring::kDepth - 1);
+    if (++lu == lu_end) {
+      ln = next_sum(ln + stride);
+      open();
+    }
+  };
+  open();
+  for (int d = 0; d < Ring::kDepth; ++d) issue();
+  // Columns 4 c4 .. 4 c4 + 3 are the lane's: with one half, and c4 = g, the
+  // lanes of a quarter warp, two g and four t, would read the same banks.
+  const int c4 = kSets == 2 ? g : g >> 1 | (g & 1) << 2;
+  const uint32_t q_at = smem_u32(ring) + t * (128 * kSets) + ((c4 ^ kSets * t) << 4);
+  const uint32_t met_at = mapa_shared(smem_u32(met), 0);
+  __syncwarp();
+  cluster_wait_acquire();
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int n = first; n < sums && ok; n = next_sum(n + stride)) {
+    const int part = n >> kSplit & (parts - 1), slot = slot0 + (n >> slot_shift);
+    const int u0 = units * part >> p.parts_log2, u1 = units * (part + 1) >> p.parts_log2;
+    float tot[kSets][2][4];
+#pragma unroll
+    for (int i = 0; i < 8 * kSets; ++i) (&tot[0][0][0])[i] = 0.f;
+    const uint16_t* x = nullptr;   // the mma's other rows are zero
+    uint4 xn[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (g == 0) {
+      x = p.rows + (int64_t)(GATE_UP ? slot / p.k : slot) * p.K + 8 * t;
+      xn[0] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128));
+      xn[1] = __ldg(reinterpret_cast<const uint4*>(x + u0 * 128 + 32));
+      for (int c = u0 * 128 + 64 * (t + 1); c < min(u1 * 128, p.K); c += 256)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(x - 8 * t + c));
+    }
+    int next_k = u0 * 128 + 64;
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+      if (!mbar_wait_warp(bar0 + 8 * stage, phase, abort_flag, p.wait_limit_ns, p.status, 2, kKernW4)) {
+        ok = false;
+        break;
+      }
+      w4_unit<GROUP, ZEROS, kSets>(tot, xn, x, next_k, p.K, u * 128, q_at + stage * Ring::kQ, scales + stage * Ring::kScale + c4 * 8,
+                               zeros + stage * Ring::kZero + c4 * 4);
+      __syncwarp();   // every lane has read the stage
+      issue();        // into the same stage
+      stage = (stage + 1) & (Ring::kDepth - 1);
+      phase ^= stage == 0;
+    }
+    if (t == 0) {   // row 0: the lane's four columns
+#pragma unroll
+      for (int set = 0; set < kSets; ++set)
+        st_shared_cluster_f32x4(met_at + (uint32_t)((n * kSets + set) * 32 + 4 * c4) * 4,
+                                make_float4(tot[set][0][0], tot[set][0][2], tot[set][1][0], tot[set][1][2]));
+    }
+  }
+  const bool adds = rank == 0 && warp == 0;
+  // down: the lane's two columns are of the first half, or of the second
+  const int64_t at = (int64_t)blockIdx.y * p.N + (lane < 16 ? 0 : half) + block * 32 + 2 * (lane & 15);
+  uint32_t extra = 0;
+  if (!GATE_UP && adds && s.y_shared) extra = *reinterpret_cast<const uint32_t*>(s.y_shared + at);
+  __syncwarp();
+  cluster_sync_all();
+  if (adds && GATE_UP) {
+    float v[2] = {0.f, 0.f};
+    const bool used = __shfl_sync(0xffffffffu, expert, 0) >= 0;
+    if (used) {
+      v[0] = met[lane];
+      v[1] = met[32 + lane];
+      for (int q = 1; q < parts; ++q) {
+        v[0] += met[q * 64 + lane];
+        v[1] += met[q * 64 + 32 + lane];
+      }
+    }
+    p.h[(int64_t)slot0 * half + block * 32 + lane] = used ? __bfloat16_as_ushort(__float2bfloat16_rn(w4_swiglu(v[0], v[1]))) : 0;
+  }
+  if (adds && !GATE_UP) {
+    float acc[2] = {0.f, 0.f};
+    for (int j = 0; j < s.per; ++j) {
+      const float w = __shfl_sync(0xffffffffu, weight, j);
+      if (__shfl_sync(0xffffffffu, expert, j) < 0) continue;
+      const float* from = met + j * parts * 64 + 2 * lane;   // the halves' columns lie together
+      float2 v = *reinterpret_cast<const float2*>(from);
+      for (int q = 1; q < parts; ++q) {
+        const float2 o = *reinterpret_cast<const float2*>(from + q * 64);
+        v.x += o.x;
+        v.y += o.y;
+      }
+      acc[0] = fmaf(w, v.x, acc[0]);
+      acc[1] = fmaf(w, v.y, acc[1]);
+    }
+    if (s.y_shared) {
+      acc[0] += bf16_lo(extra);
+      acc[1] += bf16_hi(extra);
+    }
+    *reinterpret_cast<uint32_t*>(s.y + at) = pack_bf16x2(acc[0], acc[1]);
+  }
+  if (!ok && lane == 0 && !p.stall) w4_land(bar0, Ring::kDepth, stage, phase, p.wait_limit_ns);
 }
 
 constexpr int kW4CombineThreads = 64;   // small blocks: one token's columns spread over several SMs
@@ -634,7 +849,22 @@ __global__ void __launch_bounds__(kW4CombineThreads) w4_combine_kernel(const flo
 }
 
 template <bool GATE_UP, int GROUP, bool ZEROS>
-cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_w4_slots(const W4Params& p, const W4SlotArgs& s, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
+  if (!configured[dev.ordinal].load()) {
+    const cudaError_t err = cudaFuncSetAttribute(w4_slots_kernel<GATE_UP, GROUP, ZEROS>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 w4_slots_smem<GATE_UP, GROUP, ZEROS>(16 * kW4Warps));
+    if (err != cudaSuccess) return err;
+    configured[dev.ordinal].store(1);
+  }
+  return launch_pdl(w4_slots_kernel<GATE_UP, GROUP, ZEROS>, dim3((unsigned)(p.blocks << s.cluster_log2), (unsigned)(p.slots / s.per)),
+                    dim3(kW4Threads), w4_slots_smem<GATE_UP, GROUP, ZEROS>(s.per << (p.parts_log2 + GATE_UP)), stream, 1u << s.cluster_log2, p, s);
+}
+
+template <bool GATE_UP, int GROUP, bool ZEROS>
+cudaError_t launch_w4(const W4Params& p, const W4SlotArgs& s, const DeviceInfo& dev, cudaStream_t stream) {
+  if (s.per) return launch_w4_slots<GATE_UP, GROUP, ZEROS>(p, s, dev, stream);
   static std::atomic<int> configured[kMaxDevices] = {};   // per device (a race only repeats the set-up)
   if (!configured[dev.ordinal].load()) {
     const cudaError_t err = cudaFuncSetAttribute(w4_kernel<GATE_UP, GROUP, ZEROS>,
@@ -654,15 +884,32 @@ cudaError_t launch_w4(const W4Params& p, const DeviceInfo& dev, cudaStream_t str
                     w4_smem<GROUP, ZEROS>(p.E, row_slots), stream, 1, q);
 }
 
-// The tensor maps, K's parts, and the launch of the group's kernel.
+// How w4_slots_kernel would run the call, per 0: not.  Its blocks must all be
+// on the GPU at once, two an SM, with a warp for every two sums: beyond that
+// the tokens' common experts are read again and again (down at H 2048, I 768,
+// top-8 of 128: 4 tokens with two sums a warp 11.8 us, with a warp each, in
+// two waves, 13.8, by w4_kernel 13.9; 8 tokens 26.1, by w4_kernel 22.5).
 template <bool GATE_UP>
-cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scales, const uint8_t* zeros,
+W4SlotArgs w4_slot_plan(const W4Params& p, const DeviceInfo& dev) {
+  W4SlotArgs s{};
+  const int per = GATE_UP ? 1 : p.k, sums = per << (p.parts_log2 + GATE_UP);
+  const int64_t clusters = (int64_t)p.blocks * (p.slots / per);
+  int c = 0;
+  while (c < 3 && kW4Warps << c < sums && clusters << (c + 1) <= 2 * dev.num_sms) ++c;
+  s.cluster_log2 = c;
+  s.per = clusters << c <= 2 * dev.num_sms && sums <= 2 * kW4Warps << c ? per : 0;
+  return s;
+}
+
+// The tensor maps and the launch of the group's kernel.
+template <bool GATE_UP>
+cudaError_t launch_w4_group(W4Params& p, const W4SlotArgs& s, const uint32_t* q, const uint16_t* scales, const uint8_t* zeros,
                             int64_t group, const DeviceInfo& dev, cudaStream_t stream) {
   const cuuint64_t half = p.N / 2, rows = (cuuint64_t)p.E * p.K;
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, cuuint64_t bytes, const void* base, cuuint64_t n,
                     int box_rows, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[3] = {half, 2, n}, strides[2] = {half * bytes, (cuuint64_t)p.N * bytes};
-    const cuuint32_t box[3] = {32, 2, (cuuint32_t)box_rows};
+    const cuuint32_t box[3] = {32, GATE_UP && s.per ? 1u : 2u, (cuuint32_t)box_rows};
     return encode_tensor_map_3d(map, type, base, dims, strides, box, swizzle);
   };
   const int group_rows = (int)(128 / group);
@@ -670,18 +917,32 @@ cudaError_t launch_w4_group(W4Params& p, const uint32_t* q, const uint16_t* scal
       !encode(&p.tm_scale, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, scales, rows / group, group_rows, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       (zeros && !encode(&p.tm_zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, zeros, rows / group, group_rows, CU_TENSOR_MAP_SWIZZLE_NONE)))
     return cudaErrorInvalidValue;
+  if (group == 32)
+    return zeros ? launch_w4<GATE_UP, 32, true>(p, s, dev, stream) : launch_w4<GATE_UP, 32, false>(p, s, dev, stream);
+  if (group == 64)
+    return zeros ? launch_w4<GATE_UP, 64, true>(p, s, dev, stream) : launch_w4<GATE_UP, 64, false>(p, s, dev, stream);
+  return zeros ? launch_w4<GATE_UP, 128, true>(p, s, dev, stream) : launch_w4<GATE_UP, 128, false>(p, s, dev, stream);
+}
+
+// The call's sizes, K's parts, and the device.
+W4Params w4_params(const uint16_t* rows, const int32_t* ids, int64_t T, int64_t K, int64_t N, int64_t E, int64_t k,
+                   const DeviceInfo& dev) {
+  W4Params p{};
+  p.rows = rows;
+  p.ids = ids;
+  p.K = (int)K;
+  p.N = (int)N;
+  p.E = (int)E;
+  p.k = (int)k;
+  p.slots = (int)(T * k);
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
   p.stall = dev.test_stall_producer;
   p.slots_per_row = w4_row_slots(p.E, p.k, kW4MaxSlots, W4Ring<128, false>::kBytes);
-  p.blocks = (int)(half / 32);
+  p.blocks = (int)(N / 64);
   const int units = (p.K + 127) / 128;
   p.parts_log2 = units >= 32 ? 3 : units >= 4 ? 2 : units >= 2 ? 1 : 0;
-  if (group == 32)
-    return zeros ? launch_w4<GATE_UP, 32, true>(p, dev, stream) : launch_w4<GATE_UP, 32, false>(p, dev, stream);
-  if (group == 64)
-    return zeros ? launch_w4<GATE_UP, 64, true>(p, dev, stream) : launch_w4<GATE_UP, 64, false>(p, dev, stream);
-  return zeros ? launch_w4<GATE_UP, 128, true>(p, dev, stream) : launch_w4<GATE_UP, 128, false>(p, dev, stream);
+  return p;
 }
 
 // One thread per group and 2 columns of [rows, N] bf16 weights.
@@ -772,16 +1033,9 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
 cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint32_t* q, const uint16_t* scales,
                               const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I,
                               int64_t group, uint16_t* h, const DeviceInfo& dev, cudaStream_t stream) {
-  W4Params p{};
-  p.rows = x;
-  p.ids = ids;
+  W4Params p = w4_params(x, ids, T, H, 2 * I, E, k, dev);
   p.h = h;
-  p.K = (int)H;
-  p.N = (int)(2 * I);
-  p.E = (int)E;
-  p.k = (int)k;
-  p.slots = (int)(T * k);
-  return launch_w4_group<true>(p, q, scales, zeros, group, dev, stream);
+  return launch_w4_group<true>(p, w4_slot_plan<true>(p, dev), q, scales, zeros, group, dev, stream);
 }
 
 size_t w4_down_workspace_bytes(int64_t T, int64_t k, int64_t H) { return (size_t)(T * k * H * 4); }
@@ -790,17 +1044,14 @@ cudaError_t launch_w4_down(const uint16_t* h, const int32_t* ids, const float* w
                            const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T,
                            int64_t H, int64_t E, int64_t k, int64_t I, int64_t group, uint16_t* y, void* ws,
                            const DeviceInfo& dev, cudaStream_t stream) {
-  W4Params p{};
-  p.rows = h;
-  p.ids = ids;
+  W4Params p = w4_params(h, ids, T, I, H, E, k, dev);
   p.part = static_cast<float*>(ws);
-  p.K = (int)I;
-  p.N = (int)H;
-  p.E = (int)E;
-  p.k = (int)k;
-  p.slots = (int)(T * k);
-  const cudaError_t err = launch_w4_group<false>(p, q, scales, zeros, group, dev, stream);
-  if (err != cudaSuccess) return err;
+  W4SlotArgs s = w4_slot_plan<false>(p, dev);
+  s.wt = wt;
+  s.y_shared = y_shared;
+  s.y = y;
+  const cudaError_t err = launch_w4_group<false>(p, s, q, scales, zeros, group, dev, stream);
+  if (err != cudaSuccess || s.per) return err;
   return launch_pdl(w4_combine_kernel, dim3((unsigned)((T * (H / 8) + kW4CombineThreads - 1) / kW4CombineThreads)),
                     dim3(kW4CombineThreads), 0, stream, 1, static_cast<const float*>(ws), ids, wt, y_shared, T, (int)E, (int)k, (int)H, y);
 }
