@@ -104,6 +104,28 @@ def test_masked_experts(score, bias, renorm):
     moe.sync_status()
 
 
+@pytest.mark.parametrize("E,k", [(256, 8), (60, 5), (250, 32), (32, 32)])
+@pytest.mark.parametrize("low,high", [(-110.0, 110.0), (-90.0, -70.0), (4.0, 20.0), (-1.0, 1.0)])
+def test_sigmoid_scores_are_the_rounded_steps(E, k, low, high):
+    """1 / (1 + exp(-z)), each step rounded to fp32, bit for bit: nearly equal
+    and saturated scores choose the experts that they choose, and the weights
+    are those scores, subnormal ones too."""
+    moe = lib()
+    rng = np.random.default_rng(E)
+    z = f32(rng.uniform(low, high, (700, E)))
+    z[::7, 3] = float("-inf")
+    s = 1 / (1 + torch.exp(-z))
+    zero = torch.zeros(E, device=dev())
+    ids, w = moe.route_select(z, k, bias=zero, score="sigmoid", renorm=False)
+    value = torch.where(z == float("-inf"), torch.full_like(s, float("-inf")), s)
+    want = torch.sort(value, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), want)
+    assert torch.equal(w, s.gather(1, want))
+    ids2, w2 = moe.route_select(z, k, score="sigmoid", renorm=False)   # chosen by the logits
+    assert torch.equal(w2, s.gather(1, ids2.long()))
+    moe.sync_status()
+
+
 def test_nan_and_infinite_logits():
     """A NaN is chosen first and its weight is NaN; ids stay distinct and in
     range; the other rows are untouched."""

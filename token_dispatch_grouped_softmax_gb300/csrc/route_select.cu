@@ -34,8 +34,23 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
-// 1 / (1 + exp(-z)), each step rounded to fp32.
-__device__ __forceinline__ float sigmoid(float z) { return __frcp_rn(1.f + expf(-z)); }
+// 1 / d rounded to nearest, for 1 <= d < 2^120: a Newton step in fused
+// multiply-adds from an approximation within a unit of the last place
+// (Markstein, IBM J. Res. Dev. 34, 1990); equal to the rounded quotient for
+// each of these floats.
+__device__ __forceinline__ float reciprocal(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return fmaf(r, fmaf(-d, r, 1.f), r);
+}
+
+// 1 / (1 + exp(-z)), each step rounded to fp32.  NEAR: z >= kNearest.
+constexpr float kNearest = -80.f;
+template <bool NEAR = false>
+__device__ __forceinline__ float sigmoid(float z) {
+  const float d = 1.f + expf(-z);
+  return NEAR || d <= 0x1p119f ? reciprocal(d) : __frcp_rn(d);
+}
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
@@ -129,10 +144,10 @@ __device__ __forceinline__ int find_candidates(const SelectParams& p, uint32_t (
 // them.  They are gathered one to a lane, and k rounds of two warp reductions
 // (the largest key, the lowest expert that has it) put them in order.  Where
 // more than 32 pass (large k, many equal keys) the rounds scan every key.
-// The instructions of a token bound it (845 at E = 256 with 8 groups, a third
-// of them the exact sigmoids): 15.7 us for 16384 tokens, where sorting each
-// lane's 8 keys took 21.3, and 3.6 us for 4096 tokens of E = 128 by softmax.
-// Finding the candidates by approximate sigmoids took 23.1 us.
+// The instructions of a token bound it: 13.9 us for 16384 tokens at E = 256
+// with 8 groups (15.6 with the library's reciprocal, 21.3 with a sort of each
+// lane's 8 keys, 23.1 with approximate sigmoids to find the candidates), and
+// 3.4 us for 4096 tokens of E = 128 by softmax.
 enum { kByLogit, kBySigmoid, kBySoftmax };   // what chooses
 
 template <int NV, bool QUADS, int MODE, typename Z>
@@ -186,14 +201,26 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_kernel(const Sele
       }
   }
   // the key of the value that chooses
-  auto choice_key = [&](float zi, float bi) {
+  auto choice_key = [&](float zi, float s, float bi) {
     if (MODE == kByLogit) return value_key(zi + 0.f);   // -0 to +0
-    const float s = MODE == kBySigmoid ? sigmoid(zi) : expf(zi - zmax) / zsum;
     return zi == neg_inf ? value_key(neg_inf) : value_key(s + bi);
   };
   uint32_t key[NV];
+  if (MODE == kBySigmoid) {
+    float low = v[0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) key[i] = step(i) < members ? choice_key(v[i], b[i]) : 0u;
+    for (int i = 1; i < NV; ++i) low = fminf(low, v[i]);
+    if (__all_sync(0xffffffffu, low >= kNearest)) {   // no masked expert, nor a place without one
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = value_key(sigmoid<true>(v[i]) + b[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = step(i) < members ? choice_key(v[i], sigmoid(v[i]), b[i]) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = step(i) < members ? choice_key(v[i], expf(v[i] - zmax) / zsum, b[i]) : 0u;
+  }
   uint2* mine = gathered[threadIdx.x >> 5];
   const int total = find_candidates<NV>(p, key, g, l, lane, [&](int i) { return (uint32_t)(first + step(i)); }, mine);
   const bool gather = NV > 1 && total <= 32;
