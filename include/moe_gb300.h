@@ -111,9 +111,10 @@ int moe_set_pdl(int on);
 
 /* Test hook of the failure-detection path: while on (1), the grouped GEMMs
  * and the 4-bit experts' kernels launched afterwards issue no operand loads,
- * so their bounded waits run out; the kernel then records MOE_ERR_TIMEOUT, stops its other
- * warps, frees its tensor memory and returns (outputs undefined), leaving
- * the context usable.  Off (0) by default; not for production use. */
+ * so their bounded waits run out; the kernel then records MOE_ERR_TIMEOUT,
+ * stops its other warps, frees its tensor memory and returns (outputs
+ * undefined), leaving the context usable.  Off (0) by default; not for
+ * production use. */
 int moe_test_stall_gemm_producer(int on);
 
 /* ------------------------------------------------------------------ route */
@@ -234,7 +235,8 @@ int moe_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, 
  *            rows r .. r+7 (r % 8 == 0) of column n, lowest nibble first
  *   scales   [E*K/group, N] bf16
  *   zeros    [E*K/group, N] bytes 0..15, or NULL for 8 everywhere
- * group is 32, 64 or 128 and divides K; K and I are multiples of 64.
+ * group is 32, 64 or 128 and divides K; K and I are multiples of 64, K and
+ * N at most 2^20, E at most 1024, k at most 32 (MOE_ERR_UNSUPPORTED beyond).
  *
  * Slots: ids [T, k] int32 names the expert of slot (t, j); the rows of h are
  * in slot order (no permutation).  An id of -1 is an empty slot (a padded
@@ -254,7 +256,7 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
 /* y[t] = sum_j w[t,j] (h[t,j] . Wd) (+ y_shared[t]), summed in fp32 in
  * increasing j.  h [T, k, I] bf16; w [T, k] fp32 (NULL: weight 1); y_shared
  * [T, H] bf16 or NULL; y [T, H] bf16 (out).  The workspace holds the slots'
- * fp32 products. */
+ * fp32 products (a call of few slots does without). */
 int moe_w4_down_workspace_size(int64_t T, int64_t H, int64_t k, size_t* bytes);
 int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
                         const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
