@@ -64,7 +64,7 @@ def _build_binding(verbose):
            "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
            "-I" + sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp,
-           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("%s failed on %s:\n%s\n%s" % (cmd[0], BINDING_SRC, r.stdout, r.stderr))
