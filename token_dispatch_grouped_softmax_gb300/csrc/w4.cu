@@ -112,9 +112,15 @@ __device__ __forceinline__ uint64_t w4_lists(const W4Params& p, int slot0, int s
   auto packed = [](int n) { return (uint64_t)n | 1ull << 20 | (uint64_t)((n + kW4Rows - 1) / kW4Rows) << 40; };
   auto rows_of = [&](int e) {
     int n = 0;
-    for (int w = 0; w < words; ++w) {
-      before_word[e * stride + w] = (uint16_t)n;
-      n += __popc(bits[e * stride + w]);
+    for (int w0 = 0; w0 < words; w0 += 8) {   // eight loads in flight
+      uint32_t word[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) word[i] = w0 + i < words ? bits[e * stride + w0 + i] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (w0 + i < words) before_word[e * stride + w0 + i] = (uint16_t)n;
+        n += __popc(word[i]);
+      }
     }
     return n;
   };
