@@ -52,11 +52,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Codes i and i + 4 of a word plus 128, as two bf16: 128 + code is 0x4300 |
-// code.  One lop3 with the shift before it: (a & b) | c is table 0xEA.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
+// Codes i and i + 4 of a word less their zero, as two bf16: 128 + code is
+// 0x4300 | code (one lop3 with the shift before it: (a & b) | c is table
+// 0xEA), and `offset`, 128 + zero twice, comes off exactly.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t offset) {
   uint32_t v;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(offset));
   return v;
 }
 
@@ -254,14 +256,14 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
 // x.  A rows are weight columns (two tiles a half), B columns the expert's
 // rows.
 //
-// The codes go into the mma as 128 + q, an or with no subtraction; the sum
-// over the group of (128 + zero) x, from one more mma with a tile of ones, is
-// taken off before the scale: sum (q - zero) x = sum (128 + q) x - (128 +
-// zero) sum x.  Every product is exact; the fp32 sums round at 128 + q
-// instead of q - zero, some 2^-19 of the terms, 2^10 below the bf16 result.
+// The codes go into the mma as q - zero, exact in bf16: every product is
+// exact, and the fp32 sums round at the size of the formula's own terms.
+// (128 + q in the mma, an or with no subtraction, and (128 + zero) sum x taken
+// off a group's sum rounds at 136 |x|, also where q equals the zero; one large
+// x there loses the rest.)
 //
 // Bound by the stream of the codes where it is long: 32 tokens, top-8 of 256,
-// H 7168, I 2048, groups of 128: gate_up 438 us (5.65 TB/s), down 229 (5.4).
+// H 7168, I 2048, groups of 128: gate_up 458 us (5.40 TB/s), down 232 (5.33).
 // 45 tokens, top-8 of 128, H 2048, I 768, groups of 64 with zeros: 50 us (4.1)
 // and 34 (3.0) with start, end and latency: 16 warps an SM, ALU pipe 57 %.
 template <int GROUP, bool ZEROS>
@@ -288,7 +290,7 @@ __host__ __device__ constexpr int w4_smem(int E, int slots) {
 template <int GROUP, bool ZEROS, int SETS>
 __device__ __forceinline__ void w4_unit(float (&tot)[SETS][2][4], uint4 (&xn)[2], const uint16_t* x, int& next_k, int K, int k0,
                                         uint32_t q_at, const uint8_t* scales, const uint8_t* zeros) {
-  float acc[SETS][2][4], sum[4];
+  float acc[SETS][2][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {   // 64 k each; K may end after the first
     if (j == 1 && k0 + 64 >= K) break;
@@ -311,10 +313,7 @@ __device__ __forceinline__ void w4_unit(float (&tot)[SETS][2][4], uint4 (&xn)[2]
     for (int i = 0; i < 2; ++i) {   // 32 k each
       const bool first = GROUP == 32 || (GROUP == 64 && i == 0) || (GROUP == 128 && i == 0 && j == 0);
       const bool last = GROUP == 32 || (GROUP == 64 && i == 1) || (GROUP == 128 && i == 1 && j == 1);
-      const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-      if (first) mma_16816_first(sum, ones, b[i][0], b[i][1]);
-      else mma_16816(sum, ones, b[i][0], b[i][1]);
-      mma_16816(sum, ones, b[i][2], b[i][3]);
+      const int row = GROUP == 32 ? 2 * j + i : GROUP == 64 ? j : 0;
 #pragma unroll
       for (int set = 0; set < SETS; ++set) {
         const uint32_t at = SETS == 2 ? (set ? (q_at ^ 16) + 128 : q_at) + (2 * j + i) * 1024 : (q_at ^ i << 6) + (2 * j + i) * 512;
@@ -322,32 +321,35 @@ __device__ __forceinline__ void w4_unit(float (&tot)[SETS][2][4], uint4 (&xn)[2]
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
                      : "r"(at));
+        uint32_t off[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};   // of the lane's four columns
+        if (ZEROS) {
+          const uint32_t zr = *reinterpret_cast<const uint32_t*>(zeros + (row * SETS + set) * 32);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) off[c] = __byte_perm(zr, 0x43u, 0x4040 | c << 8 | c);
+        }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st), w4_pair(word[2 * hf + 1], 2 * st),
-                                   w4_pair(word[2 * hf], 2 * st + 1), w4_pair(word[2 * hf + 1], 2 * st + 1)};
+            const uint32_t w[4] = {w4_pair(word[2 * hf], 2 * st, off[2 * hf]), w4_pair(word[2 * hf + 1], 2 * st, off[2 * hf + 1]),
+                                   w4_pair(word[2 * hf], 2 * st + 1, off[2 * hf]),
+                                   w4_pair(word[2 * hf + 1], 2 * st + 1, off[2 * hf + 1])};
             if (st == 0 && first) mma_16816_first(acc[set][hf], w, b[i][0], b[i][1]);
             else mma_16816(acc[set][hf], w, b[i][2 * st], b[i][2 * st + 1]);
           }
       }
       if (last) {
-        const int row = GROUP == 32 ? 2 * j + i : GROUP == 64 ? j : 0;
 #pragma unroll
         for (int set = 0; set < SETS; ++set) {
           const uint2 sr = *reinterpret_cast<const uint2*>(scales + (row * SETS + set) * 64);
-          uint32_t zr = 0;
-          if (ZEROS) zr = *reinterpret_cast<const uint32_t*>(zeros + (row * SETS + set) * 32);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {   // the lane's four columns
             const uint32_t sp = c < 2 ? sr.x : sr.y;
             const float scale = (c & 1) ? bf16_hi(sp) : bf16_lo(sp);
-            const float zero = ZEROS ? __uint_as_float(__byte_perm(zr, 0x43000000u, 0x7044 | c << 8)) : 136.f;   // 128 + zero: 0x43zz0000
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float& o = tot[set][c >> 1][(c & 1) * 2 + r];
-              o = fmaf(scale, fmaf(-zero, sum[r], acc[set][c >> 1][(c & 1) * 2 + r]), o);
+              o = fmaf(scale, acc[set][c >> 1][(c & 1) * 2 + r], o);
             }
           }
         }
