@@ -1,0 +1,50 @@
+"""moe_forward_w4 at batches of more rows per expert than its limit for the
+bf16 grouped GEMMs, with and without it."""
+import pytest
+import torch
+
+from gpu_helpers import dev, lib
+from test_gpu_routing_layer import layer_inputs
+
+pytestmark = pytest.mark.gpu
+
+H, E, K_TOKEN, I, I_SHARED = 256, 8, 2, 128, 192
+
+
+def layer(moe, T):
+    d, s = layer_inputs(T, T, H, E, I), layer_inputs(T + 1, T, H, 1, I_SHARED)
+    return (d, moe.W4Experts.quantize(d["gate_up"], d["down"], E, 64),
+            moe.W4Experts.quantize(s["gate_up"], s["down"], 1, 64, zeros=True))
+
+
+def test_a_token_of_the_layer_does_not_depend_on_the_batch():
+    """100 rows per expert and 400 of the shared one: each token's bits are
+    those that it has alone, or among few."""
+    moe = lib()
+    T = 400
+    d, experts, shared = layer(moe, T)
+    routing = moe.Routing(score="sigmoid", n_groups=4, top_groups=2)
+    kw = dict(shared=shared, routing=routing, balance_bias=d["bias"])
+    y, ids, w = moe.moe_forward_w4(d["x"], d["wr"], experts, K_TOKEN, **kw)
+    for a, b in ((0, 1), (5, 12), (100, 164), (399, 400)):
+        yp, idp, wp = moe.moe_forward_w4(d["x"][a:b].contiguous(), d["wr"], experts, K_TOKEN, **kw)
+        assert torch.equal(idp, ids[a:b]) and torch.equal(wp, w[a:b]) and torch.equal(yp, y[a:b])
+    moe.sync_status()
+
+
+@pytest.mark.parametrize("T", (13, 110, 400))
+def test_bf16_rows_of_routed_experts(T):
+    """With a limit of 48 rows per expert, which 400 tokens pass: bit for bit
+    the 4-bit kernels, or moe_forward on the decoded weights."""
+    moe = lib()
+    d, experts, _ = layer(moe, T)
+    limit = moe.layer.W4_MAX_ROWS_PER_EXPERT
+    y, ids, w = moe.moe_forward_w4(d["x"], d["wr"], experts, K_TOKEN, bf16_rows=limit)
+    if T * K_TOKEN > limit * E:
+        want, _ = moe.moe_forward(d["x"], d["wr"], *experts.dequantize(), K_TOKEN)
+    else:
+        want = moe.w4_down_combine(moe.w4_gate_up_swiglu(d["x"], ids, *experts.gate_up), ids, w, *experts.down)
+    assert torch.equal(y, want)
+    g = moe.DecodeGraph(T, d["wr"], experts, K_TOKEN, bf16_rows=limit)
+    assert torch.equal(g(d["x"]), y)
+    moe.sync_status()

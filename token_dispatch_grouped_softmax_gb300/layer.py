@@ -264,18 +264,31 @@ class W4Experts:
 
 # From this many rows an expert on, the 4-bit kernels' chunks of 8 rows (each
 # of which decodes the weights again) cost more than one decoding to bf16 and
-# the bf16 grouped GEMMs: measured equal at 45 rows (H 2048, E 128, I 768) and
-# 57 (H 4096, E 8, I 2048).
+# the bf16 grouped GEMMs: measured equal at 48 rows (H 2048, E 128, I 768), 51
+# (H 4096, E 8, I 2048) and 32 (H 7168, E 256, I 2048).  A value for
+# moe_forward_w4's bf16_rows.
 W4_MAX_ROWS_PER_EXPERT = 48
 
 
-def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None, routing=None, balance_bias=None):
-    """y [T, H] bf16 of a decode batch through 4-bit experts (W4Experts), and the slots' ids and w.
+def _bf16_experts(x, gate_up, down, offsets=None):
+    """x's rows (permuted, or with offsets None all of one expert's) through bf16 weights."""
+    h, _, _ = ops.grouped_gemm_gate_up_swiglu(x, None, offsets, gate_up, gate_up.shape[1] // 2)
+    return ops.grouped_gemm_down(h, offsets, down, x.shape[1])
+
+
+def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None, routing=None, balance_bias=None,
+                   bf16_rows=None):
+    """y [T, H] bf16 through 4-bit experts (W4Experts), and the slots' ids and w.
 
     route -> gate_up + SwiGLU -> down + combine, rows in slot order with no
-    permutation.  shared: a W4Experts of one expert, always active.  A batch
-    of more than W4_MAX_ROWS_PER_EXPERT rows per expert decodes the weights to
-    bf16 for this call and runs moe_forward's grouped GEMMs on them."""
+    permutation; a token's result does not depend on the batch.  shared: a
+    W4Experts of one expert, always active.
+
+    bf16_rows: where there are more rows per expert (T*k / E) than this, decode
+    the weights to bf16 for the call and run moe_forward's grouped GEMMs on
+    them.  That is faster from
+    W4_MAX_ROWS_PER_EXPERT on and less exact: the weights and each slot's
+    product are rounded to bf16.  None: never."""
     T, H = x.shape
     E = experts.n_experts
     if w_router.shape[1] != E:
@@ -286,16 +299,13 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
     if shared is not None:
         with _range("moe.shared_expert"):
             y_shared = ops.w4_down_combine(ops.w4_gate_up_swiglu(x, None, *shared.gate_up), None, None, *shared.down)
-    if T * k > W4_MAX_ROWS_PER_EXPERT * E:
-        gate_up, down = experts.dequantize()
+    if bf16_rows is not None and T * k > bf16_rows * E:
         with _range("moe.permute"):
             _, offsets, row_map, _ = ops.permute(ids, E)
         with _range("moe.permute_rows"):
             x_perm = ops.permute_rows_scatter(x, row_map, k)
-        with _range("moe.gate_up"):
-            h, _, _ = ops.grouped_gemm_gate_up_swiglu(x_perm, None, offsets, gate_up, down.shape[0] // E)
-        with _range("moe.down"):
-            y_perm = ops.grouped_gemm_down(h, offsets, down, H)
+        with _range("moe.experts"):
+            y_perm = _bf16_experts(x_perm, *experts.dequantize(), offsets)
         with _range("moe.combine"):
             return ops.unpermute_combine(y_perm, row_map, w, y_shared), ids, w
     with _range("moe.gate_up"):
@@ -312,10 +322,10 @@ class DecodeGraph:
     routing.  As ForwardGraph, it makes W_r's bf16 split once
     (``refresh_router_split()`` after changing W_r)."""
 
-    def __init__(self, T, w_router, experts, k, bias=None, shared=None, routing=None, balance_bias=None):
+    def __init__(self, T, w_router, experts, k, bias=None, shared=None, routing=None, balance_bias=None, bf16_rows=None):
         H, E = w_router.shape
         self.args = (w_router, experts, k, bias, shared)
-        self.routing, self.balance_bias = routing, balance_bias
+        self.routing, self.balance_bias, self.bf16_rows = routing, balance_bias, bf16_rows
         self.w_split = ops.route_split_weight(w_router) if ops.route_supports_split(H, E) else None
         self.x = torch.zeros((T, H), dtype=torch.bfloat16, device=w_router.device)
         side = torch.cuda.Stream()
@@ -330,7 +340,7 @@ class DecodeGraph:
 
     def _forward(self):
         return moe_forward_w4(self.x, *self.args, w_split=self.w_split, routing=self.routing,
-                              balance_bias=self.balance_bias)
+                              balance_bias=self.balance_bias, bf16_rows=self.bf16_rows)
 
     def refresh_router_split(self):
         """Re-derives W_r's split (in place, where the graph reads it) after W_r changed."""
