@@ -48,3 +48,30 @@ def test_bf16_rows_of_routed_experts(T):
     g = moe.DecodeGraph(T, d["wr"], experts, K_TOKEN, bf16_rows=limit)
     assert torch.equal(g(d["x"]), y)
     moe.sync_status()
+
+
+@pytest.mark.parametrize("T", (13, 110, 400))
+def test_bf16_rows(T):
+    """With a limit of 48 rows per expert: 13 tokens stay under it, at 110 the
+    shared expert's rows pass twice that, at 400 all do; either side is, bit for bit,
+    the 4-bit kernels or moe_forward on the decoded weights."""
+    moe = lib()
+    d, experts, shared = layer(moe, T)
+    limit = moe.layer.W4_MAX_ROWS_PER_EXPERT
+    y, ids, w = moe.moe_forward_w4(d["x"], d["wr"], experts, K_TOKEN, shared=shared, bf16_rows=limit)
+    sh_gate_up, sh_down = shared.dequantize()
+    if T * K_TOKEN > limit * E:
+        want, st = moe.moe_forward(d["x"], d["wr"], *experts.dequantize(), K_TOKEN, sh_gate_up=sh_gate_up, sh_down=sh_down)
+        assert torch.equal(ids, st.ids) and torch.equal(w, st.w)
+    else:
+        if T > 2 * limit:
+            hs, _, _ = moe.grouped_gemm_gate_up_swiglu(d["x"], None, None, sh_gate_up, I_SHARED)
+            ys = moe.grouped_gemm_down(hs, None, sh_down, H)
+        else:
+            ys = moe.w4_down_combine(moe.w4_gate_up_swiglu(d["x"], None, *shared.gate_up), None, None, *shared.down)
+        h = moe.w4_gate_up_swiglu(d["x"], ids, *experts.gate_up)
+        want = moe.w4_down_combine(h, ids, w, *experts.down, y_shared=ys)
+    assert torch.equal(y, want)
+    g = moe.DecodeGraph(T, d["wr"], experts, K_TOKEN, shared=shared, bf16_rows=limit)
+    assert torch.equal(g(d["x"]), y)
+    moe.sync_status()

@@ -286,7 +286,7 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
 
     bf16_rows: where there are more rows per expert (T*k / E) than this, decode
     the weights to bf16 for the call and run moe_forward's grouped GEMMs on
-    them.  That is faster from
+    them, and the shared expert's from twice as many tokens on.  That is faster from
     W4_MAX_ROWS_PER_EXPERT on and less exact: the weights and each slot's
     product are rounded to bf16.  None: never."""
     T, H = x.shape
@@ -298,7 +298,10 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
     y_shared = None
     if shared is not None:
         with _range("moe.shared_expert"):
-            y_shared = ops.w4_down_combine(ops.w4_gate_up_swiglu(x, None, *shared.gate_up), None, None, *shared.down)
+            if bf16_rows is not None and T > 2 * bf16_rows:   # one expert's launches: equal at 95 (I 2048) to 250 rows (H 2048, I 768)
+                y_shared = _bf16_experts(x, *shared.dequantize())
+            else:
+                y_shared = ops.w4_down_combine(ops.w4_gate_up_swiglu(x, None, *shared.gate_up), None, None, *shared.down)
     if bf16_rows is not None and T * k > bf16_rows * E:
         with _range("moe.permute"):
             _, offsets, row_map, _ = ops.permute(ids, E)
