@@ -75,3 +75,26 @@ def test_bf16_rows(T):
     g = moe.DecodeGraph(T, d["wr"], experts, K_TOKEN, shared=shared, bf16_rows=limit)
     assert torch.equal(g(d["x"]), y)
     moe.sync_status()
+
+
+def test_memory_of_the_decoded_weights():
+    """gate_up's bf16 weights are released before down's are made: the call's
+    peak stays under the two together."""
+    moe = lib()
+    T, H_, E_, I_ = 512, 1024, 64, 512
+    g = torch.Generator(device=dev()).manual_seed(1)
+    bf = lambda *s: (0.03 * torch.randn(s, generator=g, device=dev())).bfloat16()
+    gate_up, down = bf(E_ * H_, 2 * I_), bf(E_ * I_, H_)
+    both = (gate_up.numel() + down.numel()) * 2
+    experts = moe.W4Experts.quantize(gate_up, down, E_)
+    del gate_up, down
+    x, wr = bf(T, H_), bf(H_, E_).float()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    moe.moe_forward_w4(x, wr, experts, 8, bf16_rows=0)
+    moe.sync_status()
+    rows = T * 8
+    activations = 2 * (2 * rows * H_ + rows * I_ + 2 * T * H_) + 4 * T * E_ + (8 << 20)
+    assert torch.cuda.max_memory_allocated() - before < both * 2 // 3 + activations < both + activations

@@ -270,10 +270,13 @@ class W4Experts:
 W4_MAX_ROWS_PER_EXPERT = 48
 
 
-def _bf16_experts(x, gate_up, down, offsets=None):
-    """x's rows (permuted, or with offsets None all of one expert's) through bf16 weights."""
-    h, _, _ = ops.grouped_gemm_gate_up_swiglu(x, None, offsets, gate_up, gate_up.shape[1] // 2)
-    return ops.grouped_gemm_down(h, offsets, down, x.shape[1])
+def _decoded_experts(x, gate_up, down, offsets=None):
+    """x's rows (permuted, or with offsets None all of one expert's) through
+    4-bit weights that are decoded to bf16, one of the two at a time."""
+    weight = ops.w4_dequantize(*gate_up)
+    h, _, _ = ops.grouped_gemm_gate_up_swiglu(x, None, offsets, weight, weight.shape[1] // 2)
+    del weight
+    return ops.grouped_gemm_down(h, offsets, ops.w4_dequantize(*down), x.shape[1])
 
 
 def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None, routing=None, balance_bias=None,
@@ -288,7 +291,8 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
     the weights to bf16 for the call and run moe_forward's grouped GEMMs on
     them, and the shared expert's from twice as many tokens on.  That is faster from
     W4_MAX_ROWS_PER_EXPERT on and less exact: the weights and each slot's
-    product are rounded to bf16.  None: never."""
+    product are rounded to bf16.  It takes the larger of gate_up's E*H*2I and
+    down's E*I*H bf16 weights of memory for the call.  None: never."""
     T, H = x.shape
     E = experts.n_experts
     if w_router.shape[1] != E:
@@ -299,7 +303,7 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
     if shared is not None:
         with _range("moe.shared_expert"):
             if bf16_rows is not None and T > 2 * bf16_rows:   # one expert's launches: equal at 95 (I 2048) to 250 rows (H 2048, I 768)
-                y_shared = _bf16_experts(x, *shared.dequantize())
+                y_shared = _decoded_experts(x, shared.gate_up, shared.down)
             else:
                 y_shared = ops.w4_down_combine(ops.w4_gate_up_swiglu(x, None, *shared.gate_up), None, None, *shared.down)
     if bf16_rows is not None and T * k > bf16_rows * E:
@@ -308,7 +312,7 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
         with _range("moe.permute_rows"):
             x_perm = ops.permute_rows_scatter(x, row_map, k)
         with _range("moe.experts"):
-            y_perm = _bf16_experts(x_perm, *experts.dequantize(), offsets)
+            y_perm = _decoded_experts(x_perm, experts.gate_up, experts.down, offsets)
         with _range("moe.combine"):
             return ops.unpermute_combine(y_perm, row_map, w, y_shared), ids, w
     with _range("moe.gate_up"):
