@@ -215,7 +215,9 @@ class MoELayer(torch.nn.Module):
     """Routed SwiGLU experts over the fused layout gate_up [E*H, 2I], down [E*I, H].
 
     routing: a Routing; the layer then holds a balance bias (a buffer, zeros at
-    first) that update_balance_bias moves by the loads of the last forward."""
+    first) that update_balance_bias moves by the loads of the last forward.  A
+    Routing with a dense gradient (softmax without renorm) runs where no
+    gradient is asked for and is refused where one is."""
 
     def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, device="cuda", routing=None):
         super().__init__()
@@ -232,8 +234,14 @@ class MoELayer(torch.nn.Module):
 
     def forward(self, x, bias=None):
         if self.routing is not None:
-            y, self.last_counts = RoutedMoELayerFunction.apply(x, self.w_router, self.gate_up, self.down, self.k, bias,
-                                                               self.routing, self.balance_bias)
+            weights = (self.w_router, self.gate_up, self.down)
+            if torch.is_grad_enabled() and any(t.requires_grad for t in (x,) + weights):
+                y, self.last_counts = RoutedMoELayerFunction.apply(x, *weights, self.k, bias, self.routing,
+                                                                   self.balance_bias)
+            else:   # nothing is kept for a backward, and a Routing with a dense gradient runs too
+                y, st = moe_forward(x.contiguous(), *(t.contiguous() for t in weights), self.k, bias,
+                                    routing=self.routing, balance_bias=self.balance_bias)
+                self.last_counts = st.counts
             return y
         return MoELayerFunction.apply(x, self.w_router, self.gate_up, self.down, self.k, bias)
 
