@@ -48,3 +48,26 @@ def test_inference(routing):
     layer.update_balance_bias(0.5)
     assert torch.equal(layer.balance_bias, moe.route_balance_bias(before, st.counts, 0.5))
     moe.sync_status()
+
+
+def test_without_a_balance_bias():
+    """balance=False: no bias, and the choice that moe_forward makes without one,
+    by the logits: logits whose scores round to the same value keep their order."""
+    moe = lib()
+    d = layer_inputs(5, T, H, E, I)
+    d["x"][:, 0] = 2.0
+    d["wr"][:, :] *= 0.01
+    d["wr"][0] = 10.0 + 2.0 ** -8 * torch.arange(E, device=dev())   # logits of 20 and more: every sigmoid is 1
+    how = moe.Routing(score="sigmoid")
+    layer = module(moe, d, routing=how, balance=False)
+    want, st = moe.moe_forward(d["x"], d["wr"], d["gate_up"], d["down"], K_TOKEN, routing=how)
+    assert bool((st.ids > 7).all())                                 # equal scores would take the lowest experts
+    assert torch.equal(layer(d["x"]).detach(), want)
+    assert "balance_bias" not in dict(layer.named_buffers())
+    with pytest.raises(ValueError):
+        layer.update_balance_bias(0.1)
+    with torch.no_grad():
+        assert torch.equal(layer(d["x"]), want)
+    with pytest.raises(ValueError):
+        moe.MoELayer(H, E, K_TOKEN, I, device=dev(), balance=False)
+    moe.sync_status()

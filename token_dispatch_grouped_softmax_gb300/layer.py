@@ -215,16 +215,22 @@ class MoELayer(torch.nn.Module):
     """Routed SwiGLU experts over the fused layout gate_up [E*H, 2I], down [E*I, H].
 
     routing: a Routing; the layer then holds a balance bias (a buffer, zeros at
-    first) that update_balance_bias moves by the loads of the last forward.  A
+    first) that update_balance_bias moves by the loads of the last forward.
+    With a bias, of zeros too, the rounded scores plus the bias choose;
+    balance=False holds none, and where the scores order the experts as the
+    logits do, the logits choose, as in moe_forward without a bias.  A
     Routing with a dense gradient (softmax without renorm) runs where no
     gradient is asked for and is refused where one is."""
 
-    def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, device="cuda", routing=None):
+    def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, device="cuda", routing=None, balance=True):
         super().__init__()
+        if routing is None and not balance:
+            raise ValueError("balance=False needs a Routing")
         self.k = top_k
         self.routing = routing
         if routing is not None:
-            self.register_buffer("balance_bias", torch.zeros(n_experts, dtype=torch.float32, device=device))
+            bias = torch.zeros(n_experts, dtype=torch.float32, device=device) if balance else None
+            self.register_buffer("balance_bias", bias)
             self.last_counts = None
         self.w_router = torch.nn.Parameter(torch.empty(hidden, n_experts, dtype=torch.float32, device=device))
         self.gate_up = torch.nn.Parameter(torch.empty(n_experts * hidden, 2 * inter, dtype=torch.bfloat16,
@@ -247,8 +253,8 @@ class MoELayer(torch.nn.Module):
 
     def update_balance_bias(self, rate):
         """balance_bias += rate * sign(mean load - load) by the last forward's loads."""
-        if self.routing is None or self.last_counts is None:
-            raise ValueError("update_balance_bias needs a layer with a Routing after a forward")
+        if self.routing is None or self.balance_bias is None or self.last_counts is None:
+            raise ValueError("update_balance_bias needs a layer with a Routing and a balance bias, after a forward")
         ops.route_balance_bias(self.balance_bias, self.last_counts, rate, out=self.balance_bias)
 
 
