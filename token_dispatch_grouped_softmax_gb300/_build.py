@@ -3,8 +3,10 @@
 Each .cu file is compiled in parallel into _build/, then linked into a shared
 library next to this file.  The CUDA runtime is linked as a shared library so
 the process shares one runtime (current device, streams) with PyTorch.  Beside
-it _binding.so is built from csrc/binding.cpp with the host compiler: the
-Python extension of the calls of a decode step.
+it the Python extension of the calls of a decode step is built from
+csrc/binding.cpp with the host compiler, against Python's and torch's headers;
+its file's name holds both versions, so that another torch or Python builds
+its own.
 """
 from __future__ import annotations
 
@@ -20,7 +22,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,8 +45,15 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def binding_path() -> str:
+    """The extension's file, of this Python and this torch."""
+    import torch
+
+    return os.path.join(PKG, "_binding-%s%s" % (torch.__version__, sysconfig.get_config_var("EXT_SUFFIX")))
+
+
 def up_to_date() -> bool:
-    for out, deps in ((LIB, _deps()), (BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
+    for out, deps in ((LIB, _deps()), (binding_path(), [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
         if not os.path.exists(out):
             return False
         t = os.path.getmtime(out)
@@ -58,7 +66,8 @@ def _build_binding(verbose):
     import torch
 
     root = os.path.dirname(os.path.abspath(torch.__file__))
-    tmp = BINDING + ".%d.tmp" % os.getpid()
+    out = binding_path()
+    tmp = out + ".%d.tmp" % os.getpid()
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
            "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -70,11 +79,11 @@ def _build_binding(verbose):
         raise RuntimeError("%s failed on %s:\n%s\n%s" % (cmd[0], BINDING_SRC, r.stdout, r.stderr))
     if verbose and (r.stdout or r.stderr):
         print(r.stdout, r.stderr)
-    os.replace(tmp, BINDING)
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libmoe_gb300.so and _binding.so when missing or older than their sources."""
+    """Compile and link libmoe_gb300.so and the extension when missing or older than their sources."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -94,7 +103,6 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(compile_one, srcs))
-        binding.result()
     tmp = LIB + ".%d.tmp" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + \
         ["-Xlinker", "-rpath=/usr/local/cuda/lib64"]
@@ -102,6 +110,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    binding.result()   # the library needs no torch: it is there even where the extension failed
     return LIB
 
 

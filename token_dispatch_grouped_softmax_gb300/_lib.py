@@ -7,6 +7,7 @@ raises.  Build it with ``token_dispatch_grouped_softmax_gb300.build()`` (or
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import _build
@@ -111,7 +112,13 @@ def binding():
     global _binding
     if _binding is None:
         lib = load()
-        from . import _binding as ext
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError("the Python extension is not built for this Python and torch (%s); run "
+                               "token_dispatch_grouped_softmax_gb300.build()" % path)
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
         ext.bind(check, *(ctypes.cast(getattr(lib, name), P).value for name in (
             "moe_route_select", "moe_route_select_bwd", "moe_route_balance_bias", "moe_w4_gate_up_swiglu",
             "moe_w4_down_workspace_size", "moe_w4_down_combine")))
