@@ -417,9 +417,10 @@ __global__ void __launch_bounds__(32 * kSelWarps) route_select_bwd_kernel(const 
 
 // b_e += rate * sign(mean load - load_e), decided in integers: the sign of
 // sum(counts) - E * counts_e.  A launch's latency (3.3 us from cold caches).
-__global__ void __launch_bounds__(kMaxExperts) route_balance_bias_kernel(const float* __restrict__ bias,
+// out may be bias.
+__global__ void __launch_bounds__(kMaxExperts) route_balance_bias_kernel(const float* bias,
                                                                          const int32_t* __restrict__ counts, int E,
-                                                                         float rate, float* __restrict__ out) {
+                                                                         float rate, float* out) {
   pdl_wait();
   pdl_trigger();
   __shared__ long long part[32];
