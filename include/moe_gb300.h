@@ -255,8 +255,9 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
 
 /* y[t] = sum_j w[t,j] (h[t,j] . Wd) (+ y_shared[t]), summed in fp32 in
  * increasing j.  h [T, k, I] bf16; w [T, k] fp32 (NULL: weight 1); y_shared
- * [T, H] bf16 or NULL; y [T, H] bf16 (out).  The workspace holds the slots'
- * fp32 products (a call of few slots does without). */
+ * [T, H] bf16 or NULL; y [T, H] bf16 (out).  The workspace, for the slots'
+ * fp32 products, is needed by every call with T > 0 (MOE_ERR_WORKSPACE), also
+ * where the slots are so few that their products stay on chip. */
 int moe_w4_down_workspace_size(int64_t T, int64_t H, int64_t k, size_t* bytes);
 int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, const uint32_t* qweight,
                         const uint16_t* scales, const uint8_t* zeros, const uint16_t* y_shared, int64_t T, int64_t H,
@@ -267,8 +268,8 @@ int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, c
  * back.  zeros NULL: scale = bf16(max|W| / 7) of each group, codes
  * clamp(rint(W / scale) + 8, 0, 15).  With zeros: scale = bf16((max(W, 0) -
  * min(W, 0)) / 15), zero = min(rint(-min(W, 0) / scale), 15), codes
- * clamp(rint(W / scale) + zero, 0, 15).  A group of zeros has scale 0.  The weights
- * must be finite.  Dequantised: scale * (q - zero) rounded to bf16. */
+ * clamp(rint(W / scale) + zero, 0, 15).  A group of zeros has scale 0.  The weights,
+ * and max - min of a group in fp32, must be finite.  Dequantised: scale * (q - zero) rounded to bf16. */
 int moe_w4_quantize(const uint16_t* weight, int64_t rows, int64_t N, int64_t group, uint32_t* qweight,
                     uint16_t* scales, uint8_t* zeros, void* stream);
 int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t N,
