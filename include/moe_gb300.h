@@ -237,6 +237,8 @@ int moe_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, 
  *   zeros    [E*K/group, N] bytes 0..15, or NULL for 8 everywhere
  * group is 32, 64 or 128 and divides K; K and I are multiples of 64, K and
  * N at most 2^20, E at most 1024, k at most 32 (MOE_ERR_UNSUPPORTED beyond).
+ * A call takes 19 million slots T*k, and up to 134 million for few experts
+ * (MOE_ERR_UNSUPPORTED beyond).
  *
  * Slots: ids [T, k] int32 names the expert of slot (t, j); the rows of h are
  * in slot order (no permutation).  An id of -1 is an empty slot (a padded

@@ -287,7 +287,8 @@ int moe_w4_gate_up_swiglu(const uint16_t* x, const int32_t* ids, const uint32_t*
   if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
   const int rc0 = w4_check(qweight, scales, E, H, 2 * I, group);
   if (rc0 != MOE_OK) return rc0;
-  if (E > moe::kMaxExperts || H > (int64_t)1 << 20 || k > 32 || I % 64 != 0) return MOE_ERR_UNSUPPORTED;
+  if (E > moe::kMaxExperts || H > (int64_t)1 << 20 || k > 32 || I % 64 != 0 || T * k > moe::w4_max_slots(E, k))
+    return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!x || !h || !aligned16(x) || !aligned16(h) || !aligned16(zeros))) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   moe::DeviceInfo dev;
@@ -311,7 +312,7 @@ int moe_w4_down_combine(const uint16_t* h, const int32_t* ids, const float* w, c
   if (!ids && T > 0 && (E != 1 || k != 1)) return MOE_ERR_INVALID_ARG;
   const int rc0 = w4_check(qweight, scales, E, I, H, group);
   if (rc0 != MOE_OK) return rc0;
-  if (E > moe::kMaxExperts || I > (int64_t)1 << 20 || k > 32) return MOE_ERR_UNSUPPORTED;
+  if (E > moe::kMaxExperts || I > (int64_t)1 << 20 || k > 32 || T * k > moe::w4_max_slots(E, k)) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!h || !y || !aligned16(h) || !aligned16(y) || !aligned16(zeros) || !aligned16(y_shared)))
     return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < moe::w4_down_workspace_bytes(T, k, H)))

@@ -125,7 +125,9 @@ cudaError_t launch_route_select_bwd(const float* dw_part, int nparts, const int3
 cudaError_t launch_route_balance_bias(const float* bias, const int32_t* counts, int64_t E, float rate, float* out,
                                       cudaStream_t stream);
 
-// 4-bit experts of a decode batch (w4.cu).
+// 4-bit experts of a decode batch (w4.cu).  w4_max_slots: the most slots of one
+// call, for E and k within the kernels' own limits.
+int64_t w4_max_slots(int64_t E, int64_t k);
 cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint32_t* q, const uint16_t* scales,
                               const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I,
                               int64_t group, uint16_t* h, const DeviceInfo& dev, cudaStream_t stream);

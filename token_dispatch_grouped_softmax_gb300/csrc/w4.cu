@@ -938,6 +938,8 @@ cudaError_t launch_w4_group(W4Params& p, const W4SlotArgs& s, const uint32_t* q,
   return zeros ? launch_w4<GATE_UP, 128, true>(p, s, dev, stream) : launch_w4<GATE_UP, 128, false>(p, s, dev, stream);
 }
 
+int w4_slots_per_row(int E, int k) { return w4_row_slots(E, k, kW4MaxSlots, W4Ring<128, false>::kBytes); }
+
 // The call's sizes, K's parts, and the device.
 W4Params w4_params(const uint16_t* rows, const int32_t* ids, int64_t T, int64_t K, int64_t N, int64_t E, int64_t k,
                    const DeviceInfo& dev) {
@@ -952,7 +954,7 @@ W4Params w4_params(const uint16_t* rows, const int32_t* ids, int64_t T, int64_t 
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
   p.stall = dev.test_stall_producer;
-  p.slots_per_row = w4_row_slots(p.E, p.k, kW4MaxSlots, W4Ring<128, false>::kBytes);
+  p.slots_per_row = w4_slots_per_row(p.E, p.k);
   p.blocks = (int)(N / 64);
   const int units = (p.K + 127) / 128;
   p.parts_log2 = units >= 32 ? 3 : units >= 4 ? 2 : units >= 2 ? 1 : 0;
@@ -1045,6 +1047,8 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
 }
 
 }  // namespace
+
+int64_t w4_max_slots(int64_t E, int64_t k) { return 65535ll * w4_slots_per_row((int)E, (int)k); }   // launch rows of a grid
 
 cudaError_t launch_w4_gate_up(const uint16_t* x, const int32_t* ids, const uint32_t* q, const uint16_t* scales,
                               const uint8_t* zeros, int64_t T, int64_t H, int64_t E, int64_t k, int64_t I,
