@@ -188,7 +188,8 @@ int moe_route_presplit(const uint16_t* x, const uint16_t* w_split, const float* 
  *   bias    [E] fp32 or NULL
  *   ids     [T, k] int32 (out);  w [T, k] fp32 (out)
  * Limits: k <= top_groups * E / n_groups, n_groups divides E; k <= 32,
- * n_groups <= 32, E <= 1024.  A scale that is not finite is refused. */
+ * n_groups <= 32, E <= 1024, T <= 2^31 - 8, T*k < 2^31 (the gradient's too).
+ * A scale that is not finite is refused. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 #define MOE_GROUP_MAX 0

@@ -1,6 +1,13 @@
-"""The largest sizes of the 4-bit experts: refused on the host by name, not by a
-failing launch (CPU only)."""
-from test_abi_select_w4 import FAKE, UNSUPPORTED, down, gate_up, lib  # noqa: F401
+"""The largest sizes of the expert choice and of the 4-bit experts: refused on
+the host by name, not by a failing launch (CPU only)."""
+from test_abi_select_w4 import FAKE, INVALID, UNSUPPORTED, bwd, down, gate_up, lib, select  # noqa: F401
+
+
+def test_tokens_of_the_choice(lib):  # noqa: F811
+    """A block takes eight tokens, and their numbers are 32-bit."""
+    for T in (2 ** 31 - 7, 2 ** 31 - 1):
+        assert select(lib, T=T, k=1) == INVALID
+        assert bwd(lib, T=T, k=1) == INVALID
 
 
 def test_slots_of_the_4bit_experts(lib):  # noqa: F811

@@ -53,6 +53,7 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA
 int gemm_status(int rc) { return rc == 0 ? MOE_OK : (rc < 0 ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA); }
 
 constexpr int64_t kMaxI32 = 2147483647;
+constexpr int64_t kMaxSelectTokens = kMaxI32 - 7;   // eight to a block, in 32-bit numbers
 
 }  // namespace
 
@@ -103,6 +104,7 @@ bool encode_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void
 using moe::aligned16;
 using moe::cuda_status;
 using moe::kMaxI32;
+using moe::kMaxSelectTokens;
 
 extern "C" {
 
@@ -221,7 +223,7 @@ int moe_route_presplit(const uint16_t* x, const uint16_t* w_split, const float* 
 int moe_route_select(const void* logits, int logits_bf16, const float* bias, int64_t T, int64_t E, int64_t k,
                      int score, int64_t n_groups, int64_t top_groups, int group_score, int renorm, float scale,
                      int32_t* ids, float* w, void* stream) {
-  if (T < 0 || E < 1 || k < 1 || k > E || T > kMaxI32 || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || E < 1 || k < 1 || k > E || T > kMaxSelectTokens || T * k > kMaxI32) return MOE_ERR_INVALID_ARG;
   if (n_groups < 1 || top_groups < 1 || top_groups > n_groups || E % n_groups != 0 || k > top_groups * (E / n_groups))
     return MOE_ERR_INVALID_ARG;
   if (score < 0 || score > 1 || group_score < 0 || group_score > 1) return MOE_ERR_INVALID_ARG;
@@ -239,7 +241,7 @@ int moe_route_select(const void* logits, int logits_bf16, const float* bias, int
 int moe_route_select_bwd(const float* dw_part, int64_t nparts, const int32_t* row_map, const void* logits,
                          int logits_bf16, const int32_t* ids, int64_t T, int64_t E, int64_t k, int score, int renorm,
                          float scale, void* d_logits, float* dw, void* stream) {
-  if (T < 0 || E < 1 || k < 1 || k > E || nparts < 1 || nparts > kMaxI32 || T > kMaxI32 || T * k > kMaxI32)
+  if (T < 0 || E < 1 || k < 1 || k > E || nparts < 1 || nparts > kMaxI32 || T > kMaxSelectTokens || T * k > kMaxI32)
     return MOE_ERR_INVALID_ARG;
   if (score < 0 || score > 1) return MOE_ERR_INVALID_ARG;
   if (!(scale - scale == 0.f)) return MOE_ERR_INVALID_ARG;
