@@ -36,8 +36,8 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 
 // 1 / d rounded to nearest, for 1 <= d < 2^120: a Newton step in fused
 // multiply-adds from an approximation within a unit of the last place
-// (Markstein, IBM J. Res. Dev. 34, 1990); equal to the rounded quotient for
-// each of these floats.
+// (Markstein, IBM J. Res. Dev. 34, 1990).  A GPU test compares it with the
+// quotient for the d of every fp32 logit.
 __device__ __forceinline__ float reciprocal(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
