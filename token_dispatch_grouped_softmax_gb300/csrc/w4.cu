@@ -263,9 +263,9 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
 // x there loses the rest.)
 //
 // Bound by the stream of the codes where it is long: 32 tokens, top-8 of 256,
-// H 7168, I 2048, groups of 128: gate_up 458 us (5.40 TB/s), down 232 (5.33).
+// H 7168, I 2048, groups of 128: gate_up 459 us (5.39 TB/s), down 232 (5.32).
 // 45 tokens, top-8 of 128, H 2048, I 768, groups of 64 with zeros: 50 us (4.1)
-// and 34 (3.0) with start, end and latency: 16 warps an SM, ALU pipe 57 %.
+// and 35 (2.9) with start, end and latency: 16 warps an SM, ALU pipe 57 %.
 template <int GROUP, bool ZEROS>
 struct W4Ring {
   static constexpr int kRows = 128 / GROUP;   // group rows of a unit
@@ -613,8 +613,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
 // (gate_up) or both (down).  The sums meet in the first block's shared memory
 // and its first warp adds them in the order of the other kernels: the same
 // bits.  No lists, and one launch for down: one token, top-8 of 128 experts,
-// H 2048, I 768, down takes 6.0 us instead of 7.4 (4 tokens 11.8 instead of
-// 13.9); one token, top-2 of 16, H 2048, I 1408, gate_up 5.1 instead of 6.2.
+// H 2048, I 768, down takes 6.1 us instead of 7.4 (4 tokens 11.3 instead of
+// 13.3); one token, top-2 of 16, H 2048, I 1408, gate_up 5.1 instead of 6.7.
 // Halves of the columns for down too took 7.3: clusters of eight blocks.
 template <bool GATE_UP, int GROUP, bool ZEROS>
 struct W4SlotRing {
@@ -901,8 +901,8 @@ cudaError_t launch_w4(const W4Params& p, const W4SlotArgs& s, const DeviceInfo& 
 // How w4_slots_kernel would run the call, per 0: not.  Its blocks must all be
 // on the GPU at once, two an SM, with a warp for every two sums: beyond that
 // the tokens' common experts are read again and again (down at H 2048, I 768,
-// top-8 of 128: 4 tokens with two sums a warp 11.8 us, with a warp each, in
-// two waves, 13.8, by w4_kernel 13.9; 8 tokens 26.1, by w4_kernel 22.5).
+// top-8 of 128: 4 tokens with two sums a warp 11.3 us, with a warp each, in
+// two waves, 14.1, by w4_kernel 13.3; 8 tokens 22.4, by w4_kernel 21.5).
 template <bool GATE_UP>
 W4SlotArgs w4_slot_plan(const W4Params& p, const DeviceInfo& dev) {
   W4SlotArgs s{};
