@@ -278,6 +278,111 @@ int moe_w4_quantize(const uint16_t* weight, int64_t rows, int64_t N, int64_t gro
 int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t N,
                       int64_t group, uint16_t* weight, void* stream);
 
+/* --------------------------------------- the layer for a few tokens (bf16) */
+
+/* The expert layer of a decode step: y_t = sum_j w[t,j] (h[t,j] . Wd_e) with
+ * h[t,j] = silu(x_t . Wg_e) * (x_t . Wu_e), e = ids[t,j], plus a shared
+ * expert's output of weight 1.  Rows stay in slot order (no permutation) and
+ * every weight of the experts in use is read once.
+ *   x        [T, H] bf16; gate_up [E*H, 2I], down [E*I, H] bf16 (the layout
+ *            of the grouped GEMMs); sh_gate_up [H, 2 I_s], sh_down [I_s, H]
+ *            bf16, or both NULL with I_s = 0
+ *   y        [T, H] bf16 (out, rounded once)
+ * Sums are in fp32 and h is rounded to bf16.  A token's result does not
+ * depend on the other tokens of the call.
+ * H, I and I_s are multiples of 64 and at most 2^20, E at most 1024, k at
+ * most 32, E*H and E*I below 2^31, T at most 128 (MOE_ERR_UNSUPPORTED
+ * beyond).  Two calls that may run at the same time
+ * need a workspace each. */
+
+/* With the choice given: ids [T, k] int32, w [T, k] fp32.  An id of -1 is an
+ * empty slot (a padded token): it adds nothing, whatever its w; another id
+ * outside [0, E) sets MOE_ERR_DEVICE and is taken as empty.  Slots of a token
+ * may name the same expert. */
+int moe_few_experts_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes);
+int moe_few_experts(const uint16_t* x, const int32_t* ids, const float* w, const uint16_t* gate_up,
+                    const uint16_t* down, const uint16_t* sh_gate_up, const uint16_t* sh_down, int64_t T, int64_t H,
+                    int64_t E, int64_t k, int64_t I, int64_t I_s, uint16_t* y, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* The whole layer: the router's logits x . W_r (+ bias [E] fp32 or NULL) in
+ * fp32, the choice of moe_route_select on them (balance_bias is its bias;
+ * softmax, renormalised, one group: the choice of moe_route), and the above.
+ * ids [T, k] int32 and w [T, k] fp32 are outputs; w_router [H, E] fp32. */
+int moe_few_layer_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes);
+int moe_few_layer(const uint16_t* x, const float* w_router, const float* bias, const float* balance_bias,
+                  const uint16_t* gate_up, const uint16_t* down, const uint16_t* sh_gate_up, const uint16_t* sh_down,
+                  int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, int score, int64_t n_groups,
+                  int64_t top_groups, int group_score, int renorm, float scale, int32_t* ids, float* w, uint16_t* y,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------- norms around a block */
+
+/* Types of moe_block_norm's operands: these are fp32 with their bit, else bf16. */
+#define MOE_NORM_X_F32 1      /* x, r, dr, dx */
+#define MOE_NORM_WEIGHT_F32 2 /* weight, d_weight */
+#define MOE_NORM_POST_F32 4   /* post_weight, d_post_weight */
+#define MOE_NORM_GATE_F32 8   /* gate, d_gate */
+
+/* What stands between two blocks of a model: the first one's output normed
+ * (post_weight), gated, scaled and added to the residual stream, and the
+ * stream normed for the next block (RMS norms):
+ *   n_t = branch_t * post_weight / sqrt(mean(branch_t^2) + eps)   (post_weight NULL: branch_t)
+ *   r_t = residual_scale x_t + branch_scale gate_{t / (T/gates)} n_t
+ *         (gate NULL with gates 0: 1;  branch NULL: r = x, with no post_weight or gate and both scales 1)
+ *   h_t = r_t * weight / sqrt(mean(r_t^2) + eps)                  (weight NULL: no h)
+ *   x        [T, H] fp32 or bf16;  branch [T, H] bf16 or NULL
+ *   weight, post_weight [H];  gate [gates, H], gates a divisor of T: one for
+ *            every T/gates consecutive rows (1: a learned scale; T: one a row)
+ *   r        [T, H] (out) of x's type, NULL without branch; may be x itself
+ *   h        [T, H] bf16 (out), NULL without weight
+ *   stats    [2, T] fp32 (out, nullable): 1 / sqrt(mean + eps) of r and of
+ *            branch (written where the norm is), for the backward
+ * Sums are in fp32, every output is rounded once (h from the unrounded r).
+ * H is a multiple of 8 up to 8192 (MOE_ERR_UNSUPPORTED beyond); eps > 0.
+ * Without branch and without weight there is nothing to do
+ * (MOE_ERR_INVALID_ARG). */
+int moe_block_norm(const void* x, const uint16_t* branch, const void* weight, const void* post_weight,
+                   const void* gate, int types, int64_t T, int64_t H, int64_t gates, float residual_scale,
+                   float branch_scale, float eps, void* r, uint16_t* h, float* stats, void* stream);
+
+/* Its gradients for upstream dh [T, H] bf16 (of h; NULL without weight) and
+ * dr [T, H] of x's type (of r; NULL: 0): dx [T, H], d_branch [T, H] bf16,
+ * d_weight [H], d_post_weight [H], d_gate [gates, H], each of its operand's
+ * type and NULL where the operand is.  x and branch are the forward's inputs
+ * (not r) and stats what it wrote.  Outputs overlap no input.  The columns'
+ * sums over the rows have a fixed order; without rows they are zeros. */
+int moe_block_norm_bwd_workspace_size(int64_t T, int64_t H, int64_t gates, int has_weight, int has_post_weight,
+                                      size_t* bytes);
+int moe_block_norm_bwd(const uint16_t* dh, const void* dr, const void* x, const uint16_t* branch,
+                       const float* stats, const void* weight, const void* post_weight, const void* gate, int types,
+                       int64_t T, int64_t H, int64_t gates, float residual_scale, float branch_scale, void* dx,
+                       uint16_t* d_branch, void* d_weight, void* d_post_weight, void* d_gate, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------ the gradients' norm, and clipping */
+
+/* norm = sqrt(sum of all squares of n tensors); out_i = grad_i * min(1,
+ * max_norm / (norm + eps)), NaN and infinite gradients spreading as in that
+ * formula.
+ *   grads, outs   HOST arrays of n device pointers, sizes (elements) and
+ *                 fp32 (1: the tensor and its out are fp32, 0: bf16) HOST
+ *                 arrays too: they are read before the call returns.  Tensors
+ *                 of any size and alignment of their type; empty ones may be
+ *                 NULL.
+ *   outs          outs[i] may be grads[i]; otherwise outs overlap nothing.
+ *                 outs NULL: the norm alone (max_norm and eps are ignored).
+ *   norm          [1] fp32 (out), infinite where it passes fp32's range (the
+ *                 factor goes by its value all the same)
+ * Squares are summed in fp32 over 64 elements, beyond in fp64, in a fixed
+ * order; values whose squares fp32 does not hold are squared in fp64.
+ * max_norm >= 0, eps >= 0 (MOE_ERR_INVALID_ARG).  512 tensors take one launch
+ * of each of the two kernels. */
+int moe_grad_clip_workspace_size(const void* const* grads, const int64_t* sizes, const uint8_t* fp32, int64_t n,
+                                 size_t* bytes);
+int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const uint8_t* fp32, int64_t n,
+                  float max_norm, float eps, float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- permute */
 
 /* Bytes of workspace moe_permute needs: per-block expert histograms, the

@@ -14,11 +14,12 @@ from .ops import (GEMM_PAIRS_ALL, GEMM_PAIRS_GATE_UP, GEMM_PAIRS_GATE_UP_WGRAD, 
                   sync_status, unpermute_combine, unpermute_combine_bwd)
 from .ops import (route_balance_bias, route_logits, route_select, route_select_bwd, w4_dequantize, w4_down_combine, w4_gate_up_swiglu,
                   w4_quantize)
+from .ops import block_norm, block_norm_bwd, clip_grads, experts_few, grad_norm, layer_few
 from . import ep
 from .ops import ep_map_replicas, eplb_plan, sort_chunks
 from .layer import (DecodeGraph, ForwardGraph, ForwardState, MoELayer, MoELayerFunction, OverlappedForward,
                     PipelinedForward, RoutedMoELayerFunction, Routing, W4Experts, moe_backward, moe_forward,
-                    moe_forward_w4)
+                    moe_forward_few, moe_forward_w4)
 
 __all__ = [
     "build", "up_to_date", "MoEError", "lib_path", "load",
@@ -27,8 +28,9 @@ __all__ = [
     "grouped_gemm_gate_up_bwd", "gather_dx", "route_bwd_weight", "sync_status", "set_wait_limit_ns", "set_gemm_pairs",
     "GEMM_PAIRS_NONE", "GEMM_PAIRS_ALL", "GEMM_PAIRS_GATE_UP", "GEMM_PAIRS_GATE_UP_WGRAD",
     "route_logits", "route_select", "route_select_bwd", "route_balance_bias",
+    "layer_few", "experts_few", "block_norm", "block_norm_bwd", "grad_norm", "clip_grads",
     "w4_gate_up_swiglu", "w4_down_combine", "w4_quantize", "w4_dequantize",
     "set_pdl", "sort_chunks", "ep_map_replicas", "eplb_plan", "ep",
     "ForwardGraph", "ForwardState", "MoELayer", "OverlappedForward", "MoELayerFunction", "PipelinedForward", "moe_forward", "moe_backward",
-    "Routing", "RoutedMoELayerFunction", "W4Experts", "moe_forward_w4", "DecodeGraph",
+    "Routing", "RoutedMoELayerFunction", "W4Experts", "moe_forward_w4", "moe_forward_few", "DecodeGraph",
 ]

@@ -44,6 +44,15 @@ SIGNATURES = {
     "moe_w4_down_combine": [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P, SZ, P],
     "moe_w4_quantize": [P, I64, I64, I64, P, P, P, P],
     "moe_w4_dequantize": [P, P, P, I64, I64, I64, P, P],
+    "moe_few_experts_workspace_size": [I64, I64, I64, I64, I64, I64, ctypes.POINTER(SZ)],
+    "moe_few_experts": [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, P, SZ, P],
+    "moe_few_layer_workspace_size": [I64, I64, I64, I64, I64, I64, ctypes.POINTER(SZ)],
+    "moe_few_layer": [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, INT, I64, I64, INT, INT, F32, P, P, P, P, SZ, P],
+    "moe_block_norm": [P, P, P, P, P, INT, I64, I64, I64, F32, F32, F32, P, P, P, P],
+    "moe_block_norm_bwd_workspace_size": [I64, I64, I64, INT, INT, ctypes.POINTER(SZ)],
+    "moe_block_norm_bwd": [P, P, P, P, P, P, P, P, INT, I64, I64, I64, F32, F32, P, P, P, P, P, P, SZ, P],
+    "moe_grad_clip_workspace_size": [P, P, P, I64, ctypes.POINTER(SZ)],
+    "moe_grad_clip": [P, P, P, P, I64, F32, F32, P, P, SZ, P],
     "moe_permute_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
     "moe_permute": [P, P, I64, I64, I64, P, P, P, P, P, P, SZ, P],
     "moe_permute_noalloc": [P, P, I64, I64, I64, P, P, P, P, P, P],
@@ -121,7 +130,9 @@ def binding():
         spec.loader.exec_module(ext)
         ext.bind(check, *(ctypes.cast(getattr(lib, name), P).value for name in (
             "moe_route_select", "moe_route_select_bwd", "moe_route_balance_bias", "moe_w4_gate_up_swiglu",
-            "moe_w4_down_workspace_size", "moe_w4_down_combine")))
+            "moe_w4_down_workspace_size", "moe_w4_down_combine", "moe_few_experts_workspace_size", "moe_few_experts",
+            "moe_few_layer_workspace_size", "moe_few_layer", "moe_block_norm", "moe_block_norm_bwd_workspace_size",
+            "moe_block_norm_bwd", "moe_grad_clip_workspace_size", "moe_grad_clip")))
         _binding = ext
     return _binding
 

@@ -347,6 +347,212 @@ int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uin
                                                static_cast<cudaStream_t>(stream)));
 }
 
+/* --------------------------------------- the layer for a few tokens (bf16) */
+
+namespace {
+
+int few_check(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s) {
+  if (T < 0 || H < 1 || E < 1 || k < 1 || I < 1 || I_s < 0) return MOE_ERR_INVALID_ARG;
+  if (H % 64 != 0 || I % 64 != 0 || I_s % 64 != 0 || E > moe::kMaxExperts || k > 32) return MOE_ERR_UNSUPPORTED;
+  if (H > (int64_t)1 << 20 || I > (int64_t)1 << 20 || I_s > (int64_t)1 << 20 || E * H > kMaxI32 || E * I > kMaxI32)
+    return MOE_ERR_UNSUPPORTED;
+  if (T > 128) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int few_pointers(const uint16_t* x, const moe::FewWeights& w, int64_t I_s, const uint16_t* y) {
+  if (!x || !w.gate_up || !w.down || !y || !aligned16(x) || !aligned16(w.gate_up) || !aligned16(w.down) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if ((I_s != 0) != (w.sh_gate_up != nullptr) || (I_s != 0) != (w.sh_down != nullptr)) return MOE_ERR_INVALID_ARG;
+  return aligned16(w.sh_gate_up) && aligned16(w.sh_down) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+int moe_few_experts_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int rc = few_check(T, H, E, k, I, I_s);
+  if (rc != MOE_OK) return rc;
+  *bytes = moe::few_experts_workspace_bytes({T, H, E, k, I, I_s});
+  return MOE_OK;
+}
+
+int moe_few_experts(const uint16_t* x, const int32_t* ids, const float* w, const uint16_t* gate_up,
+                    const uint16_t* down, const uint16_t* sh_gate_up, const uint16_t* sh_down, int64_t T, int64_t H,
+                    int64_t E, int64_t k, int64_t I, int64_t I_s, uint16_t* y, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int rc = few_check(T, H, E, k, I, I_s);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  const moe::FewWeights weights{gate_up, down, sh_gate_up, sh_down};
+  rc = few_pointers(x, weights, I_s, y);
+  if (rc != MOE_OK || !ids || !w) return MOE_ERR_INVALID_ARG;
+  const moe::FewShape shape{T, H, E, k, I, I_s};
+  if (!workspace || !aligned16(workspace) || workspace_bytes < moe::few_experts_workspace_bytes(shape))
+    return MOE_ERR_WORKSPACE;
+  moe::DeviceInfo dev;
+  rc = moe::current_device(&dev);
+  if (rc != MOE_OK) return rc;
+  return cuda_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int moe_few_layer_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int rc = few_check(T, H, E, k, I, I_s);
+  if (rc != MOE_OK) return rc;
+  *bytes = up256(moe::few_experts_workspace_bytes({T, H, E, k, I, I_s})) + up256((size_t)(T * E) * sizeof(float)) +
+           moe::route_workspace_bytes(T, H, E);
+  return MOE_OK;
+}
+
+int moe_few_layer(const uint16_t* x, const float* w_router, const float* bias, const float* balance_bias,
+                  const uint16_t* gate_up, const uint16_t* down, const uint16_t* sh_gate_up, const uint16_t* sh_down,
+                  int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, int score, int64_t n_groups,
+                  int64_t top_groups, int group_score, int renorm, float scale, int32_t* ids, float* w, uint16_t* y,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int rc = moe_few_layer_workspace_size(T, H, E, k, I, I_s, &need);
+  if (rc != MOE_OK) return rc;
+  if (k > E || n_groups < 1 || top_groups < 1 || top_groups > n_groups || E % n_groups != 0 ||
+      k > top_groups * (E / n_groups) || score < 0 || score > 1 || group_score < 0 || group_score > 1 ||
+      !(scale - scale == 0.f))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const moe::FewWeights weights{gate_up, down, sh_gate_up, sh_down};
+  rc = few_pointers(x, weights, I_s, y);
+  if (rc != MOE_OK || !w_router || !ids || !w || !aligned16(w_router) || !aligned16(bias) || !aligned16(balance_bias))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  moe::DeviceInfo dev;
+  rc = moe::current_device(&dev);
+  if (rc != MOE_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const moe::FewShape shape{T, H, E, k, I, I_s};
+  uint8_t* at = static_cast<uint8_t*>(workspace) + up256(moe::few_experts_workspace_bytes(shape));
+  float* logits = reinterpret_cast<float*>(at);
+  cudaError_t e = moe::launch_route(x, w_router, bias, T, H, E, k, ids, w, logits, at + up256((size_t)(T * E) * sizeof(float)),
+                                    dev, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  const moe::RouteChoice c{score == MOE_SCORE_SIGMOID, group_score == MOE_GROUP_TOP2, renorm != 0, (int)n_groups,
+                           (int)top_groups, scale};
+  e = moe::launch_route_select(logits, false, balance_bias, T, E, k, c, ids, w, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  return cuda_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev, st));
+}
+
+/* --------------------------------------------- norms around a block */
+
+namespace {
+
+// The shapes and operands that both directions take.
+int norm_check(const moe::BlockNorm& n) {
+  if (n.T < 0 || n.H < 1 || n.T > kMaxI32 || n.groups < 0) return MOE_ERR_INVALID_ARG;
+  if (!(n.a - n.a == 0.f) || !(n.b - n.b == 0.f)) return MOE_ERR_INVALID_ARG;
+  if (n.H % 8 != 0 || n.H > moe::block_norm_max_width()) return MOE_ERR_UNSUPPORTED;
+  if (n.groups > 0 ? n.T % n.groups != 0 : n.g != nullptr) return MOE_ERR_INVALID_ARG;
+  if (n.T == 0) return MOE_OK;
+  if (!n.x || (!n.y && !n.w) || (n.groups > 0 && !n.g)) return MOE_ERR_INVALID_ARG;
+  if (!n.y && (n.v || n.g || n.a != 1.f || n.b != 1.f)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(n.x) || !aligned16(n.y) || !aligned16(n.w) || !aligned16(n.v) || !aligned16(n.g))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe::BlockNorm norm_of(const void* x, const uint16_t* branch, const void* weight, const void* post, const void* gate,
+                       int types, int64_t T, int64_t H, int64_t gates, float a, float b, float eps) {
+  moe::BlockNorm n;
+  n.x = x; n.y = branch; n.w = weight; n.v = post; n.g = gate;
+  n.x_f32 = (types & MOE_NORM_X_F32) != 0; n.w_f32 = (types & MOE_NORM_WEIGHT_F32) != 0;
+  n.v_f32 = (types & MOE_NORM_POST_F32) != 0; n.g_f32 = (types & MOE_NORM_GATE_F32) != 0;
+  n.T = T; n.H = H; n.groups = gates;
+  n.a = a; n.b = b; n.eps = eps;
+  return n;
+}
+
+}  // namespace
+
+int moe_block_norm(const void* x, const uint16_t* branch, const void* weight, const void* post_weight,
+                   const void* gate, int types, int64_t T, int64_t H, int64_t gates, float residual_scale,
+                   float branch_scale, float eps, void* r, uint16_t* h, float* stats, void* stream) {
+  const moe::BlockNorm n = norm_of(x, branch, weight, post_weight, gate, types, T, H, gates, residual_scale, branch_scale, eps);
+  const int rc = norm_check(n);
+  if (rc != MOE_OK) return rc;
+  if (!(eps > 0.f) || !(eps - eps == 0.f)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!branch != !r || !weight != !h || !aligned16(r) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(moe::launch_block_norm(n, r, h, stats, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_block_norm_bwd_workspace_size(int64_t T, int64_t H, int64_t gates, int has_weight, int has_post_weight,
+                                      size_t* bytes) {
+  if (!bytes || T < 0 || H < 1 || gates < 0) return MOE_ERR_INVALID_ARG;
+  if (H % 8 != 0 || H > moe::block_norm_max_width()) return MOE_ERR_UNSUPPORTED;
+  *bytes = moe::block_norm_bwd_workspace_bytes(T, H, gates, has_weight != 0, has_post_weight != 0);
+  return MOE_OK;
+}
+
+int moe_block_norm_bwd(const uint16_t* dh, const void* dr, const void* x, const uint16_t* branch,
+                       const float* stats, const void* weight, const void* post_weight, const void* gate, int types,
+                       int64_t T, int64_t H, int64_t gates, float residual_scale, float branch_scale, void* dx,
+                       uint16_t* d_branch, void* d_weight, void* d_post_weight, void* d_gate, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const moe::BlockNorm n = norm_of(x, branch, weight, post_weight, gate, types, T, H, gates, residual_scale, branch_scale, 0.f);
+  const int rc = norm_check(n);
+  if (rc != MOE_OK) return rc;
+  if (!weight != !d_weight || !post_weight != !d_post_weight || !gate != !d_gate) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_weight) || !aligned16(d_post_weight) || !aligned16(d_gate)) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!dx || !branch != !d_branch || !weight != !dh || ((weight || post_weight) && !stats)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(dh) || !aligned16(dr) || !aligned16(dx) || !aligned16(d_branch)) return MOE_ERR_INVALID_ARG;
+  }
+  const size_t need = moe::block_norm_bwd_workspace_bytes(T, H, gates, weight, post_weight);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  const moe::BlockNormGrads d{dx, d_branch, d_weight, d_post_weight, d_gate};
+  return cuda_status(moe::launch_block_norm_bwd(n, dh, dr, stats, d, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+/* ------------------------------------ the gradients' norm, and clipping */
+
+namespace {
+
+int grads_check(const void* const* grads, void* const* outs, const int64_t* sizes, const uint8_t* fp32, int64_t n) {
+  if (n < 0 || (n > 0 && (!grads || !sizes || !fp32))) return MOE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    if (sizes[i] < 0 || sizes[i] > (int64_t)1 << 44) return MOE_ERR_INVALID_ARG;
+    if (sizes[i] == 0) continue;
+    const uintptr_t mask = fp32[i] ? 3 : 1;
+    if (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) & mask)) return MOE_ERR_INVALID_ARG;
+    if (outs && (!outs[i] || (reinterpret_cast<uintptr_t>(outs[i]) & mask))) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_grad_clip_workspace_size(const void* const* grads, const int64_t* sizes, const uint8_t* fp32, int64_t n,
+                                 size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const int rc = grads_check(grads, nullptr, sizes, fp32, n);
+  if (rc != MOE_OK) return rc;
+  *bytes = moe::grad_norm_workspace_bytes({grads, nullptr, sizes, fp32, n});
+  return MOE_OK;
+}
+
+int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const uint8_t* fp32, int64_t n,
+                  float max_norm, float eps, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = grads_check(grads, outs, sizes, fp32, n);
+  if (rc != MOE_OK) return rc;
+  if (!norm || (outs && (!(max_norm >= 0.f) || !(eps >= 0.f)))) return MOE_ERR_INVALID_ARG;
+  const moe::GradList list{grads, outs, sizes, fp32, n};
+  const size_t need = moe::grad_norm_workspace_bytes(list);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  return cuda_status(moe::launch_grad_clip(list, max_norm, eps, norm, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 /* ---------------------------------------------------------------- permute */
 
 int moe_permute_workspace_size(int64_t T, int64_t k, int64_t E, size_t* bytes) {

@@ -1,5 +1,6 @@
 // The Python side of the calls whose kernels run for a few microseconds (the
-// expert choice and the 4-bit experts of a decode step): a CPython extension
+// expert choice, the experts of a decode step, a block's norms, the gradients'
+// clipping): a CPython extension
 // that checks the tensors, allocates the outputs and calls the C entry points
 // of libmoe_gb300.so on torch's current stream.  What the ctypes functions of
 // ops.py spend in the interpreter (9 us of a 12 us call) is most of such a
@@ -14,6 +15,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <type_traits>
+#include <vector>
+
 #include "../../include/moe_gb300.h"
 
 namespace {
@@ -26,6 +31,15 @@ decltype(&moe_route_balance_bias) f_route_balance_bias;
 decltype(&moe_w4_gate_up_swiglu) f_w4_gate_up_swiglu;
 decltype(&moe_w4_down_workspace_size) f_w4_down_workspace_size;
 decltype(&moe_w4_down_combine) f_w4_down_combine;
+decltype(&moe_few_experts_workspace_size) f_few_experts_workspace_size;
+decltype(&moe_few_experts) f_few_experts;
+decltype(&moe_few_layer_workspace_size) f_few_layer_workspace_size;
+decltype(&moe_few_layer) f_few_layer;
+decltype(&moe_block_norm) f_block_norm;
+decltype(&moe_block_norm_bwd_workspace_size) f_block_norm_bwd_workspace_size;
+decltype(&moe_block_norm_bwd) f_block_norm_bwd;
+decltype(&moe_grad_clip_workspace_size) f_grad_clip_workspace_size;
+decltype(&moe_grad_clip) f_grad_clip;
 PyObject* g_check;   // check(name, status) of _lib: raises MoEError
 
 [[noreturn]] void refuse(PyObject* type, const char* format, ...) {
@@ -49,7 +63,7 @@ at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, const at::Tensor& li
   return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
 
-// A contiguous CUDA tensor of the current device, of the type and number of dimensions.
+// A contiguous CUDA tensor of the current device, of the type and number of dimensions (-1: any).
 const at::Tensor& need(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t ndim,
                        at::ScalarType or_type = at::ScalarType::Undefined) {
   if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a torch.Tensor", name);
@@ -60,7 +74,7 @@ const at::Tensor& need(PyObject* o, const char* name, at::ScalarType type, const
     refuse(PyExc_ValueError, "%s is on cuda:%d but the current device is cuda:%d", name, (int)t.get_device(), device);
   if (t.scalar_type() != type && t.scalar_type() != or_type) refuse(PyExc_TypeError, "%s must be %s", name, type_name);
   if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
-  if (t.dim() != ndim) refuse(PyExc_ValueError, "%s must have %d dims", name, (int)ndim);
+  if (ndim >= 0 && t.dim() != ndim) refuse(PyExc_ValueError, "%s must have %d dims", name, (int)ndim);
   return t;
 }
 const at::Tensor& need_f32(PyObject* o, const char* name, int64_t ndim) { return need(o, name, at::kFloat, "torch.float32", ndim); }
@@ -298,18 +312,300 @@ PyObject* w4_down_combine(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   BODY_END
 }
 
+// bf16 experts gate_up [E*H, 2I], down [E*I, H] for rows of H, E of them (0: as many as gate_up holds).
+struct Experts {
+  const uint16_t *gate_up, *down;
+  int64_t E, I;
+};
+
+Experts experts(PyObject* gate_up, PyObject* down, int64_t H, int64_t E, const char* gate_up_name, const char* down_name) {
+  const at::Tensor& gu = need_bf16(gate_up, gate_up_name, 2);
+  const at::Tensor& dn = need_bf16(down, down_name, 2);
+  if (H < 1 || gu.size(0) % H != 0 || gu.size(0) == 0 || gu.size(1) % 2 != 0)
+    refuse(PyExc_ValueError, "%s must be [E*H, 2I]", gate_up_name);
+  const Experts x{ptr<uint16_t>(gu), ptr<uint16_t>(dn), gu.size(0) / H, gu.size(1) / 2};
+  if (E && x.E != E) refuse(PyExc_ValueError, "%s must be [E*H, 2I] with E = %lld", gate_up_name, (long long)E);
+  if (dn.size(0) != x.E * x.I || dn.size(1) != H) refuse(PyExc_ValueError, "%s must be [E*I, H]", down_name);
+  return x;
+}
+
+Experts shared_expert(PyObject* gate_up, PyObject* down, int64_t H) {
+  if ((gate_up == Py_None) != (down == Py_None)) refuse(PyExc_ValueError, "sh_gate_up and sh_down go together");
+  if (gate_up == Py_None) return Experts{nullptr, nullptr, 1, 0};
+  return experts(gate_up, down, H, 1, "sh_gate_up", "sh_down");
+}
+
+// (x, ids, w, gate_up, down, sh_gate_up, sh_down, out) -> y
+PyObject* few_experts(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(8)
+  BODY_BEGIN
+  const at::Tensor& x = need_bf16(a[0], "x", 2);
+  const at::Tensor& ids = need_i32(a[1], "ids", 2);
+  const at::Tensor& w = need_f32(a[2], "w", 2);
+  const int64_t T = x.size(0), H = x.size(1), k = ids.size(1);
+  if (ids.size(0) != T || w.size(0) != T || w.size(1) != k) refuse(PyExc_ValueError, "ids and w must be [T, k]");
+  const Experts e = experts(a[3], a[4], H, 0, "gate_up", "down"), sh = shared_expert(a[5], a[6], H);
+  const at::Tensor y = a[7] == Py_None ? fresh({T, H}, at::kBFloat16, x) : need_bf16(a[7], "out", 2);
+  if (y.size(0) != T || y.size(1) != H) refuse(PyExc_ValueError, "out must be [T, H]");
+  size_t bytes = 0;
+  check("moe_few_experts_workspace_size", f_few_experts_workspace_size(T, H, e.E, k, e.I, sh.I, &bytes));
+  const at::Tensor ws = fresh({(int64_t)bytes}, at::kByte, x);
+  void* st = stream();
+  run("moe_few_experts", [&] {
+    return f_few_experts(ptr<uint16_t>(x), ptr<int32_t>(ids), ptr<float>(w), e.gate_up, e.down, sh.gate_up, sh.down, T, H,
+                         e.E, k, e.I, sh.I, ptr<uint16_t>(y), ptr(ws), bytes, st);
+  });
+  return THPVariable_Wrap(y);
+  BODY_END
+}
+
+// (x, w_router, gate_up, down, k, bias, balance_bias, sh_gate_up, sh_down, score, n_groups, top_groups, group_score,
+//  renorm, scale) -> y, ids, w
+PyObject* few_layer(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(15)
+  BODY_BEGIN
+  const at::Tensor& x = need_bf16(a[0], "x", 2);
+  const at::Tensor& wr = need_f32(a[1], "w_router", 2);
+  const int64_t T = x.size(0), H = x.size(1), E = wr.size(1), k = integer(a[4]);
+  if (wr.size(0) != H || E < 1) refuse(PyExc_ValueError, "w_router must be [H, E]");
+  const Experts e = experts(a[2], a[3], H, E, "gate_up", "down"), sh = shared_expert(a[7], a[8], H);
+  const float* bias[2] = {nullptr, nullptr};
+  const char* name[2] = {"bias", "balance_bias"};
+  for (int i = 0; i < 2; ++i)
+    if (a[5 + i] != Py_None) {
+      const at::Tensor& b = need_f32(a[5 + i], name[i], 1);
+      if (b.size(0) != E) refuse(PyExc_ValueError, "%s must be [E]", name[i]);
+      bias[i] = ptr<float>(b);
+    }
+  const int64_t score = integer(a[9]), groups = integer(a[10]), top = integer(a[11]), group_score = integer(a[12]),
+                renorm = integer(a[13]);
+  const float scale = (float)real(a[14]);
+  size_t bytes = 0;
+  check("moe_few_layer_workspace_size", f_few_layer_workspace_size(T, H, E, k, e.I, sh.I, &bytes));
+  const at::Tensor y = fresh({T, H}, at::kBFloat16, x), ids = fresh({T, k}, at::kInt, x), w = fresh({T, k}, at::kFloat, x);
+  const at::Tensor ws = fresh({(int64_t)bytes}, at::kByte, x);
+  void* st = stream();
+  run("moe_few_layer", [&] {
+    return f_few_layer(ptr<uint16_t>(x), ptr<float>(wr), bias[0], bias[1], e.gate_up, e.down, sh.gate_up, sh.down, T, H, E,
+                       k, e.I, sh.I, (int)score, groups, top, (int)group_score, (int)renorm, scale, ptr<int32_t>(ids),
+                       ptr<float>(w), ptr<uint16_t>(y), ptr(ws), bytes, st);
+  });
+  PyObject* out[3] = {THPVariable_Wrap(y), THPVariable_Wrap(ids), THPVariable_Wrap(w)};
+  PyObject* r = PyTuple_Pack(3, out[0], out[1], out[2]);
+  for (PyObject* o : out) Py_XDECREF(o);
+  return r;
+  BODY_END
+}
+
+// The operands of block_norm; an absent one is undefined.
+struct Norm {
+  at::Tensor x, branch, weight, post, gate;
+  int types = 0;
+  int64_t T, H, gates = 0;
+  float a, b;
+};
+
+at::Tensor float_or_bf16(PyObject* o, const char* name, int64_t ndim) {
+  return need(o, name, at::kFloat, "torch.float32 or torch.bfloat16", ndim, at::kBFloat16);
+}
+
+// From a[0..]: x, weight, branch, post_weight, gate, residual_scale, branch_scale.
+Norm norm_operands(PyObject* const* a) {
+  Norm n;
+  n.x = float_or_bf16(a[0], "x", 2);
+  n.T = n.x.size(0);
+  n.H = n.x.size(1);
+  if (n.x.scalar_type() == at::kFloat) n.types |= MOE_NORM_X_F32;
+  auto vector = [&](PyObject* o, const char* name, int bit) {
+    at::Tensor t;
+    if (o == Py_None) return t;
+    t = float_or_bf16(o, name, 1);
+    if (t.size(0) != n.H) refuse(PyExc_ValueError, "%s must be [H]", name);
+    if (t.scalar_type() == at::kFloat) n.types |= bit;
+    return t;
+  };
+  n.weight = vector(a[1], "weight", MOE_NORM_WEIGHT_F32);
+  if (a[2] != Py_None) {
+    n.branch = need_bf16(a[2], "branch", 2);
+    if (n.branch.size(0) != n.T || n.branch.size(1) != n.H) refuse(PyExc_ValueError, "branch must be [T, H]");
+  }
+  n.post = vector(a[3], "post_weight", MOE_NORM_POST_F32);
+  n.a = (float)real(a[5]);
+  n.b = (float)real(a[6]);
+  if (!n.branch.defined()) {
+    if (!n.weight.defined()) refuse(PyExc_ValueError, "block_norm needs branch or weight");
+    if (n.post.defined() || a[4] != Py_None || n.a != 1.f || n.b != 1.f)
+      refuse(PyExc_ValueError, "post_weight, gate and the scales need branch");
+  }
+  if (a[4] != Py_None) {
+    n.gate = float_or_bf16(a[4], "gate", 2);
+    n.gates = n.gate.size(0);
+    if (n.gate.size(1) != n.H || n.gates == 0 || n.T % n.gates != 0)
+      refuse(PyExc_ValueError, "gate must be [gates, H] with gates a divisor of T");
+    if (n.gate.scalar_type() == at::kFloat) n.types |= MOE_NORM_GATE_F32;
+  }
+  return n;
+}
+
+template <typename T = void>
+T* maybe(const at::Tensor& t) {
+  return t.defined() ? ptr<T>(t) : nullptr;
+}
+at::Tensor like(const at::Tensor& t) { return t.defined() ? fresh(t.sizes(), t.scalar_type(), t) : at::Tensor(); }
+PyObject* wrap_or_none(const at::Tensor& t) {
+  if (t.defined()) return THPVariable_Wrap(t);
+  Py_RETURN_NONE;
+}
+
+// (x, weight, branch, post_weight, gate, residual_scale, branch_scale, eps, save) -> r or None, h or None, stats or None
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(9)
+  BODY_BEGIN
+  const Norm n = norm_operands(a);
+  const float eps = (float)real(a[7]);
+  at::Tensor r, h, stats;
+  if (n.branch.defined()) r = fresh({n.T, n.H}, n.x.scalar_type(), n.x);
+  if (n.weight.defined()) h = fresh({n.T, n.H}, at::kBFloat16, n.x);
+  if (integer(a[8])) stats = fresh({2, n.T}, at::kFloat, n.x);
+  void* st = stream();
+  run("moe_block_norm", [&] {
+    return f_block_norm(ptr(n.x), maybe<uint16_t>(n.branch), maybe(n.weight), maybe(n.post), maybe(n.gate), n.types, n.T,
+                        n.H, n.gates, n.a, n.b, eps, maybe(r), maybe<uint16_t>(h), maybe<float>(stats), st);
+  });
+  PyObject* out[3] = {wrap_or_none(r), wrap_or_none(h), wrap_or_none(stats)};
+  PyObject* tuple = PyTuple_Pack(3, out[0], out[1], out[2]);
+  for (PyObject* o : out) Py_XDECREF(o);
+  return tuple;
+  BODY_END
+}
+
+// (dh, dr, stats, x, weight, branch, post_weight, gate, residual_scale, branch_scale)
+//  -> dx, d_branch, d_weight, d_post_weight, d_gate (None where the operand is)
+PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(10)
+  BODY_BEGIN
+  const Norm n = norm_operands(a + 3);
+  at::Tensor dh, dr, stats;
+  if ((a[0] == Py_None) != !n.weight.defined()) refuse(PyExc_ValueError, "dh and weight go together");
+  if (a[0] != Py_None) {
+    dh = need_bf16(a[0], "dh", 2);
+    if (dh.size(0) != n.T || dh.size(1) != n.H) refuse(PyExc_ValueError, "dh must be [T, H]");
+  }
+  if (a[1] != Py_None) {
+    dr = need(a[1], "dr", n.x.scalar_type(), "of x's type", 2);
+    if (dr.size(0) != n.T || dr.size(1) != n.H) refuse(PyExc_ValueError, "dr must be [T, H]");
+  }
+  if (n.weight.defined() || n.post.defined()) {
+    stats = need_f32(a[2], "stats", 2);
+    if (stats.size(0) != 2 || stats.size(1) != n.T) refuse(PyExc_ValueError, "stats must be [2, T]");
+  }
+  const at::Tensor dx = like(n.x), d_branch = like(n.branch), d_weight = like(n.weight), d_post = like(n.post),
+                   d_gate = like(n.gate);
+  size_t bytes = 0;
+  check("moe_block_norm_bwd_workspace_size",
+        f_block_norm_bwd_workspace_size(n.T, n.H, n.gates, n.weight.defined(), n.post.defined(), &bytes));
+  const at::Tensor ws = fresh({(int64_t)bytes}, at::kByte, n.x);
+  void* st = stream();
+  run("moe_block_norm_bwd", [&] {
+    return f_block_norm_bwd(maybe<uint16_t>(dh), maybe(dr), ptr(n.x), maybe<uint16_t>(n.branch), maybe<float>(stats),
+                            maybe(n.weight), maybe(n.post), maybe(n.gate), n.types, n.T, n.H, n.gates, n.a, n.b, ptr(dx),
+                            maybe<uint16_t>(d_branch), maybe(d_weight), maybe(d_post), maybe(d_gate), ptr(ws), bytes, st);
+  });
+  PyObject* out[5] = {wrap_or_none(dx), wrap_or_none(d_branch), wrap_or_none(d_weight), wrap_or_none(d_post),
+                      wrap_or_none(d_gate)};
+  PyObject* tuple = PyTuple_Pack(5, out[0], out[1], out[2], out[3], out[4]);
+  for (PyObject* o : out) Py_XDECREF(o);
+  return tuple;
+  BODY_END
+}
+
+// (grads: a list or tuple, outs: the same or None, max_norm, eps) -> norm
+PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(4)
+  BODY_BEGIN
+  const bool clip = a[1] != Py_None;
+  if (!(PyList_Check(a[0]) || PyTuple_Check(a[0])) || (clip && !(PyList_Check(a[1]) || PyTuple_Check(a[1]))))
+    refuse(PyExc_TypeError, "grads and out must be lists or tuples of tensors");
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[0]);
+  if (n == 0) refuse(PyExc_ValueError, "grads must hold a tensor");
+  if (clip && PySequence_Fast_GET_SIZE(a[1]) != n) refuse(PyExc_ValueError, "out must hold a tensor for each of grads");
+  std::vector<const void*> src(n);
+  std::vector<void*> dst(n);
+  std::vector<int64_t> size(n);
+  std::vector<uint8_t> f32(n);
+  struct Span {
+    uintptr_t begin, end;
+    Py_ssize_t i;
+    bool out;
+  };
+  std::vector<Span> spans;
+  if (clip) spans.reserve(2 * n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* o = PySequence_Fast_GET_ITEM(a[0], i);
+    const at::Tensor& g = need(o, "a gradient", at::kFloat, "torch.float32 or torch.bfloat16", -1, at::kBFloat16);
+    src[i] = ptr(g);
+    size[i] = g.numel();
+    f32[i] = g.scalar_type() == at::kFloat;
+    if (!clip) continue;
+    PyObject* q = PySequence_Fast_GET_ITEM(a[1], i);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src[i]), bytes = (uintptr_t)size[i] * (f32[i] ? 4 : 2);
+    if (q != o) {
+      const at::Tensor& t = need(q, "a tensor of out", g.scalar_type(), "of its gradient's type", -1);
+      if (t.numel() != size[i]) refuse(PyExc_ValueError, "a tensor of out must have its gradient's size");
+      dst[i] = ptr(t);
+      if (bytes && dst[i] != src[i]) spans.push_back({at, at + bytes, i, false});
+    } else {
+      dst[i] = const_cast<void*>(src[i]);
+    }
+    const uintptr_t to = reinterpret_cast<uintptr_t>(dst[i]);
+    if (bytes) spans.push_back({to, to + bytes, i, true});
+  }
+  // what is written overlaps nothing else: a gradient that is listed twice would be scaled twice
+  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.begin < y.begin; });
+  uintptr_t end = 0, written = 0;   // of the spans so far, and of those that are written
+  for (const Span& s : spans) {
+    if (s.begin < written || (s.out && s.begin < end)) refuse(PyExc_ValueError, "a tensor of out overlaps another tensor");
+    end = std::max(end, s.end);
+    if (s.out) written = std::max(written, s.end);
+  }
+  const at::Tensor& first = THPVariable_Unpack(PySequence_Fast_GET_ITEM(a[0], 0));
+  const float max_norm = (float)real(a[2]), eps = (float)real(a[3]);
+  const at::Tensor norm = fresh({}, at::kFloat, first);
+  size_t bytes = 0;
+  check("moe_grad_clip_workspace_size", f_grad_clip_workspace_size(src.data(), size.data(), f32.data(), n, &bytes));
+  const at::Tensor ws = fresh({(int64_t)bytes}, at::kByte, first);
+  void* st = stream();
+  run("moe_grad_clip", [&] {
+    return f_grad_clip(src.data(), clip ? dst.data() : nullptr, size.data(), f32.data(), n, max_norm, eps, ptr<float>(norm),
+                       ptr(ws), bytes, st);
+  });
+  return THPVariable_Wrap(norm);
+  BODY_END
+}
+
 // (check, addresses of the entry points in the order below)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  ARGS(7)
+  ARGS(16)
   BODY_BEGIN
-  void* at[6];
-  for (int i = 0; i < 6; ++i) at[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(integer(a[i + 1])));
-  f_route_select = reinterpret_cast<decltype(f_route_select)>(at[0]);
-  f_route_select_bwd = reinterpret_cast<decltype(f_route_select_bwd)>(at[1]);
-  f_route_balance_bias = reinterpret_cast<decltype(f_route_balance_bias)>(at[2]);
-  f_w4_gate_up_swiglu = reinterpret_cast<decltype(f_w4_gate_up_swiglu)>(at[3]);
-  f_w4_down_workspace_size = reinterpret_cast<decltype(f_w4_down_workspace_size)>(at[4]);
-  f_w4_down_combine = reinterpret_cast<decltype(f_w4_down_combine)>(at[5]);
+  int next = 1;
+  auto take = [&](auto& f) {
+    f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(static_cast<uintptr_t>(integer(a[next++])));
+  };
+  take(f_route_select);
+  take(f_route_select_bwd);
+  take(f_route_balance_bias);
+  take(f_w4_gate_up_swiglu);
+  take(f_w4_down_workspace_size);
+  take(f_w4_down_combine);
+  take(f_few_experts_workspace_size);
+  take(f_few_experts);
+  take(f_few_layer_workspace_size);
+  take(f_few_layer);
+  take(f_block_norm);
+  take(f_block_norm_bwd_workspace_size);
+  take(f_block_norm_bwd);
+  take(f_grad_clip_workspace_size);
+  take(f_grad_clip);
   Py_INCREF(a[0]);
   Py_XSETREF(g_check, a[0]);
   Py_RETURN_NONE;
@@ -325,6 +621,11 @@ PyMethodDef methods[] = {
     {"route_balance_bias", FAST(route_balance_bias), nullptr},
     {"w4_gate_up_swiglu", FAST(w4_gate_up_swiglu), nullptr},
     {"w4_down_combine", FAST(w4_down_combine), nullptr},
+    {"few_experts", FAST(few_experts), nullptr},
+    {"few_layer", FAST(few_layer), nullptr},
+    {"block_norm", FAST(block_norm), nullptr},
+    {"block_norm_bwd", FAST(block_norm_bwd), nullptr},
+    {"grad_clip", FAST(grad_clip), nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};

@@ -24,6 +24,7 @@ enum : uint32_t {
   kKernCombine = 4,
   kKernRouteSelect = 5,
   kKernW4 = 6,
+  kKernFew = 7,
 };
 
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t code, uint32_t kernel,

@@ -141,6 +141,52 @@ cudaError_t launch_w4_quantize(const uint16_t* w, int64_t rows, int64_t N, int64
 cudaError_t launch_w4_dequantize(const uint32_t* q, const uint16_t* scales, const uint8_t* zeros, int64_t rows,
                                  int64_t N, int64_t group, uint16_t* w, cudaStream_t stream);
 
+// The expert layer for a few tokens (few.cu).  I_s 0: no shared expert.
+struct FewShape {
+  int64_t T, H, E, k, I, I_s;
+};
+struct FewWeights {
+  const uint16_t *gate_up, *down, *sh_gate_up, *sh_down;
+};
+size_t few_experts_workspace_bytes(const FewShape& s);
+cudaError_t launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids, const float* w,
+                               const FewWeights& weights, uint16_t* y, void* ws, const DeviceInfo& dev,
+                               cudaStream_t stream);
+
+// A block's norms with its gate and residual (block_norm.cu): x the residual
+// stream, y the block's output, w, v, g the weights of the norms and the gate
+// (each nullable), groups of consecutive rows with a gate each (0: none).
+struct BlockNorm {
+  const void* x;
+  const uint16_t* y;
+  const void *w, *v, *g;
+  int x_f32, w_f32, v_f32, g_f32;
+  int64_t T, H, groups;
+  float a, b, eps;
+};
+struct BlockNormGrads {
+  void* x;
+  uint16_t* y;
+  void *w, *v, *g;
+};
+int64_t block_norm_max_width();
+cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, cudaStream_t stream);
+size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v);
+cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const void* dr, const float* stats,
+                                  const BlockNormGrads& d, void* ws, cudaStream_t stream);
+
+// The norm of a list of gradients, and the list scaled (grad_clip.cu); dst
+// null: the norm alone.  The arrays are on the host.
+struct GradList {
+  const void* const* src;
+  void* const* dst;
+  const int64_t* size;
+  const uint8_t* f32;
+  int64_t n;
+};
+size_t grad_norm_workspace_bytes(const GradList& g);
+cudaError_t launch_grad_clip(const GradList& g, float max_norm, float eps, float* norm, void* ws, cudaStream_t stream);
+
 // Expert-parallel dispatch pieces (ep.cu).
 size_t sort_chunks_workspace_bytes(int64_t A, int64_t B);
 cudaError_t launch_sort_chunks(const int32_t* counts, int64_t A, int64_t B, int64_t N, int32_t* src_of,

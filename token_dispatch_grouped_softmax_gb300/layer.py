@@ -335,6 +335,20 @@ def moe_forward_w4(x, w_router, experts, k, bias=None, shared=None, w_split=None
         return ops.w4_down_combine(h, ids, w, *experts.down, y_shared=y_shared), ids, w
 
 
+def moe_forward_few(x, w_router, gate_up, down, k, bias=None, sh_gate_up=None, sh_down=None, routing=None,
+                    balance_bias=None):
+    """y [T, H] bf16 of a few tokens (T at most 128) through bf16 experts, and the slots' ids and w: the layer of a decode step, as
+    moe_forward_w4 for weights that are not quantised.  Rows stay in slot
+    order, the experts' products in fp32 until the tokens' sums; a token's
+    result does not depend on the batch."""
+    if routing is None:
+        if balance_bias is not None:
+            raise ValueError("balance_bias needs a Routing")
+        routing = Routing()
+    return ops.layer_few(x, w_router, gate_up, down, k, bias, balance_bias, sh_gate_up, sh_down, routing.score,
+                         routing.n_groups, routing.top_groups, routing.group_score, routing.renorm, routing.scale)
+
+
 class DecodeGraph:
     """moe_forward_w4 captured once as a CUDA graph for a fixed token count:
     write a step's tokens into ``x`` (or pass them to ``__call__``); a replay

@@ -159,7 +159,8 @@ def _choice(table, value, name):
     return table[value]
 
 
-# The functions up to w4_down_combine check their tensors, allocate and call
+# The functions up to w4_down_combine, and those of a decode step's bf16
+# experts, a block's norms and the gradients' norm, check their tensors, allocate and call
 # in the extension _binding (csrc/binding.cpp): a decode step's kernels run for
 # a few microseconds, less than the same done in Python.
 
@@ -250,6 +251,72 @@ def w4_dequantize(qweight, scales, zeros=None):
     w = torch.empty((rows, N), dtype=_BF16, device=qweight.device)
     call("moe_w4_dequantize", _p(qweight), _p(scales), _p(zeros), rows, N, group, _p(w), _stream())
     return w
+
+
+# ------------------------------------------- the layer for a few tokens
+
+def experts_few(x, ids, w, gate_up, down, sh_gate_up=None, sh_down=None, out=None):
+    """y [T, H] bf16 with y_t = sum_j w[t, j] (silu(x_t . Wg) * (x_t . Wu)) . Wd,
+    e = ids[t, j] (-1: an empty slot, adds nothing), plus the shared expert's
+    output: the bf16 experts of a decode step in slot order, each weight read
+    once (moe_few_experts).
+
+    x [T, H] bf16, ids [T, k] int32, w [T, k] fp32, gate_up [E*H, 2I], down
+    [E*I, H], sh_gate_up [H, 2 I_s], sh_down [I_s, H] bf16; T at most 128."""
+    return binding().few_experts(x, ids, w, gate_up, down, sh_gate_up, sh_down, out)
+
+
+def layer_few(x, w_router, gate_up, down, k, bias=None, balance_bias=None, sh_gate_up=None, sh_down=None, score="softmax",
+              n_groups=1, top_groups=1, group_score="top2", renorm=True, scale=1.0):
+    """y [T, H] bf16, ids [T, k] int32 and w [T, k] fp32: route_logits,
+    route_select and experts_few as one call (moe_few_layer)."""
+    return binding().few_layer(x, w_router, gate_up, down, k, bias, balance_bias, sh_gate_up, sh_down,
+                               _choice(_SCORES, score, "score"), n_groups, top_groups,
+                               _choice(_GROUP_SCORES, group_score, "group_score"), bool(renorm), scale)
+
+
+# ------------------------------------------------- norms around a block
+
+def block_norm(x, weight=None, branch=None, post_weight=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6,
+               save_for_backward=False):
+    """(r, h, stats): what stands between two blocks of a model, fused.
+
+    r = residual_scale x + branch_scale gate n, with n the block's output
+    branch [T, H] bf16, normed by post_weight where that is given, and
+    h = rms_norm(r) weight [T, H] bf16, the next block's input.  x [T, H] (the
+    residual stream) and r are fp32 or bf16; weight, post_weight [H] and gate
+    [gates, H] fp32 or bf16, gates a divisor of T (a gate for every T / gates
+    consecutive rows; 1: a learned scale; T: one a row).  Without branch r is
+    None and h norms x; without weight h is None.  stats [2, T] fp32 with
+    save_for_backward, else None, for block_norm_bwd (moe_block_norm)."""
+    return binding().block_norm(x, weight, branch, post_weight, gate, residual_scale, branch_scale, eps,
+                                bool(save_for_backward))
+
+
+def block_norm_bwd(dh, dr, x, stats, weight=None, branch=None, post_weight=None, gate=None, residual_scale=1.0,
+                   branch_scale=1.0):
+    """dict(dx, d_branch, d_weight, d_post_weight, d_gate) of block_norm for
+    upstream dh (of h; None without weight) and dr (of r; None: 0), each of
+    its operand's type and None where the operand is.  x and branch are the
+    forward's inputs (moe_block_norm_bwd)."""
+    return dict(zip(("dx", "d_branch", "d_weight", "d_post_weight", "d_gate"),
+                    binding().block_norm_bwd(dh, dr, stats, x, weight, branch, post_weight, gate, residual_scale,
+                                             branch_scale)))
+
+
+# -------------------------------------- the gradients' norm, and clipping
+
+def grad_norm(grads):
+    """The 2-norm over a list of gradients (fp32 or bf16, of any shapes) as an
+    fp32 scalar on the device."""
+    return binding().grad_clip(grads, None, 0.0, 0.0)
+
+
+def clip_grads(grads, max_norm, out=None, eps=1e-6):
+    """Scales the gradients by min(1, max_norm / (norm + eps)) and returns
+    their norm (grad_norm's).  In place, or into out: a list of tensors of the
+    same sizes and types that overlap nothing (out[i] may be grads[i])."""
+    return binding().grad_clip(grads, grads if out is None else out, max_norm, eps)
 
 
 def permute(ids, E, w=None):
