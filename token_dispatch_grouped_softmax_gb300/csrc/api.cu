@@ -395,8 +395,8 @@ int moe_few_experts(const uint16_t* x, const int32_t* ids, const float* w, const
   moe::DeviceInfo dev;
   rc = moe::current_device(&dev);
   if (rc != MOE_OK) return rc;
-  return cuda_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev,
-                                             static_cast<cudaStream_t>(stream)));
+  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev,
+                                                  static_cast<cudaStream_t>(stream)));
 }
 
 int moe_few_layer_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes) {
@@ -441,7 +441,7 @@ int moe_few_layer(const uint16_t* x, const float* w_router, const float* bias, c
                            (int)top_groups, scale};
   e = moe::launch_route_select(logits, false, balance_bias, T, E, k, c, ids, w, st);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  return cuda_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev, st));
+  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev, st));
 }
 
 /* --------------------------------------------- norms around a block */

@@ -149,9 +149,9 @@ struct FewWeights {
   const uint16_t *gate_up, *down, *sh_gate_up, *sh_down;
 };
 size_t few_experts_workspace_bytes(const FewShape& s);
-cudaError_t launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids, const float* w,
-                               const FewWeights& weights, uint16_t* y, void* ws, const DeviceInfo& dev,
-                               cudaStream_t stream);
+// 0 = enqueued, -1 = tensor map rejected, 1 = launch failed
+int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids, const float* w, const FewWeights& weights,
+                       uint16_t* y, void* ws, const DeviceInfo& dev, cudaStream_t stream);
 
 // A block's norms with its gate and residual (block_norm.cu): x the residual
 // stream, y the block's output, w, v, g the weights of the norms and the gate
