@@ -367,8 +367,6 @@ int few_pointers(const uint16_t* x, const moe::FewWeights& w, int64_t I_s, const
   return aligned16(w.sh_gate_up) && aligned16(w.sh_down) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
-size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 }  // namespace
 
 int moe_few_experts_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int64_t I, int64_t I_s, size_t* bytes) {
@@ -395,7 +393,7 @@ int moe_few_experts(const uint16_t* x, const int32_t* ids, const float* w, const
   moe::DeviceInfo dev;
   rc = moe::current_device(&dev);
   if (rc != MOE_OK) return rc;
-  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev,
+  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, false, dev,
                                                   static_cast<cudaStream_t>(stream)));
 }
 
@@ -403,8 +401,7 @@ int moe_few_layer_workspace_size(int64_t T, int64_t H, int64_t E, int64_t k, int
   if (!bytes) return MOE_ERR_INVALID_ARG;
   const int rc = few_check(T, H, E, k, I, I_s);
   if (rc != MOE_OK) return rc;
-  *bytes = up256(moe::few_experts_workspace_bytes({T, H, E, k, I, I_s})) + up256((size_t)(T * E) * sizeof(float)) +
-           moe::route_workspace_bytes(T, H, E);
+  *bytes = moe::few_experts_workspace_bytes({T, H, E, k, I, I_s});
   return MOE_OK;
 }
 
@@ -432,16 +429,12 @@ int moe_few_layer(const uint16_t* x, const float* w_router, const float* bias, c
   if (rc != MOE_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const moe::FewShape shape{T, H, E, k, I, I_s};
-  uint8_t* at = static_cast<uint8_t*>(workspace) + up256(moe::few_experts_workspace_bytes(shape));
-  float* logits = reinterpret_cast<float*>(at);
-  cudaError_t e = moe::launch_route(x, w_router, bias, T, H, E, k, ids, w, logits, at + up256((size_t)(T * E) * sizeof(float)),
-                                    dev, st);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
   const moe::RouteChoice c{score == MOE_SCORE_SIGMOID, group_score == MOE_GROUP_TOP2, renorm != 0, (int)n_groups,
                            (int)top_groups, scale};
-  e = moe::launch_route_select(logits, false, balance_bias, T, E, k, c, ids, w, st);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, dev, st));
+  if (moe::launch_few_route(shape, x, w_router, bias, balance_bias, c, ids, w, static_cast<uint32_t*>(workspace),
+                            moe::few_experts_counters(shape), dev, st) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return moe::gemm_status(moe::launch_few_experts(shape, x, ids, w, weights, y, workspace, true, dev, st));
 }
 
 /* --------------------------------------------- norms around a block */

@@ -70,6 +70,12 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// n / d with magic = floor((2^32 - 1) / d): at most one too small before the fix.
+__device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t d, uint32_t magic) {
+  const uint32_t q = __umulhi(n, magic);
+  return q + (n - q * d >= d);
+}
+
 // ------------------------------------------- programmatic dependent launch
 // Every kernel here is launched with programmatic stream serialization, so
 // it may start while the kernel before it on the stream still runs.

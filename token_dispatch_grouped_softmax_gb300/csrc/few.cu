@@ -12,7 +12,7 @@
 // waits only for units that running blocks have drawn: no block has to be
 // resident for another to go on.
 //
-//   warp 3        draws the units, little ahead of the loads.
+//   warp 3        draws the units, one ahead of the loads.
 //   warp 0        keeps a ring of 128 x 128 tiles of the weights full by TMA.  It waits for nothing but free stages:
 //                 while h is not ready, down's weights already arrive.
 //   warp 1        gathers the rows' 128 values of K for each tile (TMA
@@ -45,16 +45,16 @@ constexpr int kFewStage = kFewTile + 2 * kFewHalf;
 constexpr int kFewMaxStages = 5;
 constexpr int kFewParts = 8;                   // of K, at most
 constexpr int kFewAcc = 8;                     // accumulators in TMEM
+constexpr uint32_t kFewTmem = kFewAcc * kFewRows;   // columns
 constexpr int kFewQueue = 16;                  // units between warp 3 and the epilogue
-constexpr int kFewAhead = 2;                   // units that warp 3 has drawn beyond warp 0's
-constexpr int kFewSmem = 232448;               // what a block may have (227 KB)
-constexpr int kPrepThreads = 1024;
+constexpr int kFewSmem = 232448 - 256;         // what a block may have (227 KB) but for its static variables
 
-enum : uint32_t { kFewSitePrep = 1, kFewSiteTile = 2, kFewSiteRows = 3, kFewSiteMma = 4, kFewSiteEpi = 5, kFewSiteHidden = 6, kFewSiteUnits = 7 };
+enum : uint32_t { kFewSiteIds = 1, kFewSiteTile = 2, kFewSiteRows = 3, kFewSiteMma = 4, kFewSiteEpi = 5, kFewSiteHidden = 6, kFewSiteUnits = 7 };
 
 // One of an expert's two products: K rows in parts of part_k, N columns in tiles.
 struct FewProduct {
   int K, parts, part_k, tiles;
+  uint32_t units_magic, tiles_magic;   // of tiles * parts, and of tiles (div_by)
 };
 
 struct FewEntry {       // an expert in use
@@ -83,70 +83,66 @@ struct FewParams {      // 64-byte aligned through its CUtensorMap members
   uint32_t* done;       // [entries + 1] finished tiles of h of each entry, the shared expert's last
   uint32_t* hidden;     // [chunks + shared chunks][tiles] parts of a gate_up tile that are there
   uint32_t* arrived;    // [tiles of down][T] slots' parts of a token's columns that are there
-  int* head;            // entries, chunks
-  FewEntry* entries;
-  uint16_t* list;       // slots by expert
-  uint16_t* of_chunk;   // entry of a chunk
-  uint8_t* valid;       // slots of a token that name an expert
   float *part_gu, *part_sh_gu, *part_dn, *part_sh_dn;
   uint16_t *h, *sh_h;
   uint32_t* status;
   uint64_t wait_limit_ns;
   FewProduct gu, dn, sh_gu, sh_dn;
   int T, H, E, k, I, I_s;
+  uint32_t k_magic;
   int max_entries, max_chunks, sh_chunks;
-  int zero_words;       // counters from `ticket` on
   int stages;
   int stall;
 };
 
 // --------------------------------------------------------------- the lists
 
-// One block: clears the counters and sorts the slots by expert (stable).
-__global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_constant__ FewParams p) {
-  extern __shared__ int few_prep_smem[];
-  int* ids = few_prep_smem;                    // [S]
-  int* first = ids + p.T * p.k;                // [E] counts, then the first place
-  __shared__ int warp_sums[2][32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slots = p.T * p.k;
-  for (int i = tid; i < p.zero_words; i += kPrepThreads) p.ticket[i] = 0;
-  for (int e = tid; e < p.E; e += kPrepThreads) first[e] = 0;
+// What every block makes of the ids for itself (a launch of its own would take
+// longer): the slots sorted by expert, stable, so that every block's are the
+// same.
+struct FewLists {
+  FewEntry* entries;
+  uint16_t* of_chunk;   // entry of a chunk
+  uint16_t* list;       // slots by expert
+  uint32_t* valid;      // which slots of a token name an expert
+  float* w;             // [S]
+};
+
+// Returns the chunks.  room: [S + E] ints that are free.
+__device__ __forceinline__ int few_lists(const FewParams& p, const FewLists& out, int* room) {
+  __shared__ int warp_sums[2][kFewThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slots = p.T * p.k;
+  int *ids = room, *first = room + (slots + 3) / 4 * 4;
+  for (int e = tid; e < p.E; e += kFewThreads) first[e] = 0;
   bool bad = false;
-  for (int i = tid; i < slots; i += kPrepThreads) {
+  for (int i = tid; i < slots; i += kFewThreads) {
     int e = p.ids[i];
     if (e < 0 || e >= p.E) {
       bad |= e != -1;
       e = -1;
     }
     ids[i] = e;
+    out.w[i] = p.w[i];
   }
-  if (bad) report_status(p.status, kStatusDevice, kKernFew, kFewSitePrep);
+  if (bad) report_status(p.status, kStatusDevice, kKernFew, kFewSiteIds);
   __syncthreads();
-  int rank[4];                                 // slots <= 4096
+  for (int i = tid; i < slots; i += kFewThreads)
+    if (ids[i] >= 0) atomicAdd(&first[ids[i]], 1);
+  if (tid < p.T) {
+    uint32_t n = 0;
+    for (int j = 0; j < p.k; ++j) n |= (uint32_t)(ids[tid * p.k + j] >= 0) << j;
+    out.valid[tid] = n;
+  }
+  __syncthreads();
+  // rows, chunks and entries before each expert, two experts a thread
+  int rows[2], chunks[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int i = tid + q * kPrepThreads;
-    rank[q] = -1;
-    if (i < slots && ids[i] >= 0) {
-      int r = 0;
-      for (int j = 0; j < i; ++j) r += ids[j] == ids[i];
-      rank[q] = r;
-      atomicAdd(&first[ids[i]], 1);
-    }
+  for (int i = 0; i < 2; ++i) {
+    rows[i] = 2 * tid + i < p.E ? first[2 * tid + i] : 0;
+    chunks[i] = (rows[i] + kFewRows - 1) / kFewRows;
   }
-  for (int t = tid; t < p.T; t += kPrepThreads) {
-    int n = 0;
-    for (int j = 0; j < p.k; ++j) n += ids[t * p.k + j] >= 0;
-    p.valid[t] = (uint8_t)n;
-  }
-  __syncthreads();
-  // experts in order: rows, chunks and entries before each (E <= 1024: one a thread)
-  const int rows = tid < p.E ? first[tid] : 0;
-  const int chunks = (rows + kFewRows - 1) / kFewRows;
-  int a = rows, b = chunks << 16 | (rows > 0);   // inclusive sums: rows; chunks and entries
+  int a = rows[0] + rows[1], b = (chunks[0] + chunks[1]) << 16 | ((rows[0] > 0) + (rows[1] > 0));   // inclusive sums
+  const int a0 = a, b0 = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
@@ -161,27 +157,43 @@ __global__ void __launch_bounds__(kPrepThreads) few_prep_kernel(const __grid_con
   }
   __syncthreads();
   int all = 0;
-  for (int i = 0; i < kPrepThreads / 32; ++i) {
+#pragma unroll
+  for (int i = 0; i < kFewThreads / 32; ++i) {
+    const int n = warp_sums[1][i];
     if (i < warp) {
       a += warp_sums[0][i];
-      b += warp_sums[1][i];
+      b += n;
     }
-    all += warp_sums[1][i];
+    all += n;
   }
-  const int row0 = a - rows, chunk0 = (b >> 16) - chunks, entry = (b & 0xFFFF) - (rows > 0);
-  if (tid < p.E) first[tid] = row0;
-  if (rows > 0) {
-    p.entries[entry] = FewEntry{tid, row0, rows, chunk0};
-    for (int c = 0; c < chunks; ++c) p.of_chunk[chunk0 + c] = (uint16_t)entry;
-  }
-  if (tid == 0) {
-    p.head[0] = all & 0xFFFF;
-    p.head[1] = all >> 16;
+  int row0 = a - a0, chunk0 = (b - b0) >> 16, entry = (b - b0) & 0xFFFF;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * tid + i;
+    if (e < p.E) first[e] = row0;
+    if (rows[i] > 0) {
+      out.entries[entry] = FewEntry{e, row0, rows[i], chunk0};
+      for (int c = 0; c < chunks[i]; ++c) out.of_chunk[chunk0 + c] = (uint16_t)entry;
+      ++entry;
+    }
+    row0 += rows[i];
+    chunk0 += chunks[i];
   }
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (rank[q] >= 0) p.list[first[ids[tid + q * kPrepThreads]] + rank[q]] = (uint16_t)(tid + q * kPrepThreads);
+#pragma unroll 1
+  for (int i = tid; i < slots; i += kFewThreads) {
+    const int e = ids[i];
+    if (e < 0) continue;
+    int at = first[e], j = 0;   // and the expert's slots before this one
+#pragma unroll 1
+    for (; j + 4 <= i; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(ids + j);
+      at += (o.x == e) + (o.y == e) + (o.z == e) + (o.w == e);
+    }
+    for (; j < i; ++j) at += ids[j] == e;
+    out.list[at] = (uint16_t)i;
+  }
+  return all >> 16;
 }
 
 // --------------------------------------------------------------- the units
@@ -210,7 +222,7 @@ __device__ __forceinline__ FewUnit few_unit(const FewParams& p, const FewEntry* 
   const uint32_t per = f.tiles * f.parts;
   int entry = 0, chunk0 = 0, n_chunks = p.sh_chunks, rows = p.T, row0 = 0, expert = 0;
   if (!x.shared) {
-    entry = of_chunk[u / per];
+    entry = of_chunk[div_by(u, per, f.units_magic)];
     const FewEntry e = entries[entry];
     chunk0 = e.chunk0;
     rows = e.rows;
@@ -221,18 +233,29 @@ __device__ __forceinline__ FewUnit few_unit(const FewParams& p, const FewEntry* 
   // an expert's chunks read the same weights one after another, then come the
   // tiles, whose columns lie side by side, then the parts
   const uint32_t local = u - chunk0 * per;
-  const int c = local % n_chunks;
-  const uint32_t at = local / n_chunks;
+  const uint32_t at = n_chunks == 1 ? local : local / n_chunks;
+  const int c = (int)(local - at * n_chunks);
   x.entry = x.shared ? p.max_entries : entry;
   x.chunk = (x.shared ? p.max_chunks : chunk0) + c;
   x.row0 = row0 + c * kFewRows;
   x.rows = min(kFewRows, rows - c * kFewRows);
-  x.tile = at % f.tiles;
-  x.part = at / f.tiles;
+  x.part = (int)div_by(at, f.tiles, f.tiles_magic);
+  x.tile = (int)at - x.part * f.tiles;
   x.k0 = x.part * f.part_k;
   x.halves = min(f.part_k, f.K - x.k0) / 64;
   x.w_row = expert * f.K + x.k0;
   return x;
+}
+
+// A bounded wait whose first try is in line.  With few tokens a block runs
+// most of its code once, so that fetching it counts: it is kept short.
+struct FewWait {
+  volatile int* abort;
+  uint64_t limit_ns;
+  uint32_t* status;
+};
+__device__ __noinline__ bool few_wait_more(uint32_t bar, uint32_t parity, const FewWait& w, uint32_t site) {
+  return mbar_wait_bounded(bar, parity, w.abort, w.limit_ns, w.status, site, kKernFew);
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -262,11 +285,12 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-constexpr size_t few_tables_bytes(int64_t entries, int64_t chunks, int64_t slots) {
-  return (size_t)(entries * sizeof(FewEntry) + (chunks + slots) * sizeof(uint16_t) + 15) & ~(size_t)15;
+constexpr size_t few_tables_bytes(int64_t entries, int64_t chunks, int64_t slots, int64_t T) {
+  return (size_t)(entries * sizeof(FewEntry) + (T + slots) * 4 + (chunks + slots) * sizeof(uint16_t) + 15) & ~(size_t)15;
 }
-constexpr int kFewBars = 3 * kFewMaxStages + 2 * kFewAcc + 2 * kFewQueue + kFewAhead + 1;
-constexpr size_t kFewFixed = kFewBars * 8 + kFewQueue * sizeof(FewUnit) + 64;
+constexpr int kFewBars = 3 * kFewMaxStages + 2 * kFewAcc + 2 * kFewQueue + 2;
+constexpr int kFewSwap = 8 * 128;              // floats of a group: eight rows of its unit
+constexpr size_t kFewFixed = (kFewBars * 8 + kFewQueue * sizeof(FewUnit) + 64 + kFewGroups * kFewSwap * 4 + 15) & ~15;
 
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ uint8_t few_smem_raw[];
@@ -276,8 +300,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kFewQueue);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* group_word = tmem_slot + 2;        // [groups]
+  float* swap = reinterpret_cast<float*>(tmem_slot + 16);
   FewEntry* entries = reinterpret_cast<FewEntry*>(smem + p.stages * kFewStage + kFewFixed);
-  uint16_t* of_chunk = reinterpret_cast<uint16_t*>(entries + p.max_entries);
+  uint32_t* valid = reinterpret_cast<uint32_t*>(entries + p.max_entries);
+  float* w = reinterpret_cast<float*>(valid + p.T);
+  uint16_t* of_chunk = reinterpret_cast<uint16_t*>(w + p.T * p.k);
   uint16_t* list = of_chunk + p.max_chunks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = smem_u32(smem), bar0 = smem_u32(bars);
@@ -289,7 +316,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   auto read_bar = [&](int a) { return bar0 + 8u * (3 * kFewMaxStages + kFewAcc + a); };  // it has been read
   auto unit_bar = [&](int q) { return bar0 + 8u * (3 * kFewMaxStages + 2 * kFewAcc + q); };
   auto seen_bar = [&](int q) { return bar0 + 8u * (3 * kFewMaxStages + 2 * kFewAcc + kFewQueue + q); };
-  auto begun_bar = [&](int i) { return bar0 + 8u * (3 * kFewMaxStages + 2 * kFewAcc + 2 * kFewQueue + i); };   // warp 0 has taken a unit
+  const uint32_t issued_bar = bar0 + 8u * (kFewBars - 2);   // a unit's last loads are being issued
   const uint32_t drain_bar = bar0 + 8u * (kFewBars - 1);
 
   if (tid == 0) {
@@ -306,7 +333,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       mbar_init(unit_bar(q), 1);
       mbar_init(seen_bar(q), 7);   // warps 0 to 2, four warps of a group
     }
-    for (int i = 0; i < kFewAhead; ++i) mbar_init(begun_bar(i), 1);
+    mbar_init(issued_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -316,28 +343,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     tma_prefetch_desc(&p.tm_h);
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(tmem_slot), kFewAcc * kFewRows);
+    tmem_alloc(smem_u32(tmem_slot), kFewTmem);
     tmem_relinquish();
   }
   pdl_wait();
   pdl_trigger();
-  const int n_entries = p.head[0], n_chunks = p.head[1];
-  for (int i = tid; i < n_entries; i += kFewThreads) entries[i] = p.entries[i];
-  for (int i = tid; i < n_chunks; i += kFewThreads) of_chunk[i] = p.of_chunk[i];
-  for (int i = tid; i < p.T * p.k; i += kFewThreads) list[i] = p.list[i];
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x)   // tokens without an expert
-    if (p.valid[t] == 0 && p.I_s == 0)
-      for (int c = tid * 8; c < p.H; c += kFewThreads * 8)
-        *reinterpret_cast<uint4*>(p.y + (int64_t)t * p.H + c) = make_uint4(0, 0, 0, 0);
+  uint32_t next = 0;
+  if (tid == 96) next = atomicAdd(p.ticket, 1u);   // warp 3's first, while the slots are sorted
+  const int n_chunks = few_lists(p, FewLists{entries, of_chunk, list, valid, w}, reinterpret_cast<int*>(smem));
+  fence_proxy_async_smem();   // the sort's writes into the ring, before TMA's
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x)   // tokens without an expert
+    if (valid[t] == 0 && p.I_s == 0)
+      for (int c = tid * 8; c < p.H; c += kFewThreads * 8)
+        *reinterpret_cast<uint4*>(p.y + (int64_t)t * p.H + c) = make_uint4(0, 0, 0, 0);
+  const FewWait bounds{abort_flag, p.wait_limit_ns, p.status};
   auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-    return mbar_wait_bounded(bar, parity, abort_flag, p.wait_limit_ns, p.status, site, kKernFew);
+    return mbar_try_wait(bar, parity) || few_wait_more(bar, parity, bounds, site);
   };
-  auto wait_warp = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-    return mbar_wait_warp(bar, parity, abort_flag, p.wait_limit_ns, p.status, site, kKernFew);
+  auto wait_warp = [&](uint32_t bar, uint32_t parity, uint32_t site) {   // every lane acquires the phase itself
+    return __all_sync(0xffffffffu, wait(bar, parity, site));
   };
   // after an early stop: a stage's copies have landed (bounded)
   auto land = [&](uint32_t bar, uint32_t parity) {
@@ -348,12 +376,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
   if (warp == 3) {
     if (lane == 0) {
-      uint32_t next = atomicAdd(p.ticket, 1u);
       for (int i = 0, ends = 0; ends < kFewGroups; ++i) {
         const FewUnit x = few_unit(p, entries, of_chunk, n_chunks, next);
         const int q = i % kFewQueue;
-        // no further ahead of the loads, so that the blocks draw evenly
-        if (i >= kFewAhead && x.kind != kEnd && !wait(begun_bar(i % kFewAhead), (i / kFewAhead - 1) & 1, kFewSiteUnits)) break;
         if (!wait(seen_bar(q), (i / kFewQueue & 1) ^ 1u, kFewSiteUnits)) break;
         queue[q] = x;
         mbar_arrive(unit_bar(q));
@@ -361,6 +386,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           ++ends;
           continue;
         }
+        // the next only once this one's loads are out, so that the blocks draw
+        // evenly; the ring's loads in flight cover the draw
+        if (!wait(issued_bar, i & 1, kFewSiteUnits)) break;
         next = atomicAdd(p.ticket, 1u);
       }
     }
@@ -375,7 +403,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         if (!ok) break;
         const FewUnit x = queue[q];
         mbar_arrive(seen_bar(q));
-        mbar_arrive(begun_bar(i % kFewAhead));
         if (x.kind == kEnd) break;
         const CUtensorMap* map = x.kind == kGateUp ? (x.shared ? &p.tm_sh_gate_up : &p.tm_gate_up)
                                                    : (x.shared ? &p.tm_sh_down : &p.tm_down);
@@ -385,6 +412,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         for (int s = 0; s < x.halves; s += 2) {
           ok = wait(free_bar(stage), phase ^ 1u, kFewSiteTile);
           if (!ok) break;
+          if (s + 2 >= x.halves) mbar_arrive(issued_bar);
           if (!p.stall) {
             const uint32_t dst = ring + stage * kFewStage;
             mbar_arrive_expect_tx(tile_bar(stage), both ? kFewTile : kFewTile / 2);
@@ -419,7 +447,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int at = x.row0 + min(4 * lane + r, x.rows - 1);
-        row[r] = x.shared ? at : x.kind == kDown ? list[at] : list[at] / p.k;
+        row[r] = x.shared ? at : x.kind == kDown ? list[at] : (int)div_by(list[at], p.k, p.k_magic);
       }
       const CUtensorMap* map = x.kind == kGateUp ? &p.tm_x : x.shared ? &p.tm_sh_h : &p.tm_h;
       const int groups = (x.rows + 3) / 4;
@@ -531,110 +559,141 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
       const bool gate_up = x.kind == kGateUp;
       const int I = x.shared ? p.I_s : p.I;
       const FewProduct& f = gate_up ? (x.shared ? p.sh_gu : p.gu) : (x.shared ? p.sh_dn : p.dn);
+      auto row_of = [&](int r) { return x.shared ? x.row0 + r : (int)list[x.row0 + r]; };   // a slot, or the token
+      uint16_t* h = (x.shared ? p.sh_h : p.h) + 64 * x.tile + (m & 63);
+      // h is rounded as the grouped GEMMs round it: an operand of the tensor cores
+      auto store_h = [&](int r, float g, float u) {
+        h[(int64_t)row_of(r) * I] = __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef(g, 1.0f + __expf(-g)) * u));
+      };
       float* part = gate_up ? (x.shared ? p.part_sh_gu : p.part_gu) : (x.shared ? p.part_sh_dn : p.part_dn);
       const int width = gate_up ? 2 * I : p.H;
       const int c = gate_up ? (m < 64 ? 64 * x.tile + m : I + 64 * x.tile + m - 64) : 128 * x.tile + m;
-      if (c < width) {
+      const bool whole = gate_up && f.parts == 1;
+      float* rows = swap + group * kFewSwap;   // [8][128]
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r) {
-          if (r < x.rows) {
-            const int row = x.shared ? x.row0 + r : list[x.row0 + r];
-            __stcg(part + ((int64_t)row * f.parts + x.part) * width + c, v[r]);
-          }
+      for (int r0 = 0; r0 < kFewRows; r0 += 8) {
+        if (r0 >= x.rows) break;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) rows[128 * r + m] = v[r0 + r];
+        const int n = min(8, x.rows - r0);
+        if (whole) {   // gate in lanes 0..63, up in 64..127
+          group_sync(group);
+#pragma unroll 1
+          for (int r = m >> 6; r < n; r += 2) store_h(r0 + r, rows[128 * r + (m & 63)], rows[128 * r + 64 + (m & 63)]);
+          group_sync(group);
+        } else if (c < width) {
+#pragma unroll 1
+          for (int r = 0; r < n; ++r) __stcg(part + ((int64_t)row_of(r0 + r) * f.parts + x.part) * width + c, rows[128 * r + m]);
         }
       }
-      group_sync(group);
-      if (m < 32) __threadfence();   // the group's stores, before the counts
-      if (gate_up) {
-        if (m == 0) group_word[group] = atomicAdd(p.hidden + (x.shared ? (int64_t)p.max_chunks * p.gu.tiles + (int64_t)(x.chunk - p.max_chunks) * f.tiles
-                                                                       : (int64_t)x.chunk * f.tiles) + x.tile, 1u);
+      if (!whole) {
         group_sync(group);
-        if (group_word[group] + 1 != (uint32_t)f.parts) continue;
-        __threadfence();
-        uint16_t* h = x.shared ? p.sh_h : p.h;
-        const int n = 64 * x.tile + (m & 63);
-        for (int r = m >> 6; r < x.rows; r += 2) {
-          const int row = x.shared ? x.row0 + r : list[x.row0 + r];
-          const float* from = part + (int64_t)row * f.parts * width + n;
-          float g = 0.f, u = 0.f;
-#pragma unroll
-          for (int j = 0; j < kFewParts; ++j)
-            if (j < f.parts) {
-              g += __ldcg(from + (int64_t)j * width);
-              u += __ldcg(from + (int64_t)j * width + I);
+        if (m < 32) {
+          __threadfence();   // the group's stores, before the counts
+          uint32_t answer = 0;
+          if (gate_up) {
+            if (m == 0) {
+              const int64_t at = x.shared ? (int64_t)p.max_chunks * p.gu.tiles + (int64_t)(x.chunk - p.max_chunks) * f.tiles
+                                          : (int64_t)x.chunk * f.tiles;
+              answer = atomicAdd(p.hidden + at + x.tile, 1u) + 1 == (uint32_t)f.parts;
             }
-          // rounded as the grouped GEMMs round it: an operand of the tensor cores
-          h[(int64_t)row * I + n] = __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef(g, 1.0f + __expf(-g)) * u));
-        }
-        fence_proxy_async_all();   // h is read by TMA
-        group_sync(group);
-        if (m == 0) {
-          __threadfence();
-          atomicAdd(p.done + x.entry, 1u);
-        }
-      } else {
-        if (m < 32) {   // the rows' tokens whose columns are complete
-          int t = 0;
-          bool last = false;
-          if (m < x.rows) {
-            t = x.shared ? x.row0 + m : list[x.row0 + m] / p.k;
-            const uint32_t all = (uint32_t)p.valid[t] * p.dn.parts + (p.I_s ? p.sh_dn.parts : 0);
-            last = atomicAdd(p.arrived + (int64_t)x.tile * p.T + t, 1u) + 1 == all;
+          } else {           // the rows' tokens whose columns are complete
+            bool last = false;
+            if (m < x.rows) {
+              const int t = x.shared ? x.row0 + m : (int)div_by(list[x.row0 + m], p.k, p.k_magic);
+              const uint32_t all = (uint32_t)__popc(valid[t]) * p.dn.parts + (p.I_s ? p.sh_dn.parts : 0);
+              last = atomicAdd(p.arrived + (int64_t)x.tile * p.T + t, 1u) + 1 == all;
+            }
+            answer = __ballot_sync(0xffffffffu, last);
           }
-          const uint32_t mask = __ballot_sync(0xffffffffu, last);
-          if (m == 0) group_word[group] = mask;
+          if (m == 0) group_word[group] = answer;
         }
         group_sync(group);
         uint32_t mask = group_word[group];
-        if (mask) __threadfence();
-        while (mask) {
-          const int r = __ffs(mask) - 1;
-          mask &= mask - 1;
-          if (c >= p.H) continue;
-          const int t = x.shared ? x.row0 + r : list[x.row0 + r] / p.k;
-          float y = 0.f;
-          for (int j0 = 0; j0 < p.k; j0 += 4) {   // four slots' parts in flight
-            float s[4], wt[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int slot = t * p.k + j0 + j;
-              const bool in = j0 + j < p.k && (uint32_t)p.ids[slot] < (uint32_t)p.E;
-              wt[j] = in ? p.w[slot] : 0.f;
-              s[j] = 0.f;
-              const float* from = p.part_dn + (int64_t)slot * p.dn.parts * p.H + c;
-#pragma unroll
-              for (int l = 0; l < kFewParts; ++l)
-                if (in && l < p.dn.parts) s[j] += __ldcg(from + (int64_t)l * p.H);
+        if (mask == 0) continue;
+        __threadfence();
+        if (gate_up) {
+          for (int r = m >> 6; r < x.rows; r += 2) {
+            const float* from = part + (int64_t)row_of(r) * f.parts * width + 64 * x.tile + (m & 63);
+            float g = 0.f, u = 0.f;
+#pragma unroll 4
+            for (int j = 0; j < f.parts; ++j) {
+              g += __ldcg(from + (int64_t)j * width);
+              u += __ldcg(from + (int64_t)j * width + I);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y = fmaf(wt[j], s[j], y);
+            store_h(r, g, u);
           }
-          if (p.I_s) {
-            const float* from = p.part_sh_dn + (int64_t)t * p.sh_dn.parts * p.H + c;
-            float s = 0.f;
+        } else {
+          if (c >= p.H) continue;
+          for (; mask; mask &= mask - 1) {
+            const int r = __ffs(mask) - 1;
+            const int t = x.shared ? x.row0 + r : (int)div_by(list[x.row0 + r], p.k, p.k_magic);
+            const uint32_t used = valid[t];
+            float y = 0.f;
+            if (p.dn.parts == 1) {
+              const float* from = p.part_dn + (int64_t)t * p.k * p.H + c;
+#pragma unroll 1
+              for (int j0 = 0; j0 < p.k; j0 += 8) {   // eight slots' loads in flight
+                float s[8];
 #pragma unroll
-            for (int l = 0; l < kFewParts; ++l)
-              if (l < p.sh_dn.parts) s += __ldcg(from + (int64_t)l * p.H);
-            y += s;
+                for (int j = 0; j < 8; ++j) s[j] = used >> j0 >> j & 1u ? __ldcg(from + (int64_t)(j0 + j) * p.H) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (used >> j0 >> j & 1u) y = fmaf(w[t * p.k + j0 + j], s[j], y);
+              }
+            } else {
+#pragma unroll 1
+              for (int j = 0; j < p.k; ++j) {
+                if (!(used >> j & 1u)) continue;
+                const float* from = p.part_dn + (int64_t)(t * p.k + j) * p.dn.parts * p.H + c;
+                float s = 0.f;
+#pragma unroll 4
+                for (int l = 0; l < p.dn.parts; ++l) s += __ldcg(from + (int64_t)l * p.H);
+                y = fmaf(w[t * p.k + j], s, y);
+              }
+            }
+            if (p.I_s) {
+              const float* from = p.part_sh_dn + (int64_t)t * p.sh_dn.parts * p.H + c;
+              float s = 0.f;
+#pragma unroll 4
+              for (int l = 0; l < p.sh_dn.parts; ++l) s += __ldcg(from + (int64_t)l * p.H);
+              y += s;
+            }
+            p.y[(int64_t)t * p.H + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
           }
-          p.y[(int64_t)t * p.H + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
         }
+        if (!gate_up) continue;
+      }
+      fence_proxy_async_all();   // h is read by TMA
+      group_sync(group);
+      if (m == 0) {
+        __threadfence();
+        atomicAdd(p.done + x.entry, 1u);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) tmem_dealloc(tmem, kFewAcc * kFewRows);
+  if (warp == 2) tmem_dealloc(tmem, kFewTmem);
 }
 
-// K in at most 8 parts of at least 256 rows, whole stages.
-FewProduct few_product(int64_t K, int64_t tiles) {
-  FewProduct f;
+// A unit takes the whole of K where one token's slots make kFewUnits units of
+// a product, so that a decoded token keeps most SMs busy: its sums stay in
+// TMEM, and h needs no partial sums through memory.  With fewer units K is
+// split: in at most 8 parts of at least 256 rows, whole stages.  K, the tiles
+// and k alone decide, so that a token's sums do not depend on the batch.
+constexpr int64_t kFewUnits = 96;
+FewProduct few_product(int64_t K, int64_t tiles, int64_t slots) {
+  FewProduct f = {};
+  if (K == 0 || tiles == 0) return f;
   f.K = (int)K;
   f.tiles = (int)tiles;
-  const int64_t parts = std::min<int64_t>(kFewParts, std::max<int64_t>(1, K / 256)), stages = (K + kFewK - 1) / kFewK;
+  const int64_t stages = (K + kFewK - 1) / kFewK, wanted = (kFewUnits + tiles * slots - 1) / (tiles * slots);
+  const int64_t parts = std::min({(int64_t)kFewParts, std::max<int64_t>(1, K / 256), wanted});
   f.part_k = (int)((stages + parts - 1) / parts * kFewK);
-  f.parts = K ? (int)((K + f.part_k - 1) / f.part_k) : 0;
+  f.parts = (int)((K + f.part_k - 1) / f.part_k);
+  f.units_magic = 0xFFFFFFFFu / (uint32_t)(f.tiles * f.parts);
+  f.tiles_magic = 0xFFFFFFFFu / (uint32_t)f.tiles;
   return f;
 }
 
@@ -643,15 +702,15 @@ FewProduct few_product(int64_t K, int64_t tiles) {
 struct FewPlan {
   FewProduct gu, dn, sh_gu, sh_dn;
   int64_t slots, max_entries, max_chunks, sh_chunks, zero_words;
-  size_t done, hidden, arrived, head, entries, list, of_chunk, valid, part_gu, part_sh_gu, part_dn, part_sh_dn, h, sh_h, bytes;
+  size_t done, hidden, arrived, part_gu, part_sh_gu, part_dn, part_sh_dn, h, sh_h, bytes;
 };
 
 FewPlan few_plan(const FewShape& s) {
   FewPlan f;
-  f.gu = few_product(s.H, s.I / 64);
-  f.dn = few_product(s.I, (s.H + 127) / 128);
-  f.sh_gu = few_product(s.I_s ? s.H : 0, s.I_s / 64);
-  f.sh_dn = few_product(s.I_s, s.I_s ? (s.H + 127) / 128 : 0);
+  f.gu = few_product(s.H, s.I / 64, s.k);
+  f.dn = few_product(s.I, (s.H + 127) / 128, s.k);
+  f.sh_gu = few_product(s.H, s.I_s / 64, 1);
+  f.sh_dn = few_product(s.I_s, (s.H + 127) / 128, 1);
   f.slots = s.T * s.k;
   f.max_entries = std::min(s.E, f.slots);
   f.max_chunks = std::min(f.slots, f.max_entries + f.slots / kFewRows);
@@ -667,14 +726,9 @@ FewPlan few_plan(const FewShape& s) {
   f.hidden = take((f.max_chunks * f.gu.tiles + f.sh_chunks * f.sh_gu.tiles) * 4);
   f.arrived = take(f.dn.tiles * s.T * 4);
   f.zero_words = at / 4;
-  f.head = take(8);
-  f.entries = take(f.max_entries * sizeof(FewEntry));
-  f.list = take(f.slots * 2);
-  f.of_chunk = take(f.max_chunks * 2);
-  f.valid = take(s.T);
   at = (at + 255) & ~(size_t)255;
-  f.part_gu = take((size_t)f.slots * f.gu.parts * 2 * s.I * 4);
-  f.part_sh_gu = take((size_t)s.T * f.sh_gu.parts * 2 * s.I_s * 4);
+  f.part_gu = take(f.gu.parts > 1 ? (size_t)f.slots * f.gu.parts * 2 * s.I * 4 : 0);
+  f.part_sh_gu = take(f.sh_gu.parts > 1 ? (size_t)s.T * f.sh_gu.parts * 2 * s.I_s * 4 : 0);
   f.part_dn = take((size_t)f.slots * f.dn.parts * s.H * 4);
   f.part_sh_dn = take((size_t)s.T * f.sh_dn.parts * s.H * 4);
   f.h = take((size_t)f.slots * s.I * 2);
@@ -694,9 +748,10 @@ bool few_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
 }  // namespace
 
 size_t few_experts_workspace_bytes(const FewShape& s) { return few_plan(s).bytes; }
+int64_t few_experts_counters(const FewShape& s) { return few_plan(s).zero_words; }
 
 int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids, const float* w, const FewWeights& weights,
-                       uint16_t* y, void* ws, const DeviceInfo& dev, cudaStream_t stream) {
+                       uint16_t* y, void* ws, bool counters_clear, const DeviceInfo& dev, cudaStream_t stream) {
   const FewPlan f = few_plan(s);
   uint8_t* base = static_cast<uint8_t*>(ws);
   FewParams p;
@@ -705,11 +760,6 @@ int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids,
   p.done = reinterpret_cast<uint32_t*>(base + f.done);
   p.hidden = reinterpret_cast<uint32_t*>(base + f.hidden);
   p.arrived = reinterpret_cast<uint32_t*>(base + f.arrived);
-  p.head = reinterpret_cast<int*>(base + f.head);
-  p.entries = reinterpret_cast<FewEntry*>(base + f.entries);
-  p.list = reinterpret_cast<uint16_t*>(base + f.list);
-  p.of_chunk = reinterpret_cast<uint16_t*>(base + f.of_chunk);
-  p.valid = base + f.valid;
   p.part_gu = reinterpret_cast<float*>(base + f.part_gu);
   p.part_sh_gu = reinterpret_cast<float*>(base + f.part_sh_gu);
   p.part_dn = reinterpret_cast<float*>(base + f.part_dn);
@@ -721,9 +771,9 @@ int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids,
   p.stall = dev.test_stall_producer;
   p.gu = f.gu; p.dn = f.dn; p.sh_gu = f.sh_gu; p.sh_dn = f.sh_dn;
   p.T = (int)s.T; p.H = (int)s.H; p.E = (int)s.E; p.k = (int)s.k; p.I = (int)s.I; p.I_s = (int)s.I_s;
+  p.k_magic = 0xFFFFFFFFu / (uint32_t)s.k;
   p.max_entries = (int)f.max_entries; p.max_chunks = (int)f.max_chunks; p.sh_chunks = (int)f.sh_chunks;
-  p.zero_words = (int)f.zero_words;
-  const size_t tables = few_tables_bytes(f.max_entries, f.max_chunks, f.slots);
+  const size_t tables = few_tables_bytes(f.max_entries, f.max_chunks, f.slots, s.T);
   p.stages = (int)std::min<size_t>(kFewMaxStages, (kFewSmem - 1024 - kFewFixed - tables) / kFewStage);
   if (!few_map(&p.tm_gate_up, weights.gate_up, s.E * s.H, 2 * s.I, kFewK) || !few_map(&p.tm_down, weights.down, s.E * s.I, s.H, kFewK) ||
       !few_map(&p.tm_x, x, s.T, s.H, 1) || !few_map(&p.tm_h, p.h, f.slots, s.I, 1))
@@ -736,8 +786,7 @@ int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids,
     if (cudaFuncSetAttribute(few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess) return 1;
     configured[dev.ordinal].store(1);
   }
-  const size_t prep_smem = (size_t)(f.slots + s.E) * sizeof(int);
-  if (launch_pdl(few_prep_kernel, dim3(1), dim3(kPrepThreads), prep_smem, stream, 1, p) != cudaSuccess) return 1;
+  if (!counters_clear && cudaMemsetAsync(ws, 0, f.zero_words * 4, stream) != cudaSuccess) return 1;
   const size_t smem = 1024 + (size_t)p.stages * kFewStage + kFewFixed + tables;
   return launch_pdl(few_kernel, dim3((unsigned)dev.num_sms), dim3(kFewThreads), smem, stream, 1, p) == cudaSuccess ? 0 : 1;
 }

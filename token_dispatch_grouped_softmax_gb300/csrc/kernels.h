@@ -149,9 +149,13 @@ struct FewWeights {
   const uint16_t *gate_up, *down, *sh_gate_up, *sh_down;
 };
 size_t few_experts_workspace_bytes(const FewShape& s);
-// 0 = enqueued, -1 = tensor map rejected, 1 = launch failed
+int64_t few_experts_counters(const FewShape& s);   // words at the workspace's begin that are 0 before the launch
+cudaError_t launch_few_route(const FewShape& s, const uint16_t* x, const float* w_router, const float* bias,
+                             const float* balance, const RouteChoice& c, int32_t* ids, float* w, uint32_t* zero,
+                             int64_t zero_words, const DeviceInfo& dev, cudaStream_t stream);
+// counters_clear: they are 0.  0 = enqueued, -1 = tensor map rejected, 1 = launch failed
 int launch_few_experts(const FewShape& s, const uint16_t* x, const int32_t* ids, const float* w, const FewWeights& weights,
-                       uint16_t* y, void* ws, const DeviceInfo& dev, cudaStream_t stream);
+                       uint16_t* y, void* ws, bool counters_clear, const DeviceInfo& dev, cudaStream_t stream);
 
 // A block's norms with its gate and residual (block_norm.cu): x the residual
 // stream, y the block's output, w, v, g the weights of the norms and the gate

@@ -62,12 +62,6 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t offse
   return v;
 }
 
-// n / d with magic = floor((2^32 - 1) / d): at most one too small before the fix.
-__device__ __forceinline__ uint32_t w4_div(uint32_t n, uint32_t d, uint32_t magic) {
-  const uint32_t q = __umulhi(n, magic);
-  return q + (n - q * d >= d);
-}
-
 // The experts of the slots of this launch row, and each expert's slots in
 // increasing order (every block sorts for itself and must find the same
 // chunks).  bits is scratch, zeroed, [E] rows of w4_bit_row(slots) words: bit i of row
@@ -409,12 +403,12 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
   const int half = p.N / 2;
   if (GATE_UP && p.ids) w4_zero_rows(p, slot0, slots);
   // this block's items: an even share, the first blocks one more
-  const uint32_t items = chunks * (uint32_t)p.blocks, share = w4_div(items, gridDim.x, p.grid_magic), more = items - share * gridDim.x;
+  const uint32_t items = chunks * (uint32_t)p.blocks, share = div_by(items, gridDim.x, p.grid_magic), more = items - share * gridDim.x;
   const int begin = (int)(blockIdx.x * share + min(blockIdx.x, more));
   const int end = begin + (int)share + (blockIdx.x < more ? 1 : 0);
   if (begin >= end) return;
   // the expert of its first chunk
-  const int first_chunk = (int)w4_div(begin, p.blocks, p.blocks_magic);
+  const int first_chunk = (int)div_by(begin, p.blocks, p.blocks_magic);
   for (int i = tid; i < (int)(found >> 32); i += kW4Threads)
     if (first_chunk >= act[i].chunk0 && first_chunk < act[i].chunk0 + (act[i].rows + kW4Rows - 1) / kW4Rows) *first_act = i;
   fence_proxy_async_smem();   // the sort's writes into the rings, before TMA's
@@ -446,7 +440,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
       if (item >= end) continue;
       lu = lrun < whole ? 0 : part_u0;
       lu_end = lrun < whole ? units : part_u1;
-      const int chunk = (int)w4_div(item, p.blocks, p.blocks_magic);
+      const int chunk = (int)div_by(item, p.blocks, p.blocks_magic);
       while (chunk >= act[la].chunk0 + chunks_of(act[la])) ++la;
       const int expert = act[la].expert;
       lcol = (item - chunk * p.blocks) * 32;
@@ -495,7 +489,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] = 0.f;
     if (item < end) {
-      const int chunk = (int)w4_div(item, p.blocks, p.blocks_magic);
+      const int chunk = (int)div_by(item, p.blocks, p.blocks_magic);
       block = item - chunk * p.blocks;
       while (chunk >= act[ca].chunk0 + chunks_of(act[ca])) ++ca;
       a = act[ca];
