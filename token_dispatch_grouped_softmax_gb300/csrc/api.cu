@@ -477,7 +477,10 @@ int moe_block_norm(const void* x, const uint16_t* branch, const void* weight, co
   if (!(eps > 0.f) || !(eps - eps == 0.f)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!branch != !r || !weight != !h || !aligned16(r) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(moe::launch_block_norm(n, r, h, stats, static_cast<cudaStream_t>(stream)));
+  moe::DeviceInfo dev;
+  const int rc_dev = moe::current_device(&dev);
+  if (rc_dev != MOE_OK) return rc_dev;
+  return cuda_status(moe::launch_block_norm(n, r, h, stats, dev, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_block_norm_bwd_workspace_size(int64_t T, int64_t H, int64_t gates, int has_weight, int has_post_weight,
@@ -504,8 +507,11 @@ int moe_block_norm_bwd(const uint16_t* dh, const void* dr, const void* x, const 
   }
   const size_t need = moe::block_norm_bwd_workspace_bytes(T, H, gates, weight, post_weight);
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  moe::DeviceInfo dev;
+  const int rc_dev = moe::current_device(&dev);
+  if (rc_dev != MOE_OK) return rc_dev;
   const moe::BlockNormGrads d{dx, d_branch, d_weight, d_post_weight, d_gate};
-  return cuda_status(moe::launch_block_norm_bwd(n, dh, dr, stats, d, workspace, static_cast<cudaStream_t>(stream)));
+  return cuda_status(moe::launch_block_norm_bwd(n, dh, dr, stats, d, workspace, dev, static_cast<cudaStream_t>(stream)));
 }
 
 /* ------------------------------------ the gradients' norm, and clipping */

@@ -14,8 +14,15 @@
 // that is not rounded yet, and the backward computes r again from x and y
 // instead of reading the rounded one (the same bytes).
 //
-// A row belongs to TPR threads, each with 8 consecutive columns, and a block
-// of up to 1024 threads holds several rows at a time.
+// The bytes bound both directions.  A row belongs to a row group of H / 8
+// threads (whole warps), 8 consecutive columns each, so that a row's
+// quantities stay in registers between its sums; a block of up to 1024
+// threads holds several row groups and is alone on its SM.  Each row group
+// takes a range of consecutive rows and has a ring in shared memory that bulk
+// copies keep full, one thread of the group issuing them: the loads in flight
+// do not depend on the registers, nor on the barriers of a row's sums.
+// Consecutive rows keep the columns' sums of the backward in registers until
+// the range ends, and a gate's group ends at most twice inside a range.
 #include <algorithm>
 
 #include "kernels.h"
@@ -25,7 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxH = 8192;
-constexpr int kNormBlocks = 152;   // GB300's SMs; fixed, as the order of the columns' sums goes by it
+constexpr int kNormBlocks = 152;        // GB300's SMs; fixed, as the order of the columns' sums goes by it
+constexpr int kNormThreads = 1024;
+constexpr int kNormSmem = 200 * 1024;   // of a block: the rings and the operands that rows share
+constexpr int kNormMaxStages = 4;
 
 __device__ __forceinline__ void load8(const float* p, float* v) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -49,28 +59,11 @@ __device__ __forceinline__ void fill8(float* v, float c) {
   for (int i = 0; i < 8; ++i) v[i] = c;
 }
 
-// Sums over a row's threads.  Two buffers in turn: a thread writes a buffer
-// again only after the barrier of the sum in between, which every thread
-// reaches after reading it.
-struct RowSum {
-  float* buf;       // [2][warps of the block]
-  int warps;        // of a row
-  int warps_block;
-  int turn = 0;
-
-  __device__ __forceinline__ float operator()(float v) {
-    v = warp_sum(v);
-    if (warps == 1) return v;
-    const int w = threadIdx.x >> 5;
-    float* b = buf + turn * warps_block + threadIdx.y * warps;
-    if ((threadIdx.x & 31) == 0) b[w] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"(32 * warps) : "memory");
-    turn ^= 1;
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += b[i];
-    return s;
-  }
-};
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 struct NormParams {
   const void* x;
@@ -83,7 +76,7 @@ struct NormParams {
   const void* dr;
   void* dx;
   uint16_t* dy;
-  float* parts;           // [grid][sums][H], then [virtual blocks][2][H] of the gate's groups
+  float* parts;           // [grid][sums][H], then [row groups][2][H] of the gate's groups
   void* dg;               // finished groups are written here
   int64_t T;
   int H;
@@ -92,194 +85,414 @@ struct NormParams {
   float a, b, eps;
   int w_f32, v_f32, g_f32;
   int n_sums;             // columns' sums over all rows: dw, dv, dg with one group
+  int stages;
+  int shared_params;      // w, v and a single g have room in shared memory
+  uint32_t* status;
+  uint64_t wait_limit_ns;
 };
 
-template <typename X>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams p) {
-  __shared__ float sums[2 * 32];
-  pdl_wait();
-  pdl_trigger();
-  const int c = threadIdx.x * 8;
-  const bool mine = c < p.H;
-  RowSum row_sum{sums, (int)blockDim.x >> 5, (int)(blockDim.x * blockDim.y) >> 5};
-  float w[8], v[8], g[8];
-  fill8(w, 1.f);
-  fill8(v, 1.f);
-  fill8(g, 1.f);
-  if (mine) {
-    if (p.w) load8(p.w, p.w_f32, c, w);
-    if (p.v) load8(p.v, p.v_f32, c, v);
-    if (p.groups == 1) load8(p.g, p.g_f32, c, g);
-  }
-  const X* x = static_cast<const X*>(p.x);
-  const float inv = 1.f / (float)p.H;
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < p.T; t += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t at = t * p.H + c;
-    float r[8], y[8];
-    fill8(r, 0.f);
-    fill8(y, 0.f);
-    if (mine) {
-      load8(x + at, r);
-      if (p.y) load8(p.y + at, y);
-    }
-    if (p.y) {
-      if (p.v) {
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
-        const float s = rsqrtf(row_sum(q) * inv + p.eps);
-        if (p.stats && threadIdx.x == 0) p.stats[p.T + t] = s;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= s * v[i];
-      }
-      if (p.groups > 1 && mine) load8(p.g, p.g_f32, t / p.gate_rows * p.H + c, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = fmaf(p.a, r[i], p.b * (g[i] * y[i]));
-      if (mine) store8(static_cast<X*>(p.r) + at, r);
-    }
-    if (p.w) {
-      float q = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(r[i], r[i], q);
-      if (!mine) q = 0.f;
-      const float s = rsqrtf(row_sum(q) * inv + p.eps);
-      if (p.stats && threadIdx.x == 0) p.stats[t] = s;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] *= s * w[i];
-      if (mine) store8(p.h + at, r);
-    }
-  }
-}
-
-// A virtual block (one row's threads of a block) takes a range of consecutive
-// rows, so that its columns' sums stay in registers and a gate's group ends
-// at most twice inside a range.
+// The first of row group v's rows, of n row groups.
 __device__ __host__ __forceinline__ int64_t norm_first_row(int64_t T, int64_t n, int64_t v) {
   const int64_t share = T / n, more = T - share * n;
   return v * share + (v < more ? v : more);
 }
+// The row group of a row.
+__device__ __forceinline__ int64_t norm_group_of(int64_t T, int64_t n, int64_t row) {
+  const int64_t share = T / n, more = T - share * n;
+  return row < more * (share + 1) ? row / (share + 1) : more + (row - more * (share + 1)) / share;
+}
 
-template <typename X>
-__global__ void __launch_bounds__(1024, 1) block_norm_bwd_kernel(const NormParams p) {
-  __shared__ float sums[2 * 32];
+__device__ __noinline__ void norm_wait_more(uint32_t bar, uint32_t phase, volatile int* abort, uint64_t limit_ns, uint32_t* status) {
+  mbar_wait_bounded(bar, phase, abort, limit_ns, status, 1, kKernNorm);
+}
+
+// A row group: its rows, its ring and its sums.
+struct RowGroup {
+  // the stream that this thread copies, if any: a thread of another warp for
+  // each where the row group has as many, as all wait for the slowest
+  const uint8_t* src;     // its first row of the range
+  uint32_t bytes, offset; // of a row; in a stage
+  uint8_t* ring;
+  uint32_t row_bytes;     // of a stage
+  uint32_t bar;
+  int rows;
+  float* buf;             // [2][32]: the warps' partial sums, then zeros
+  int turn;
+  volatile int* abort;
+
+  __device__ __forceinline__ int warps() const { return blockDim.x >> 5; }
+  __device__ __forceinline__ void sync() const {
+    if (warps() == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"((int)blockDim.x) : "memory");
+  }
+  // The sum over the row's threads.  Two buffers in turn: a thread writes one
+  // again only after the barrier of the sum in between, which every thread
+  // reaches after reading it.
+  __device__ __forceinline__ float sum(float v) {
+    v = warp_sum(v);
+    const int n = warps();
+    if (n == 1) return v;
+    float* b = buf + turn * 32;
+    if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
+    sync();
+    turn ^= 1;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(b + i);
+      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
+  }
+  __device__ __forceinline__ void issue(int i, int stage) const {   // row i of the range
+    if (!src) return;
+    mbar_arrive_expect_tx(bar + 8 * stage, bytes);
+    bulk_load(smem_u32(ring) + stage * row_bytes + offset, src + (int64_t)i * bytes, bytes, bar + 8 * stage);
+  }
+  // Row i has landed.  A wait that runs out is reported; the rows are then
+  // undefined, and the kernel goes on to its end.
+  __device__ __forceinline__ const uint8_t* wait(const NormParams& p, int stage, uint32_t phase) const {
+    const uint32_t b = bar + 8 * stage;
+    if (!mbar_try_wait(b, phase)) norm_wait_more(b, phase, abort, p.wait_limit_ns, p.status);
+    return ring + stage * row_bytes;
+  }
+  // Between two barriers of row i, all of row i - 1's reads are done: its
+  // stage takes the row `stages` after it.
+  __device__ __forceinline__ void refill(const NormParams& p, int i, int stage) const {
+    if (i > 0 && i - 1 + p.stages < rows) issue(i - 1 + p.stages, stage == 0 ? p.stages - 1 : stage - 1);
+  }
+};
+
+struct NormSetup {
+  RowGroup rg;
+  const void *w, *v, *g;  // w, v and a single gate: in shared memory where they fit
+};
+
+// The block's shared memory: the row groups' rings, then w, v and a single g.
+__device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* smem, const void* const (&src)[4],
+                                                const int (&elem)[4], int64_t begin, int rows) {
+  __shared__ uint64_t bars[32 * kNormMaxStages];
+  __shared__ __align__(16) float sums[32 * 64];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, ty = threadIdx.y;
+  NormSetup s;
+  RowGroup& g = s.rg;
+  g.row_bytes = 0;
+  g.src = nullptr;
+  g.bytes = g.offset = 0;
+  int n = 0, n_src = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) n_src += src[k] != nullptr;
+  const int step = g.warps() >= n_src ? 32 : 1;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (src[k]) {
+      const uint32_t bytes = (uint32_t)p.H * elem[k];
+      if ((int)threadIdx.x == n * step) {
+        g.src = static_cast<const uint8_t*>(src[k]) + begin * bytes;
+        g.bytes = bytes;
+        g.offset = g.row_bytes;
+      }
+      g.row_bytes += bytes;
+      ++n;
+    }
+  g.rows = rows;
+  g.bar = smem_u32(bars) + 8 * ty * p.stages;
+  g.buf = sums + 64 * ty;
+  g.turn = 0;
+  g.abort = &abort_flag;
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < (int)blockDim.y * p.stages; ++i) mbar_init(smem_u32(bars) + 8 * i, n_src);
+    fence_mbar_init();
+  }
+  for (int i = tid; i < 32 * 64; i += blockDim.x * blockDim.y) sums[i] = 0.f;
+  g.ring = smem + (size_t)ty * p.stages * g.row_bytes;
+  uint8_t* at = smem + (size_t)blockDim.y * p.stages * g.row_bytes;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
+  for (int i = 0; i < p.stages && i < rows; ++i) g.issue(i, i);
+  const int threads = blockDim.x * blockDim.y;
+  auto share = [&](const void* from, int f32) -> const void* {
+    if (!from || !p.shared_params) return from;
+    uint8_t* to = at;
+    const int bytes = p.H * (f32 ? 4 : 2);
+    for (int i = tid * 16; i < bytes; i += threads * 16)
+      *reinterpret_cast<uint4*>(to + i) = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + i));
+    at += bytes;
+    return to;
+  };
+  s.w = share(p.w, p.w_f32);
+  s.v = share(p.v, p.v_f32);
+  s.g = p.groups > 1 ? p.g : share(p.g, p.g_f32);
+  __syncthreads();
+  return s;
+}
+
+// Where a row is among the gate's groups.
+struct GatePlace {
+  int group = 0, left = 0;   // its group, and the group's rows from it on
+  __device__ __forceinline__ GatePlace(const NormParams& p, int64_t begin, int rows) {
+    if (p.groups > 1 && rows > 0) {
+      group = (int)(begin / p.gate_rows);
+      left = (int)((group + 1) * p.gate_rows - begin);
+    }
+  }
+  __device__ __forceinline__ bool ends() { return --left == 0; }
+  __device__ __forceinline__ void next(const NormParams& p) {
+    ++group;
+    left = (int)p.gate_rows;
+  }
+  __device__ __forceinline__ int64_t first(const NormParams& p) const { return p.groups > 1 ? (int64_t)group * p.H : 0; }
+};
+
+// Y: there is a block's output (y); W, V, G: w, v, g.
+template <typename X, bool Y, bool W, bool V, bool G>
+__global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t norm_smem[];
   const int c = threadIdx.x * 8;
   const bool mine = c < p.H;
-  RowSum row_sum{sums, (int)blockDim.x >> 5, (int)(blockDim.x * blockDim.y) >> 5};
-  const X* x = static_cast<const X*>(p.x);
+  const int64_t n = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t begin = norm_first_row(p.T, n, me);
+  const int rows = (int)(norm_first_row(p.T, n, me + 1) - begin);
+  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, nullptr, nullptr}, {(int)sizeof(X), 2, 0, 0}, begin, rows);
+  RowGroup& rg = s.rg;
+  const float inv = 1.f / (float)p.H;
+  int stage = 0;
+  uint32_t phase = 0;
+  GatePlace gate(p, begin, G ? rows : 0);
+  for (int i = 0; i < rows; ++i) {
+    const int64_t t = begin + i, at = t * p.H + c;
+    float g[8], r[8], y[8];
+    fill8(r, 0.f);
+    fill8(y, 0.f);
+    fill8(g, 0.f);
+    if (G && mine) load8(s.g, p.g_f32, gate.first(p) + c, g);
+    const uint8_t* row = rg.wait(p, stage, phase);
+    if (mine) {
+      load8(reinterpret_cast<const X*>(row) + c, r);
+      if (Y) load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c, y);
+    }
+    if (V) {
+      float q = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q = fmaf(y[k], y[k], q);
+      const float sy = rsqrtf(rg.sum(q) * inv + p.eps);
+      rg.refill(p, i, stage);
+      if (p.stats && threadIdx.x == 0) p.stats[p.T + t] = sy;
+      float v[8];
+      fill8(v, 0.f);
+      if (mine) load8(s.v, p.v_f32, c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= sy * v[k];
+    }
+    if (Y) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[k] = fmaf(p.a, r[k], p.b * (G ? g[k] * y[k] : y[k]));
+      if (mine) store8(static_cast<X*>(p.r) + at, r);
+    }
+    if (W) {
+      float q = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q = fmaf(r[k], r[k], q);
+      const float sr = rsqrtf(rg.sum(mine ? q : 0.f) * inv + p.eps);
+      if (!V) rg.refill(p, i, stage);
+      if (p.stats && threadIdx.x == 0) p.stats[t] = sr;
+      if (mine) {
+        float w[8];
+        load8(s.w, p.w_f32, c, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] *= sr * w[k];
+        store8(p.h + at, r);
+      }
+    }
+    if (!V && !W) {
+      rg.sync();
+      rg.refill(p, i, stage);
+    }
+    if (G && p.groups > 1 && gate.ends()) gate.next(p);
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+template <typename X, bool Y, bool W, bool V, bool G>
+__global__ void __launch_bounds__(kNormThreads, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const int c = threadIdx.x * 8;
+  const bool mine = c < p.H;
+  const int64_t n = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t begin = norm_first_row(p.T, n, me);
+  const int rows = (int)(norm_first_row(p.T, n, me + 1) - begin);
+  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, p.dh, p.dr}, {(int)sizeof(X), 2, 2, (int)sizeof(X)}, begin, rows);
+  RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
   float dw[8], dv[8], dg[8];
   fill8(dw, 0.f);
   fill8(dv, 0.f);
   fill8(dg, 0.f);
-  const int64_t n = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t begin = norm_first_row(p.T, n, me), end = norm_first_row(p.T, n, me + 1);
-  for (int64_t t = begin; t < end; ++t) {
-    const int64_t at = t * p.H + c;
-    float r[8], y[8], g[8], d[8];
-    fill8(r, 0.f);
-    fill8(y, 0.f);
-    fill8(g, 1.f);
+  int stage = 0;
+  uint32_t phase = 0;
+  GatePlace gate(p, begin, G ? rows : 0);
+  float next_r = 0.f, next_y = 0.f;   // the next row's statistics
+  auto stats = [&](int i) {
+    if (i >= rows) return;
+    if (W) next_r = p.stats[begin + i];
+    if (V) next_y = p.stats[p.T + begin + i];
+  };
+  stats(0);
+  for (int i = 0; i < rows; ++i) {
+    const int64_t at = (begin + i) * p.H + c;
+    const float sr = next_r, sy = next_y;
+    stats(i + 1);
+    // Between the sums a thread keeps r and dh w alone, and reads the row's
+    // other operands from shared memory again: registers for 1024 threads.
+    const uint8_t* row = rg.wait(p, stage, phase);
+    const uint16_t* row_y = reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c;
+    const uint16_t* row_dh = row_y + (Y ? p.H : 0);
+    const X* row_dr = reinterpret_cast<const X*>(row_dh - c + (W ? p.H : 0)) + c;
+    auto load_y = [&](float (&y)[8]) {   // normed, without v
+      load8(row_y, y);
+      if (V) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] *= sy;
+      }
+    };
+    float d[8];
     fill8(d, 0.f);
-    float s_y = 1.f;
-    if (mine) {
-      load8(x + at, r);
-      if (p.y) load8(p.y + at, y);
-      if (p.dr) load8(static_cast<const X*>(p.dr) + at, d);
-      if (p.g) load8(p.g, p.g_f32, (p.groups > 1 ? t / p.gate_rows * p.H : 0) + c, g);
-    }
-    float v[8];
-    fill8(v, 1.f);
-    if (p.v) {
-      s_y = p.stats[p.T + t];
-      if (mine) load8(p.v, p.v_f32, c, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= s_y;
-    }
-    if (p.y) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = fmaf(p.a, r[i], p.b * (g[i] * (y[i] * v[i])));
-    }
-    if (p.w) {
-      float u[8], w[8];
+    if (W) {
+      float r[8], u[8], q = 0.f;
+      fill8(r, 0.f);
       fill8(u, 0.f);
-      fill8(w, 0.f);
       if (mine) {
-        load8(p.dh + at, u);
-        load8(p.w, p.w_f32, c, w);
-      }
-      const float s = p.stats[t];
-      float q = 0.f;
+        load8(reinterpret_cast<const X*>(row) + c, r);
+        if (Y) {
+          float y[8], o[8];
+          load_y(y);
+          if (V) {
+            load8(s.v, p.v_f32, c, o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[i] *= s;
-        dw[i] = fmaf(u[i], r[i], dw[i]);
-        u[i] *= w[i];
-        q = fmaf(u[i], r[i], q);
-      }
-      q = row_sum(q) * inv;
+            for (int k = 0; k < 8; ++k) y[k] *= o[k];
+          }
+          if (G) {
+            load8(s.g, p.g_f32, gate.first(p) + c, o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = fmaf(s, u[i] - r[i] * q, d[i]);
-    }
+            for (int k = 0; k < 8; ++k) y[k] *= o[k];
+          }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = p.a * d[i];
-    if (mine) store8(static_cast<X*>(p.dx) + at, r);
-    if (p.y) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[i] *= p.b;
-        dg[i] = fmaf(d[i], y[i] * v[i], dg[i]);
-        d[i] *= g[i];
-      }
-      if (p.v) {
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dv[i] = fmaf(d[i], y[i], dv[i]);
-          d[i] *= v[i];
-          q = fmaf(d[i], y[i], q);
+          for (int k = 0; k < 8; ++k) r[k] = fmaf(p.a, r[k], p.b * y[k]);
         }
-        q = row_sum(q) * inv;
+        load8(row_dh, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = s_y * (d[i] - y[i] * q);
+        for (int k = 0; k < 8; ++k) {
+          r[k] *= sr;
+          dw[k] = fmaf(u[k], r[k], dw[k]);
+        }
+        float w[8];
+        load8(s.w, p.w_f32, c, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          u[k] *= w[k];
+          q = fmaf(u[k], r[k], q);
+        }
+      }
+      q = rg.sum(q) * inv;
+      rg.refill(p, i, stage);
+      if (mine && p.dr) load8(row_dr, d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = fmaf(sr, u[k] - r[k] * q, d[k]);
+    } else if (mine && p.dr) {
+      load8(row_dr, d);
+    }
+    if (mine) {
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = p.a * d[k];
+      store8(static_cast<X*>(p.dx) + at, o);
+    }
+    if (Y) {
+      float y[8], q = 0.f;
+      fill8(y, 0.f);
+      if (mine) {
+        if (G || V) load_y(y);
+        float v[8];
+        if (V) load8(s.v, p.v_f32, c, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] *= p.b;
+        if (G) {
+          float g[8];
+          load8(s.g, p.g_f32, gate.first(p) + c, g);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            dg[k] = fmaf(d[k], V ? y[k] * v[k] : y[k], dg[k]);
+            d[k] *= g[k];
+          }
+        }
+        if (V) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            dv[k] = fmaf(d[k], y[k], dv[k]);
+            d[k] *= v[k];
+            q = fmaf(d[k], y[k], q);
+          }
+        }
+      }
+      if (V) {
+        q = rg.sum(q) * inv;
+        if (!W) rg.refill(p, i, stage);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = sy * (d[k] - y[k] * q);
       }
       if (mine) store8(p.dy + at, d);
     }
-    if (p.groups > 1 && ((t + 1) % p.gate_rows == 0 || t + 1 == end)) {
-      const int64_t group = t / p.gate_rows;
-      if (mine) {
-        if (group * p.gate_rows >= begin && (group + 1) * p.gate_rows <= end) {
-          if (p.g_f32) store8(static_cast<float*>(p.dg) + group * p.H + c, dg);
-          else store8(static_cast<uint16_t*>(p.dg) + group * p.H + c, dg);
-        } else {
-          const int64_t slot = 2 * me + (group != begin / p.gate_rows);
-          store8(p.parts + ((int64_t)gridDim.x * p.n_sums + slot) * p.H + c, dg);
+    if (!V && !W) {
+      rg.sync();
+      rg.refill(p, i, stage);
+    }
+    if (G && p.groups > 1) {
+      const bool ends = gate.ends();
+      if (ends || i + 1 == rows) {
+        if (mine) {
+          const int64_t first = gate.group * p.gate_rows;
+          if (ends && first >= begin) {
+            if (p.g_f32) store8(static_cast<float*>(p.dg) + gate.first(p) + c, dg);
+            else store8(static_cast<uint16_t*>(p.dg) + gate.first(p) + c, dg);
+          } else {   // the range's first group, or its last
+            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * me + (first > begin)) * p.H + c, dg);
+          }
         }
+        fill8(dg, 0.f);
+        gate.next(p);
       }
-      fill8(dg, 0.f);
+    }
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
-  // the block's rows' sums, in the order of its rows' threads
-  extern __shared__ float block_sums[];   // [H], with more than one row
+  // the block's sums, its row groups in order, through the rings' memory
+  __syncthreads();
+  float* block_sums = reinterpret_cast<float*>(norm_smem);   // [H]
   int k = 0;
   auto add_up = [&](const float (&sum)[8]) {
     for (int ty = 0; ty < (int)blockDim.y; ++ty) {
       if (blockDim.y > 1) __syncthreads();
       if ((int)threadIdx.y != ty || !mine) continue;
-      float s[8];
-      fill8(s, 0.f);
-      if (ty > 0) load8(block_sums + c, s);
+      float q[8];
+      fill8(q, 0.f);
+      if (ty > 0) load8(block_sums + c, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += sum[i];
-      if (ty + 1 < (int)blockDim.y) store8(block_sums + c, s);
-      else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H + c, s);
+      for (int j = 0; j < 8; ++j) q[j] += sum[j];
+      if (ty + 1 < (int)blockDim.y) store8(block_sums + c, q);
+      else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H + c, q);
     }
     ++k;
   };
-  if (p.w) add_up(dw);
-  if (p.v) add_up(dv);
-  if (p.groups == 1) add_up(dg);
+  if (W) add_up(dw);
+  if (V) add_up(dv);
+  if (G && p.groups == 1) add_up(dg);
 }
 
 struct NormSumParams {
@@ -289,13 +502,14 @@ struct NormSumParams {
   int n_sums, blocks;     // sums over all rows
   void* dg;
   int dg_f32;
-  int64_t T, groups, gate_rows, virtual_blocks;
+  int64_t T, groups, gate_rows, row_groups;
   int H;
 };
 
-// The sums of the blocks' parts: blockIdx.y < n_sums a sum over all rows, and
-// from there on the gate's group that the range of virtual block
-// blockIdx.y - n_sums + 1 is the second to touch.
+// The sums of the parts: blockIdx.y < n_sums a sum over all rows; beyond, a
+// gate's group that several ranges share: group blockIdx.y - n_sums where
+// there are no more groups than ranges, else the one that range
+// blockIdx.y - n_sums + 1 goes on with.
 __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumParams p) {
   __shared__ float4 part[32][32];
   pdl_wait();
@@ -303,36 +517,33 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumParam
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 128 + 4 * lane;
   const bool mine = c < p.H;
-  const float* first;
-  int64_t n, pitch, group = 0;
-  int64_t first_v = 0;
   const bool whole = (int)blockIdx.y < p.n_sums;
-  if (whole) {
-    first = p.parts + (int64_t)blockIdx.y * p.H;
-    n = p.blocks;
-    pitch = (int64_t)p.n_sums * p.H;
-  } else {
-    const int64_t vb = blockIdx.y - p.n_sums + 1, start = norm_first_row(p.T, p.virtual_blocks, vb);
-    if (start >= p.T) return;
-    group = start / p.gate_rows;
-    const int64_t row0 = group * p.gate_rows;
-    first_v = vb - 1;
-    if (start == row0 || norm_first_row(p.T, p.virtual_blocks, first_v) > row0) return;   // no group spans here, or not its first two
-    int64_t last = vb;
-    while (last + 1 < p.virtual_blocks && norm_first_row(p.T, p.virtual_blocks, last + 1) < row0 + p.gate_rows) ++last;
-    n = last - first_v + 1;
-    first = p.parts + (int64_t)p.blocks * p.n_sums * p.H;
-    pitch = 0;
+  const float* first = p.parts + (int64_t)blockIdx.y * p.H;   // of the first part; the others: `rest` + i * pitch
+  const float* rest = first;
+  int64_t n = p.blocks, pitch = (int64_t)p.n_sums * p.H, group = 0;
+  if (!whole) {
+    const int64_t y = blockIdx.y - p.n_sums;
+    int64_t from;
+    if (p.groups <= p.row_groups) {
+      group = y;
+      from = norm_group_of(p.T, p.row_groups, group * p.gate_rows);
+    } else {
+      const int64_t start = norm_first_row(p.T, p.row_groups, y + 1);
+      group = start / p.gate_rows;
+      from = norm_group_of(p.T, p.row_groups, group * p.gate_rows);
+      if (start == group * p.gate_rows || from != y) return;
+    }
+    const int64_t to = norm_group_of(p.T, p.row_groups, (group + 1) * p.gate_rows - 1);
+    if (from == to) return;   // within one range, which wrote it
+    n = to - from + 1;
+    pitch = 2 * p.H;
+    rest = p.parts + ((int64_t)p.blocks * p.n_sums + 2 * from) * p.H;
+    first = rest + (norm_first_row(p.T, p.row_groups, from) < group * p.gate_rows ? p.H : 0);
   }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (mine) {
     for (int64_t i = warp; i < n; i += 32) {
-      const float* at = first + i * pitch + c;
-      if (!whole) {
-        const int64_t v = first_v + i;
-        at = first + (2 * v + (norm_first_row(p.T, p.virtual_blocks, v) / p.gate_rows != group)) * p.H + c;
-      }
-      const float4 q = *reinterpret_cast<const float4*>(at);
+      const float4 q = *reinterpret_cast<const float4*>((i == 0 ? first : rest + i * pitch) + c);
       s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
   }
@@ -344,56 +555,111 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumParam
       s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
     }
     void* out = whole ? p.out[blockIdx.y] : p.dg;
-    const int64_t at = (whole ? 0 : group * p.H) + c;
+    const int64_t at = group * p.H + c;
     if (whole ? p.f32[blockIdx.y] : p.dg_f32) *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
     else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
-dim3 norm_block(int64_t T, int64_t H, int sms, int max_threads) {
+// A launch's shape.  row_bytes: of a row's streams; params: of w, v and a
+// single gate, which stay in global memory where two stages do not fit beside
+// them.
+struct NormShape {
+  dim3 block;
+  int grid, stages, shared_params;
+  size_t smem;
+};
+NormShape norm_shape(int64_t T, int64_t H, size_t row_bytes, size_t params) {
+  NormShape s;
   const int tpr = (int)((H / 8 + 31) / 32 * 32);
-  int rows = std::min(max_threads / tpr, 15);   // barriers 1 .. 15 belong to rows
-  if (tpr == 32) rows = max_threads / tpr;      // a warp needs none
-  rows = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + sms - 1) / sms));
-  return dim3(tpr, rows);
+  int rows = kNormThreads / tpr;
+  if (tpr > 32) rows = std::min(rows, 15);   // row groups' barriers 1 .. 15; a warp needs none
+  rows = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
+  rows = (int)std::max<size_t>(1, std::min<size_t>(rows, kNormSmem / (2 * row_bytes)));
+  s.shared_params = params + 2 * rows * row_bytes <= kNormSmem;
+  const size_t room = kNormSmem - (s.shared_params ? params : 0);
+  s.stages = (int)std::min<size_t>(kNormMaxStages, room / (rows * row_bytes));
+  s.block = dim3(tpr, rows);
+  s.grid = (int)std::min<int64_t>((T + rows - 1) / rows, kNormBlocks);
+  s.smem = (size_t)rows * s.stages * row_bytes + (s.shared_params ? params : 0);
+  return s;
 }
 
-struct NormBwdShape {
-  dim3 block;
-  int grid, n_sums;
-};
-NormBwdShape norm_bwd_shape(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
-  NormBwdShape s;
-  s.block = norm_block(T, H, kNormBlocks, 1024);
-  s.grid = (int)std::min<int64_t>((T + s.block.y - 1) / s.block.y, kNormBlocks);
-  s.n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
-  return s;
+size_t norm_params_bytes(const BlockNorm& n) {
+  return (size_t)n.H * ((n.w ? (n.w_f32 ? 4 : 2) : 0) + (n.v ? (n.v_f32 ? 4 : 2) : 0) + (n.groups == 1 ? (n.g_f32 ? 4 : 2) : 0));
+}
+
+NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo& dev) {
+  NormParams p = {};
+  p.x = n.x; p.y = n.y; p.w = n.w; p.v = n.v; p.g = n.g;
+  p.T = n.T; p.H = (int)n.H; p.groups = n.groups; p.gate_rows = n.groups ? n.T / n.groups : n.T;
+  p.a = n.a; p.b = n.b; p.eps = n.eps;
+  p.w_f32 = n.w_f32; p.v_f32 = n.v_f32; p.g_f32 = n.g_f32;
+  p.stages = s.stages;
+  p.shared_params = s.shared_params;
+  p.status = dev.status;
+  p.wait_limit_ns = dev.wait_limit_ns;
+  return p;
+}
+
+using NormKernel = void (*)(NormParams);
+
+template <typename X>
+NormKernel norm_kernel(bool bwd, const BlockNorm& n) {
+  const int which = (n.w ? 1 : 0) | (n.v ? 2 : 0) | (n.g ? 4 : 0);
+  if (!n.y) return bwd ? block_norm_bwd_kernel<X, false, true, false, false> : block_norm_kernel<X, false, true, false, false>;
+#define MOE_NORM(i) \
+  case i: return bwd ? block_norm_bwd_kernel<X, true, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0> \
+                     : block_norm_kernel<X, true, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0>;
+  switch (which) {
+    MOE_NORM(0) MOE_NORM(1) MOE_NORM(2) MOE_NORM(3) MOE_NORM(4) MOE_NORM(5) MOE_NORM(6)
+    default: MOE_NORM(7)
+  }
+#undef MOE_NORM
+}
+
+cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const NormParams& p, const DeviceInfo& dev,
+                        cudaStream_t stream) {
+  const NormKernel kernel = n.x_f32 ? norm_kernel<float>(bwd, n) : norm_kernel<uint16_t>(bwd, n);
+  // per-device set-up, cached (a race between host threads only repeats it)
+  static std::atomic<int> configured[kMaxDevices][2][2][9] = {};
+  std::atomic<int>& done = configured[dev.ordinal][bwd][n.x_f32 != 0][n.y ? (n.w ? 1 : 0) | (n.v ? 2 : 0) | (n.g ? 4 : 0) : 8];
+  if (!done.load()) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kNormSmem);
+    if (e != cudaSuccess) return e;
+    done.store(1);
+  }
+  return launch_pdl(kernel, dim3(s.grid), s.block, s.smem, stream, 1, p);
+}
+
+NormShape norm_bwd_shape(int64_t T, int64_t H, bool x_f32, bool y, bool w, bool dr, size_t params) {
+  return norm_shape(T, H, (size_t)H * ((x_f32 ? 4 : 2) * (dr ? 2 : 1) + (y ? 2 : 0) + (w ? 2 : 0)), params);
 }
 
 }  // namespace
 
 int64_t block_norm_max_width() { return kNormMaxH; }
 
-cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, cudaStream_t stream) {
-  NormParams p = {};
-  p.x = n.x; p.y = n.y; p.w = n.w; p.v = n.v; p.g = n.g;
+cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
+                              cudaStream_t stream) {
+  const NormShape s = norm_shape(n.T, n.H, (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n));
+  NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
-  p.T = n.T; p.H = (int)n.H; p.groups = n.groups; p.gate_rows = n.groups ? n.T / n.groups : n.T;
-  p.a = n.a; p.b = n.b; p.eps = n.eps;
-  p.w_f32 = n.w_f32; p.v_f32 = n.v_f32; p.g_f32 = n.g_f32;
-  const dim3 block = norm_block(n.T, n.H, 4 * kNormBlocks, 256);
-  const int per_sm = 2048 / (int)(block.x * block.y);
-  const unsigned grid = (unsigned)std::min<int64_t>((n.T + block.y - 1) / block.y, (int64_t)kNormBlocks * per_sm);
-  return launch_pdl(n.x_f32 ? block_norm_kernel<float> : block_norm_kernel<uint16_t>, dim3(grid), block, 0, stream, 1, p);
+  return norm_launch(false, n, s, p, dev, stream);
 }
 
+// The most that any types and any dr take: row groups are fewest bytes a row.
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
-  const NormBwdShape s = norm_bwd_shape(T, H, groups, w, v);
-  return sizeof(float) * (size_t)H * ((size_t)s.grid * s.n_sums + (groups > 1 ? (size_t)2 * s.grid * s.block.y : 0));
+  if (T == 0) return 0;
+  const NormShape s = norm_shape(T, H, (size_t)H * (w ? 4 : 2), 0);
+  const size_t n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
+  const size_t blocks = std::min<int64_t>(T, kNormBlocks);
+  return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const void* dr, const float* stats,
-                                  const BlockNormGrads& d, void* ws, cudaStream_t stream) {
+                                  const BlockNormGrads& d, void* ws, const DeviceInfo& dev, cudaStream_t stream) {
   if (n.T == 0) {   // sums over no rows
     const struct { void* out; int f32; int64_t rows; } zero[] = {{d.w, n.w_f32, 1}, {d.v, n.v_f32, 1}, {d.g, n.g_f32, n.groups}};
     for (const auto& z : zero)
@@ -403,35 +669,28 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
       }
     return cudaSuccess;
   }
-  NormParams p = {};
-  p.x = n.x; p.y = n.y; p.w = n.w; p.v = n.v; p.g = n.g;
+  const NormShape s = norm_bwd_shape(n.T, n.H, n.x_f32, n.y, n.w, dr, norm_params_bytes(n));
+  NormParams p = norm_params(n, s, dev);
   p.stats = const_cast<float*>(stats);
   p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g;
   p.parts = static_cast<float*>(ws);
-  p.T = n.T; p.H = (int)n.H; p.groups = n.groups; p.gate_rows = n.groups ? n.T / n.groups : n.T;
-  p.a = n.a; p.b = n.b; p.eps = n.eps;
-  p.w_f32 = n.w_f32; p.v_f32 = n.v_f32; p.g_f32 = n.g_f32;
-  const NormBwdShape s = norm_bwd_shape(n.T, n.H, n.groups, n.w, n.v);
-  p.n_sums = s.n_sums;
-  const size_t smem = s.block.y > 1 ? (size_t)n.H * sizeof(float) : 0;
-  cudaError_t e = launch_pdl(n.x_f32 ? block_norm_bwd_kernel<float> : block_norm_bwd_kernel<uint16_t>, dim3(s.grid),
-                             s.block, smem, stream, 1, p);
-  if (e != cudaSuccess) return e;
   NormSumParams q = {};
   q.parts = p.parts;
   int k = 0;
   if (n.w) { q.out[k] = d.w; q.f32[k++] = n.w_f32; }
   if (n.v) { q.out[k] = d.v; q.f32[k++] = n.v_f32; }
   if (n.groups == 1) { q.out[k] = d.g; q.f32[k++] = n.g_f32; }
-  q.n_sums = k;
+  p.n_sums = q.n_sums = k;
+  const cudaError_t e = norm_launch(true, n, s, p, dev, stream);
+  if (e != cudaSuccess) return e;
   q.blocks = s.grid;
   q.dg = d.g;
   q.dg_f32 = n.g_f32;
   q.T = n.T; q.groups = n.groups; q.gate_rows = p.gate_rows; q.H = p.H;
-  q.virtual_blocks = (int64_t)s.grid * s.block.y;
-  const unsigned spans = n.groups > 1 && p.gate_rows > 1 ? (unsigned)(q.virtual_blocks - 1) : 0;
-  if (k + spans == 0) return cudaSuccess;
-  return launch_pdl(block_norm_sum_kernel, dim3((unsigned)((n.H + 127) / 128), k + spans), dim3(1024), 0, stream, 1, q);
+  q.row_groups = (int64_t)s.grid * s.block.y;
+  const int64_t shared = n.groups > 1 && p.gate_rows > 1 ? (n.groups <= q.row_groups ? n.groups : q.row_groups - 1) : 0;
+  if (k + shared == 0) return cudaSuccess;
+  return launch_pdl(block_norm_sum_kernel, dim3((unsigned)((n.H + 127) / 128), (unsigned)(k + shared)), dim3(1024), 0, stream, 1, q);
 }
 
 }  // namespace moe

@@ -25,6 +25,7 @@ enum : uint32_t {
   kKernRouteSelect = 5,
   kKernW4 = 6,
   kKernFew = 7,
+  kKernNorm = 8,
 };
 
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t code, uint32_t kernel,

@@ -682,7 +682,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 // TMEM, and h needs no partial sums through memory.  With fewer units K is
 // split: in at most 8 parts of at least 256 rows, whole stages.  K, the tiles
 // and k alone decide, so that a token's sums do not depend on the batch.
-constexpr int64_t kFewUnits = 96;
+// Measured with 48 and with 96: 7 tokens of H 1600, top-5 of 60, I 704 (55
+// units of gate_up) 43 and 50 us; 4 tokens of H 4096, top-2 of 8, I 1024 (32)
+// 42 and 44; one token of it 30.7 and 29.6.
+constexpr int64_t kFewUnits = 48;
 FewProduct few_product(int64_t K, int64_t tiles, int64_t slots) {
   FewProduct f = {};
   if (K == 0 || tiles == 0) return f;

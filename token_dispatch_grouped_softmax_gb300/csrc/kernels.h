@@ -174,10 +174,11 @@ struct BlockNormGrads {
   void *w, *v, *g;
 };
 int64_t block_norm_max_width();
-cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, cudaStream_t stream);
+cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
+                              cudaStream_t stream);
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v);
 cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const void* dr, const float* stats,
-                                  const BlockNormGrads& d, void* ws, cudaStream_t stream);
+                                  const BlockNormGrads& d, void* ws, const DeviceInfo& dev, cudaStream_t stream);
 
 // The norm of a list of gradients, and the list scaled (grad_clip.cu); dst
 // null: the norm alone.  The arrays are on the host.
