@@ -15,9 +15,9 @@
 // instead of reading the rounded one (the same bytes).
 //
 // The bytes bound both directions.  A row belongs to a row group of H / 8
-// threads (whole warps), 8 consecutive columns each, so that a row's
-// quantities stay in registers between its sums; a block of up to 1024
-// threads holds several row groups and is alone on its SM.  Each row group
+// threads (whole warps; the backward's of H / 16), so that a row's quantities
+// stay in registers between its sums; a block holds several row groups and is
+// alone on its SM.  Each row group
 // takes a range of consecutive rows and has a ring in shared memory that bulk
 // copies keep full, one thread of the group issuing them: the loads in flight
 // do not depend on the registers, nor on the barriers of a row's sums.
@@ -37,27 +37,76 @@ constexpr int kNormThreads = 1024;
 constexpr int kNormSmem = 200 * 1024;   // of a block: the rings and the operands that rows share
 constexpr int kNormMaxStages = 4;
 
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Eight columns of a thread, as four pairs for the packed fp32 instructions
+// (two products, sums or fused ones an instruction, each rounded as alone).
+struct F8 {
+  float2 v[4];
+};
+__device__ __forceinline__ uint64_t bits(const float2& a) { return reinterpret_cast<const uint64_t&>(a); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return reinterpret_cast<float2&>(d);
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) { unpack8(*reinterpret_cast<const uint4*>(p), v); }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return reinterpret_cast<float2&>(d);
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) { *reinterpret_cast<uint4*>(p) = pack8(v); }
-
-// 8 values of an fp32 or bf16 vector.
-__device__ __forceinline__ void load8(const void* p, bool f32, int64_t at, float* v) {
-  if (f32) load8(static_cast<const float*>(p) + at, v);
-  else load8(static_cast<const uint16_t*>(p) + at, v);
-}
-__device__ __forceinline__ void fill8(float* v, float c) {
+__device__ __forceinline__ F8 fill8(float c) {
+  F8 r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = c;
+  for (int k = 0; k < 4; ++k) r.v[k] = make_float2(c, c);
+  return r;
 }
+__device__ __forceinline__ void mul8(F8& a, const F8& b) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) a.v[k] = mul2(a.v[k], b.v[k]);
+}
+__device__ __forceinline__ void mul8(F8& a, float b) { mul8(a, fill8(b)); }
+// a b + c into c
+__device__ __forceinline__ void fma8(const F8& a, const F8& b, F8& c) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c.v[k] = fma2(a.v[k], b.v[k], c.v[k]);
+}
+__device__ __forceinline__ float dot8(const F8& a, const F8& b) {
+  float2 s = mul2(a.v[0], b.v[0]);
+#pragma unroll
+  for (int k = 1; k < 4; ++k) s = fma2(a.v[k], b.v[k], s);
+  return s.x + s.y;
+}
+
+__device__ __forceinline__ F8 load8(const float* p) {
+  F8 r;
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  r.v[0] = make_float2(a.x, a.y); r.v[1] = make_float2(a.z, a.w);
+  r.v[2] = make_float2(b.x, b.y); r.v[3] = make_float2(b.z, b.w);
+  return r;
+}
+__device__ __forceinline__ F8 load8(const uint16_t* p) {
+  F8 r;
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  r.v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x)); r.v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+  r.v[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z)); r.v[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
+  return r;
+}
+__device__ __forceinline__ void store8(float* p, const F8& a) {
+  *reinterpret_cast<float4*>(p) = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const F8& a) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(a.v[0].x, a.v[0].y), pack_bf16x2(a.v[1].x, a.v[1].y),
+                                            pack_bf16x2(a.v[2].x, a.v[2].y), pack_bf16x2(a.v[3].x, a.v[3].y));
+}
+
+// A vector that rows share, fp32 or bf16.
+struct Shared {
+  const void* p;
+  bool f32;
+  __device__ __forceinline__ F8 load(int64_t at) const {
+    return f32 ? load8(static_cast<const float*>(p) + at) : load8(static_cast<const uint16_t*>(p) + at);
+  }
+};
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -92,13 +141,13 @@ struct NormParams {
 };
 
 // The first of row group v's rows, of n row groups.
-__device__ __host__ __forceinline__ int64_t norm_first_row(int64_t T, int64_t n, int64_t v) {
-  const int64_t share = T / n, more = T - share * n;
-  return v * share + (v < more ? v : more);
+__device__ __forceinline__ uint32_t norm_first_row(uint32_t T, uint32_t n, uint32_t v) {
+  const uint32_t share = T / n, more = T - share * n;
+  return v * share + min(v, more);
 }
 // The row group of a row.
-__device__ __forceinline__ int64_t norm_group_of(int64_t T, int64_t n, int64_t row) {
-  const int64_t share = T / n, more = T - share * n;
+__device__ __forceinline__ uint32_t norm_group_of(uint32_t T, uint32_t n, uint32_t row) {
+  const uint32_t share = T / n, more = T - share * n;
   return row < more * (share + 1) ? row / (share + 1) : more + (row - more * (share + 1)) / share;
 }
 
@@ -136,12 +185,7 @@ struct RowGroup {
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     sync();
     turn ^= 1;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(b + i);
-      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
-    }
-    return (s.x + s.y) + (s.z + s.w);
+    return warp_sum(b[threadIdx.x & 31]);
   }
   __device__ __forceinline__ void issue(int i, int stage) const {   // row i of the range
     if (!src) return;
@@ -164,7 +208,7 @@ struct RowGroup {
 
 struct NormSetup {
   RowGroup rg;
-  const void *w, *v, *g;  // w, v and a single gate: in shared memory where they fit
+  Shared w, v, g;         // w, v and a single gate: fp32 in shared memory where they fit
 };
 
 // The block's shared memory: the row groups' rings, then w, v and a single g.
@@ -213,18 +257,17 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
   pdl_trigger();
   for (int i = 0; i < p.stages && i < rows; ++i) g.issue(i, i);
   const int threads = blockDim.x * blockDim.y;
-  auto share = [&](const void* from, int f32) -> const void* {
-    if (!from || !p.shared_params) return from;
-    uint8_t* to = at;
-    const int bytes = p.H * (f32 ? 4 : 2);
-    for (int i = tid * 16; i < bytes; i += threads * 16)
-      *reinterpret_cast<uint4*>(to + i) = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + i));
-    at += bytes;
-    return to;
+  auto share = [&](const void* from, int f32) {
+    const Shared given{from, f32 != 0};
+    if (!from || !p.shared_params) return given;
+    float* to = reinterpret_cast<float*>(at);
+    for (int i = tid * 8; i < p.H; i += threads * 8) store8(to + i, given.load(i));
+    at += p.H * 4;
+    return Shared{to, true};
   };
   s.w = share(p.w, p.w_f32);
   s.v = share(p.v, p.v_f32);
-  s.g = p.groups > 1 ? p.g : share(p.g, p.g_f32);
+  s.g = p.groups > 1 ? Shared{p.g, p.g_f32 != 0} : share(p.g, p.g_f32);
   __syncthreads();
   return s;
 }
@@ -252,65 +295,63 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const int c = threadIdx.x * 8;
   const bool mine = c < p.H;
-  const int64_t n = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t begin = norm_first_row(p.T, n, me);
-  const int rows = (int)(norm_first_row(p.T, n, me + 1) - begin);
+  const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
+  const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
   NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, nullptr, nullptr}, {(int)sizeof(X), 2, 0, 0}, begin, rows);
   RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
   int stage = 0;
   uint32_t phase = 0;
   GatePlace gate(p, begin, G ? rows : 0);
+  X* out_r = static_cast<X*>(p.r) + begin * p.H + c;
+  uint16_t* out_h = p.h + begin * p.H + c;
+  F8 w = fill8(0.f), v = fill8(0.f), g = fill8(0.f);
+  if (mine) {
+    if (W) w = s.w.load(c);
+    if (V) v = s.v.load(c);
+    if (G && rows > 0) g = s.g.load(gate.first(p) + c);
+  }
+  const F8 a = fill8(p.a);
   for (int i = 0; i < rows; ++i) {
-    const int64_t t = begin + i, at = t * p.H + c;
-    float g[8], r[8], y[8];
-    fill8(r, 0.f);
-    fill8(y, 0.f);
-    fill8(g, 0.f);
-    if (G && mine) load8(s.g, p.g_f32, gate.first(p) + c, g);
     const uint8_t* row = rg.wait(p, stage, phase);
+    F8 r = fill8(0.f), y = fill8(0.f);
     if (mine) {
-      load8(reinterpret_cast<const X*>(row) + c, r);
-      if (Y) load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c, y);
+      r = load8(reinterpret_cast<const X*>(row) + c);
+      if (Y) y = load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c);
     }
     if (V) {
-      float q = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q = fmaf(y[k], y[k], q);
-      const float sy = rsqrtf(rg.sum(q) * inv + p.eps);
+      const float sy = rsqrtf(rg.sum(dot8(y, y)) * inv + p.eps);
       rg.refill(p, i, stage);
-      if (p.stats && threadIdx.x == 0) p.stats[p.T + t] = sy;
-      float v[8];
-      fill8(v, 0.f);
-      if (mine) load8(s.v, p.v_f32, c, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] *= sy * v[k];
+      if (p.stats && threadIdx.x == 0) p.stats[p.T + begin + i] = sy;
+      mul8(y, sy);
+      mul8(y, v);
     }
     if (Y) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = fmaf(p.a, r[k], p.b * (G ? g[k] * y[k] : y[k]));
-      if (mine) store8(static_cast<X*>(p.r) + at, r);
+      if (G) mul8(y, g);
+      mul8(y, p.b);
+      fma8(a, r, y);
+      r = y;
+      if (mine) store8(out_r, r);
     }
     if (W) {
-      float q = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q = fmaf(r[k], r[k], q);
-      const float sr = rsqrtf(rg.sum(mine ? q : 0.f) * inv + p.eps);
+      const float sr = rsqrtf(rg.sum(mine ? dot8(r, r) : 0.f) * inv + p.eps);
       if (!V) rg.refill(p, i, stage);
-      if (p.stats && threadIdx.x == 0) p.stats[t] = sr;
-      if (mine) {
-        float w[8];
-        load8(s.w, p.w_f32, c, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] *= sr * w[k];
-        store8(p.h + at, r);
-      }
+      if (p.stats && threadIdx.x == 0) p.stats[begin + i] = sr;
+      mul8(r, sr);
+      mul8(r, w);
+      if (mine) store8(out_h, r);
     }
     if (!V && !W) {
       rg.sync();
       rg.refill(p, i, stage);
     }
-    if (G && p.groups > 1 && gate.ends()) gate.next(p);
+    if (G && p.groups > 1 && gate.ends()) {
+      gate.next(p);
+      if (mine && i + 1 < rows) g = s.g.load(gate.first(p) + c);
+    }
+    if (Y) out_r += p.H;
+    if (W) out_h += p.H;
     if (++stage == p.stages) {
       stage = 0;
       phase ^= 1u;
@@ -318,24 +359,37 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
   }
 }
 
+// A thread has two groups of 8 columns here, H / 16 threads to a row, and the
+// block half the threads: the columns' sums and what is kept between a row's
+// sums take up to 128 registers (with 8 columns and 64 registers the operands
+// of a gate or of v spill: 135 us for 8191 x 2048 with all of them).
 template <typename X, bool Y, bool W, bool V, bool G>
-__global__ void __launch_bounds__(kNormThreads, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  const int c = threadIdx.x * 8;
-  const bool mine = c < p.H;
-  const int64_t n = (int64_t)gridDim.x * blockDim.y, me = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t begin = norm_first_row(p.T, n, me);
-  const int rows = (int)(norm_first_row(p.T, n, me + 1) - begin);
+  constexpr bool kKeepG = !V;   // a gate's row stays in registers
+  int c[2];
+  bool mine[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    c[j] = (threadIdx.x + j * blockDim.x) * 8;
+    mine[j] = c[j] < p.H;
+  }
+  const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
+  const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
   NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, p.dh, p.dr}, {(int)sizeof(X), 2, 2, (int)sizeof(X)}, begin, rows);
   RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
-  float dw[8], dv[8], dg[8];
-  fill8(dw, 0.f);
-  fill8(dv, 0.f);
-  fill8(dg, 0.f);
+  F8 dw[2], dv[2], dg[2], gate_row[2];
   int stage = 0;
   uint32_t phase = 0;
   GatePlace gate(p, begin, G ? rows : 0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    dw[j] = dv[j] = dg[j] = gate_row[j] = fill8(0.f);
+    if (G && kKeepG && mine[j] && rows > 0) gate_row[j] = s.g.load(gate.first(p) + c[j]);
+  }
+  auto gate_of = [&](int j) { return kKeepG ? gate_row[j] : s.g.load(gate.first(p) + c[j]); };
   float next_r = 0.f, next_y = 0.f;   // the next row's statistics
   auto stats = [&](int i) {
     if (i >= rows) return;
@@ -343,109 +397,100 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_bwd_kernel(const _
     if (V) next_y = p.stats[p.T + begin + i];
   };
   stats(0);
+  X* out_x = static_cast<X*>(p.dx) + begin * p.H;
+  uint16_t* out_y = p.dy + begin * p.H;
+  const uint32_t at_y = p.H * sizeof(X), at_dh = at_y + (Y ? p.H * 2 : 0), at_dr = at_dh + (W ? p.H * 2 : 0);
   for (int i = 0; i < rows; ++i) {
-    const int64_t at = (begin + i) * p.H + c;
     const float sr = next_r, sy = next_y;
     stats(i + 1);
     // Between the sums a thread keeps r and dh w alone, and reads the row's
-    // other operands from shared memory again: registers for 1024 threads.
+    // other operands from shared memory again.
     const uint8_t* row = rg.wait(p, stage, phase);
-    const uint16_t* row_y = reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c;
-    const uint16_t* row_dh = row_y + (Y ? p.H : 0);
-    const X* row_dr = reinterpret_cast<const X*>(row_dh - c + (W ? p.H : 0)) + c;
-    auto load_y = [&](float (&y)[8]) {   // normed, without v
-      load8(row_y, y);
-      if (V) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= sy;
-      }
+    auto load_y = [&](int j) {   // normed, without v
+      F8 y = load8(reinterpret_cast<const uint16_t*>(row + at_y) + c[j]);
+      if (V) mul8(y, sy);
+      return y;
     };
-    float d[8];
-    fill8(d, 0.f);
+    auto load_dr = [&](int j) {
+      return mine[j] && p.dr ? load8(reinterpret_cast<const X*>(row + at_dr) + c[j]) : fill8(0.f);
+    };
+    F8 d[2];
     if (W) {
-      float r[8], u[8], q = 0.f;
-      fill8(r, 0.f);
-      fill8(u, 0.f);
-      if (mine) {
-        load8(reinterpret_cast<const X*>(row) + c, r);
+      F8 r[2];
+      float q = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {   // d: dh w
+        r[j] = d[j] = fill8(0.f);
+        if (!mine[j]) continue;
+        r[j] = load8(reinterpret_cast<const X*>(row) + c[j]);
         if (Y) {
-          float y[8], o[8];
-          load_y(y);
-          if (V) {
-            load8(s.v, p.v_f32, c, o);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= o[k];
-          }
-          if (G) {
-            load8(s.g, p.g_f32, gate.first(p) + c, o);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= o[k];
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) r[k] = fmaf(p.a, r[k], p.b * y[k]);
+          F8 y = load_y(j);
+          if (V) mul8(y, s.v.load(c[j]));
+          if (G) mul8(y, gate_of(j));
+          mul8(y, p.b);
+          fma8(fill8(p.a), r[j], y);
+          r[j] = y;
         }
-        load8(row_dh, u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          r[k] *= sr;
-          dw[k] = fmaf(u[k], r[k], dw[k]);
-        }
-        float w[8];
-        load8(s.w, p.w_f32, c, w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          u[k] *= w[k];
-          q = fmaf(u[k], r[k], q);
-        }
+        mul8(r[j], sr);
+        d[j] = load8(reinterpret_cast<const uint16_t*>(row + at_dh) + c[j]);
+        fma8(d[j], r[j], dw[j]);
+        mul8(d[j], s.w.load(c[j]));
+        q += dot8(d[j], r[j]);
       }
       q = rg.sum(q) * inv;
       rg.refill(p, i, stage);
-      if (mine && p.dr) load8(row_dr, d);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = fmaf(sr, u[k] - r[k] * q, d[k]);
-    } else if (mine && p.dr) {
-      load8(row_dr, d);
+      for (int j = 0; j < 2; ++j) {   // d = dr + s_r (dh w - r q)
+        fma8(fill8(-q), r[j], d[j]);
+        F8 o = load_dr(j);
+        fma8(fill8(sr), d[j], o);
+        d[j] = o;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) d[j] = load_dr(j);
     }
-    if (mine) {
-      float o[8];
+    float q = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = p.a * d[k];
-      store8(static_cast<X*>(p.dx) + at, o);
+    for (int j = 0; j < 2; ++j) {
+      if (!mine[j]) continue;
+      F8 o = d[j];
+      mul8(o, p.a);
+      store8(out_x + c[j], o);
+      if (!Y) continue;
+      mul8(d[j], p.b);
+      if (!G && !V) continue;
+      const F8 y = load_y(j);
+      if (V) {
+        const F8 v = s.v.load(c[j]);
+        if (G) {
+          F8 m = y;
+          mul8(m, v);
+          fma8(d[j], m, dg[j]);
+          mul8(d[j], gate_of(j));
+        }
+        fma8(d[j], y, dv[j]);
+        mul8(d[j], v);
+        q += dot8(d[j], y);
+      } else {
+        fma8(d[j], y, dg[j]);
+        mul8(d[j], gate_of(j));
+      }
+    }
+    if (V) {
+      q = rg.sum(q) * inv;
+      if (!W) rg.refill(p, i, stage);
     }
     if (Y) {
-      float y[8], q = 0.f;
-      fill8(y, 0.f);
-      if (mine) {
-        if (G || V) load_y(y);
-        float v[8];
-        if (V) load8(s.v, p.v_f32, c, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] *= p.b;
-        if (G) {
-          float g[8];
-          load8(s.g, p.g_f32, gate.first(p) + c, g);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            dg[k] = fmaf(d[k], V ? y[k] * v[k] : y[k], dg[k]);
-            d[k] *= g[k];
-          }
-        }
+      for (int j = 0; j < 2; ++j) {
+        if (!mine[j]) continue;
         if (V) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            dv[k] = fmaf(d[k], y[k], dv[k]);
-            d[k] *= v[k];
-            q = fmaf(d[k], y[k], q);
-          }
+          fma8(fill8(-q), load_y(j), d[j]);
+          mul8(d[j], sy);
         }
+        store8(out_y + c[j], d[j]);
       }
-      if (V) {
-        q = rg.sum(q) * inv;
-        if (!W) rg.refill(p, i, stage);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = sy * (d[k] - y[k] * q);
-      }
-      if (mine) store8(p.dy + at, d);
     }
     if (!V && !W) {
       rg.sync();
@@ -454,19 +499,24 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_bwd_kernel(const _
     if (G && p.groups > 1) {
       const bool ends = gate.ends();
       if (ends || i + 1 == rows) {
-        if (mine) {
-          const int64_t first = gate.group * p.gate_rows;
-          if (ends && first >= begin) {
-            if (p.g_f32) store8(static_cast<float*>(p.dg) + gate.first(p) + c, dg);
-            else store8(static_cast<uint16_t*>(p.dg) + gate.first(p) + c, dg);
-          } else {   // the range's first group, or its last
-            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * me + (first > begin)) * p.H + c, dg);
-          }
-        }
-        fill8(dg, 0.f);
+        const int64_t first = gate.group * p.gate_rows, at = gate.first(p);
         gate.next(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (!mine[j]) continue;
+          if (ends && first >= begin) {
+            if (p.g_f32) store8(static_cast<float*>(p.dg) + at + c[j], dg[j]);
+            else store8(static_cast<uint16_t*>(p.dg) + at + c[j], dg[j]);
+          } else {   // the range's first group, or its last
+            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H + c[j], dg[j]);
+          }
+          dg[j] = fill8(0.f);
+          if (kKeepG && i + 1 < rows) gate_row[j] = s.g.load(gate.first(p) + c[j]);
+        }
       }
     }
+    out_x += p.H;
+    if (Y) out_y += p.H;
     if (++stage == p.stages) {
       stage = 0;
       phase ^= 1u;
@@ -476,17 +526,17 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_bwd_kernel(const _
   __syncthreads();
   float* block_sums = reinterpret_cast<float*>(norm_smem);   // [H]
   int k = 0;
-  auto add_up = [&](const float (&sum)[8]) {
+  auto add_up = [&](F8 (&sum)[2]) {
     for (int ty = 0; ty < (int)blockDim.y; ++ty) {
       if (blockDim.y > 1) __syncthreads();
-      if ((int)threadIdx.y != ty || !mine) continue;
-      float q[8];
-      fill8(q, 0.f);
-      if (ty > 0) load8(block_sums + c, q);
+      if ((int)threadIdx.y != ty) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] += sum[j];
-      if (ty + 1 < (int)blockDim.y) store8(block_sums + c, q);
-      else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H + c, q);
+      for (int j = 0; j < 2; ++j) {
+        if (!mine[j]) continue;
+        if (ty > 0) fma8(fill8(1.f), load8(block_sums + c[j]), sum[j]);
+        if (ty + 1 < (int)blockDim.y) store8(block_sums + c[j], sum[j]);
+        else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H + c[j], sum[j]);
+      }
     }
     ++k;
   };
@@ -502,7 +552,7 @@ struct NormSumParams {
   int n_sums, blocks;     // sums over all rows
   void* dg;
   int dg_f32;
-  int64_t T, groups, gate_rows, row_groups;
+  uint32_t T, groups, gate_rows, row_groups;
   int H;
 };
 
@@ -510,54 +560,59 @@ struct NormSumParams {
 // gate's group that several ranges share: group blockIdx.y - n_sums where
 // there are no more groups than ranges, else the one that range
 // blockIdx.y - n_sums + 1 goes on with.
-__global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumParams p) {
-  __shared__ float4 part[32][32];
+constexpr int kNormSumWarps = 16;
+__global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(const __grid_constant__ NormSumParams p) {
+  __shared__ float2 part[kNormSumWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 128 + 4 * lane;
+  const int c = blockIdx.x * 64 + 2 * lane;
   const bool mine = c < p.H;
   const bool whole = (int)blockIdx.y < p.n_sums;
   const float* first = p.parts + (int64_t)blockIdx.y * p.H;   // of the first part; the others: `rest` + i * pitch
   const float* rest = first;
-  int64_t n = p.blocks, pitch = (int64_t)p.n_sums * p.H, group = 0;
+  int64_t pitch = (int64_t)p.n_sums * p.H;
+  uint32_t n = p.blocks, group = 0;
   if (!whole) {
-    const int64_t y = blockIdx.y - p.n_sums;
-    int64_t from;
+    const uint32_t y = blockIdx.y - p.n_sums;
+    uint32_t from;
     if (p.groups <= p.row_groups) {
       group = y;
       from = norm_group_of(p.T, p.row_groups, group * p.gate_rows);
     } else {
-      const int64_t start = norm_first_row(p.T, p.row_groups, y + 1);
+      const uint32_t start = norm_first_row(p.T, p.row_groups, y + 1);
       group = start / p.gate_rows;
+      if (start == group * p.gate_rows) return;
       from = norm_group_of(p.T, p.row_groups, group * p.gate_rows);
-      if (start == group * p.gate_rows || from != y) return;
+      if (from != y) return;
     }
-    const int64_t to = norm_group_of(p.T, p.row_groups, (group + 1) * p.gate_rows - 1);
+    const uint32_t to = norm_group_of(p.T, p.row_groups, (group + 1) * p.gate_rows - 1);
     if (from == to) return;   // within one range, which wrote it
     n = to - from + 1;
     pitch = 2 * p.H;
-    rest = p.parts + ((int64_t)p.blocks * p.n_sums + 2 * from) * p.H;
+    rest = p.parts + ((int64_t)p.blocks * p.n_sums + 2 * (int64_t)from) * p.H;
     first = rest + (norm_first_row(p.T, p.row_groups, from) < group * p.gate_rows ? p.H : 0);
   }
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 s = make_float2(0.f, 0.f);
   if (mine) {
-    for (int64_t i = warp; i < n; i += 32) {
-      const float4 q = *reinterpret_cast<const float4*>((i == 0 ? first : rest + i * pitch) + c);
-      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+#pragma unroll 4
+    for (uint32_t i = warp; i < n; i += kNormSumWarps) {
+      const float2 q = *reinterpret_cast<const float2*>((i == 0 ? first : rest + i * pitch) + c);
+      s.x += q.x; s.y += q.y;
     }
   }
   part[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && mine) {
-    for (int i = 1; i < 32; ++i) {
-      const float4 q = part[i][lane];
-      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+#pragma unroll
+    for (int i = 1; i < kNormSumWarps; ++i) {
+      const float2 q = part[i][lane];
+      s.x += q.x; s.y += q.y;
     }
     void* out = whole ? p.out[blockIdx.y] : p.dg;
-    const int64_t at = group * p.H + c;
-    if (whole ? p.f32[blockIdx.y] : p.dg_f32) *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = s;
-    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    const int64_t at = (int64_t)group * p.H + c;
+    if (whole ? p.f32[blockIdx.y] : p.dg_f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = s;
+    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16x2(s.x, s.y);
   }
 }
 
@@ -569,10 +624,10 @@ struct NormShape {
   int grid, stages, shared_params;
   size_t smem;
 };
-NormShape norm_shape(int64_t T, int64_t H, size_t row_bytes, size_t params) {
+NormShape norm_shape(int64_t T, int64_t H, int columns, size_t row_bytes, size_t params) {   // columns of a thread
   NormShape s;
-  const int tpr = (int)((H / 8 + 31) / 32 * 32);
-  int rows = kNormThreads / tpr;
+  const int tpr = (int)((H + columns - 1) / columns + 31) / 32 * 32;
+  int rows = kNormThreads * 8 / columns / tpr;
   if (tpr > 32) rows = std::min(rows, 15);   // row groups' barriers 1 .. 15; a warp needs none
   rows = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
   rows = (int)std::max<size_t>(1, std::min<size_t>(rows, kNormSmem / (2 * row_bytes)));
@@ -586,7 +641,7 @@ NormShape norm_shape(int64_t T, int64_t H, size_t row_bytes, size_t params) {
 }
 
 size_t norm_params_bytes(const BlockNorm& n) {
-  return (size_t)n.H * ((n.w ? (n.w_f32 ? 4 : 2) : 0) + (n.v ? (n.v_f32 ? 4 : 2) : 0) + (n.groups == 1 ? (n.g_f32 ? 4 : 2) : 0));
+  return (size_t)n.H * 4 * ((n.w ? 1 : 0) + (n.v ? 1 : 0) + (n.groups == 1 ? 1 : 0));   // as fp32
 }
 
 NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo& dev) {
@@ -634,7 +689,7 @@ cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const 
 }
 
 NormShape norm_bwd_shape(int64_t T, int64_t H, bool x_f32, bool y, bool w, bool dr, size_t params) {
-  return norm_shape(T, H, (size_t)H * ((x_f32 ? 4 : 2) * (dr ? 2 : 1) + (y ? 2 : 0) + (w ? 2 : 0)), params);
+  return norm_shape(T, H, 16, (size_t)H * ((x_f32 ? 4 : 2) * (dr ? 2 : 1) + (y ? 2 : 0) + (w ? 2 : 0)), params);
 }
 
 }  // namespace
@@ -643,7 +698,7 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const NormShape s = norm_shape(n.T, n.H, (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n));
+  const NormShape s = norm_shape(n.T, n.H, 8, (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n));
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
   return norm_launch(false, n, s, p, dev, stream);
@@ -652,7 +707,7 @@ cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* s
 // The most that any types and any dr take: row groups are fewest bytes a row.
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
   if (T == 0) return 0;
-  const NormShape s = norm_shape(T, H, (size_t)H * (w ? 4 : 2), 0);
+  const NormShape s = norm_shape(T, H, 16, (size_t)H * (w ? 4 : 2), 0);
   const size_t n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
   const size_t blocks = std::min<int64_t>(T, kNormBlocks);
   return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
@@ -686,11 +741,11 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
   q.blocks = s.grid;
   q.dg = d.g;
   q.dg_f32 = n.g_f32;
-  q.T = n.T; q.groups = n.groups; q.gate_rows = p.gate_rows; q.H = p.H;
-  q.row_groups = (int64_t)s.grid * s.block.y;
-  const int64_t shared = n.groups > 1 && p.gate_rows > 1 ? (n.groups <= q.row_groups ? n.groups : q.row_groups - 1) : 0;
+  q.T = (uint32_t)n.T; q.groups = (uint32_t)n.groups; q.gate_rows = (uint32_t)p.gate_rows; q.H = p.H;
+  q.row_groups = (uint32_t)s.grid * s.block.y;
+  const int64_t shared = n.groups > 1 && p.gate_rows > 1 ? (n.groups <= q.row_groups ? n.groups : (int64_t)q.row_groups - 1) : 0;
   if (k + shared == 0) return cudaSuccess;
-  return launch_pdl(block_norm_sum_kernel, dim3((unsigned)((n.H + 127) / 128), (unsigned)(k + shared)), dim3(1024), 0, stream, 1, q);
+  return launch_pdl(block_norm_sum_kernel, dim3((unsigned)((n.H + 63) / 64), (unsigned)(k + shared)), dim3(32 * kNormSumWarps), 0, stream, 1, q);
 }
 
 }  // namespace moe
