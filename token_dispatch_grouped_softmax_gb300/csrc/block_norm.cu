@@ -34,10 +34,10 @@ namespace {
 constexpr int kNormMaxH = 8192;
 constexpr int kNormBlocks = 152;        // GB300's SMs; fixed, as the order of the columns' sums goes by it
 constexpr int kNormThreads = 1024;
-constexpr int kNormSmem = 200 * 1024;   // of a block: the rings and the operands that rows share
+constexpr int kNormSmem = 216 * 1024;   // of a block: the rings and the operands that rows share
 constexpr int kNormMaxStages = 4;
 
-// Eight columns of a thread, as four pairs for the packed fp32 instructions
+// Eight columns of a thread (Columns), as four pairs for the packed fp32 instructions
 // (two products, sums or fused ones an instruction, each rounded as alone).
 struct F8 {
   float2 v[4];
@@ -76,35 +76,57 @@ __device__ __forceinline__ float dot8(const F8& a, const F8& b) {
   return s.x + s.y;
 }
 
-__device__ __forceinline__ F8 load8(const float* p) {
-  F8 r;
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  r.v[0] = make_float2(a.x, a.y); r.v[1] = make_float2(a.z, a.w);
-  r.v[2] = make_float2(b.x, b.y); r.v[3] = make_float2(b.z, b.w);
+// A warp has 256 consecutive columns, and a lane four of either half of them:
+// 16-byte accesses of fp32 then lie side by side, in shared memory without
+// bank conflicts and in global memory in whole sectors.
+struct Columns {
+  int a, b;          // the first of either four
+  bool in_a, in_b;   // within the row
+  __device__ __forceinline__ Columns() {}
+  __device__ __forceinline__ Columns(int warp, int H) {
+    a = 256 * warp + 4 * (threadIdx.x & 31);
+    b = a + 128;
+    in_a = a < H;
+    in_b = b < H;
+  }
+};
+
+__device__ __forceinline__ void load4(const float* p, float2* v) {
+  const float4 q = *reinterpret_cast<const float4*>(p);
+  v[0] = make_float2(q.x, q.y);
+  v[1] = make_float2(q.z, q.w);
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float2* v) {
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+  v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+}
+__device__ __forceinline__ void store4(float* p, const float2* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float2* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+}
+// A thread's columns of a row, zeros beyond it.
+template <typename T>
+__device__ __forceinline__ F8 load8(const T* row, const Columns& c) {
+  F8 r = fill8(0.f);
+  if (c.in_a) load4(row + c.a, r.v);
+  if (c.in_b) load4(row + c.b, r.v + 2);
   return r;
 }
-__device__ __forceinline__ F8 load8(const uint16_t* p) {
-  F8 r;
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  r.v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x)); r.v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
-  r.v[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z)); r.v[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
-  return r;
-}
-__device__ __forceinline__ void store8(float* p, const F8& a) {
-  *reinterpret_cast<float4*>(p) = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
-}
-__device__ __forceinline__ void store8(uint16_t* p, const F8& a) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(a.v[0].x, a.v[0].y), pack_bf16x2(a.v[1].x, a.v[1].y),
-                                            pack_bf16x2(a.v[2].x, a.v[2].y), pack_bf16x2(a.v[3].x, a.v[3].y));
+template <typename T>
+__device__ __forceinline__ void store8(T* row, const Columns& c, const F8& v) {
+  if (c.in_a) store4(row + c.a, v.v);
+  if (c.in_b) store4(row + c.b, v.v + 2);
 }
 
-// A vector that rows share, fp32 or bf16.
+// Vectors that rows share, fp32 or bf16.
 struct Shared {
   const void* p;
   bool f32;
-  __device__ __forceinline__ F8 load(int64_t at) const {
-    return f32 ? load8(static_cast<const float*>(p) + at) : load8(static_cast<const uint16_t*>(p) + at);
+  __device__ __forceinline__ F8 load(int64_t at, const Columns& c) const {
+    return f32 ? load8(static_cast<const float*>(p) + at, c) : load8(static_cast<const uint16_t*>(p) + at, c);
   }
 };
 
@@ -261,7 +283,12 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
     const Shared given{from, f32 != 0};
     if (!from || !p.shared_params) return given;
     float* to = reinterpret_cast<float*>(at);
-    for (int i = tid * 8; i < p.H; i += threads * 8) store8(to + i, given.load(i));
+    for (int i = tid * 4; i < p.H; i += threads * 4) {
+      float2 v[2];
+      if (given.f32) load4(static_cast<const float*>(from) + i, v);
+      else load4(static_cast<const uint16_t*>(from) + i, v);
+      store4(to + i, v);
+    }
     at += p.H * 4;
     return Shared{to, true};
   };
@@ -293,8 +320,7 @@ struct GatePlace {
 template <typename X, bool Y, bool W, bool V, bool G>
 __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  const int c = threadIdx.x * 8;
-  const bool mine = c < p.H;
+  const Columns c(threadIdx.x >> 5, p.H);
   const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
   const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
@@ -304,22 +330,17 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
   int stage = 0;
   uint32_t phase = 0;
   GatePlace gate(p, begin, G ? rows : 0);
-  X* out_r = static_cast<X*>(p.r) + begin * p.H + c;
-  uint16_t* out_h = p.h + begin * p.H + c;
+  X* out_r = static_cast<X*>(p.r) + begin * p.H;
+  uint16_t* out_h = p.h + begin * p.H;
   F8 w = fill8(0.f), v = fill8(0.f), g = fill8(0.f);
-  if (mine) {
-    if (W) w = s.w.load(c);
-    if (V) v = s.v.load(c);
-    if (G && rows > 0) g = s.g.load(gate.first(p) + c);
-  }
+  if (W) w = s.w.load(0, c);
+  if (V) v = s.v.load(0, c);
+  if (G && rows > 0) g = s.g.load(gate.first(p), c);
   const F8 a = fill8(p.a);
   for (int i = 0; i < rows; ++i) {
     const uint8_t* row = rg.wait(p, stage, phase);
-    F8 r = fill8(0.f), y = fill8(0.f);
-    if (mine) {
-      r = load8(reinterpret_cast<const X*>(row) + c);
-      if (Y) y = load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)) + c);
-    }
+    F8 r = load8(reinterpret_cast<const X*>(row), c), y = fill8(0.f);
+    if (Y) y = load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)), c);
     if (V) {
       const float sy = rsqrtf(rg.sum(dot8(y, y)) * inv + p.eps);
       rg.refill(p, i, stage);
@@ -332,15 +353,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
       mul8(y, p.b);
       fma8(a, r, y);
       r = y;
-      if (mine) store8(out_r, r);
+      store8(out_r, c, r);
     }
     if (W) {
-      const float sr = rsqrtf(rg.sum(mine ? dot8(r, r) : 0.f) * inv + p.eps);
+      const float sr = rsqrtf(rg.sum(dot8(r, r)) * inv + p.eps);
       if (!V) rg.refill(p, i, stage);
       if (p.stats && threadIdx.x == 0) p.stats[begin + i] = sr;
       mul8(r, sr);
       mul8(r, w);
-      if (mine) store8(out_h, r);
+      store8(out_h, c, r);
     }
     if (!V && !W) {
       rg.sync();
@@ -348,7 +369,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
     }
     if (G && p.groups > 1 && gate.ends()) {
       gate.next(p);
-      if (mine && i + 1 < rows) g = s.g.load(gate.first(p) + c);
+      if (i + 1 < rows) g = s.g.load(gate.first(p), c);
     }
     if (Y) out_r += p.H;
     if (W) out_h += p.H;
@@ -367,13 +388,7 @@ template <typename X, bool Y, bool W, bool V, bool G>
 __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
   constexpr bool kKeepG = !V;   // a gate's row stays in registers
-  int c[2];
-  bool mine[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    c[j] = (threadIdx.x + j * blockDim.x) * 8;
-    mine[j] = c[j] < p.H;
-  }
+  const Columns c[2] = {Columns(threadIdx.x >> 5, p.H), Columns((threadIdx.x + blockDim.x) >> 5, p.H)};
   const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
   const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
@@ -387,9 +402,9 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     dw[j] = dv[j] = dg[j] = gate_row[j] = fill8(0.f);
-    if (G && kKeepG && mine[j] && rows > 0) gate_row[j] = s.g.load(gate.first(p) + c[j]);
+    if (G && kKeepG && rows > 0) gate_row[j] = s.g.load(gate.first(p), c[j]);
   }
-  auto gate_of = [&](int j) { return kKeepG ? gate_row[j] : s.g.load(gate.first(p) + c[j]); };
+  auto gate_of = [&](int j) { return kKeepG ? gate_row[j] : s.g.load(gate.first(p), c[j]); };
   float next_r = 0.f, next_y = 0.f;   // the next row's statistics
   auto stats = [&](int i) {
     if (i >= rows) return;
@@ -407,12 +422,12 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     // other operands from shared memory again.
     const uint8_t* row = rg.wait(p, stage, phase);
     auto load_y = [&](int j) {   // normed, without v
-      F8 y = load8(reinterpret_cast<const uint16_t*>(row + at_y) + c[j]);
+      F8 y = load8(reinterpret_cast<const uint16_t*>(row + at_y), c[j]);
       if (V) mul8(y, sy);
       return y;
     };
     auto load_dr = [&](int j) {
-      return mine[j] && p.dr ? load8(reinterpret_cast<const X*>(row + at_dr) + c[j]) : fill8(0.f);
+      return p.dr ? load8(reinterpret_cast<const X*>(row + at_dr), c[j]) : fill8(0.f);
     };
     F8 d[2];
     if (W) {
@@ -420,21 +435,19 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
       float q = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {   // d: dh w
-        r[j] = d[j] = fill8(0.f);
-        if (!mine[j]) continue;
-        r[j] = load8(reinterpret_cast<const X*>(row) + c[j]);
+        r[j] = load8(reinterpret_cast<const X*>(row), c[j]);
         if (Y) {
           F8 y = load_y(j);
-          if (V) mul8(y, s.v.load(c[j]));
+          if (V) mul8(y, s.v.load(0, c[j]));
           if (G) mul8(y, gate_of(j));
           mul8(y, p.b);
           fma8(fill8(p.a), r[j], y);
           r[j] = y;
         }
         mul8(r[j], sr);
-        d[j] = load8(reinterpret_cast<const uint16_t*>(row + at_dh) + c[j]);
+        d[j] = load8(reinterpret_cast<const uint16_t*>(row + at_dh), c[j]);
         fma8(d[j], r[j], dw[j]);
-        mul8(d[j], s.w.load(c[j]));
+        mul8(d[j], s.w.load(0, c[j]));
         q += dot8(d[j], r[j]);
       }
       q = rg.sum(q) * inv;
@@ -453,16 +466,15 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     float q = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if (!mine[j]) continue;
       F8 o = d[j];
       mul8(o, p.a);
-      store8(out_x + c[j], o);
+      store8(out_x, c[j], o);
       if (!Y) continue;
       mul8(d[j], p.b);
       if (!G && !V) continue;
       const F8 y = load_y(j);
       if (V) {
-        const F8 v = s.v.load(c[j]);
+        const F8 v = s.v.load(0, c[j]);
         if (G) {
           F8 m = y;
           mul8(m, v);
@@ -484,12 +496,11 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     if (Y) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (!mine[j]) continue;
-        if (V) {
+          if (V) {
           fma8(fill8(-q), load_y(j), d[j]);
           mul8(d[j], sy);
         }
-        store8(out_y + c[j], d[j]);
+        store8(out_y, c[j], d[j]);
       }
     }
     if (!V && !W) {
@@ -503,15 +514,14 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
         gate.next(p);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (!mine[j]) continue;
-          if (ends && first >= begin) {
-            if (p.g_f32) store8(static_cast<float*>(p.dg) + at + c[j], dg[j]);
-            else store8(static_cast<uint16_t*>(p.dg) + at + c[j], dg[j]);
+              if (ends && first >= begin) {
+            if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], dg[j]);
+            else store8(static_cast<uint16_t*>(p.dg) + at, c[j], dg[j]);
           } else {   // the range's first group, or its last
-            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H + c[j], dg[j]);
+            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H, c[j], dg[j]);
           }
           dg[j] = fill8(0.f);
-          if (kKeepG && i + 1 < rows) gate_row[j] = s.g.load(gate.first(p) + c[j]);
+          if (kKeepG && i + 1 < rows) gate_row[j] = s.g.load(gate.first(p), c[j]);
         }
       }
     }
@@ -532,10 +542,9 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
       if ((int)threadIdx.y != ty) continue;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (!mine[j]) continue;
-        if (ty > 0) fma8(fill8(1.f), load8(block_sums + c[j]), sum[j]);
-        if (ty + 1 < (int)blockDim.y) store8(block_sums + c[j], sum[j]);
-        else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H + c[j], sum[j]);
+          if (ty > 0) fma8(fill8(1.f), load8(block_sums, c[j]), sum[j]);
+        if (ty + 1 < (int)blockDim.y) store8(block_sums, c[j], sum[j]);
+        else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H, c[j], sum[j]);
       }
     }
     ++k;
