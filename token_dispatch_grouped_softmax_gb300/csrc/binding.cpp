@@ -535,38 +535,48 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   std::vector<uint8_t> f32(n);
   struct Span {
     uintptr_t begin, end;
-    Py_ssize_t i;
-    bool out;
+    bool operator<(const Span& o) const { return begin < o.begin; }
   };
-  std::vector<Span> spans;
-  if (clip) spans.reserve(2 * n);
+  std::vector<Span> reads, writes;   // of what is read alone, and of what is written
+  const int device = c10::cuda::current_device();   // need() asks for it each time
+  auto tensor = [&](PyObject* o, const char* name, at::ScalarType type, at::ScalarType or_type) -> const at::Tensor& {
+    if (THPVariable_Check(o)) {
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (t.is_cuda() && t.get_device() == device && (t.scalar_type() == type || t.scalar_type() == or_type) && t.is_contiguous()) return t;
+    }
+    return need(o, name, type, or_type == at::kBFloat16 ? "torch.float32 or torch.bfloat16" : "of its gradient's type", -1, or_type);
+  };
   for (Py_ssize_t i = 0; i < n; ++i) {
     PyObject* o = PySequence_Fast_GET_ITEM(a[0], i);
-    const at::Tensor& g = need(o, "a gradient", at::kFloat, "torch.float32 or torch.bfloat16", -1, at::kBFloat16);
+    const at::Tensor& g = tensor(o, "a gradient", at::kFloat, at::kBFloat16);
     src[i] = ptr(g);
     size[i] = g.numel();
     f32[i] = g.scalar_type() == at::kFloat;
     if (!clip) continue;
+    dst[i] = const_cast<void*>(src[i]);
     PyObject* q = PySequence_Fast_GET_ITEM(a[1], i);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(src[i]), bytes = (uintptr_t)size[i] * (f32[i] ? 4 : 2);
     if (q != o) {
-      const at::Tensor& t = need(q, "a tensor of out", g.scalar_type(), "of its gradient's type", -1);
+      const at::Tensor& t = tensor(q, "a tensor of out", g.scalar_type(), at::ScalarType::Undefined);
       if (t.numel() != size[i]) refuse(PyExc_ValueError, "a tensor of out must have its gradient's size");
       dst[i] = ptr(t);
-      if (bytes && dst[i] != src[i]) spans.push_back({at, at + bytes, i, false});
-    } else {
-      dst[i] = const_cast<void*>(src[i]);
     }
-    const uintptr_t to = reinterpret_cast<uintptr_t>(dst[i]);
-    if (bytes) spans.push_back({to, to + bytes, i, true});
+    const uintptr_t bytes = (uintptr_t)size[i] * (f32[i] ? 4 : 2), from = reinterpret_cast<uintptr_t>(src[i]),
+                    to = reinterpret_cast<uintptr_t>(dst[i]);
+    if (bytes == 0) continue;
+    if (to != from) reads.push_back({from, from + bytes});
+    writes.push_back({to, to + bytes});
   }
   // what is written overlaps nothing else: a gradient that is listed twice would be scaled twice
-  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.begin < y.begin; });
-  uintptr_t end = 0, written = 0;   // of the spans so far, and of those that are written
-  for (const Span& s : spans) {
-    if (s.begin < written || (s.out && s.begin < end)) refuse(PyExc_ValueError, "a tensor of out overlaps another tensor");
-    end = std::max(end, s.end);
-    if (s.out) written = std::max(written, s.end);
+  for (std::vector<Span>* v : {&reads, &writes})
+    if (!std::is_sorted(v->begin(), v->end())) std::sort(v->begin(), v->end());
+  uintptr_t end = 0;
+  auto read = reads.begin();
+  for (const Span& s : writes) {
+    if (s.begin < end) refuse(PyExc_ValueError, "a tensor of out overlaps another one of out");
+    end = s.end;
+    while (read != reads.end() && read->end <= s.begin) ++read;
+    for (auto r = read; r != reads.end() && r->begin < s.end; ++r)
+      if (r->end > s.begin) refuse(PyExc_ValueError, "a tensor of out overlaps a gradient");
   }
   const at::Tensor& first = THPVariable_Unpack(PySequence_Fast_GET_ITEM(a[0], 0));
   const float max_norm = (float)real(a[2]), eps = (float)real(a[3]);

@@ -136,6 +136,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+enum { kInGlobal, kAsGiven, kAsFp32 };   // the last two in shared memory
+
 struct NormParams {
   const void* x;
   const uint16_t* y;
@@ -157,7 +159,7 @@ struct NormParams {
   int w_f32, v_f32, g_f32;
   int n_sums;             // columns' sums over all rows: dw, dv, dg with one group
   int stages;
-  int shared_params;      // w, v and a single g have room in shared memory
+  int shared_params;      // where w, v and a single g are
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -230,7 +232,7 @@ struct RowGroup {
 
 struct NormSetup {
   RowGroup rg;
-  Shared w, v, g;         // w, v and a single gate: fp32 in shared memory where they fit
+  Shared w, v, g;         // w, v and a single gate: in shared memory where they fit
 };
 
 // The block's shared memory: the row groups' rings, then w, v and a single g.
@@ -282,15 +284,22 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
   auto share = [&](const void* from, int f32) {
     const Shared given{from, f32 != 0};
     if (!from || !p.shared_params) return given;
-    float* to = reinterpret_cast<float*>(at);
-    for (int i = tid * 4; i < p.H; i += threads * 4) {
-      float2 v[2];
-      if (given.f32) load4(static_cast<const float*>(from) + i, v);
-      else load4(static_cast<const uint16_t*>(from) + i, v);
-      store4(to + i, v);
+    uint8_t* to = at;
+    if (p.shared_params == kAsFp32) {
+      for (int i = tid * 4; i < p.H; i += threads * 4) {
+        float2 v[2];
+        if (given.f32) load4(static_cast<const float*>(from) + i, v);
+        else load4(static_cast<const uint16_t*>(from) + i, v);
+        store4(reinterpret_cast<float*>(to) + i, v);
+      }
+      at += p.H * 4;
+      return Shared{to, true};
     }
-    at += p.H * 4;
-    return Shared{to, true};
+    const int bytes = p.H * (f32 ? 4 : 2);
+    for (int i = tid * 16; i < bytes; i += threads * 16)
+      *reinterpret_cast<uint4*>(to + i) = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + i));
+    at += bytes;
+    return Shared{to, given.f32};
   };
   s.w = share(p.w, p.w_f32);
   s.v = share(p.v, p.v_f32);
@@ -651,32 +660,35 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
   }
 }
 
-// A launch's shape.  row_bytes: of a row's streams; params: of w, v and a
-// single gate, which stay in global memory where two stages do not fit beside
-// them.
+// A launch's shape.  row_bytes: of a row's streams; params, wide: of w, v and
+// a single gate as given and as fp32.  They are kept as fp32 where two stages
+// fit beside them (16384 x 7168, bf16, backward: 200 us, as given 212), else as
+// given (4096 x 4096, fp32 stream, bf16 weights: 83 us, from global memory 94).
 struct NormShape {
   dim3 block;
   int grid, stages, shared_params;
   size_t smem;
 };
-NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t params) {   // of a block; of 8 columns
+NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t params, size_t wide) {   // of a block; of 8 columns
   NormShape s;
   const int tpr = (int)((H + 256 * groups - 1) / (256 * groups) * 32);
   int rows = threads / tpr;
   if (tpr > 32) rows = std::min(rows, 15);   // row groups' barriers 1 .. 15; a warp needs none
   rows = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
   rows = (int)std::max<size_t>(1, std::min<size_t>(rows, kNormSmem / (2 * row_bytes)));
-  s.shared_params = params + 2 * rows * row_bytes <= kNormSmem;
-  const size_t room = kNormSmem - (s.shared_params ? params : 0);
+  s.shared_params = 2 * rows * row_bytes + wide <= kNormSmem ? kAsFp32 : 2 * rows * row_bytes + params <= kNormSmem ? kAsGiven : kInGlobal;
+  params = s.shared_params == kAsFp32 ? wide : s.shared_params == kAsGiven ? params : 0;
+  const size_t room = kNormSmem - params;
   s.stages = (int)std::min<size_t>(kNormMaxStages, room / (rows * row_bytes));
   s.block = dim3(tpr, rows);
   s.grid = (int)std::min<int64_t>((T + rows - 1) / rows, kNormBlocks);
-  s.smem = (size_t)rows * s.stages * row_bytes + (s.shared_params ? params : 0);
+  s.smem = (size_t)rows * s.stages * row_bytes + params;
   return s;
 }
 
+size_t norm_wide_bytes(const BlockNorm& n) { return (size_t)n.H * 4 * ((n.w != nullptr) + (n.v != nullptr) + (n.groups == 1)); }
 size_t norm_params_bytes(const BlockNorm& n) {
-  return (size_t)n.H * 4 * ((n.w ? 1 : 0) + (n.v ? 1 : 0) + (n.groups == 1 ? 1 : 0));   // as fp32
+  return (size_t)n.H * ((n.w ? (n.w_f32 ? 4 : 2) : 0) + (n.v ? (n.v_f32 ? 4 : 2) : 0) + (n.groups == 1 ? (n.g_f32 ? 4 : 2) : 0));
 }
 
 NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo& dev) {
@@ -723,8 +735,9 @@ cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const 
   return launch_pdl(kernel, dim3(s.grid), s.block, s.smem, stream, 1, p);
 }
 
-NormShape norm_bwd_shape(int64_t T, int64_t H, bool x_f32, bool y, bool w, bool dr, size_t params) {
-  return norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * ((x_f32 ? 4 : 2) * (dr ? 2 : 1) + (y ? 2 : 0) + (w ? 2 : 0)), params);
+NormShape norm_bwd_shape(const BlockNorm& n, bool dr) {
+  return norm_shape(n.T, n.H, kNormThreads / 2, 2, (size_t)n.H * ((n.x_f32 ? 4 : 2) * (dr ? 2 : 1) + (n.y ? 2 : 0) + (n.w ? 2 : 0)),
+                    norm_params_bytes(n), norm_wide_bytes(n));
 }
 
 }  // namespace
@@ -733,7 +746,8 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const NormShape s = norm_shape(n.T, n.H, kNormThreads, kNormGroups(n.v && n.w), (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n));
+  const NormShape s = norm_shape(n.T, n.H, kNormThreads, kNormGroups(n.v && n.w), (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n),
+                                 norm_wide_bytes(n));
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
   return norm_launch(false, n, s, p, dev, stream);
@@ -742,7 +756,7 @@ cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* s
 // The most that any types and any dr take: row groups are fewest bytes a row.
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
   if (T == 0) return 0;
-  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0);
+  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, 0);
   const size_t n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
   const size_t blocks = std::min<int64_t>(T, kNormBlocks);
   return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
@@ -759,7 +773,7 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
       }
     return cudaSuccess;
   }
-  const NormShape s = norm_bwd_shape(n.T, n.H, n.x_f32, n.y, n.w, dr, norm_params_bytes(n));
+  const NormShape s = norm_bwd_shape(n, dr != nullptr);
   NormParams p = norm_params(n, s, dev);
   p.stats = const_cast<float*>(stats);
   p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g;

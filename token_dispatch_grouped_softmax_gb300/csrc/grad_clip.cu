@@ -20,16 +20,29 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kClipChunk = 1 << 14;      // elements
-constexpr int kClipTensors = 512;        // of one launch: 14 KB of parameters
-constexpr int kClipBlocks = 4 * 152;     // four to an SM of GB300; fixed, as the order of the sums goes by it
+constexpr int kClipTensors = 512;        // of one launch: 17 KB of parameters
+constexpr int kClipBlocks = 8 * 152;     // eight to an SM of GB300; fixed, as the order of the sums goes by it
 
 struct ClipList {
   const void* src[kClipTensors];
   void* dst[kClipTensors];
   int64_t size[kClipTensors];            // elements; fp32 tensors as ~size
   int first_chunk[kClipTensors + 1];
+  uint16_t start[kClipBlocks];           // the tensor of a block's first chunk
   int n;
 };
+
+// A block's chunks: consecutive ones, so that it looks its first tensor up and
+// walks on from there (a search among the parameters is a chain of misses in
+// the constant cache: 97 small tensors took 11 us to scale).
+struct ClipRange {
+  int begin, end;
+};
+__device__ __host__ __forceinline__ ClipRange clip_range(int chunks, int blocks, int block) {
+  const int share = chunks / blocks, more = chunks - share * blocks;
+  const int begin = block * share + (block < more ? block : more);
+  return ClipRange{begin, begin + share + (block < more ? 1 : 0)};
+}
 
 struct ClipChunk {
   int tensor;
@@ -42,22 +55,17 @@ __device__ __host__ __forceinline__ int clip_head(const void* p, bool f32) {
   return (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (f32 ? 4 : 2);
 }
 
-// Chunk `at` of the list: chunk i of a tensor holds elements head + 2^14 i on,
-// and the first the head too, so that every chunk's vectors are aligned.
-__device__ __forceinline__ ClipChunk clip_chunk(const ClipList& list, int at) {
-  int lo = 0, hi = list.n - 1;           // the largest tensor whose first chunk is at most `at`
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (list.first_chunk[mid] <= at) lo = mid;
-    else hi = mid - 1;
-  }
+// Chunk `at` of the list, of tensor `tensor`: chunk i of a tensor holds
+// elements head + 2^14 i on, and the first the head too, so that every chunk's
+// vectors are aligned.
+__device__ __forceinline__ ClipChunk clip_chunk(const ClipList& list, int tensor, int at) {
   ClipChunk c;
-  c.tensor = lo;
-  int64_t size = list.size[lo];
+  c.tensor = tensor;
+  int64_t size = list.size[tensor];
   c.f32 = size < 0;
   if (c.f32) size = ~size;
-  const int i = at - list.first_chunk[lo];
-  const int head = clip_head(list.src[lo], c.f32);
+  const int i = at - list.first_chunk[tensor];
+  const int head = clip_head(list.src[tensor], c.f32);
   c.begin = i == 0 ? 0 : head + (int64_t)i * kClipChunk;
   c.end = min(head + (int64_t)(i + 1) * kClipChunk, size);
   return c;
@@ -93,9 +101,11 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
   double total = 0.0;
-  const int chunks = list.first_chunk[list.n];
-  for (int at = blockIdx.x; at < chunks; at += gridDim.x) {
-    const ClipChunk c = clip_chunk(list, at);
+  const ClipRange range = clip_range(list.first_chunk[list.n], gridDim.x, blockIdx.x);
+  int tensor = list.start[blockIdx.x];
+  for (int at = range.begin; at < range.end; ++at) {
+    while (at >= list.first_chunk[tensor + 1]) ++tensor;
+    const ClipChunk c = clip_chunk(list, tensor, at);
     const void* src = list.src[c.tensor];
     const int head = clip_head(src, c.f32);
     float s = 0.f;
@@ -137,8 +147,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const __grid_co
   }
 }
 
-// The norm from the blocks' sums, the same bits in every block that computes it.
-__device__ __forceinline__ double clip_norm(const double* parts, int n) {
+// The sum of the blocks' sums, the same bits in every block that computes it.
+__device__ __forceinline__ double clip_sum(const double* parts, int n) {
   __shared__ double warps[kClipThreads / 32];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kClipThreads) s += parts[i];
@@ -148,31 +158,39 @@ __device__ __forceinline__ double clip_norm(const double* parts, int n) {
   __syncthreads();
   s = 0.0;
   for (int i = 0; i < kClipThreads / 32; ++i) s += warps[i];
-  return sqrt(s);
+  return s;
 }
 
 __global__ void __launch_bounds__(kClipThreads) grad_norm_sum_kernel(const double* parts, int n, float* norm) {
   pdl_wait();
   pdl_trigger();
-  const double v = clip_norm(parts, n);
-  if (threadIdx.x == 0) *norm = (float)v;
+  const double s = clip_sum(parts, n);
+  if (threadIdx.x == 0) *norm = (float)sqrt(s);
 }
 
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ ClipList list, const double* parts,
                                                                   int n, float max_norm, float eps, float* norm) {
   pdl_wait();
   pdl_trigger();
-  const double total = clip_norm(parts, n);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
-  double factor = max_norm / (total + eps);
-  if (factor > 1.0) factor = 1.0;   // NaN stays
-  // a factor below fp32's normal range, of gradients near the range's end, in two steps
-  const float step = factor < 0x1p-64 ? 0x1p-64f : 1.f, scale = (float)(factor < 0x1p-64 ? factor * 0x1p64 : factor);
+  __shared__ float2 scale_step;
+  const double sum = clip_sum(parts, n);
+  if (threadIdx.x == 0) {
+    const double total = sqrt(sum);
+    if (norm && blockIdx.x == 0) *norm = (float)total;
+    double factor = max_norm / (total + eps);
+    if (factor > 1.0) factor = 1.0;   // NaN stays
+    // a factor below fp32's normal range, of gradients near the range's end, in two steps
+    scale_step = factor < 0x1p-64 ? make_float2((float)(factor * 0x1p64), 0x1p-64f) : make_float2((float)factor, 1.f);
+  }
+  __syncthreads();
+  const float scale = scale_step.x, step = scale_step.y;
   auto scaled = [&](float v) { return v * scale * step; };
-  const int chunks = list.first_chunk[list.n];
+  const ClipRange range = clip_range(list.first_chunk[list.n], gridDim.x, blockIdx.x);
+  int tensor = blockIdx.x + 1 < gridDim.x ? list.start[blockIdx.x + 1] : list.n - 1;
   // from the last chunk on: those are the ones that the L2 still holds
-  for (int at = chunks - 1 - blockIdx.x; at >= 0; at -= gridDim.x) {
-    const ClipChunk c = clip_chunk(list, at);
+  for (int at = range.end - 1; at >= range.begin; --at) {
+    while (at < list.first_chunk[tensor]) --tensor;
+    const ClipChunk c = clip_chunk(list, tensor, at);
     const void* src = list.src[c.tensor];
     void* dst = list.dst[c.tensor];
     if (scale == 1.f && src == dst) continue;
@@ -240,6 +258,12 @@ ClipLaunch clip_launch(const GradList& g, int64_t first, ClipList* list) {
     list->n = l.n;
   }
   l.grid = (int)std::min<int64_t>(chunks, (int64_t)kClipBlocks);
+  if (list)
+    for (int b = 0, i = 0; b < l.grid; ++b) {
+      const int at = clip_range((int)chunks, l.grid, b).begin;
+      while (at >= list->first_chunk[i + 1]) ++i;
+      list->start[b] = (uint16_t)i;
+    }
   return l;
 }
 
