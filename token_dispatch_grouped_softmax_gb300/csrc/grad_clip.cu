@@ -28,21 +28,12 @@ struct ClipList {
   void* dst[kClipTensors];
   int64_t size[kClipTensors];            // elements; fp32 tensors as ~size
   int first_chunk[kClipTensors + 1];
-  uint16_t start[kClipBlocks];           // the tensor of a block's first chunk
+  // the tensor of a block's first chunk, from where it walks on (a search among
+  // the parameters is a chain of misses in the constant cache: 97 small tensors
+  // took 11 us to scale)
+  uint16_t start[kClipBlocks];
   int n;
 };
-
-// A block's chunks: consecutive ones, so that it looks its first tensor up and
-// walks on from there (a search among the parameters is a chain of misses in
-// the constant cache: 97 small tensors took 11 us to scale).
-struct ClipRange {
-  int begin, end;
-};
-__device__ __host__ __forceinline__ ClipRange clip_range(int chunks, int blocks, int block) {
-  const int share = chunks / blocks, more = chunks - share * blocks;
-  const int begin = block * share + (block < more ? block : more);
-  return ClipRange{begin, begin + share + (block < more ? 1 : 0)};
-}
 
 struct ClipChunk {
   int tensor;
@@ -101,9 +92,9 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
   double total = 0.0;
-  const ClipRange range = clip_range(list.first_chunk[list.n], gridDim.x, blockIdx.x);
+  const int chunks = list.first_chunk[list.n];
   int tensor = list.start[blockIdx.x];
-  for (int at = range.begin; at < range.end; ++at) {
+  for (int at = blockIdx.x; at < chunks; at += gridDim.x) {
     while (at >= list.first_chunk[tensor + 1]) ++tensor;
     const ClipChunk c = clip_chunk(list, tensor, at);
     const void* src = list.src[c.tensor];
@@ -185,10 +176,9 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
   __syncthreads();
   const float scale = scale_step.x, step = scale_step.y;
   auto scaled = [&](float v) { return v * scale * step; };
-  const ClipRange range = clip_range(list.first_chunk[list.n], gridDim.x, blockIdx.x);
-  int tensor = blockIdx.x + 1 < gridDim.x ? list.start[blockIdx.x + 1] : list.n - 1;
+  int tensor = list.start[blockIdx.x];
   // from the last chunk on: those are the ones that the L2 still holds
-  for (int at = range.end - 1; at >= range.begin; --at) {
+  for (int at = list.first_chunk[list.n] - 1 - blockIdx.x; at >= 0; at -= gridDim.x) {
     while (at < list.first_chunk[tensor]) --tensor;
     const ClipChunk c = clip_chunk(list, tensor, at);
     const void* src = list.src[c.tensor];
@@ -235,7 +225,7 @@ struct ClipLaunch {
   int64_t first;
   int n, grid;
 };
-ClipLaunch clip_launch(const GradList& g, int64_t first, ClipList* list) {
+ClipLaunch clip_launch(const GradList& g, int64_t first, bool backward, ClipList* list) {   // chunks from the last on
   ClipLaunch l{first, (int)std::min<int64_t>(kClipTensors, g.n - first), 0};
   int64_t chunks = 0;
   for (int i = 0; i < l.n; ++i) {
@@ -258,10 +248,14 @@ ClipLaunch clip_launch(const GradList& g, int64_t first, ClipList* list) {
     list->n = l.n;
   }
   l.grid = (int)std::min<int64_t>(chunks, (int64_t)kClipBlocks);
-  if (list)
+  if (list && !backward)
     for (int b = 0, i = 0; b < l.grid; ++b) {
-      const int at = clip_range((int)chunks, l.grid, b).begin;
-      while (at >= list->first_chunk[i + 1]) ++i;
+      while (b >= list->first_chunk[i + 1]) ++i;
+      list->start[b] = (uint16_t)i;
+    }
+  if (list && backward)
+    for (int b = 0, i = l.n - 1; b < l.grid; ++b) {
+      while ((int)chunks - 1 - b < list->first_chunk[i]) --i;
       list->start[b] = (uint16_t)i;
     }
   return l;
@@ -272,7 +266,7 @@ ClipLaunch clip_launch(const GradList& g, int64_t first, ClipList* list) {
 size_t grad_norm_workspace_bytes(const GradList& g) {
   size_t parts = 0;
   for (int64_t at = 0; at < g.n;) {
-    const ClipLaunch l = clip_launch(g, at, nullptr);
+    const ClipLaunch l = clip_launch(g, at, false, nullptr);
     parts += l.grid;
     at += l.n;
   }
@@ -284,7 +278,7 @@ cudaError_t launch_grad_clip(const GradList& g, float max_norm, float eps, float
   double* parts = static_cast<double*>(ws);
   int n = 0;
   for (int64_t at = 0; at < g.n;) {
-    const ClipLaunch l = clip_launch(g, at, &list);
+    const ClipLaunch l = clip_launch(g, at, false, &list);
     if (l.grid > 0) {
       const cudaError_t e = launch_pdl(grad_norm_kernel, dim3(l.grid), dim3(kClipThreads), 0, stream, 1, list, parts + n);
       if (e != cudaSuccess) return e;
@@ -295,7 +289,7 @@ cudaError_t launch_grad_clip(const GradList& g, float max_norm, float eps, float
   if (!g.dst || n == 0)
     return launch_pdl(grad_norm_sum_kernel, dim3(1), dim3(kClipThreads), 0, stream, 1, (const double*)parts, n, norm);
   for (int64_t at = 0; at < g.n;) {
-    const ClipLaunch l = clip_launch(g, at, &list);
+    const ClipLaunch l = clip_launch(g, at, true, &list);
     if (l.grid > 0) {
       const cudaError_t e = launch_pdl(grad_scale_kernel, dim3(l.grid), dim3(kClipThreads), 0, stream, 1, list,
                                        (const double*)parts, n, max_norm, eps, norm);
