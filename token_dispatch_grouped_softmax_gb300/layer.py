@@ -251,11 +251,113 @@ class MoELayer(torch.nn.Module):
             return y
         return MoELayerFunction.apply(x, self.w_router, self.gate_up, self.down, self.k, bias)
 
+    @torch.no_grad()
+    def decode(self, x, bias=None):
+        """y of a few tokens (at most 128) in two launches (moe_forward_few);
+        nothing is kept for a backward or for the balance bias."""
+        return moe_forward_few(x.contiguous(), self.w_router, self.gate_up, self.down, self.k, bias, routing=self.routing,
+                               balance_bias=None if self.routing is None else self.balance_bias)[0]
+
     def update_balance_bias(self, rate):
         """balance_bias += rate * sign(mean load - load) by the last forward's loads."""
         if self.routing is None or self.balance_bias is None or self.last_counts is None:
             raise ValueError("update_balance_bias needs a layer with a Routing and a balance bias, after a forward")
         ops.route_balance_bias(self.balance_bias, self.last_counts, rate, out=self.balance_bias)
+
+
+class BlockNormFunction(torch.autograd.Function):
+    """ops.block_norm as (r, h) with its gradients; an operand that is None has none."""
+
+    @staticmethod
+    def forward(ctx, x, weight, branch, post_weight, gate, residual_scale, branch_scale, eps):
+        t = [None if v is None else v.contiguous() for v in (x, weight, branch, post_weight, gate)]
+        r, h, stats = ops.block_norm(t[0], t[1], t[2], t[3], t[4], residual_scale, branch_scale, eps, save_for_backward=True)
+        ctx.save_for_backward(*t, stats)
+        ctx.scales = residual_scale, branch_scale
+        ctx.set_materialize_grads(False)
+        return r, h
+
+    @staticmethod
+    def backward(ctx, dr, dh):
+        x, weight, branch, post_weight, gate, stats = ctx.saved_tensors
+        if weight is None:
+            dh = None
+        elif dh is None:
+            dh = torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
+        else:
+            dh = dh.contiguous()
+        dr = dr.contiguous() if dr is not None and branch is not None else None
+        g = ops.block_norm_bwd(dh, dr, x, stats, weight, branch, post_weight, gate, *ctx.scales)
+        return g["dx"], g["d_weight"], g["d_branch"], g["d_post_weight"], g["d_gate"], None, None, None
+
+
+def block_norm(x, weight=None, branch=None, post_weight=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6):
+    """(r, h) of ops.block_norm, with gradients for the operands that ask for them."""
+    given = (x, weight, branch, post_weight, gate)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in given):
+        return BlockNormFunction.apply(*given, residual_scale, branch_scale, eps)
+    t = [None if v is None else v.contiguous() for v in given]
+    return ops.block_norm(*t, residual_scale, branch_scale, eps)[:2]
+
+
+class MoEBlock(torch.nn.Module):
+    """A model's block around a MoELayer: the residual stream normed, the
+    layer, and its output added to the stream, by default as it is:
+
+        r = residual_scale x + branch_scale gate norm(layer(norm(x)))
+
+    post_norm norms the layer's output, learned_scale multiplies it by a
+    learned [H] vector, and forward takes a gate of its own (block_norm's).
+    The stream is fp32 or bf16; the layer runs in bf16.  A run of blocks fuses
+    each block's end with the next one's norm: ``r, h = block(x, h,
+    next_norm=following.norm)``."""
+
+    def __init__(self, layer, eps=1e-6, post_norm=False, learned_scale=None, residual_scale=1.0, branch_scale=1.0):
+        super().__init__()
+        H, device = layer.w_router.shape[0], layer.w_router.device
+        self.layer, self.eps = layer, eps
+        self.residual_scale, self.branch_scale = residual_scale, branch_scale
+        vector = lambda v: torch.nn.Parameter(torch.full((H,), float(v), dtype=torch.float32, device=device))
+        self.norm = vector(1.0)
+        self.post_norm = vector(1.0) if post_norm else None
+        self.scale = vector(learned_scale) if learned_scale is not None else None
+
+    def _around(self, run, x, h, next_norm, gate):
+        if self.scale is not None:
+            if gate is not None:
+                raise ValueError("a block with a learned scale takes no gate")
+            gate = self.scale.unsqueeze(0)
+        if h is None:
+            h = block_norm(x, self.norm, eps=self.eps)[1]
+        return block_norm(x, next_norm, run(h), self.post_norm, gate, self.residual_scale, self.branch_scale, self.eps)
+
+    def forward(self, x, h=None, next_norm=None, gate=None, bias=None):
+        """(r, h of the next block or None): x [T, H] the stream, h the stream
+        normed already (by the block before), next_norm the next block's norm
+        weight, bias the layer's."""
+        return self._around(lambda t: self.layer(t, bias), x, h, next_norm, gate)
+
+    @torch.no_grad()
+    def decode(self, x, h=None, next_norm=None, gate=None, bias=None):
+        """forward of a few tokens through MoELayer.decode."""
+        return self._around(lambda t: self.layer.decode(t, bias), x, h, next_norm, gate)
+
+
+@torch.no_grad()
+def clip_grad_norm(parameters, max_norm, eps=1e-6):
+    """Scales the parameters' gradients in place so that their 2-norm is at
+    most max_norm, and returns the norm they had (ops.clip_grads); parameters
+    without a gradient are left out, one that is given twice counts once."""
+    grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
+    return ops.clip_grads(grads, max_norm, eps=eps)
+
+
+@dataclass
+class BF16Experts:
+    """The experts' weights in bf16: gate_up [E*H, 2I], down [E*I, H] and the number of experts."""
+    gate_up: torch.Tensor
+    down: torch.Tensor
+    n_experts: int
 
 
 @dataclass
@@ -350,18 +452,25 @@ def moe_forward_few(x, w_router, gate_up, down, k, bias=None, sh_gate_up=None, s
 
 
 class DecodeGraph:
-    """moe_forward_w4 captured once as a CUDA graph for a fixed token count:
-    write a step's tokens into ``x`` (or pass them to ``__call__``); a replay
-    is one launch and writes ``y``, ``ids`` and ``w``, which the next replay
-    overwrites.  Routing stays on the device, so one capture serves any
-    routing.  As ForwardGraph, it makes W_r's bf16 split once
-    (``refresh_router_split()`` after changing W_r)."""
+    """A decode step captured once as a CUDA graph for a fixed token count:
+    moe_forward_w4 for W4Experts, moe_forward_few for BF16Experts (at most 128
+    tokens).  Write a step's tokens into ``x`` (or pass them to ``__call__``);
+    a replay is one launch and writes ``y``, ``ids`` and ``w``, which the next
+    replay overwrites.  Routing stays on the device, so one capture serves any
+    routing.  As ForwardGraph, with 4-bit experts it makes W_r's bf16 split once
+    (``refresh_router_split()`` after changing W_r); with bf16 ones W_r is read
+    as it is."""
 
     def __init__(self, T, w_router, experts, k, bias=None, shared=None, routing=None, balance_bias=None, bf16_rows=None):
         H, E = w_router.shape
         self.args = (w_router, experts, k, bias, shared)
         self.routing, self.balance_bias, self.bf16_rows = routing, balance_bias, bf16_rows
-        self.w_split = ops.route_split_weight(w_router) if ops.route_supports_split(H, E) else None
+        self.few = isinstance(experts, BF16Experts)
+        if self.few and (bf16_rows is not None or not (shared is None or isinstance(shared, BF16Experts))):
+            raise ValueError("bf16 experts take a shared expert in bf16 and no bf16_rows")
+        if self.few and experts.n_experts != E:
+            raise ValueError("w_router must be [H, E] for the experts' E")
+        self.w_split = ops.route_split_weight(w_router) if not self.few and ops.route_supports_split(H, E) else None
         self.x = torch.zeros((T, H), dtype=torch.bfloat16, device=w_router.device)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -374,6 +483,10 @@ class DecodeGraph:
             self.y, self.ids, self.w = self._forward()
 
     def _forward(self):
+        if self.few:
+            w_router, experts, k, bias, shared = self.args
+            sh = (shared.gate_up, shared.down) if shared is not None else (None, None)
+            return moe_forward_few(self.x, w_router, experts.gate_up, experts.down, k, bias, *sh, self.routing, self.balance_bias)
         return moe_forward_w4(self.x, *self.args, w_split=self.w_split, routing=self.routing,
                               balance_bias=self.balance_bias, bf16_rows=self.bf16_rows)
 
