@@ -217,6 +217,29 @@ def test_layer(T, kw):
     close(y, reference(x, ids, w, gu, dn, sgu, sdn))
 
 
+@pytest.mark.parametrize("E", (1, 2, 3, 33, 255, 256, 260, 511, 513, 1000, 1021, 1024))
+@pytest.mark.parametrize("T", (1, 3, 9))
+def test_layer_any_number_of_experts(E, T):
+    """The router's ids and weights for every layout of its columns, with the experts' own weights small."""
+    moe = lib()
+    H, I, k = 64 * (1 + E % 3), 64, min(E, 1 + E % 5)
+    g = torch.Generator(device=dev()).manual_seed(E)
+    x = torch.randn((T, H), generator=g, device=dev()).to(torch.bfloat16)
+    gu, dn = weights(E, H, I, E)
+    # logits a step of 2^-8 apart at least: no near ties
+    wr = torch.zeros((H, E), device=dev())
+    x[:, 0] = 1.0
+    wr[0] = torch.randperm(E, generator=g, device=dev()) * 2.0 ** -7
+    wr[1:] = 2.0 ** -14 * torch.randn((H - 1, E), generator=g, device=dev()) / H ** 0.5
+    y, ids, w = moe.layer_few(x, wr, gu, dn, k)
+    z = x.double() @ wr.double()
+    want = z.sort(1, descending=True).indices[:, :k]
+    assert torch.equal(ids.long(), want)
+    p = torch.softmax(z.gather(1, want), 1)
+    assert bool(((w.double() - p).abs() <= 2.0 ** -18 * p).all())
+    close(y, reference(x, ids, w, gu, dn))
+
+
 def test_layer_masked_and_tied_experts():
     """Logits of -inf (masked by the bias), and equal ones, which go to the lower index."""
     moe = lib()

@@ -5,7 +5,7 @@
 // A cluster of 16 blocks takes up to 8 tokens.  Each block reads its share of
 // W_r's rows once (fp32, as it lies) and holds the tokens' partial logits;
 // the block that chooses for a token adds the 16 parts through distributed
-// shared memory, and its first warp chooses.  W_r's bytes and a few dependent
+// shared memory.  W_r's bytes and a few dependent
 // steps bound it: with one cluster 16 SMs read W_r.  Products are fp32 FMAs:
 // 8 tokens a read of W_r leave them far below the loads.
 #include <algorithm>
@@ -32,79 +32,81 @@ struct FewRouteParams {
   int zero_words;
   int T, H, E, k;
   int rows;            // of W_r a block reads
+  int x_floats;        // room of x's rows, and of a token's logits after them
   int groups, top_groups, per_group;
   int sigmoid, top2, renorm, by_logit;
   float scale;
 };
 
-// The k best of a token's experts: one warp, lane l with experts l, l + 32,
-// ..; z the logits, key room for their keys (both [E] in shared memory).
-template <int NV>
-__device__ __noinline__ void choose(const FewRouteParams& p, const float* z, uint32_t* keys, int t) {
-  const int lane = threadIdx.x & 31;
+// The k best of a token's experts, by the whole block: every expert counts the
+// ones before it.  (One warp that takes the best k times runs through four
+// times the code once, and fetching that cost 5 us of the launch's 9.)
+// z: the logits; keys: room for the experts' keys, [E] and three more.
+__device__ __forceinline__ void choose(const FewRouteParams& p, const float* z, uint32_t* keys, int t) {
+  __shared__ uint32_t strength[32];   // of the groups
+  __shared__ int chosen_at[32];
+  const int tid = threadIdx.x, lane = tid & 31;
   const float neg_inf = __uint_as_float(0xFF800000u);
+  const bool grouped = p.top_groups < p.groups;
   float zmax = neg_inf, zsum = 1.f;
-  if (!p.sigmoid) {
+  if (!p.sigmoid && !(p.renorm && p.by_logit)) {   // every warp for itself
+#pragma unroll 1
     for (int e = lane; e < p.E; e += 32) zmax = fmaxf(zmax, z[e]);
     zmax = warp_max(zmax);
     zsum = 0.f;
+#pragma unroll 1
     for (int e = lane; e < p.E; e += 32) zsum += z[e] == neg_inf ? 0.f : expf(z[e] - zmax);
     zsum = warp_sum(zsum);
   }
-  uint32_t key[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = 0;
+#pragma unroll 1
+  for (int e = tid; e < ((p.E + 3) & ~3); e += kRouteThreads) {
+    float v = neg_inf;
     if (e < p.E) {
-      float v = z[e] + 0.f;   // -0 to +0
+      v = z[e] + 0.f;   // -0 to +0
       if (!p.by_logit && v != neg_inf)
         v = (p.sigmoid ? sigmoid(v) : expf(v - zmax) / zsum) + (p.balance ? p.balance[e] : 0.f);
-      key[i] = value_key(v);
     }
+    keys[e] = e < p.E ? value_key(v) : 0u;
   }
-  if (p.top_groups < p.groups) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
-    __syncwarp();
-    uint32_t mine = 0;
-    if (lane < p.groups) {
+  __syncthreads();
+  if (grouped) {
+    if (tid < p.groups) {
       uint32_t m1 = 0, m2 = 0;   // the group's two largest
-      for (int e = lane * p.per_group; e < (lane + 1) * p.per_group; ++e) {
-        m2 = max(m2, min(m1, keys[e]));
-        m1 = max(m1, keys[e]);
+#pragma unroll 4
+      for (int e = tid * p.per_group; e < (tid + 1) * p.per_group; ++e) {
+        const uint32_t key = keys[e];
+        m2 = max(m2, min(m1, key));
+        m1 = max(m1, key);
       }
-      mine = p.top2 && m2 > value_key(neg_inf) ? value_key(key_value(m1) + key_value(m2)) : m1;
+      strength[tid] = p.top2 && m2 > value_key(neg_inf) ? value_key(key_value(m1) + key_value(m2)) : m1;
     }
-    int rank = 0;                // groups before this one
-    for (int g = 0; g < p.groups; ++g) {
-      const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
-      rank += other > mine || (other == mine && g < lane);
+    __syncthreads();
+#pragma unroll 1
+    for (int e = tid; e < p.E; e += kRouteThreads) {
+      const int group = e / p.per_group;
+      const uint32_t mine = strength[group];
+      int before = 0;
+#pragma unroll 1
+      for (int g = 0; g < p.groups; ++g) before += strength[g] > mine || (strength[g] == mine && g < group);
+      if (before >= p.top_groups) keys[e] = 0;
     }
-    const uint32_t out = __ballot_sync(0xffffffffu, rank >= p.top_groups);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      if (e < p.E && (out >> (e / p.per_group) & 1u)) key[i] = 0;
-    }
+    __syncthreads();
   }
-  int chosen = 0;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (key[i] == top) at = lane + 32 * i;
-    const uint32_t low = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((uint32_t)(lane + 32 * i) == low) key[i] = 0;
-    if (lane == j) chosen = (int)low;
+#pragma unroll 1
+  for (int e = tid; e < p.E; e += kRouteThreads) {
+    const uint32_t key = keys[e];
+    if (key == 0) continue;      // of a group that is out
+    int before = 0;              // equal keys go to the lower expert
+#pragma unroll 2
+    for (int i = 0; i < p.E; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + i);
+      before += (q.x > key - (i < e)) + (q.y > key - (i + 1 < e)) + (q.z > key - (i + 2 < e)) + (q.w > key - (i + 3 < e));
+    }
+    if (before < p.k) chosen_at[before] = e;
   }
+  __syncthreads();
+  if (tid >= 32) return;
+  const int chosen = lane < p.k ? chosen_at[lane] : 0;
   float s = 0.f;
   const float zc = lane < p.k ? z[chosen] : neg_inf;
   if (p.sigmoid) {
@@ -128,7 +130,7 @@ template <int TT, int V>
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_constant__ FewRouteParams p) {
   extern __shared__ float few_route_smem[];
   float* xs = few_route_smem;                    // [rows][TT]
-  float* part = xs + kRouteRows * TT;            // [row groups][TT][E]; the first of them: the block's sums
+  float* part = xs + p.x_floats;                 // [row groups][TT][E]; the first of them: the block's sums
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, rank = (int)cluster_ctarank();
@@ -223,18 +225,14 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     }
   }
   cluster_sync_all();   // no block leaves while its sums are read; z is complete too
-  if (chooses && tid < 32) {
-    uint32_t* keys = reinterpret_cast<uint32_t*>(part);
-    if (p.E <= 128) choose<4>(p, z, keys, t);
-    else if (p.E <= 256) choose<8>(p, z, keys, t);
-    else choose<32>(p, z, keys, t);
-  }
+  if (chooses) choose(p, z, reinterpret_cast<uint32_t*>(part), t);
 }
 
 template <int TT, int V>
-cudaError_t launch(const FewRouteParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch(FewRouteParams p, const DeviceInfo& dev, cudaStream_t stream) {
   const int per_row = (p.E + V - 1) / V, row_groups = std::max(1, kRouteThreads / per_row);
-  const size_t smem = sizeof(float) * ((size_t)std::max(kRouteRows * TT, p.E) + (size_t)row_groups * TT * p.E);
+  p.x_floats = std::max(kRouteRows * TT, (p.E + 3) / 4 * 4);
+  const size_t smem = sizeof(float) * ((size_t)p.x_floats + (size_t)row_groups * TT * p.E + 4);   // the keys' last four pad
   static std::atomic<int> configured[kMaxDevices] = {};
   if (!configured[dev.ordinal].load()) {
     cudaError_t e = cudaFuncSetAttribute(few_route_kernel<TT, V>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
