@@ -98,20 +98,53 @@ struct FewParams {      // 64-byte aligned through its CUtensorMap members
 // --------------------------------------------------------------- the lists
 
 // What every block makes of the ids for itself (a launch of its own would take
-// longer): the slots sorted by expert, stable, so that every block's are the
-// same.
+// longer): the slots grouped by expert, in an order that the ids fix, so that
+// every block's are the same: experts in increasing order, or with up to 32
+// slots as they first appear.
 struct FewLists {
   FewEntry* entries;
   uint16_t* of_chunk;   // entry of a chunk
   uint16_t* list;       // slots by expert
   uint32_t* valid;      // which slots of a token name an expert
   float* w;             // [S]
+  int* chunks;          // their number
 };
 
-// Returns the chunks.  room: [S + E] ints that are free.
-__device__ __forceinline__ int few_lists(const FewParams& p, const FewLists& out, int* room) {
+// room: [S + E] ints that are free.
+__device__ __forceinline__ void few_lists(const FewParams& p, const FewLists& out, int* room) {
   __shared__ int warp_sums[2][kFewThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slots = p.T * p.k;
+  if (slots <= 32) {   // one warp, a slot to a lane: no barriers
+    if (warp > 0) return;
+    int e = -1;
+    if (lane < slots) {
+      e = p.ids[lane];
+      out.w[lane] = p.w[lane];
+      if (e < 0 || e >= p.E) {
+        if (e != -1) report_status(p.status, kStatusDevice, kKernFew, kFewSiteIds);
+        e = -1;
+      }
+    }
+    const uint32_t used = __ballot_sync(0xffffffffu, e >= 0), same = __match_any_sync(0xffffffffu, e), below = (1u << lane) - 1u;
+    const bool leads = e >= 0 && (same & below) == 0;
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    int end = leads ? __popc(same) : 0;   // of the expert's rows in the list
+    const int rows = end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += x;
+    }
+    const int row0 = __shfl_sync(0xffffffffu, end - rows, __ffs(same) - 1), entry = __popc(leaders & below);
+    if (leads) {
+      out.entries[entry] = FewEntry{e, row0, rows, entry};   // at most 32 rows: one chunk
+      out.of_chunk[entry] = (uint16_t)entry;
+    }
+    if (e >= 0) out.list[row0 + __popc(same & below)] = (uint16_t)lane;
+    if (lane < p.T) out.valid[lane] = used >> lane * p.k & (0xFFFFFFFFu >> (32 - p.k));
+    if (lane == 0) *out.chunks = __popc(leaders);
+    return;
+  }
   int *ids = room, *first = room + (slots + 3) / 4 * 4;
   for (int e = tid; e < p.E; e += kFewThreads) first[e] = 0;
   bool bad = false;
@@ -193,7 +226,7 @@ __device__ __forceinline__ int few_lists(const FewParams& p, const FewLists& out
     for (; j < i; ++j) at += ids[j] == e;
     out.list[at] = (uint16_t)i;
   }
-  return all >> 16;
+  if (tid == 0) *out.chunks = all >> 16;
 }
 
 // --------------------------------------------------------------- the units
@@ -300,6 +333,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kFewQueue);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* group_word = tmem_slot + 2;        // [groups]
+  int* n_chunks = reinterpret_cast<int*>(tmem_slot + 2 + kFewGroups);
   float* swap = reinterpret_cast<float*>(tmem_slot + 16);
   FewEntry* entries = reinterpret_cast<FewEntry*>(smem + p.stages * kFewStage + kFewFixed);
   uint32_t* valid = reinterpret_cast<uint32_t*>(entries + p.max_entries);
@@ -350,7 +384,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   pdl_trigger();
   uint32_t next = 0;
   if (tid == 96) next = atomicAdd(p.ticket, 1u);   // warp 3's first, while the slots are sorted
-  const int n_chunks = few_lists(p, FewLists{entries, of_chunk, list, valid, w}, reinterpret_cast<int*>(smem));
+  few_lists(p, FewLists{entries, of_chunk, list, valid, w, n_chunks}, reinterpret_cast<int*>(smem));
   fence_proxy_async_smem();   // the sort's writes into the ring, before TMA's
   tc_fence_before();
   __syncthreads();
@@ -377,7 +411,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
   if (warp == 3) {
     if (lane == 0) {
       for (int i = 0, ends = 0; ends < kFewGroups; ++i) {
-        const FewUnit x = few_unit(p, entries, of_chunk, n_chunks, next);
+        const FewUnit x = few_unit(p, entries, of_chunk, *n_chunks, next);
         const int q = i % kFewQueue;
         if (!wait(seen_bar(q), (i / kFewQueue & 1) ^ 1u, kFewSiteUnits)) break;
         queue[q] = x;
