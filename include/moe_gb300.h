@@ -287,7 +287,7 @@ int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uin
  *   x        [T, H] bf16; gate_up [E*H, 2I], down [E*I, H] bf16 (the layout
  *            of the grouped GEMMs); sh_gate_up [H, 2 I_s], sh_down [I_s, H]
  *            bf16, or both NULL with I_s = 0
- *   y        [T, H] bf16 (out, rounded once)
+ *   y        [T, H] bf16 (out, rounded once); overlaps no input
  * Sums are in fp32 and h is rounded to bf16.  A token's result does not
  * depend on the other tokens of the call.
  * H, I and I_s are multiples of 64 and at most 2^20, E at most 1024, k at

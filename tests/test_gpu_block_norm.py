@@ -269,6 +269,23 @@ def test_in_a_graph_and_on_another_stream():
     assert all(torch.equal(out[n], want[n]) for n in want)
 
 
+@pytest.mark.parametrize("x", ("bf16", "f32"))
+def test_in_place(x):
+    """The C entry with r the memory of x, at sizes where rows are loaded ahead of the ones that are written."""
+    import ctypes
+
+    moe = lib()
+    d, _ = inputs(2000, 512, x=x, post="f32", gates=1)
+    want = moe.block_norm(d["x"], d["weight"], d["branch"], d["post_weight"], d["gate"])
+    h, P = torch.empty_like(want[1]), ctypes.c_void_p
+    p = lambda t: P(t.data_ptr())
+    types = 2 | 4 | 8 | (1 if x == "f32" else 0)
+    rc = moe.load().moe_block_norm(p(d["x"]), p(d["branch"]), p(d["weight"]), p(d["post_weight"]), p(d["gate"]), types, 2000, 512, 1, 1.0, 1.0,
+                                   EPS, p(d["x"]), p(h), None, P(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0 and torch.equal(d["x"], want[0]) and torch.equal(h, want[1])
+    moe.sync_status()
+
+
 def test_refusals():
     moe = lib()
     d, up = inputs(12, 64, post="f32", gates=3)

@@ -76,7 +76,7 @@ def close(y, want):
     assert rel < 2.0 ** -7, rel
 
 
-SHAPES = [(1, 64, 1, 1, 64, 0), (1, 128, 8, 2, 64, 0), (1, 2048, 128, 8, 768, 0), (3, 192, 5, 3, 320, 64), (2, 1600, 60, 5, 704, 0),
+SHAPES = [(1, 64, 1, 1, 64, 0), (2, 1024, 4, 1, 64, 3200), (70, 1024, 4, 1, 64, 3200), (40, 512, 40, 4, 1024, 64), (1, 128, 8, 2, 64, 0), (1, 2048, 128, 8, 768, 0), (3, 192, 5, 3, 320, 64), (2, 1600, 60, 5, 704, 0),
           (16, 2048, 32, 8, 768, 768), (64, 256, 16, 8, 128, 192), (128, 128, 8, 8, 64, 64), (37, 1088, 24, 6, 448, 896), (5, 7168, 16, 8, 2048, 2048),
           (33, 64, 64, 32, 64, 64), (9, 4096, 8, 2, 64, 0), (4, 64, 4, 1, 8192, 0), (128, 320, 3, 1, 192, 0), (31, 512, 1024, 32, 64, 0)]
 

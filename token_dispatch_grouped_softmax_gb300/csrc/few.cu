@@ -89,7 +89,7 @@ struct FewParams {      // 64-byte aligned through its CUtensorMap members
   // workspace
   uint32_t* ticket;
   uint32_t* done;       // [entries + 1] finished tiles of h of each entry, the shared expert's last
-  uint32_t* hidden;     // [chunks + shared chunks][tiles] parts of a gate_up tile that are there
+  uint32_t* hidden;     // [chunks, shared chunks][tiles] parts of a gate_up tile that are there, of a product in parts
   uint32_t* arrived;    // [tiles of down][T] slots' parts of a token's columns that are there
   float *part_gu, *part_sh_gu, *part_dn, *part_sh_dn;
   uint16_t *h, *sh_h;
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
           uint32_t answer = 0;
           if (gate_up) {
             if (m == 0) {
-              const int64_t at = x.shared ? (int64_t)p.max_chunks * p.gu.tiles + (int64_t)(x.chunk - p.max_chunks) * f.tiles
+              const int64_t at = x.shared ? (int64_t)p.max_chunks * (p.gu.parts > 1 ? p.gu.tiles : 0) + (int64_t)(x.chunk - p.max_chunks) * f.tiles
                                           : (int64_t)x.chunk * f.tiles;
               answer = atomicAdd(p.hidden + at + x.tile, 1u) + 1 == (uint32_t)f.parts;
             }
@@ -769,7 +769,7 @@ FewPlan few_plan(const FewShape& s) {
   };
   take(16);   // the ticket
   f.done = take((f.max_entries + 1) * 4);
-  f.hidden = take((f.max_chunks * f.gu.tiles + f.sh_chunks * f.sh_gu.tiles) * 4);
+  f.hidden = take((f.max_chunks * (f.gu.parts > 1 ? f.gu.tiles : 0) + f.sh_chunks * (f.sh_gu.parts > 1 ? f.sh_gu.tiles : 0)) * 4);
   f.arrived = take(f.dn.tiles * s.T * 4);
   f.zero_words = at / 4;
   at = (at + 255) & ~(size_t)255;
