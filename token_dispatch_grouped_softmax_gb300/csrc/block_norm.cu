@@ -215,6 +215,10 @@ struct RowGroup {
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     sync();
     turn ^= 1;
+    if (n <= 8) {   // a few: in every thread, without shuffles
+      const float4 q = *reinterpret_cast<const float4*>(b), r = *reinterpret_cast<const float4*>(b + 4);
+      return ((q.x + q.y) + (q.z + q.w)) + ((r.x + r.y) + (r.z + r.w));
+    }
     return warp_sum(b[threadIdx.x & 31]);
   }
   __device__ __forceinline__ void issue(int i, int stage) const {   // row i of the range
