@@ -17,18 +17,17 @@
 // The bytes bound both directions.  A row belongs to a row group of H / 8
 // threads (whole warps; the backward's of H / 16), so that a row's quantities
 // stay in registers between its sums; a block holds several row groups and is
-// alone on its SM.  Each row group
-// takes a range of consecutive rows and has a ring in shared memory that bulk
-// copies keep full, one thread of the group issuing them: the loads in flight
-// do not depend on the registers, nor on the barriers of a row's sums.
+// alone on its SM.  Each row group takes a range of consecutive rows and has a
+// ring in shared memory that bulk copies keep full: the loads in flight do not
+// depend on the registers, nor on the barriers of a row's sums.
 // Consecutive rows keep the columns' sums of the backward in registers until
 // the range ends, and a gate's group ends at most twice inside a range.
 //
 // Measured: 16384 x 7168 in bf16 with a gate for each 1024 rows 148 us forward
 // (940 MB, 6.4 TB/s) and 195 backward with the sums (1.4 GB, 7.2 TB/s).  With
 // both norms a row has two sums to wait for, and its bytes take less time than
-// they do: 8191 x 2048, fp32 stream, 40 us forward (5.0 TB/s), 71 backward
-// (4.3); instructions issue half of the time.
+// they do: 8191 x 2048, fp32 stream, 40 us forward (5.0 TB/s), 68 backward
+// (4.5); instructions issue half of the time.
 #include <algorithm>
 
 #include "kernels.h"

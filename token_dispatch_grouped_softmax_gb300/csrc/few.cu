@@ -6,24 +6,26 @@
 // With few rows an expert the weights' bytes are the cost: each weight of the
 // experts in use has to come from HBM once.  One launch streams them all.  A
 // unit of work is 128 columns of one expert's weight (64 gate and the 64 up
-// columns beside them, or 128 of down) by a part of its K rows, for up to 32
-// rows of that expert; gate_up's units come before down's.  Blocks draw units
+// columns beside them, or 128 of down) by the whole of its K rows or a part,
+// for up to 32 rows of that expert; gate_up's units come before down's.  Blocks draw units
 // by tickets in that order, so that a block that waits for an expert's h
 // waits only for units that running blocks have drawn: no block has to be
 // resident for another to go on.
 //
 //   warp 3        draws the units, one ahead of the loads.
-//   warp 0        keeps a ring of 128 x 128 tiles of the weights full by TMA.  It waits for nothing but free stages:
-//                 while h is not ready, down's weights already arrive.
+//   warp 0        keeps a ring of 128 x 128 tiles of the weights full by TMA.
+//                 It waits for nothing but free stages: while h is not ready,
+//                 down's weights already arrive.
 //   warp 1        gathers the rows' 128 values of K for each tile (TMA
 //                 gather4), for down once the expert's h is complete.
 //   warp 2        issues tcgen05.mma, the weights as A (M = 128 columns,
 //                 MN-major as they lie) and the rows as B (N = 32): the
 //                 accumulator has a column of the weight in each TMEM lane.
-//   warps 4..19   four groups take the units in turn: TMEM to the unit's fp32
-//                 partial sums in the workspace; whoever adds the last part
-//                 of a tile sums the parts in order and writes h, and of a
-//                 token's columns y.
+//   warps 4..19   four groups take the units in turn, from TMEM.  gate_up over
+//                 the whole of K becomes h at once; other sums go to the
+//                 workspace in fp32, and whoever adds the last part of a tile
+//                 sums the parts in order and writes h, or of a token's
+//                 columns y.
 //
 // The parts of K depend on the shape alone, so a token's sums have one order
 // and its result does not depend on the batch.
