@@ -577,21 +577,27 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     }
   }
   // the block's sums, its row groups in order, through the rings' memory
-  __syncthreads();
-  float* block_sums = reinterpret_cast<float*>(norm_smem);   // [H]
+  float* sums = reinterpret_cast<float*>(norm_smem);   // [row groups][H]
   int k = 0;
-  auto add_up = [&](F8 (&sum)[2]) {
-    for (int ty = 0; ty < (int)blockDim.y; ++ty) {
-      if (blockDim.y > 1) __syncthreads();
-      if ((int)threadIdx.y != ty) continue;
+  auto add_up = [&](const F8 (&sum)[2]) {
+    float* out = p.parts + ((int64_t)blockIdx.x * p.n_sums + k++) * p.H;
+    if (blockDim.y == 1) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-          if (ty > 0) fma8(fill8(1.f), load8(block_sums, c[j]), sum[j]);
-        if (ty + 1 < (int)blockDim.y) store8(block_sums, c[j], sum[j]);
-        else store8(p.parts + ((int64_t)blockIdx.x * p.n_sums + k) * p.H, c[j], sum[j]);
-      }
+      for (int j = 0; j < 2; ++j) store8(out, c[j], sum[j]);
+      return;
     }
-    ++k;
+    __syncthreads();   // the rows, or the sums before, have been read
+#pragma unroll
+    for (int j = 0; j < 2; ++j) store8(sums + threadIdx.y * p.H, c[j], sum[j]);
+    __syncthreads();
+    for (int i = 4 * (threadIdx.y * blockDim.x + threadIdx.x); i < p.H; i += 4 * blockDim.x * blockDim.y) {
+      float4 q = *reinterpret_cast<const float4*>(sums + i);
+      for (int ty = 1; ty < (int)blockDim.y; ++ty) {
+        const float4 r = *reinterpret_cast<const float4*>(sums + ty * p.H + i);
+        q.x += r.x; q.y += r.y; q.z += r.z; q.w += r.w;
+      }
+      *reinterpret_cast<float4*>(out + i) = q;
+    }
   };
   if (W) add_up(dw);
   if (V) add_up(dv);
@@ -648,10 +654,19 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
   }
   float2 s = make_float2(0.f, 0.f);
   if (mine) {
-#pragma unroll 4
-    for (uint32_t i = warp; i < n; i += kNormSumWarps) {
-      const float2 q = *reinterpret_cast<const float2*>((i == 0 ? first : rest + i * pitch) + c);
-      s.x += q.x; s.y += q.y;
+    // all of a warp's parts in flight together (152 parts: ten)
+    for (uint32_t i0 = warp; i0 < n; i0 += 10 * kNormSumWarps) {
+      float2 q[10];
+#pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        const uint32_t i = i0 + k * kNormSumWarps;
+        q[k] = make_float2(0.f, 0.f);
+        if (i < n) q[k] = *reinterpret_cast<const float2*>((i == 0 ? first : rest + i * pitch) + c);
+      }
+#pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        s.x += q[k].x; s.y += q[k].y;
+      }
     }
   }
   part[warp][lane] = s;
