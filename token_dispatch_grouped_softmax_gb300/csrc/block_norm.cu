@@ -156,6 +156,7 @@ struct NormParams {
   uint16_t* dy;
   float* parts;           // [grid][sums][H], then [row groups][2][H] of the gate's groups
   void* dg;               // finished groups are written here
+  void *dw, *dv;          // written by a launch of one block, as its only group's dg
   int64_t T;
   int H;
   int64_t gate_rows;      // rows of a gate's group
@@ -579,29 +580,30 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   // the block's sums, its row groups in order, through the rings' memory
   float* sums = reinterpret_cast<float*>(norm_smem);   // [row groups][H]
   int k = 0;
-  auto add_up = [&](const F8 (&sum)[2]) {
+  auto add_up = [&](const F8 (&sum)[2], void* final, int f32) {
     float* out = p.parts + ((int64_t)blockIdx.x * p.n_sums + k++) * p.H;
-    if (blockDim.y == 1) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) store8(out, c[j], sum[j]);
-      return;
-    }
+    auto put = [&](int i, const float2 (&v)[2]) {   // four columns from i on
+      if (gridDim.x > 1) store4(out + i, v);
+      else if (f32) store4(static_cast<float*>(final) + i, v);
+      else store4(static_cast<uint16_t*>(final) + i, v);
+    };
     __syncthreads();   // the rows, or the sums before, have been read
 #pragma unroll
     for (int j = 0; j < 2; ++j) store8(sums + threadIdx.y * p.H, c[j], sum[j]);
     __syncthreads();
     for (int i = 4 * (threadIdx.y * blockDim.x + threadIdx.x); i < p.H; i += 4 * blockDim.x * blockDim.y) {
-      float4 q = *reinterpret_cast<const float4*>(sums + i);
+      float2 q[2], r[2];
+      load4(sums + i, q);
       for (int ty = 1; ty < (int)blockDim.y; ++ty) {
-        const float4 r = *reinterpret_cast<const float4*>(sums + ty * p.H + i);
-        q.x += r.x; q.y += r.y; q.z += r.z; q.w += r.w;
+        load4(sums + ty * p.H + i, r);
+        q[0].x += r[0].x; q[0].y += r[0].y; q[1].x += r[1].x; q[1].y += r[1].y;
       }
-      *reinterpret_cast<float4*>(out + i) = q;
+      put(i, q);
     }
   };
-  if (W) add_up(dw);
-  if (V) add_up(dv);
-  if (G && p.groups == 1) add_up(dg);
+  if (W) add_up(dw, p.dw, p.w_f32);
+  if (V) add_up(dv, p.dv, p.v_f32);
+  if (G && p.groups == 1) add_up(dg, p.dg, p.g_f32);
 }
 
 struct NormSumParams {
@@ -688,18 +690,21 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
 // a single gate as given and as fp32.  They are kept as fp32 where two stages
 // fit beside them (16384 x 7168, bf16, backward: 200 us, as given 212), else as
 // given (4096 x 4096, fp32 stream, bf16 weights: 83 us, from global memory 94).
+// one_block: as many rows as one block holds take one, which needs no sums of
+// sums (forward and backward of 8 x 256 6.4 us, in blocks of a row 7.7).
 struct NormShape {
   dim3 block;
   int grid, stages, shared_params;
   size_t smem;
 };
-NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t params, size_t wide) {   // of a block; of 8 columns
+NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t params, size_t wide,   // of a block; of 8 columns
+                     bool one_block) {
   NormShape s;
   const int tpr = (int)((H + 256 * groups - 1) / (256 * groups) * 32);
   int rows = threads / tpr;
   if (tpr > 32) rows = std::min(rows, 15);   // row groups' barriers 1 .. 15; a warp needs none
-  rows = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
   rows = (int)std::max<size_t>(1, std::min<size_t>(rows, kNormSmem / (2 * row_bytes)));
+  rows = one_block && T <= rows ? (int)T : (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
   s.shared_params = 2 * rows * row_bytes + wide <= kNormSmem ? kAsFp32 : 2 * rows * row_bytes + params <= kNormSmem ? kAsGiven : kInGlobal;
   params = s.shared_params == kAsFp32 ? wide : s.shared_params == kAsGiven ? params : 0;
   const size_t room = kNormSmem - params;
@@ -761,7 +766,7 @@ cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const 
 
 NormShape norm_bwd_shape(const BlockNorm& n, bool dr) {
   return norm_shape(n.T, n.H, kNormThreads / 2, 2, (size_t)n.H * ((n.x_f32 ? 4 : 2) * (dr ? 2 : 1) + (n.y ? 2 : 0) + (n.w ? 2 : 0)),
-                    norm_params_bytes(n), norm_wide_bytes(n));
+                    norm_params_bytes(n), norm_wide_bytes(n), n.groups <= 1 || n.groups == n.T);   // no gate's rows to join
 }
 
 }  // namespace
@@ -771,7 +776,7 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
   const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32), (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n),
-                                 norm_wide_bytes(n));
+                                 norm_wide_bytes(n), false);
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
   return norm_launch(false, n, s, p, dev, stream);
@@ -780,7 +785,7 @@ cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* s
 // The most that any types and any dr take: row groups are fewest bytes a row.
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
   if (T == 0) return 0;
-  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, 0);
+  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, 0, true);
   const size_t n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
   const size_t blocks = std::min<int64_t>(T, kNormBlocks);
   return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
@@ -800,7 +805,7 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
   const NormShape s = norm_bwd_shape(n, dr != nullptr);
   NormParams p = norm_params(n, s, dev);
   p.stats = const_cast<float*>(stats);
-  p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g;
+  p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g; p.dw = d.w; p.dv = d.v;
   p.parts = static_cast<float*>(ws);
   NormSumParams q = {};
   q.parts = p.parts;
@@ -817,7 +822,7 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
   q.T = (uint32_t)n.T; q.groups = (uint32_t)n.groups; q.gate_rows = (uint32_t)p.gate_rows; q.H = p.H;
   q.row_groups = (uint32_t)s.grid * s.block.y;
   const int64_t shared = n.groups > 1 && p.gate_rows > 1 ? (n.groups <= q.row_groups ? n.groups : (int64_t)q.row_groups - 1) : 0;
-  if (k + shared == 0) return cudaSuccess;
+  if (s.grid == 1 || k + shared == 0) return cudaSuccess;
   return launch_pdl(block_norm_sum_kernel, dim3((unsigned)((n.H + 63) / 64), (unsigned)(k + shared)), dim3(32 * kNormSumWarps), 0, stream, 1, q);
 }
 
