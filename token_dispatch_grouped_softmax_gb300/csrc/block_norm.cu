@@ -10,6 +10,11 @@
 //   dx = a d,  dg = sum_rows b d n,  q = b d g,  dv = sum_rows q y s_y
 //   dy = s_y (q v - y s_y mean(q v y s_y))           (without v: dy = q)
 //
+// Rows that share v and g share K = b g v, one vector, and the backward needs
+// one columns' sum for both: u = sum_rows d y s_y, dv = b g u, dg = b v u
+// (8191 x 2048, fp32 stream, backward: 44 us, with a vector and a sum for each
+// 67; 4096 x 7168 84, with each 158).
+//
 // Every sum is in fp32 and every output is rounded once: h comes from the r
 // that is not rounded yet, and the backward computes r again from x and y
 // instead of reading the rounded one (the same bytes).
@@ -24,10 +29,9 @@
 // the range ends, and a gate's group ends at most twice inside a range.
 //
 // Measured: 16384 x 7168 in bf16 with a gate for each 1024 rows 148 us forward
-// (940 MB, 6.4 TB/s) and 195 backward with the sums (1.4 GB, 7.2 TB/s).  With
-// both norms a row has two sums to wait for, and its bytes take less time than
-// they do: 8191 x 2048, fp32 stream, 40 us forward (5.0 TB/s), 68 backward
-// (4.5); instructions issue half of the time.
+// (940 MB, 6.4 TB/s) and 174 backward with the sums (1.4 GB, some of it from the
+// L2).  With both norms a row has two sums to wait for: 8191 x 2048, fp32
+// stream, 37 us forward (5.5 TB/s), 44 backward (6.9).
 #include <algorithm>
 
 #include "kernels.h"
@@ -133,6 +137,10 @@ struct Shared {
   __device__ __forceinline__ F8 load(int64_t at, const Columns& c) const {
     return f32 ? load8(static_cast<const float*>(p) + at, c) : load8(static_cast<const uint16_t*>(p) + at, c);
   }
+  __device__ __forceinline__ void load4(int at, float2* v) const {
+    if (f32) moe::load4(static_cast<const float*>(p) + at, v);
+    else moe::load4(static_cast<const uint16_t*>(p) + at, v);
+  }
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -141,7 +149,36 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-enum { kInGlobal, kAsGiven, kAsFp32 };   // the last two in shared memory
+// What y is multiplied by: b alone; a vector that all rows share, K = b g v of
+// v and a single gate, whichever there are; v and a gate for each group of
+// rows; v and a row's own gate, which is one of its streams.
+enum { kPlain, kVector, kGroups, kOwnGate };
+
+// The columns' sums' way out: of sum_rows dh r s_r into dw; with kVector of
+// u = sum_rows d y s_y into dv = b g u and dg = b v u, else of dv as it is.
+struct SumsOut {
+  void *dw, *dv, *dg;
+  const void *v, *g;
+  int w_f32, v_f32, g_f32;
+  int vector;
+  float b;
+};
+__device__ __forceinline__ float2 get2(const void* p, int f32, int64_t at) {
+  if (f32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+  const uint32_t q = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
+  return make_float2(bf16_lo(q), bf16_hi(q));
+}
+__device__ __forceinline__ void put2(void* p, int f32, int64_t at, float2 v) {
+  if (f32) *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = v;
+  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + at) = pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ void sums_out(const SumsOut& o, bool of_w, int c, float2 u) {
+  if (of_w) return put2(o.dw, o.w_f32, c, u);
+  if (!o.vector) return put2(o.dv, o.v_f32, c, u);
+  u = mul2(u, make_float2(o.b, o.b));
+  if (o.v) put2(o.dv, o.v_f32, c, o.g ? mul2(u, get2(o.g, o.g_f32, c)) : u);
+  if (o.g) put2(o.dg, o.g_f32, c, o.v ? mul2(u, get2(o.v, o.v_f32, c)) : u);
+}
 
 struct NormParams {
   const void* x;
@@ -156,16 +193,16 @@ struct NormParams {
   uint16_t* dy;
   float* parts;           // [grid][sums][H], then [row groups][2][H] of the gate's groups
   void* dg;               // finished groups are written here
-  void *dw, *dv;          // written by a launch of one block, as its only group's dg
+  SumsOut out;            // for a launch of one block
   int64_t T;
   int H;
   int64_t gate_rows;      // rows of a gate's group
   int64_t groups;
   float a, b, eps;
   int w_f32, v_f32, g_f32;
-  int n_sums;             // columns' sums over all rows: dw, dv, dg with one group
+  int n_sums;             // columns' sums over all rows: w's, then v's or K's
   int stages;
-  int shared_params;      // where w, v and a single g are
+  int vectors_shared;     // w and v are in shared memory (always but with a row's own gates)
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -187,10 +224,11 @@ __device__ __noinline__ void norm_wait_more(uint32_t bar, uint32_t phase, volati
 
 // A row group: its rows, its ring and its sums.
 struct RowGroup {
+  static constexpr uint32_t kPrefetch = 0xffffffffu;
   // the stream that this thread copies, if any: a thread of another warp for
   // each where the row group has as many, as all wait for the slowest
   const uint8_t* src;     // its first row of the range
-  uint32_t bytes, offset; // of a row; in a stage
+  uint32_t bytes, offset; // of a row; in a stage (kPrefetch: into the L2 instead)
   uint8_t* ring;
   uint32_t row_bytes;     // of a stage
   uint32_t bar;
@@ -223,6 +261,10 @@ struct RowGroup {
   }
   __device__ __forceinline__ void issue(int i, int stage) const {   // row i of the range
     if (!src) return;
+    if (offset == kPrefetch) {
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src + (int64_t)i * bytes), "r"(bytes) : "memory");
+      return;
+    }
     mbar_arrive_expect_tx(bar + 8 * stage, bytes);
     bulk_load(smem_u32(ring) + stage * row_bytes + offset, src + (int64_t)i * bytes, bytes, bar + 8 * stage);
   }
@@ -242,12 +284,15 @@ struct RowGroup {
 
 struct NormSetup {
   RowGroup rg;
-  Shared w, v, g;         // w, v and a single gate: in shared memory where they fit
+  const float *w, *k;     // in shared memory, fp32: w; K or v
 };
 
-// The block's shared memory: the row groups' rings, then w, v and a single g.
-__device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* smem, const void* const (&src)[4],
-                                                const int (&elem)[4], int64_t begin, int rows) {
+// A row's streams, in a stage's order; kGate: a gate of every row's own.
+enum { kX, kY, kDh, kDr, kGate };
+
+// The block's shared memory: the row groups' rings, then w and K or v.
+__device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* smem, const void* const (&src)[5],
+                                                const int (&elem)[5], int64_t begin, int rows, bool dr_staged, bool vector) {
   __shared__ uint64_t bars[32 * kNormMaxStages];
   __shared__ __align__(16) float sums[32 * 64];
   __shared__ int abort_flag;
@@ -257,20 +302,24 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
   g.row_bytes = 0;
   g.src = nullptr;
   g.bytes = g.offset = 0;
-  int n = 0, n_src = 0;
+  int n = 0, n_src = 0, n_staged = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) n_src += src[k] != nullptr;
+  for (int k = 0; k < 5; ++k) {
+    n_src += src[k] != nullptr;
+    n_staged += src[k] != nullptr && (k != kDr || dr_staged);
+  }
   const int step = g.warps() >= n_src ? 32 : 1;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < 5; ++k)
     if (src[k]) {
       const uint32_t bytes = (uint32_t)p.H * elem[k];
+      const bool staged = k != kDr || dr_staged;
       if ((int)threadIdx.x == n * step) {
         g.src = static_cast<const uint8_t*>(src[k]) + begin * bytes;
         g.bytes = bytes;
-        g.offset = g.row_bytes;
+        g.offset = staged ? g.row_bytes : RowGroup::kPrefetch;
       }
-      g.row_bytes += bytes;
+      if (staged) g.row_bytes += bytes;
       ++n;
     }
   g.rows = rows;
@@ -280,7 +329,7 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
   g.abort = &abort_flag;
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < (int)blockDim.y * p.stages; ++i) mbar_init(smem_u32(bars) + 8 * i, n_src);
+    for (int i = 0; i < (int)blockDim.y * p.stages; ++i) mbar_init(smem_u32(bars) + 8 * i, n_staged);
     fence_mbar_init();
   }
   for (int i = tid; i < 32 * 64; i += blockDim.x * blockDim.y) sums[i] = 0.f;
@@ -291,29 +340,31 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
   pdl_trigger();
   for (int i = 0; i < p.stages && i < rows; ++i) g.issue(i, i);
   const int threads = blockDim.x * blockDim.y;
-  auto share = [&](const void* from, int f32) {
-    const Shared given{from, f32 != 0};
-    if (!from || !p.shared_params) return given;
-    uint8_t* to = at;
-    if (p.shared_params == kAsFp32) {
-      for (int i = tid * 4; i < p.H; i += threads * 4) {
-        float2 v[2];
-        if (given.f32) load4(static_cast<const float*>(from) + i, v);
-        else load4(static_cast<const uint16_t*>(from) + i, v);
-        store4(reinterpret_cast<float*>(to) + i, v);
-      }
-      at += p.H * 4;
-      return Shared{to, true};
+  float* to = reinterpret_cast<float*>(at);
+  auto share = [&](const void* from, int f32, const void* times, int times_f32, float b) {
+    const float* given = to;
+    const Shared v{from, f32 != 0}, g{times, times_f32 != 0};
+    for (int i = tid * 4; i < p.H; i += threads * 4) {
+      float2 q[2] = {make_float2(b, b), make_float2(b, b)}, t[2];
+      const Shared* const both[2] = {&v, &g};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (both[k]->p) {
+          both[k]->load4(i, t);
+          q[0] = mul2(q[0], t[0]);
+          q[1] = mul2(q[1], t[1]);
+        }
+      store4(to + i, q);
     }
-    const int bytes = p.H * (f32 ? 4 : 2);
-    for (int i = tid * 16; i < bytes; i += threads * 16)
-      *reinterpret_cast<uint4*>(to + i) = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + i));
-    at += bytes;
-    return Shared{to, given.f32};
+    to += p.H;
+    return given;
   };
-  s.w = share(p.w, p.w_f32);
-  s.v = share(p.v, p.v_f32);
-  s.g = p.groups > 1 ? Shared{p.g, p.g_f32 != 0} : share(p.g, p.g_f32);
+  s.w = s.k = nullptr;
+  if (p.vectors_shared) {
+    if (p.w) s.w = share(p.w, p.w_f32, nullptr, 0, 1.f);
+    if (vector) s.k = share(p.v, p.v_f32, p.g, p.g_f32, p.b);
+    else if (p.v) s.k = share(p.v, p.v_f32, nullptr, 0, 1.f);
+  }
   __syncthreads();
   return s;
 }
@@ -322,7 +373,7 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
 struct GatePlace {
   int group = 0, left = 0;   // its group, and the group's rows from it on
   __device__ __forceinline__ GatePlace(const NormParams& p, int64_t begin, int rows) {
-    if (p.groups > 1 && rows > 0) {
+    if (rows > 0) {
       group = (int)(begin / p.gate_rows);
       left = (int)((group + 1) * p.gate_rows - begin);
     }
@@ -332,7 +383,7 @@ struct GatePlace {
     ++group;
     left = (int)p.gate_rows;
   }
-  __device__ __forceinline__ int64_t first(const NormParams& p) const { return p.groups > 1 ? (int64_t)group * p.H : 0; }
+  __device__ __forceinline__ int64_t first(const NormParams& p) const { return (int64_t)group * p.H; }
 };
 
 // Groups of 8 columns of a thread of the forward: with two sums to wait for in
@@ -342,7 +393,7 @@ struct GatePlace {
 constexpr __host__ __device__ int norm_groups(bool two_sums, bool x_f32) { return two_sums && x_f32 ? 2 : 1; }
 
 // Y: there is a block's output (y); W, V, G: w, v, g.
-template <typename X, bool Y, bool W, bool V, bool G>
+template <typename X, bool Y, bool W, bool V, int G>
 __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
   constexpr int N = norm_groups(V && W, sizeof(X) == 4);
@@ -352,19 +403,26 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
   const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
   const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
-  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, nullptr, nullptr}, {(int)sizeof(X), 2, 0, 0}, begin, rows);
+  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, nullptr, nullptr, G == kOwnGate ? p.g : nullptr},
+                           {(int)sizeof(X), 2, 0, 0, p.g_f32 ? 4 : 2}, begin, rows, true, G == kVector);
   RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
   int stage = 0;
   uint32_t phase = 0;
-  GatePlace gate(p, begin, G ? rows : 0);
-  constexpr bool kKeepG = !V;   // a gate's row stays in registers
-  F8 gate_row[N];
+  GatePlace gate(p, begin, G == kGroups ? rows : 0);
+  F8 group_k[N];   // K of the group, in registers
+  const bool shared = G != kOwnGate || p.vectors_shared;
+  auto load_w = [&](int j) { return shared ? load8(s.w, c[j]) : Shared{p.w, p.w_f32 != 0}.load(0, c[j]); };
+  auto load_v = [&](int j) { return shared ? load8(s.k, c[j]) : Shared{p.v, p.v_f32 != 0}.load(0, c[j]); };
   auto next_gate = [&]() {
 #pragma unroll
-    for (int j = 0; j < N; ++j) gate_row[j] = s.g.load(gate.first(p), c[j]);
+    for (int j = 0; j < N; ++j) {
+      group_k[j] = Shared{p.g, p.g_f32 != 0}.load(gate.first(p), c[j]);
+      if (V) mul8(group_k[j], load_v(j));
+      mul8(group_k[j], p.b);
+    }
   };
-  if (G && kKeepG && rows > 0) next_gate();
+  if (G == kGroups && rows > 0) next_gate();
   X* out_r = static_cast<X*>(p.r) + begin * p.H;
   uint16_t* out_h = p.h + begin * p.H;
   auto squares = [](const F8 (&v)[N]) {
@@ -375,8 +433,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
   };
   for (int i = 0; i < rows; ++i) {
     const uint8_t* row = rg.wait(p, stage, phase);
+    const Shared own{row + p.H * (sizeof(X) + 2), p.g_f32 != 0};
     F8 r[N], y[N];
-    float sy = p.b;   // the factor of y, s_y among it
+    float sy = G == kVector || G == kGroups ? 1.f : p.b;   // the factor of y, s_y among it
     if (Y) {
 #pragma unroll
       for (int j = 0; j < N; ++j) y[j] = load8(reinterpret_cast<const uint16_t*>(row + p.H * sizeof(X)), c[j]);
@@ -391,8 +450,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
     for (int j = 0; j < N; ++j) {
       r[j] = load8(reinterpret_cast<const X*>(row), c[j]);
       if (!Y) continue;
-      if (V) mul8(y[j], s.v.load(0, c[j]));
-      if (G) mul8(y[j], kKeepG ? gate_row[j] : s.g.load(gate.first(p), c[j]));
+      if (G == kGroups) mul8(y[j], group_k[j]);
+      else if (V || G == kVector) mul8(y[j], load_v(j));
+      if (G == kOwnGate) mul8(y[j], own.load(0, c[j]));
       mul8(r[j], p.a);
       fma8(y[j], fill8(sy), r[j]);
       store8(out_r, c[j], r[j]);
@@ -404,7 +464,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         mul8(r[j], sr);
-        mul8(r[j], s.w.load(0, c[j]));
+        mul8(r[j], load_w(j));
         store8(out_h, c[j], r[j]);
       }
     }
@@ -412,9 +472,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
       rg.sync();
       rg.refill(p, i, stage);
     }
-    if (G && p.groups > 1 && gate.ends()) {
+    if (G == kGroups && gate.ends()) {
       gate.next(p);
-      if (kKeepG && i + 1 < rows) next_gate();
+      if (i + 1 < rows) next_gate();
     }
     if (Y) out_r += p.H;
     if (W) out_h += p.H;
@@ -429,27 +489,38 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
 // block half the threads: the columns' sums and what is kept between a row's
 // sums take up to 128 registers (with 8 columns and 64 registers the operands
 // of a gate or of v spill: 135 us for 8191 x 2048 with all of them).
-template <typename X, bool Y, bool W, bool V, bool G>
+template <typename X, bool Y, bool W, bool V, int G, bool R>
 __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  constexpr bool kKeepG = !V;   // a gate's row stays in registers
   const Columns c[2] = {Columns(threadIdx.x >> 5, p.H), Columns((threadIdx.x + blockDim.x) >> 5, p.H)};
   const uint32_t n = gridDim.x * blockDim.y, me = blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t begin = norm_first_row((uint32_t)p.T, n, me);
   const int rows = (int)(norm_first_row((uint32_t)p.T, n, me + 1) - begin);
-  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, p.dh, p.dr}, {(int)sizeof(X), 2, 2, (int)sizeof(X)}, begin, rows);
+  NormSetup s = norm_setup(p, norm_smem, {p.x, p.y, p.dh, p.dr, G == kOwnGate ? p.g : nullptr},
+                           {(int)sizeof(X), 2, 2, (int)sizeof(X), p.g_f32 ? 4 : 2}, begin, rows, R, G == kVector);
   RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
-  F8 dw[2], dv[2], dg[2], gate_row[2];
+  F8 dw[2], dv[2], u[2], group_k[2];   // u: of all rows with K, else of the gate's group, whose K stays here
+  const Shared gates{p.g, p.g_f32 != 0};
+  const bool shared = G != kOwnGate || p.vectors_shared;
+  auto load_w = [&](int j) { return shared ? load8(s.w, c[j]) : Shared{p.w, p.w_f32 != 0}.load(0, c[j]); };
+  auto load_v = [&](int j) { return shared ? load8(s.k, c[j]) : Shared{p.v, p.v_f32 != 0}.load(0, c[j]); };
   int stage = 0;
   uint32_t phase = 0;
-  GatePlace gate(p, begin, G ? rows : 0);
+  GatePlace gate(p, begin, G == kGroups ? rows : 0);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    dw[j] = dv[j] = dg[j] = gate_row[j] = fill8(0.f);
-    if (G && kKeepG && rows > 0) gate_row[j] = s.g.load(gate.first(p), c[j]);
+    dw[j] = dv[j] = u[j] = fill8(0.f);
   }
-  auto gate_of = [&](int j) { return kKeepG ? gate_row[j] : s.g.load(gate.first(p), c[j]); };
+  auto next_gate = [&](int j) {
+    group_k[j] = gates.load(gate.first(p), c[j]);
+    if (V) mul8(group_k[j], load_v(j));
+    mul8(group_k[j], p.b);
+  };
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (G == kGroups && rows > 0) next_gate(j);
+  auto load_k = [&](int j) { return G == kGroups ? group_k[j] : load_v(j); };
   float next_r = 0.f, next_y = 0.f;   // the next row's statistics
   auto stats = [&](int i) {
     if (i >= rows) return;
@@ -460,19 +531,23 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   X* out_x = static_cast<X*>(p.dx) + begin * p.H;
   uint16_t* out_y = p.dy + begin * p.H;
   const uint32_t at_y = p.H * sizeof(X), at_dh = at_y + (Y ? p.H * 2 : 0), at_dr = at_dh + (W ? p.H * 2 : 0);
+  const uint32_t at_gate = at_dr + (R && p.dr ? p.H * sizeof(X) : 0);
   for (int i = 0; i < rows; ++i) {
     const float sr = next_r, sy = next_y;
     stats(i + 1);
     // Between the sums a thread keeps r and dh w alone, and reads the row's
     // other operands from shared memory again.
     const uint8_t* row = rg.wait(p, stage, phase);
+    auto own_of = [&](int j) { return Shared{row + at_gate, p.g_f32 != 0}.load(0, c[j]); };
     auto load_y = [&](int j) {   // normed, without v
       F8 y = load8(reinterpret_cast<const uint16_t*>(row + at_y), c[j]);
       if (V) mul8(y, sy);
       return y;
     };
     auto load_dr = [&](int j) {
-      return p.dr ? load8(reinterpret_cast<const X*>(row + at_dr), c[j]) : fill8(0.f);
+      if (!p.dr) return fill8(0.f);
+      return R ? load8(reinterpret_cast<const X*>(row + at_dr), c[j])
+               : load8(static_cast<const X*>(p.dr) + (begin + i) * p.H, c[j]);
     };
     F8 d[2];
     if (W) {
@@ -483,16 +558,16 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
         r[j] = load8(reinterpret_cast<const X*>(row), c[j]);
         if (Y) {
           F8 y = load_y(j);
-          if (V) mul8(y, s.v.load(0, c[j]));
-          if (G) mul8(y, gate_of(j));
-          mul8(y, p.b);
+          if (V || G == kVector || G == kGroups) mul8(y, load_k(j));
+          if (G == kOwnGate) mul8(y, own_of(j));
+          if (G == kPlain || G == kOwnGate) mul8(y, p.b);
           fma8(fill8(p.a), r[j], y);
           r[j] = y;
         }
         mul8(r[j], sr);
         d[j] = load8(reinterpret_cast<const uint16_t*>(row + at_dh), c[j]);
         fma8(d[j], r[j], dw[j]);
-        mul8(d[j], s.w.load(0, c[j]));
+        mul8(d[j], load_w(j));
         q += dot8(d[j], r[j]);
       }
       q = rg.sum(q) * inv;
@@ -515,24 +590,28 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
       mul8(o, p.a);
       store8(out_x, c[j], o);
       if (!Y) continue;
-      mul8(d[j], p.b);
-      if (!G && !V) continue;
+      if (G == kPlain || G == kOwnGate) mul8(d[j], p.b);
+      if (G == kPlain) continue;
       const F8 y = load_y(j);
-      if (V) {
-        const F8 v = s.v.load(0, c[j]);
-        if (G) {
-          F8 m = y;
+      if (G == kOwnGate) {   // dg of this row, b d times its n
+        F8 m = y;
+        mul8(m, d[j]);
+        const F8 g = own_of(j);
+        if (V) {
+          const F8 v = load_v(j);
+          fma8(m, g, dv[j]);
           mul8(m, v);
-          fma8(d[j], m, dg[j]);
-          mul8(d[j], gate_of(j));
+          mul8(d[j], v);
         }
-        fma8(d[j], y, dv[j]);
-        mul8(d[j], v);
-        q += dot8(d[j], y);
+        const int64_t at = (begin + i) * p.H;
+        if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], m);
+        else store8(static_cast<uint16_t*>(p.dg) + at, c[j], m);
+        mul8(d[j], g);
       } else {
-        fma8(d[j], y, dg[j]);
-        mul8(d[j], gate_of(j));
+        fma8(d[j], y, u[j]);
+        mul8(d[j], load_k(j));
       }
+      if (V) q += dot8(d[j], y);
     }
     if (V) {
       q = rg.sum(q) * inv;
@@ -541,7 +620,7 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     if (Y) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-          if (V) {
+        if (V) {
           fma8(fill8(-q), load_y(j), d[j]);
           mul8(d[j], sy);
         }
@@ -552,21 +631,26 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
       rg.sync();
       rg.refill(p, i, stage);
     }
-    if (G && p.groups > 1) {
+    if (G == kGroups) {   // dg = b v u, and g's part of dv
       const bool ends = gate.ends();
       if (ends || i + 1 == rows) {
         const int64_t first = gate.group * p.gate_rows, at = gate.first(p);
         gate.next(p);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-              if (ends && first >= begin) {
-            if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], dg[j]);
-            else store8(static_cast<uint16_t*>(p.dg) + at, c[j], dg[j]);
-          } else {   // the range's first group, or its last
-            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H, c[j], dg[j]);
+          mul8(u[j], p.b);
+          if (V) {
+            fma8(u[j], gates.load(at, c[j]), dv[j]);
+            mul8(u[j], load_v(j));
           }
-          dg[j] = fill8(0.f);
-          if (kKeepG && i + 1 < rows) gate_row[j] = s.g.load(gate.first(p), c[j]);
+          if (ends && first >= begin) {
+            if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], u[j]);
+            else store8(static_cast<uint16_t*>(p.dg) + at, c[j], u[j]);
+          } else {   // the range's first group, or its last
+            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H, c[j], u[j]);
+          }
+          u[j] = fill8(0.f);
+          if (i + 1 < rows) next_gate(j);
         }
       }
     }
@@ -580,13 +664,8 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   // the block's sums, its row groups in order, through the rings' memory
   float* sums = reinterpret_cast<float*>(norm_smem);   // [row groups][H]
   int k = 0;
-  auto add_up = [&](const F8 (&sum)[2], void* final, int f32) {
+  auto add_up = [&](const F8 (&sum)[2], bool of_w) {
     float* out = p.parts + ((int64_t)blockIdx.x * p.n_sums + k++) * p.H;
-    auto put = [&](int i, const float2 (&v)[2]) {   // four columns from i on
-      if (gridDim.x > 1) store4(out + i, v);
-      else if (f32) store4(static_cast<float*>(final) + i, v);
-      else store4(static_cast<uint16_t*>(final) + i, v);
-    };
     __syncthreads();   // the rows, or the sums before, have been read
 #pragma unroll
     for (int j = 0; j < 2; ++j) store8(sums + threadIdx.y * p.H, c[j], sum[j]);
@@ -598,21 +677,23 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
         load4(sums + ty * p.H + i, r);
         q[0].x += r[0].x; q[0].y += r[0].y; q[1].x += r[1].x; q[1].y += r[1].y;
       }
-      put(i, q);
+      if (gridDim.x > 1) {
+        store4(out + i, q);
+      } else {
+        sums_out(p.out, of_w, i, q[0]);
+        sums_out(p.out, of_w, i + 2, q[1]);
+      }
     }
   };
-  if (W) add_up(dw, p.dw, p.w_f32);
-  if (V) add_up(dv, p.dv, p.v_f32);
-  if (G && p.groups == 1) add_up(dg, p.dg, p.g_f32);
+  if (W) add_up(dw, true);
+  if (G == kVector) add_up(u, false);
+  else if (V) add_up(dv, false);
 }
 
 struct NormSumParams {
   const float* parts;
-  void* out[3];
-  int f32[3];
+  SumsOut out;
   int n_sums, blocks;     // sums over all rows
-  void* dg;
-  int dg_f32;
   uint32_t T, groups, gate_rows, row_groups;
   int H;
 };
@@ -679,46 +760,41 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
       const float2 q = part[i][lane];
       s.x += q.x; s.y += q.y;
     }
-    void* out = whole ? p.out[blockIdx.y] : p.dg;
-    const int64_t at = (int64_t)group * p.H + c;
-    if (whole ? p.f32[blockIdx.y] : p.dg_f32) *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = s;
-    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at) = pack_bf16x2(s.x, s.y);
+    if (whole) sums_out(p.out, blockIdx.y == 0 && p.out.dw, c, s);
+    else put2(p.out.dg, p.out.g_f32, (int64_t)group * p.H + c, s);
   }
 }
 
-// A launch's shape.  row_bytes: of a row's streams; params, wide: of w, v and
-// a single gate as given and as fp32.  They are kept as fp32 where two stages
-// fit beside them (16384 x 7168, bf16, backward: 200 us, as given 212), else as
-// given (4096 x 4096, fp32 stream, bf16 weights: 83 us, from global memory 94).
+// A launch's shape.  row_bytes: of a row's streams; vectors: of w and K or v
+// as fp32, which stay in global memory where two stages of one row do not fit
+// beside them (a row's own gates at H 7168 and more).
 // one_block: as many rows as one block holds take one, which needs no sums of
 // sums (forward and backward of 8 x 256 6.4 us, in blocks of a row 7.7).
 struct NormShape {
   dim3 block;
-  int grid, stages, shared_params;
+  int grid, stages, vectors_shared;
   size_t smem;
 };
-NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t params, size_t wide,   // of a block; of 8 columns
-                     bool one_block) {
+NormShape norm_shape(int64_t T, int64_t H, int threads, int groups, size_t row_bytes, size_t vectors, bool one_block) {   // groups of 8 columns
   NormShape s;
   const int tpr = (int)((H + 256 * groups - 1) / (256 * groups) * 32);
+  s.vectors_shared = 2 * row_bytes + vectors <= kNormSmem;
+  if (!s.vectors_shared) vectors = 0;
+  const size_t room = kNormSmem - vectors;
   int rows = threads / tpr;
   if (tpr > 32) rows = std::min(rows, 15);   // row groups' barriers 1 .. 15; a warp needs none
-  rows = (int)std::max<size_t>(1, std::min<size_t>(rows, kNormSmem / (2 * row_bytes)));
+  rows = (int)std::max<size_t>(1, std::min<size_t>(rows, room / (2 * row_bytes)));
   rows = one_block && T <= rows ? (int)T : (int)std::max<int64_t>(1, std::min<int64_t>(rows, (T + kNormBlocks - 1) / kNormBlocks));
-  s.shared_params = 2 * rows * row_bytes + wide <= kNormSmem ? kAsFp32 : 2 * rows * row_bytes + params <= kNormSmem ? kAsGiven : kInGlobal;
-  params = s.shared_params == kAsFp32 ? wide : s.shared_params == kAsGiven ? params : 0;
-  const size_t room = kNormSmem - params;
   s.stages = (int)std::min<size_t>(kNormMaxStages, room / (rows * row_bytes));
   s.block = dim3(tpr, rows);
   s.grid = (int)std::min<int64_t>((T + rows - 1) / rows, kNormBlocks);
-  s.smem = (size_t)rows * s.stages * row_bytes + params;
+  s.smem = (size_t)rows * s.stages * row_bytes + vectors;
   return s;
 }
 
-size_t norm_wide_bytes(const BlockNorm& n) { return (size_t)n.H * 4 * ((n.w != nullptr) + (n.v != nullptr) + (n.groups == 1)); }
-size_t norm_params_bytes(const BlockNorm& n) {
-  return (size_t)n.H * ((n.w ? (n.w_f32 ? 4 : 2) : 0) + (n.v ? (n.v_f32 ? 4 : 2) : 0) + (n.groups == 1 ? (n.g_f32 ? 4 : 2) : 0));
-}
+size_t norm_vectors_bytes(const BlockNorm& n) { return (size_t)n.H * 4 * ((n.w != nullptr) + (n.v || n.groups == 1)); }
+bool own_gate(const BlockNorm& n) { return n.groups > 1 && n.groups == n.T; }
+size_t norm_gate_bytes(const BlockNorm& n) { return own_gate(n) ? (size_t)n.H * (n.g_f32 ? 4 : 2) : 0; }
 
 NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo& dev) {
   NormParams p = {};
@@ -727,7 +803,7 @@ NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo&
   p.a = n.a; p.b = n.b; p.eps = n.eps;
   p.w_f32 = n.w_f32; p.v_f32 = n.v_f32; p.g_f32 = n.g_f32;
   p.stages = s.stages;
-  p.shared_params = s.shared_params;
+  p.vectors_shared = s.vectors_shared;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
   return p;
@@ -735,26 +811,33 @@ NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo&
 
 using NormKernel = void (*)(NormParams);
 
-template <typename X>
+int norm_kind(const BlockNorm& n) { return own_gate(n) ? kOwnGate : n.groups > 1 ? kGroups : n.v || n.g ? kVector : kPlain; }
+
+template <typename X, bool R, bool W, bool V, int G>
+NormKernel norm_kernel(bool bwd) {
+  return bwd ? block_norm_bwd_kernel<X, true, W, V, G, R> : block_norm_kernel<X, true, W, V, G>;
+}
+template <typename X, bool R>
 NormKernel norm_kernel(bool bwd, const BlockNorm& n) {
-  const int which = (n.w ? 1 : 0) | (n.v ? 2 : 0) | (n.g ? 4 : 0);
-  if (!n.y) return bwd ? block_norm_bwd_kernel<X, false, true, false, false> : block_norm_kernel<X, false, true, false, false>;
-#define MOE_NORM(i) \
-  case i: return bwd ? block_norm_bwd_kernel<X, true, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0> \
-                     : block_norm_kernel<X, true, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0>;
-  switch (which) {
-    MOE_NORM(0) MOE_NORM(1) MOE_NORM(2) MOE_NORM(3) MOE_NORM(4) MOE_NORM(5) MOE_NORM(6)
-    default: MOE_NORM(7)
+  if (!n.y) return bwd ? block_norm_bwd_kernel<X, false, true, false, kPlain, R> : block_norm_kernel<X, false, true, false, kPlain>;
+#define MOE_NORM(G) \
+  case G: return n.w ? (n.v ? norm_kernel<X, R, true, true, G>(bwd) : norm_kernel<X, R, true, false, G>(bwd)) \
+                     : (n.v ? norm_kernel<X, R, false, true, G>(bwd) : norm_kernel<X, R, false, false, G>(bwd));
+  switch (norm_kind(n)) {
+    MOE_NORM(kVector) MOE_NORM(kGroups) MOE_NORM(kOwnGate)
+    default: return n.w ? norm_kernel<X, R, true, false, kPlain>(bwd) : norm_kernel<X, R, false, false, kPlain>(bwd);
   }
 #undef MOE_NORM
 }
 
-cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const NormParams& p, const DeviceInfo& dev,
+cudaError_t norm_launch(bool bwd, bool dr_staged, const BlockNorm& n, const NormShape& s, const NormParams& p, const DeviceInfo& dev,
                         cudaStream_t stream) {
-  const NormKernel kernel = n.x_f32 ? norm_kernel<float>(bwd, n) : norm_kernel<uint16_t>(bwd, n);
+  const NormKernel kernel = n.x_f32 ? (dr_staged ? norm_kernel<float, true>(bwd, n) : norm_kernel<float, false>(bwd, n))
+                                    : (dr_staged ? norm_kernel<uint16_t, true>(bwd, n) : norm_kernel<uint16_t, false>(bwd, n));
   // per-device set-up, cached (a race between host threads only repeats it)
-  static std::atomic<int> configured[kMaxDevices][2][2][9] = {};
-  std::atomic<int>& done = configured[dev.ordinal][bwd][n.x_f32 != 0][n.y ? (n.w ? 1 : 0) | (n.v ? 2 : 0) | (n.g ? 4 : 0) : 8];
+  static std::atomic<int> configured[kMaxDevices][2][2][2][17] = {};
+  std::atomic<int>& done = configured[dev.ordinal][bwd][dr_staged][n.x_f32 != 0]
+                                       [n.y ? (n.w ? 1 : 0) | (n.v ? 2 : 0) | norm_kind(n) << 2 : 16];
   if (!done.load()) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kNormSmem);
@@ -764,9 +847,20 @@ cudaError_t norm_launch(bool bwd, const BlockNorm& n, const NormShape& s, const 
   return launch_pdl(kernel, dim3(s.grid), s.block, s.smem, stream, 1, p);
 }
 
-NormShape norm_bwd_shape(const BlockNorm& n, bool dr) {
-  return norm_shape(n.T, n.H, kNormThreads / 2, 2, (size_t)n.H * ((n.x_f32 ? 4 : 2) * (dr ? 2 : 1) + (n.y ? 2 : 0) + (n.w ? 2 : 0)),
-                    norm_params_bytes(n), norm_wide_bytes(n), n.groups <= 1 || n.groups == n.T);   // no gate's rows to join
+// dr stays out of the ring where it leaves no room for two stages (the others
+// take 12 bytes a column at most, 192 KB), for w and K or v, or for as many row
+// groups.  Its rows are then prefetched into the L2 (4096 x 7168, fp32 stream,
+// both norms: 80 us, with w and v read from global memory instead 97).
+NormShape norm_bwd_shape(const BlockNorm& n, bool dr, bool* dr_staged) {
+  const size_t dr_bytes = dr ? (size_t)n.H * (n.x_f32 ? 4 : 2) : 0;
+  const size_t others = (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0) + (n.w ? 2 : 0)) + norm_gate_bytes(n);
+  const auto shape = [&](size_t row_bytes) {
+    return norm_shape(n.T, n.H, kNormThreads / 2, 2, row_bytes, norm_vectors_bytes(n),
+                      n.groups <= 1 || n.groups == n.T);   // no gate's rows to join
+  };
+  const NormShape with = shape(others + dr_bytes), without = shape(others);
+  *dr_staged = with.stages >= 2 && with.vectors_shared == without.vectors_shared && with.block.y == without.block.y;
+  return *dr_staged ? with : without;
 }
 
 }  // namespace
@@ -775,18 +869,18 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32), (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)), norm_params_bytes(n),
-                                 norm_wide_bytes(n), false);
+  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32), 
+                                 (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)) + norm_gate_bytes(n), norm_vectors_bytes(n), false);
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
-  return norm_launch(false, n, s, p, dev, stream);
+  return norm_launch(false, true, n, s, p, dev, stream);
 }
 
 // The most that any types and any dr take: row groups are fewest bytes a row.
 size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool w, bool v) {
   if (T == 0) return 0;
-  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, 0, true);
-  const size_t n_sums = (w ? 1 : 0) + (v ? 1 : 0) + (groups == 1 ? 1 : 0);
+  const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, true);
+  const size_t n_sums = (w ? 1 : 0) + (v || groups == 1 ? 1 : 0);
   const size_t blocks = std::min<int64_t>(T, kNormBlocks);
   return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
 }
@@ -802,23 +896,21 @@ cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const 
       }
     return cudaSuccess;
   }
-  const NormShape s = norm_bwd_shape(n, dr != nullptr);
+  bool dr_staged;
+  const NormShape s = norm_bwd_shape(n, dr != nullptr, &dr_staged);
   NormParams p = norm_params(n, s, dev);
   p.stats = const_cast<float*>(stats);
-  p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g; p.dw = d.w; p.dv = d.v;
+  p.dh = dh; p.dr = dr; p.dx = d.x; p.dy = d.y; p.dg = d.g;
+  p.out = {n.w ? d.w : nullptr, d.v, d.g, n.v, n.g, n.w_f32, n.v_f32, n.g_f32, norm_kind(n) == kVector, n.b};
   p.parts = static_cast<float*>(ws);
   NormSumParams q = {};
   q.parts = p.parts;
-  int k = 0;
-  if (n.w) { q.out[k] = d.w; q.f32[k++] = n.w_f32; }
-  if (n.v) { q.out[k] = d.v; q.f32[k++] = n.v_f32; }
-  if (n.groups == 1) { q.out[k] = d.g; q.f32[k++] = n.g_f32; }
+  q.out = p.out;
+  const int k = (n.w ? 1 : 0) + (n.v || n.groups == 1 ? 1 : 0);
   p.n_sums = q.n_sums = k;
-  const cudaError_t e = norm_launch(true, n, s, p, dev, stream);
+  const cudaError_t e = norm_launch(true, dr_staged, n, s, p, dev, stream);
   if (e != cudaSuccess) return e;
   q.blocks = s.grid;
-  q.dg = d.g;
-  q.dg_f32 = n.g_f32;
   q.T = (uint32_t)n.T; q.groups = (uint32_t)n.groups; q.gate_rows = (uint32_t)p.gate_rows; q.H = p.H;
   q.row_groups = (uint32_t)s.grid * s.block.y;
   const int64_t shared = n.groups > 1 && p.gate_rows > 1 ? (n.groups <= q.row_groups ? n.groups : (int64_t)q.row_groups - 1) : 0;
