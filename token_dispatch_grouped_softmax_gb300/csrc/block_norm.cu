@@ -191,7 +191,7 @@ struct NormParams {
   const void* dr;
   void* dx;
   uint16_t* dy;
-  float* parts;           // [grid][sums][H], then [row groups][2][H] of the gate's groups
+  float* parts;           // [grid][sums][H], then [row groups][norm_slots][H] of the gate's groups
   void* dg;               // finished groups are written here
   SumsOut out;            // for a launch of one block
   int64_t T;
@@ -206,6 +206,10 @@ struct NormParams {
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
+
+// Rows of the workspace for a range among several of a gate's groups: its first
+// group's sum, its last one's, and dv's where there is one.
+constexpr __host__ __device__ int norm_slots(bool v) { return v ? 3 : 2; }
 
 // The first of row group v's rows, of n row groups.
 __device__ __forceinline__ uint32_t norm_first_row(uint32_t T, uint32_t n, uint32_t v) {
@@ -388,15 +392,18 @@ struct GatePlace {
 
 // Groups of 8 columns of a thread of the forward: with two sums to wait for in
 // a row of an fp32 stream, two, so that twice as many rows are under way (8191
-// x 2048, both norms: 39.8 us, with one group 47.0; but of a bf16 stream 29.2,
-// with one group 26.7, and with one norm 16384 x 7168 162, with one group 147).
-constexpr __host__ __device__ int norm_groups(bool two_sums, bool x_f32) { return two_sums && x_f32 ? 2 : 1; }
+// x 2048, both norms: 36.7 us, with one group 37.4; but of a bf16 stream 29.2,
+// with one group 26.7, and with one norm 16384 x 7168 162, with one group 147),
+// unless a group's K takes the registers (4096 x 7168, 4 gates: 60, with two 77).
+constexpr __host__ __device__ int norm_groups(bool two_sums, bool x_f32, int kind) {
+  return two_sums && x_f32 && kind != kGroups ? 2 : 1;
+}
 
 // Y: there is a block's output (y); W, V, G: w, v, g.
 template <typename X, bool Y, bool W, bool V, int G>
 __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
-  constexpr int N = norm_groups(V && W, sizeof(X) == 4);
+  constexpr int N = norm_groups(V && W, sizeof(X) == 4, G);
   Columns c[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) c[j] = Columns((threadIdx.x + j * blockDim.x) >> 5, p.H);
@@ -487,8 +494,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
 
 // A thread has two groups of 8 columns here, H / 16 threads to a row, and the
 // block half the threads: the columns' sums and what is kept between a row's
-// sums take up to 128 registers (with 8 columns and 64 registers the operands
-// of a gate or of v spill: 135 us for 8191 x 2048 with all of them).
+// sums take up to 128 registers (with 8 columns a thread and 64 registers they spill).
 template <typename X, bool Y, bool W, bool V, int G, bool R>
 __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t norm_smem[];
@@ -500,6 +506,10 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
                            {(int)sizeof(X), 2, 2, (int)sizeof(X), p.g_f32 ? 4 : 2}, begin, rows, R, G == kVector);
   RowGroup& rg = s.rg;
   const float inv = 1.f / (float)p.H;
+  // Of several groups' gates dv is added up in the workspace, at the groups'
+  // ends: its registers hold K (8192 x 2048 in bf16, 8 gates: 39 us; with dv
+  // in registers too 60, with K from shared and global memory 58).
+  float* slots = p.parts + ((int64_t)gridDim.x * p.n_sums + norm_slots(V) * (int64_t)me) * p.H;
   F8 dw[2], dv[2], u[2], group_k[2];   // u: of all rows with K, else of the gate's group, whose K stays here
   const Shared gates{p.g, p.g_f32 != 0};
   const bool shared = G != kOwnGate || p.vectors_shared;
@@ -640,14 +650,16 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
         for (int j = 0; j < 2; ++j) {
           mul8(u[j], p.b);
           if (V) {
-            fma8(u[j], gates.load(at, c[j]), dv[j]);
+            F8 sum = first > begin ? load8(slots + 2 * p.H, c[j]) : fill8(0.f);
+            fma8(u[j], gates.load(at, c[j]), sum);
+            store8(slots + 2 * p.H, c[j], sum);
             mul8(u[j], load_v(j));
           }
           if (ends && first >= begin) {
             if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], u[j]);
             else store8(static_cast<uint16_t*>(p.dg) + at, c[j], u[j]);
           } else {   // the range's first group, or its last
-            store8(p.parts + ((int64_t)gridDim.x * p.n_sums + 2 * (int64_t)me + (first > begin)) * p.H, c[j], u[j]);
+            store8(slots + (first > begin ? p.H : 0), c[j], u[j]);
           }
           u[j] = fill8(0.f);
           if (i + 1 < rows) next_gate(j);
@@ -687,7 +699,13 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   };
   if (W) add_up(dw, true);
   if (G == kVector) add_up(u, false);
-  else if (V) add_up(dv, false);
+  else if (V) {
+    if (G == kGroups && rows > 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) dv[j] = load8(slots + 2 * p.H, c[j]);
+    }
+    add_up(dv, false);
+  }
 }
 
 struct NormSumParams {
@@ -731,8 +749,8 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
     const uint32_t to = norm_group_of(p.T, p.row_groups, (group + 1) * p.gate_rows - 1);
     if (from == to) return;   // within one range, which wrote it
     n = to - from + 1;
-    pitch = 2 * p.H;
-    rest = p.parts + ((int64_t)p.blocks * p.n_sums + 2 * (int64_t)from) * p.H;
+    pitch = norm_slots(p.out.v) * p.H;
+    rest = p.parts + ((int64_t)p.blocks * p.n_sums + norm_slots(p.out.v) * (int64_t)from) * p.H;
     first = rest + (norm_first_row(p.T, p.row_groups, from) < group * p.gate_rows ? p.H : 0);
   }
   float2 s = make_float2(0.f, 0.f);
@@ -869,7 +887,7 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32), 
+  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32, norm_kind(n)), 
                                  (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)) + norm_gate_bytes(n), norm_vectors_bytes(n), false);
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
@@ -882,7 +900,7 @@ size_t block_norm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t groups, bool
   const NormShape s = norm_shape(T, H, kNormThreads / 2, 2, (size_t)H * (w ? 4 : 2), 0, true);
   const size_t n_sums = (w ? 1 : 0) + (v || groups == 1 ? 1 : 0);
   const size_t blocks = std::min<int64_t>(T, kNormBlocks);
-  return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 ? 2 * blocks * s.block.y : 0));
+  return sizeof(float) * (size_t)H * (blocks * n_sums + (groups > 1 && groups != T ? norm_slots(v) * blocks * s.block.y : 0));
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dh, const void* dr, const float* stats,
