@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(32 * kNormSumWarps) block_norm_sum_kernel(cons
 
 // A launch's shape.  row_bytes: of a row's streams; vectors: of w and K or v
 // as fp32, which stay in global memory where two stages of one row do not fit
-// beside them (a row's own gates at H 7168 and more).
+// beside them (a row's own gates beyond H 6912).
 // one_block: as many rows as one block holds take one, which needs no sums of
 // sums (forward and backward of 8 x 256 6.4 us, in blocks of a row 7.7).
 struct NormShape {
@@ -887,7 +887,7 @@ int64_t block_norm_max_width() { return kNormMaxH; }
 
 cudaError_t launch_block_norm(const BlockNorm& n, void* r, uint16_t* h, float* stats, const DeviceInfo& dev,
                               cudaStream_t stream) {
-  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32, norm_kind(n)), 
+  const NormShape s = norm_shape(n.T, n.H, kNormThreads, norm_groups(n.v && n.w, n.x_f32, norm_kind(n)),
                                  (size_t)n.H * ((n.x_f32 ? 4 : 2) + (n.y ? 2 : 0)) + norm_gate_bytes(n), norm_vectors_bytes(n), false);
   NormParams p = norm_params(n, s, dev);
   p.r = r; p.h = h; p.stats = stats;
