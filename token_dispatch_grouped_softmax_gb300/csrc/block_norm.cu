@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   // Of several groups' gates dv is added up in the workspace, at the groups'
   // ends: its registers hold K (8192 x 2048 in bf16, 8 gates: 39 us; with dv
   // in registers too 60, with K from shared and global memory 58).
-  float* slots = p.parts + ((int64_t)gridDim.x * p.n_sums + norm_slots(V) * (int64_t)me) * p.H;
+  auto slot = [&](int k) { return p.parts + ((int64_t)gridDim.x * p.n_sums + norm_slots(V) * (int64_t)me + k) * p.H; };
   F8 dw[2], dv[2], u[2], group_k[2];   // u: of all rows with K, else of the gate's group, whose K stays here
   const Shared gates{p.g, p.g_f32 != 0};
   const bool shared = G != kOwnGate || p.vectors_shared;
@@ -650,16 +650,16 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
         for (int j = 0; j < 2; ++j) {
           mul8(u[j], p.b);
           if (V) {
-            F8 sum = first > begin ? load8(slots + 2 * p.H, c[j]) : fill8(0.f);
+            F8 sum = first > begin ? load8(slot(2), c[j]) : fill8(0.f);
             fma8(u[j], gates.load(at, c[j]), sum);
-            store8(slots + 2 * p.H, c[j], sum);
+            store8(slot(2), c[j], sum);
             mul8(u[j], load_v(j));
           }
           if (ends && first >= begin) {
             if (p.g_f32) store8(static_cast<float*>(p.dg) + at, c[j], u[j]);
             else store8(static_cast<uint16_t*>(p.dg) + at, c[j], u[j]);
           } else {   // the range's first group, or its last
-            store8(slots + (first > begin ? p.H : 0), c[j], u[j]);
+            store8(slot(first > begin), c[j], u[j]);
           }
           u[j] = fill8(0.f);
           if (i + 1 < rows) next_gate(j);
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
   else if (V) {
     if (G == kGroups && rows > 0) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) dv[j] = load8(slots + 2 * p.H, c[j]);
+      for (int j = 0; j < 2; ++j) dv[j] = load8(slot(2), c[j]);
     }
     add_up(dv, false);
   }
