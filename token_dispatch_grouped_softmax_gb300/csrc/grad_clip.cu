@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
     const ClipChunk c = clip_chunk(list, tensor, at);
     const void* src = list.src[c.tensor];
     void* dst = list.dst[c.tensor];
-    if (scale == 1.f && src == dst) continue;
+    if (scale == 1.f && step == 1.f && src == dst) continue;
     const int head = clip_head(src, c.f32);
     const bool aligned = clip_head(dst, c.f32) == head;
     if (c.f32) {
