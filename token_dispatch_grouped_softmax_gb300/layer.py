@@ -14,6 +14,7 @@ gate_up_bwd -> gather_dx.
 from __future__ import annotations
 
 import contextlib
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -172,6 +173,37 @@ def moe_backward(dy, st: ForwardState, w_router, gate_up, down, want_dw_router=F
     return out
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Its arguments after the first as they are; differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.detach() for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the layer's and the norms' gradients cannot be differentiated again: their kernels record no graph")
+
+
+def _first_order(backward):
+    """For a Function's backward whose kernels record no graph: its gradients
+    under create_graph=True raise when they are differentiated, where the terms
+    through them would be missing.  (torch's once_differentiable does so only
+    where the incoming gradient has a graph, which a sum's has not.)"""
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = list(backward(ctx, *grads))
+        given = [i for i, g in enumerate(out) if g is not None]
+        if torch.is_grad_enabled() and given:
+            for i, g in zip(given, _NoSecondDerivative.apply(torch.zeros((), requires_grad=True), *(out[i] for i in given))):
+                out[i] = g
+        return tuple(out)
+
+    return run
+
+
 class MoELayerFunction(torch.autograd.Function):
     """y = MoE(x); gradients for x, W_r, gate_up and down (fp32 W_r grad)."""
 
@@ -184,6 +216,7 @@ class MoELayerFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         w_router, gate_up, down = ctx.saved_tensors
         g = moe_backward(dy.contiguous(), ctx.st, w_router, gate_up, down,
@@ -205,6 +238,7 @@ class RoutedMoELayerFunction(torch.autograd.Function):
         return y, st.counts
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, _):
         w_router, gate_up, down = ctx.saved_tensors
         g = moe_backward(dy.contiguous(), ctx.st, w_router, gate_up, down, want_dw_router=ctx.needs_input_grad[1])
@@ -278,6 +312,7 @@ class BlockNormFunction(torch.autograd.Function):
         return r, h
 
     @staticmethod
+    @_first_order
     def backward(ctx, dr, dh):
         x, weight, branch, post_weight, gate, stats = ctx.saved_tensors
         if weight is None:
