@@ -24,3 +24,37 @@ def test_a_factor_around_2_to_the_minus_64(small, t, inplace):
     assert abs(float(norm) - norm64) <= NORM * norm64
     half = torch.finfo(t).eps / 2
     assert bool(((out[0].double() - want).abs() <= (2 * NORM + half) * want.abs()).all()), out[0]
+
+
+def test_what_is_written_has_a_new_version():
+    """A tensor that autograd keeps for a backward and that a call then writes is noticed there."""
+    moe = lib()
+    a, b = torch.ones(8, device=dev()), torch.ones(8, device=dev())
+    for call, out in ((lambda: moe.clip_grads([a], 1.0), a), (lambda: moe.clip_grads([a], 1.0, out=[b]), b)):
+        leaf = torch.ones(8, device=dev(), requires_grad=True)
+        y = (leaf * out).sum()
+        version = out._version
+        call()
+        assert out._version > version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    version = a._version
+    moe.clip_grads([a], 1.0, out=[b])
+    moe.grad_norm([a])
+    assert a._version == version          # only read
+    x = torch.ones((1, 64), dtype=torch.bfloat16, device=dev())
+    gate_up, down = torch.ones((64, 128), dtype=torch.bfloat16, device=dev()), torch.ones((64, 64), dtype=torch.bfloat16, device=dev())
+    y = torch.zeros_like(x)
+    version = y._version
+    moe.experts_few(x, torch.zeros((1, 1), dtype=torch.int32, device=dev()), torch.ones((1, 1), device=dev()), gate_up, down, out=y)
+    assert y._version > version
+    bias = torch.zeros(4, device=dev())
+    version = bias._version
+    moe.route_balance_bias(bias, torch.ones(4, dtype=torch.int32, device=dev()), 0.1, out=bias)
+    assert bias._version > version
+    with torch.inference_mode():
+        kept = [torch.full((4,), 2.0, device=dev())]
+        moe.clip_grads(kept, 1.0)
+    moe.clip_grads(kept, 1.0)             # an inference tensor has no version, and is scaled as before
+    assert float(kept[0].norm()) <= 1.0 + 1e-5
+    moe.sync_status()

@@ -104,6 +104,12 @@ T* ptr(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
+// After a call that wrote into a tensor it was given: autograd, where it keeps
+// the tensor, has to know that it changed.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   PyObject* x = THPVariable_Wrap(a);
   PyObject* y = THPVariable_Wrap(b);
@@ -213,6 +219,7 @@ PyObject* route_balance_bias(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (out.size(0) != E) refuse(PyExc_ValueError, "out must be [E]");
   void* st = stream();
   run("moe_route_balance_bias", [&] { return f_route_balance_bias(ptr<float>(bias), ptr<int32_t>(counts), E, rate, ptr<float>(out), st); });
+  if (a[3] != Py_None) written(out);
   return THPVariable_Wrap(out);
   BODY_END
 }
@@ -308,6 +315,7 @@ PyObject* w4_down_combine(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return f_w4_down_combine(ptr<uint16_t>(h), ids, wt, w.q, w.scales, w.zeros, shared, T, w.N, w.E, k, I, w.group,
                              ptr<uint16_t>(y), ptr(ws), bytes, st);
   });
+  if (a[7] != Py_None) written(y);
   return THPVariable_Wrap(y);
   BODY_END
 }
@@ -355,6 +363,7 @@ PyObject* few_experts(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return f_few_experts(ptr<uint16_t>(x), ptr<int32_t>(ids), ptr<float>(w), e.gate_up, e.down, sh.gate_up, sh.down, T, H,
                          e.E, k, e.I, sh.I, ptr<uint16_t>(y), ptr(ws), bytes, st);
   });
+  if (a[7] != Py_None) written(y);
   return THPVariable_Wrap(y);
   BODY_END
 }
@@ -589,6 +598,9 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return f_grad_clip(src.data(), clip ? dst.data() : nullptr, size.data(), f32.data(), n, max_norm, eps, ptr<float>(norm),
                        ptr(ws), bytes, st);
   });
+  if (clip)   // the list as it is now: another thread may have changed it meanwhile
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(a[1]); ++i)
+      if (THPVariable_Check(PySequence_Fast_GET_ITEM(a[1], i))) written(THPVariable_Unpack(PySequence_Fast_GET_ITEM(a[1], i)));
   return THPVariable_Wrap(norm);
   BODY_END
 }
