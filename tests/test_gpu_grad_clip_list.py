@@ -58,3 +58,58 @@ def test_what_is_written_has_a_new_version():
     moe.clip_grads(kept, 1.0)             # an inference tensor has no version, and is scaled as before
     assert float(kept[0].norm()) <= 1.0 + 1e-5
     moe.sync_status()
+
+
+LAYOUTS = {"transposed": ((96, 40), lambda t: t.t()), "odd transposed": ((33, 7), lambda t: t.t()), "permuted": ((5, 6, 7), lambda t: t.permute(2, 0, 1)),
+           "channels last": ((3, 8, 5, 4), lambda t: t.to(memory_format=torch.channels_last)), "sizes of one": ((1, 9, 1), lambda t: t.permute(2, 1, 0))}
+
+
+@pytest.mark.parametrize("name", sorted(LAYOUTS))
+@pytest.mark.parametrize("t", (torch.float32, torch.bfloat16))
+def test_dense_layouts(name, t):
+    """A gradient has its parameter's strides, whatever they are."""
+    moe = lib()
+    shape, layout = LAYOUTS[name]
+    g = torch.Generator(device=dev()).manual_seed(3)
+    first = torch.randn(shape, generator=g, device=dev()).to(t)
+    grads = [layout(first), torch.randn((50,), generator=g, device=dev()).to(t)]
+    want = float(sum(v.double().square().sum() for v in grads).sqrt())
+    refs = [v.double() / (want + 1e-6) for v in grads]
+    half = torch.finfo(t).eps / 2
+
+    def close(got):
+        for o, r in zip(got, refs):
+            assert bool(((o.double() - r).abs() <= (2 * NORM + half) * r.abs()).all())
+
+    assert abs(float(moe.grad_norm(grads)) - want) <= NORM * want
+    out = [torch.full_like(v, 3.0) for v in grads]           # of the same strides
+    assert abs(float(moe.clip_grads(grads, 1.0, out=out)) - want) <= NORM * want
+    close(out)
+    moe.clip_grads(grads, 1.0)
+    close(grads)
+
+
+def test_a_transposed_parameter():
+    moe = lib()
+    w = torch.nn.Parameter(torch.randn((64, 32), generator=torch.Generator().manual_seed(1)).to(dev()).t())
+    b = torch.nn.Parameter(torch.zeros(64, device=dev()))
+    x = torch.randn((10, 64), generator=torch.Generator().manual_seed(2)).to(dev())
+    ((x + b) @ w.t()).square().sum().backward()
+    assert not w.grad.is_contiguous()
+    before = w.grad.double()
+    want = float((before.square().sum() + b.grad.double().square().sum()).sqrt())
+    norm = moe.clip_grad_norm([w, b], 0.5 * want)
+    assert abs(float(norm) - want) <= NORM * want
+    assert bool(((w.grad.double() - 0.5 * before).abs() <= (2 * NORM + 2.0 ** -24) * before.abs()).all())
+
+
+def test_layouts_that_are_refused():
+    """Gaps, overlaps, and an out whose elements lie elsewhere."""
+    moe = lib()
+    a = torch.ones((6, 8), device=dev())
+    for grads, out in (([a[:, :4]], None), ([a[::2]], None), ([a[:1].expand(6, 8)], None), ([a.t()], [torch.ones((8, 6), device=dev())]),
+                       ([a], [torch.ones((8, 6), device=dev()).t()]), ([a.t()], [torch.ones(48, device=dev())]),
+                       ([a[:, :4].contiguous()], [a[:, :4]])):
+        with pytest.raises(ValueError):
+            moe.clip_grads(grads, 1.0, out=out)
+    assert bool((a == 1).all())

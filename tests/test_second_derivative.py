@@ -31,7 +31,7 @@ def test_refused(loss):
     plain, = torch.autograd.grad(loss(x * x), x)
     assert torch.equal(g.detach(), plain)
     with pytest.raises(RuntimeError, match="differentiated again"):
-        (g * g).sum().backward()
+        (loss(square()(x)) + (g * g).sum()).backward()     # a penalty on the gradient beside the loss
 
 
 def test_first_derivatives_are_as_before():

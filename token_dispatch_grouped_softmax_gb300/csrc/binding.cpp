@@ -63,7 +63,8 @@ at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, const at::Tensor& li
   return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
 
-// A contiguous CUDA tensor of the current device, of the type and number of dimensions (-1: any).
+// A contiguous CUDA tensor of the current device, of the type and number of
+// dimensions (-1: any layout of any dimensions that fills its memory).
 const at::Tensor& need(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t ndim,
                        at::ScalarType or_type = at::ScalarType::Undefined) {
   if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a torch.Tensor", name);
@@ -73,8 +74,12 @@ const at::Tensor& need(PyObject* o, const char* name, at::ScalarType type, const
   if (t.get_device() != device)   // the kernels run on the current device and would be handed another GPU's memory
     refuse(PyExc_ValueError, "%s is on cuda:%d but the current device is cuda:%d", name, (int)t.get_device(), device);
   if (t.scalar_type() != type && t.scalar_type() != or_type) refuse(PyExc_TypeError, "%s must be %s", name, type_name);
+  if (ndim < 0) {
+    if (!t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, "%s must fill its memory: no gaps, no overlaps", name);
+    return t;
+  }
   if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
-  if (ndim >= 0 && t.dim() != ndim) refuse(PyExc_ValueError, "%s must have %d dims", name, (int)ndim);
+  if (t.dim() != ndim) refuse(PyExc_ValueError, "%s must have %d dims", name, (int)ndim);
   return t;
 }
 const at::Tensor& need_f32(PyObject* o, const char* name, int64_t ndim) { return need(o, name, at::kFloat, "torch.float32", ndim); }
@@ -528,6 +533,15 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   BODY_END
 }
 
+// Elements at the same places of both tensors' memory belong together.
+bool same_layout(const at::Tensor& a, const at::Tensor& b) {
+  if (a.is_contiguous() && b.is_contiguous()) return true;   // in order, whatever the shapes
+  if (a.sizes() != b.sizes()) return false;
+  for (int64_t d = 0; d < a.dim(); ++d)
+    if (a.size(d) > 1 && a.stride(d) != b.stride(d)) return false;
+  return true;
+}
+
 // (grads: a list or tuple, outs: the same or None, max_norm, eps) -> norm
 PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   ARGS(4)
@@ -551,7 +565,8 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   auto tensor = [&](PyObject* o, const char* name, at::ScalarType type, at::ScalarType or_type) -> const at::Tensor& {
     if (THPVariable_Check(o)) {
       const at::Tensor& t = THPVariable_Unpack(o);
-      if (t.is_cuda() && t.get_device() == device && (t.scalar_type() == type || t.scalar_type() == or_type) && t.is_contiguous()) return t;
+      if (t.is_cuda() && t.get_device() == device && (t.scalar_type() == type || t.scalar_type() == or_type) && t.is_non_overlapping_and_dense())
+        return t;
     }
     return need(o, name, type, or_type == at::kBFloat16 ? "torch.float32 or torch.bfloat16" : "of its gradient's type", -1, or_type);
   };
@@ -567,6 +582,7 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (q != o) {
       const at::Tensor& t = tensor(q, "a tensor of out", g.scalar_type(), at::ScalarType::Undefined);
       if (t.numel() != size[i]) refuse(PyExc_ValueError, "a tensor of out must have its gradient's size");
+      if (!same_layout(g, t)) refuse(PyExc_ValueError, "a tensor of out must have its gradient's strides");
       dst[i] = ptr(t);
     }
     const uintptr_t bytes = (uintptr_t)size[i] * (f32[i] ? 4 : 2), from = reinterpret_cast<uintptr_t>(src[i]),

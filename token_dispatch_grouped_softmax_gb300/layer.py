@@ -382,7 +382,9 @@ class MoEBlock(torch.nn.Module):
 def clip_grad_norm(parameters, max_norm, eps=1e-6):
     """Scales the parameters' gradients in place so that their 2-norm is at
     most max_norm, and returns the norm they had (ops.clip_grads); parameters
-    without a gradient are left out, one that is given twice counts once."""
+    without a gradient are left out, one that is given twice counts once; none
+    with a gradient is a ValueError.  A gradient may have any dense layout, as
+    that of a transposed parameter."""
     grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
     return ops.clip_grads(grads, max_norm, eps=eps)
 

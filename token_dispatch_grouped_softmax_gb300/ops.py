@@ -307,15 +307,15 @@ def block_norm_bwd(dh, dr, x, stats, weight=None, branch=None, post_weight=None,
 # -------------------------------------- the gradients' norm, and clipping
 
 def grad_norm(grads):
-    """The 2-norm over a list of gradients (fp32 or bf16, of any shapes) as an
-    fp32 scalar on the device."""
+    """The 2-norm over a list of gradients (fp32 or bf16, of any shapes, in any
+    dense layout) as an fp32 scalar on the device."""
     return binding().grad_clip(grads, None, 0.0, 0.0)
 
 
 def clip_grads(grads, max_norm, out=None, eps=1e-6):
     """Scales the gradients by min(1, max_norm / (norm + eps)) and returns
     their norm (grad_norm's).  In place, or into out: a list of tensors of the
-    same sizes and types that overlap nothing (out[i] may be grads[i])."""
+    same sizes, types and strides that overlap nothing (out[i] may be grads[i])."""
     return binding().grad_clip(grads, grads if out is None else out, max_norm, eps)
 
 
