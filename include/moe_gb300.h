@@ -110,9 +110,10 @@ int moe_set_gemm_pairs(int mode);
 int moe_set_pdl(int on);
 
 /* Test hook of the failure-detection path: while on (1), the grouped GEMMs
- * and the 4-bit experts' kernels launched afterwards issue no operand loads,
- * so their bounded waits run out; the kernel then records MOE_ERR_TIMEOUT,
- * stops its other warps, frees its tensor memory and returns (outputs
+ * and the 4-bit and few-token experts' kernels launched afterwards issue no
+ * operand loads, and the norms around a block none of x, so that their bounded
+ * waits run out; the kernel then records MOE_ERR_TIMEOUT, waits (bounded too)
+ * for its copies in flight, frees its tensor memory and returns (outputs
  * undefined), leaving the context usable.  Off (0) by default; not for
  * production use. */
 int moe_test_stall_gemm_producer(int on);

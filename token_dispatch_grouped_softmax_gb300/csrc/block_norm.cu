@@ -205,6 +205,7 @@ struct NormParams {
   int vectors_shared;     // w and v are in shared memory (always but with a row's own gates)
   uint32_t* status;
   uint64_t wait_limit_ns;
+  int stall;              // test hook: no copies of x
 };
 
 // Rows of the workspace for a range among several of a gate's groups: its first
@@ -222,20 +223,35 @@ __device__ __forceinline__ uint32_t norm_group_of(uint32_t T, uint32_t n, uint32
   return row < more * (share + 1) ? row / (share + 1) : more + (row - more * (share + 1)) / share;
 }
 
-__device__ __noinline__ void norm_wait_more(uint32_t bar, uint32_t phase, volatile int* abort, uint64_t limit_ns, uint32_t* status) {
-  mbar_wait_bounded(bar, phase, abort, limit_ns, status, 1, kKernNorm);
+__device__ __noinline__ bool norm_wait_more(uint32_t bar, uint32_t phase, volatile int* abort, uint64_t limit_ns, uint32_t* status) {
+  return mbar_wait_bounded(bar, phase, abort, limit_ns, status, 1, kKernNorm);
+}
+
+// After a wait for row i that ran out, by a thread that copies a stream: its
+// copies of rows i .. end - 1 are in flight, and nobody may write the ring or
+// leave before them.  Bounded too: a phase lacks what other threads did not copy.
+__device__ __noinline__ void norm_land(uint32_t bar, int i, int end, int stage, uint32_t phase, int stages, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  for (; i < end; ++i) {
+    while (!mbar_try_wait(bar + 8 * stage, phase) && globaltimer_ns() - t0 < limit_ns) {
+    }
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
 }
 
 // A row group: its rows, its ring and its sums.
 struct RowGroup {
-  static constexpr uint32_t kPrefetch = 0xffffffffu;
+  static constexpr uint32_t kPrefetch = 0xffffffffu, kGivenUp = 0xffffffffu;
   // the stream that this thread copies, if any: a thread of another warp for
   // each where the row group has as many, as all wait for the slowest
   const uint8_t* src;     // its first row of the range
   uint32_t bytes, offset; // of a row; in a stage (kPrefetch: into the L2 instead)
   uint8_t* ring;
   uint32_t row_bytes;     // of a stage
-  uint32_t bar;
+  uint32_t bar;           // kGivenUp: this thread's wait ran out
   int rows;
   float* buf;             // [2][32]: the warps' partial sums, then zeros
   int turn;
@@ -272,11 +288,18 @@ struct RowGroup {
     mbar_arrive_expect_tx(bar + 8 * stage, bytes);
     bulk_load(smem_u32(ring) + stage * row_bytes + offset, src + (int64_t)i * bytes, bytes, bar + 8 * stage);
   }
-  // Row i has landed.  A wait that runs out is reported; the rows are then
-  // undefined, and the kernel goes on to its end.
-  __device__ __forceinline__ const uint8_t* wait(const NormParams& p, int stage, uint32_t phase) const {
+  // Row i has landed.  A thread whose wait runs out reports it, lets its copies
+  // in flight land, and neither waits nor copies from then on: a stage whose
+  // phase did not complete takes no further copy.  All threads go on through
+  // the same barriers to the kernel's end, over rows that are undefined.
+  __device__ __forceinline__ const uint8_t* wait(const NormParams& p, int i, int stage, uint32_t phase) {
     const uint32_t b = bar + 8 * stage;
-    if (!mbar_try_wait(b, phase)) norm_wait_more(b, phase, abort, p.wait_limit_ns, p.status);
+    if (bar != kGivenUp && !mbar_try_wait(b, phase) && !norm_wait_more(b, phase, abort, p.wait_limit_ns, p.status)) {
+      // refill() has issued the rows below i - 1 + stages
+      if (src && offset != kPrefetch) norm_land(bar, i, min(rows, max(i - 1, 0) + p.stages), stage, phase, p.stages, p.wait_limit_ns);
+      src = nullptr;
+      bar = kGivenUp;
+    }
     return ring + stage * row_bytes;
   }
   // Between two barriers of row i, all of row i - 1's reads are done: its
@@ -319,7 +342,7 @@ __device__ __forceinline__ NormSetup norm_setup(const NormParams& p, uint8_t* sm
       const uint32_t bytes = (uint32_t)p.H * elem[k];
       const bool staged = k != kDr || dr_staged;
       if ((int)threadIdx.x == n * step) {
-        g.src = static_cast<const uint8_t*>(src[k]) + begin * bytes;
+        g.src = k == kX && p.stall ? nullptr : static_cast<const uint8_t*>(src[k]) + begin * bytes;
         g.bytes = bytes;
         g.offset = staged ? g.row_bytes : RowGroup::kPrefetch;
       }
@@ -439,7 +462,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) block_norm_kernel(const __gri
     return q;
   };
   for (int i = 0; i < rows; ++i) {
-    const uint8_t* row = rg.wait(p, stage, phase);
+    const uint8_t* row = rg.wait(p, i, stage, phase);
     const Shared own{row + p.H * (sizeof(X) + 2), p.g_f32 != 0};
     F8 r[N], y[N];
     float sy = G == kVector || G == kGroups ? 1.f : p.b;   // the factor of y, s_y among it
@@ -547,7 +570,7 @@ __global__ void __launch_bounds__(kNormThreads / 2, 1) block_norm_bwd_kernel(con
     stats(i + 1);
     // Between the sums a thread keeps r and dh w alone, and reads the row's
     // other operands from shared memory again.
-    const uint8_t* row = rg.wait(p, stage, phase);
+    const uint8_t* row = rg.wait(p, i, stage, phase);
     auto own_of = [&](int j) { return Shared{row + at_gate, p.g_f32 != 0}.load(0, c[j]); };
     auto load_y = [&](int j) {   // normed, without v
       F8 y = load8(reinterpret_cast<const uint16_t*>(row + at_y), c[j]);
@@ -824,6 +847,7 @@ NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo&
   p.vectors_shared = s.vectors_shared;
   p.status = dev.status;
   p.wait_limit_ns = dev.wait_limit_ns;
+  p.stall = dev.test_stall_producer;
   return p;
 }
 

@@ -55,7 +55,7 @@ struct DeviceInfo {
   int num_sms;
   uint32_t* status;        // device address of the status word
   uint64_t wait_limit_ns;  // bound of every device-side spin wait
-  int test_stall_producer; // test hook of the bounded-wait path (grouped GEMMs)
+  int test_stall_producer; // test hook of the bounded waits' paths
   int gemm_pairs;          // CTA pairs: 0 none, 1 every forward / dgrad grouped GEMM, 2 forward gate_up only,
                            // 3 forward gate_up and the weight-gradient GEMMs
 };
