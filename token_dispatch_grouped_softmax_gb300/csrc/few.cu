@@ -651,12 +651,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             }
             answer = __ballot_sync(0xffffffffu, last);
           }
+          // the counts, before the group's loads of the parts: by the lanes that
+          // counted, so that the barrier carries it to the others
+          __threadfence();
           if (m == 0) group_word[group] = answer;
         }
         group_sync(group);
         uint32_t mask = group_word[group];
         if (mask == 0) continue;
-        __threadfence();
         if (gate_up) {
           for (int r = m >> 6; r < x.rows; r += 2) {
             const float* from = part + (int64_t)row_of(r) * f.parts * width + 64 * x.tile + (m & 63);
