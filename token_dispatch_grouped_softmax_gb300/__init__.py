@@ -18,7 +18,7 @@ from .ops import block_norm, block_norm_bwd, clip_grads, experts_few, grad_norm,
 from . import ep
 from .ops import ep_map_replicas, eplb_plan, sort_chunks
 from .layer import (BF16Experts, BlockNormFunction, DecodeGraph, ForwardGraph, ForwardState, MoEBlock, MoELayer, MoELayerFunction,
-                    OverlappedForward, PipelinedForward, RoutedMoELayerFunction, Routing, W4Experts, clip_grad_norm, moe_backward, moe_forward,
+                    OverlappedForward, PipelinedForward, RoutedMoELayerFunction, Routing, W4Experts, block_norm_autograd, clip_grad_norm, moe_backward, moe_forward,
                     moe_forward_few, moe_forward_w4)
 
 __all__ = [
@@ -33,5 +33,5 @@ __all__ = [
     "set_pdl", "sort_chunks", "ep_map_replicas", "eplb_plan", "ep",
     "ForwardGraph", "ForwardState", "MoELayer", "OverlappedForward", "MoELayerFunction", "PipelinedForward", "moe_forward", "moe_backward",
     "Routing", "RoutedMoELayerFunction", "W4Experts", "moe_forward_w4", "moe_forward_few", "DecodeGraph",
-    "BF16Experts", "BlockNormFunction", "MoEBlock", "clip_grad_norm",
+    "BF16Experts", "BlockNormFunction", "MoEBlock", "block_norm_autograd", "clip_grad_norm",
 ]

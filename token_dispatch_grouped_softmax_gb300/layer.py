@@ -326,13 +326,18 @@ class BlockNormFunction(torch.autograd.Function):
         return g["dx"], g["d_weight"], g["d_branch"], g["d_post_weight"], g["d_gate"], None, None, None
 
 
-def block_norm(x, weight=None, branch=None, post_weight=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6):
-    """(r, h) of ops.block_norm, with gradients for the operands that ask for them."""
+def block_norm_autograd(x, weight=None, branch=None, post_weight=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6):
+    """(r, h) of ops.block_norm, with gradients for the operands that ask for
+    them: the norms outside a MoEBlock, such as the one after the last block,
+    ``block_norm_autograd(x, weight)[1]``."""
     given = (x, weight, branch, post_weight, gate)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in given):
         return BlockNormFunction.apply(*given, residual_scale, branch_scale, eps)
     t = [None if v is None else v.contiguous() for v in given]
     return ops.block_norm(*t, residual_scale, branch_scale, eps)[:2]
+
+
+block_norm = block_norm_autograd   # in this module; the package's block_norm is ops.block_norm
 
 
 class MoEBlock(torch.nn.Module):
@@ -363,8 +368,8 @@ class MoEBlock(torch.nn.Module):
                 raise ValueError("a block with a learned scale takes no gate")
             gate = self.scale.unsqueeze(0)
         if h is None:
-            h = block_norm(x, self.norm, eps=self.eps)[1]
-        return block_norm(x, next_norm, run(h), self.post_norm, gate, self.residual_scale, self.branch_scale, self.eps)
+            h = block_norm_autograd(x, self.norm, eps=self.eps)[1]
+        return block_norm_autograd(x, next_norm, run(h), self.post_norm, gate, self.residual_scale, self.branch_scale, self.eps)
 
     def forward(self, x, h=None, next_norm=None, gate=None, bias=None):
         """(r, h of the next block or None): x [T, H] the stream, h the stream

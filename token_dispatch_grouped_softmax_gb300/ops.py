@@ -288,7 +288,8 @@ def block_norm(x, weight=None, branch=None, post_weight=None, gate=None, residua
     [gates, H] fp32 or bf16, gates a divisor of T (a gate for every T / gates
     consecutive rows; 1: a learned scale; T: one a row).  Without branch r is
     None and h norms x; without weight h is None.  stats [2, T] fp32 with
-    save_for_backward, else None, for block_norm_bwd (moe_block_norm)."""
+    save_for_backward, else None, for block_norm_bwd (moe_block_norm).  As every
+    operator here it records no gradients: block_norm_autograd does."""
     return binding().block_norm(x, weight, branch, post_weight, gate, residual_scale, branch_scale, eps,
                                 bool(save_for_backward))
 
