@@ -29,3 +29,19 @@ def test_the_same_bits_again(shape):
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
     moe.sync_status()
+
+
+def test_an_out_that_overlaps_an_input_is_refused():
+    """Tokens' outputs are written while other tokens' inputs are still read."""
+    moe = lib()
+    x, ids, w, gu, dn, sgu, sdn = make(6, 128, 8, 2, 64, 64)
+    buffer = torch.zeros((12, 128), dtype=torch.bfloat16, device=dev())
+    buffer[:6] = x
+    rows = buffer[:6]
+    for bad in ((rows, rows), (rows, buffer[1:7]), (rows, buffer[5:11]), (x, gu.view(-1, 128)[3:9]), (x, dn[:6]), (x, sdn[58:64]), (x, sgu.view(-1, 128)[:6])):
+        with pytest.raises(ValueError, match="overlaps"):
+            moe.experts_few(bad[0], ids, w, gu, dn, sgu, sdn, out=bad[1])
+    assert torch.equal(rows, x)
+    y = moe.experts_few(rows, ids, w, gu, dn, sgu, sdn, out=buffer[6:])      # beside it
+    assert torch.equal(y, moe.experts_few(x, ids, w, gu, dn, sgu, sdn)) and torch.equal(rows, x)
+    moe.sync_status()

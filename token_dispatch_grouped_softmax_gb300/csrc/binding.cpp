@@ -348,6 +348,12 @@ Experts shared_expert(PyObject* gate_up, PyObject* down, int64_t H) {
   return experts(gate_up, down, H, 1, "sh_gate_up", "sh_down");
 }
 
+// Both contiguous.
+bool overlap(const at::Tensor& a, const at::Tensor& b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.data_ptr()), q = reinterpret_cast<uintptr_t>(b.data_ptr());
+  return a.nbytes() && b.nbytes() && p < q + b.nbytes() && q < p + a.nbytes();
+}
+
 // (x, ids, w, gate_up, down, sh_gate_up, sh_down, out) -> y
 PyObject* few_experts(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   ARGS(8)
@@ -360,6 +366,8 @@ PyObject* few_experts(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Experts e = experts(a[3], a[4], H, 0, "gate_up", "down"), sh = shared_expert(a[5], a[6], H);
   const at::Tensor y = a[7] == Py_None ? fresh({T, H}, at::kBFloat16, x) : need_bf16(a[7], "out", 2);
   if (y.size(0) != T || y.size(1) != H) refuse(PyExc_ValueError, "out must be [T, H]");
+  for (int i = 0; i < 7 && a[7] != Py_None; ++i)
+    if (a[i] != Py_None && overlap(y, THPVariable_Unpack(a[i]))) refuse(PyExc_ValueError, "out overlaps an input");
   size_t bytes = 0;
   check("moe_few_experts_workspace_size", f_few_experts_workspace_size(T, H, e.E, k, e.I, sh.I, &bytes));
   const at::Tensor ws = fresh({(int64_t)bytes}, at::kByte, x);

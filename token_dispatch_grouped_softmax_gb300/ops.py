@@ -262,7 +262,8 @@ def experts_few(x, ids, w, gate_up, down, sh_gate_up=None, sh_down=None, out=Non
     once (moe_few_experts).
 
     x [T, H] bf16, ids [T, k] int32, w [T, k] fp32, gate_up [E*H, 2I], down
-    [E*I, H], sh_gate_up [H, 2 I_s], sh_down [I_s, H] bf16; T at most 128."""
+    [E*I, H], sh_gate_up [H, 2 I_s], sh_down [I_s, H] bf16; T at most 128; out
+    overlaps no input."""
     return binding().few_experts(x, ids, w, gate_up, down, sh_gate_up, sh_down, out)
 
 
