@@ -197,7 +197,6 @@ struct NormParams {
   int64_t T;
   int H;
   int64_t gate_rows;      // rows of a gate's group
-  int64_t groups;
   float a, b, eps;
   int w_f32, v_f32, g_f32;
   int n_sums;             // columns' sums over all rows: w's, then v's or K's
@@ -840,7 +839,7 @@ size_t norm_gate_bytes(const BlockNorm& n) { return own_gate(n) ? (size_t)n.H * 
 NormParams norm_params(const BlockNorm& n, const NormShape& s, const DeviceInfo& dev) {
   NormParams p = {};
   p.x = n.x; p.y = n.y; p.w = n.w; p.v = n.v; p.g = n.g;
-  p.T = n.T; p.H = (int)n.H; p.groups = n.groups; p.gate_rows = n.groups ? n.T / n.groups : n.T;
+  p.T = n.T; p.H = (int)n.H; p.gate_rows = n.groups ? n.T / n.groups : n.T;
   p.a = n.a; p.b = n.b; p.eps = n.eps;
   p.w_f32 = n.w_f32; p.v_f32 = n.v_f32; p.g_f32 = n.g_f32;
   p.stages = s.stages;
