@@ -284,7 +284,8 @@ int moe_w4_dequantize(const uint32_t* qweight, const uint16_t* scales, const uin
 /* The expert layer of a decode step: y_t = sum_j w[t,j] (h[t,j] . Wd_e) with
  * h[t,j] = silu(x_t . Wg_e) * (x_t . Wu_e), e = ids[t,j], plus a shared
  * expert's output of weight 1.  Rows stay in slot order (no permutation) and
- * every weight of the experts in use is read once.
+ * every weight of the experts in use is read once for every 32 of its expert's
+ * rows.
  *   x        [T, H] bf16; gate_up [E*H, 2I], down [E*I, H] bf16 (the layout
  *            of the grouped GEMMs); sh_gate_up [H, 2 I_s], sh_down [I_s, H]
  *            bf16, or both NULL with I_s = 0

@@ -28,10 +28,12 @@
 // Consecutive rows keep the columns' sums of the backward in registers until
 // the range ends, and a gate's group ends at most twice inside a range.
 //
-// Measured: 16384 x 7168 in bf16 with a gate for each 1024 rows 148 us forward
-// (940 MB, 6.4 TB/s) and 174 backward with the sums (1.4 GB, some of it from the
-// L2).  With both norms a row has two sums to wait for: 8191 x 2048, fp32
-// stream, 37 us forward (5.5 TB/s), 44 backward (6.9).
+// Measured on inputs that come from HBM: 16384 x 7168 in bf16 with a gate for
+// each 1024 rows 156 us forward (940 MB, 6.0 TB/s) and 224 backward with the sums
+// (1.41 GB, 6.3 TB/s).  With both norms a row has two sums to wait for: 8191 x
+// 2048, fp32 stream, 37.5 us forward (201 MB, 5.4 TB/s), 56.5 backward (302 MB,
+// 5.3).  The figures beside the choices, above and below, compare variants on one
+// set of inputs used again and again, which the L2 holds in part: they are lower.
 #include <algorithm>
 
 #include "kernels.h"

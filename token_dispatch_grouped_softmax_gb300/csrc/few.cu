@@ -4,7 +4,8 @@
 //   y_t = sum_j w[t, j] (h[t, j] . Wd_e)  (+ the shared expert's, weight 1)
 //
 // With few rows an expert the weights' bytes are the cost: each weight of the
-// experts in use has to come from HBM once.  One launch streams them all.  A
+// experts in use has to come from HBM once (an expert of more than 32 rows loads
+// it again for every 32, one after another, out of the L2).  One launch streams them all.  A
 // unit of work is 128 columns of one expert's weight (64 gate and the 64 up
 // columns beside them, or 128 of down) by the whole of its K rows or a part,
 // for up to 32 rows of that expert; gate_up's units come before down's.  Blocks draw units
@@ -31,10 +32,15 @@
 // and its result does not depend on the batch.
 //
 // Measured (device time, weights from HBM): 16 tokens of H 2048, top-8 of 128,
-// I 768 121 us, 778 MB at 6.4 TB/s (the copy rate is 6.77); 64 tokens 189; one
+// I 768 126 us for 777 MB (82 experts in use), 6.2 TB/s (the copy rate is 6.7); 64
+// tokens 192, 128 tokens 222, both for 1.2 GB; one
 // token 27 us for 75 MB: there the dependent steps count (the lists 1 us, the
 // first tile 3, h to down 4, down's rows and the sum 6), and 96 blocks read
-// gate_up at 50 GB/s a microsecond each.  The tensor pipe is 5 to 9 % busy
+// gate_up's 512 KB each in 10 us.  Beyond 32 slots a slot's place in the
+// lists is counted over the slots before it, by every block and before the first
+// load: a call with weights of next to nothing (H 64, I 64, E 128) takes 19 us with
+// 128 slots, 29 with 512, 50 with 1024, 156 with 2048 and 373 with 4096 (128 tokens,
+// top-32; with H 2048, I 768 713).  The tensor pipe is 5 to 9 % busy
 // whether the weights are A or B: MMAs of 32 rows or of 16, four accumulators
 // in turn instead of one, and weights as B with N = 128 all took the same time.
 #include <algorithm>

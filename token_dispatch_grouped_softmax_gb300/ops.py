@@ -259,7 +259,7 @@ def experts_few(x, ids, w, gate_up, down, sh_gate_up=None, sh_down=None, out=Non
     """y [T, H] bf16 with y_t = sum_j w[t, j] (silu(x_t . Wg) * (x_t . Wu)) . Wd,
     e = ids[t, j] (-1: an empty slot, adds nothing), plus the shared expert's
     output: the bf16 experts of a decode step in slot order, each weight read
-    once (moe_few_experts).
+    once for every 32 of its expert's rows (moe_few_experts).
 
     x [T, H] bf16, ids [T, k] int32, w [T, k] fp32, gate_up [E*H, 2I], down
     [E*I, H], sh_gate_up [H, 2 I_s], sh_down [I_s, H] bf16; T at most 128; out
